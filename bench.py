@@ -59,7 +59,7 @@ from topology_scheduled_gb300.workloads import WORKLOADS, make_qkv, random_densi
 DEFAULT_WORKLOAD = "b2h32s32768"
 # the attention kernel's sources: a traffic record applies only to the build it was taken on
 ATTN_SOURCES = [os.path.join(ROOT, "topology_scheduled_gb300", "csrc", f)
-                for f in ("attention.cu", "tsa_device.cuh", "tsa_internal.h")]
+                for f in ("attention.cu", "attention_kernel.cuh", "score_terms.cuh", "tsa_device.cuh", "tsa_internal.h")]
 
 
 def parse():

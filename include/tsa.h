@@ -62,6 +62,9 @@ typedef enum {
     TSA_ERR_DEVICE = 9             /* device: another device-side check failed             */
 } tsa_status;
 
+/* Most buckets of a relative position bias (tsa_biased_attention_fwd). */
+#define TSA_MAX_BUCKETS 256
+
 typedef enum { TSA_F16 = 0, TSA_BF16 = 1 } tsa_dtype;
 
 /* Human-readable name of a status code (static storage; never NULL). */
@@ -303,6 +306,61 @@ tsa_status tsa_scheduled_attention_backward(const void *Q, const void *K, const 
                                             tsa_dtype dtype, int64_t B, int64_t H, int64_t S,
                                             int64_t D, int64_t block, float scale, void *workspace,
                                             size_t workspace_bytes, tsa_stream_t stream);
+
+/*
+ * Scheduled attention with a learned relative position bias: for query q and key k of lane l,
+ * head h = l mod H,
+ *   z = scale * <Q[l][q], K[l][k]> + bias[h][b],   b the last bucket with starts[b] <= q - k,
+ * and O = softmax(z over the allowed keys) V, with the allowed keys of tsa_scheduled_attention.
+ *
+ *   Q, K, V       in,  [B*H, S, D] of `dtype`, 16-byte aligned.
+ *   row_ptr, col_idx  the CSR of `block`-token blocks; nnz_cap: entries of col_idx.  A row that
+ *                 points outside them is empty and reported, as any bad row.
+ *   bias          in,  [H, num_buckets] of `dtype` on the device.  A bias of -1e30 or less (the
+ *                 lowest bf16 value, -inf) leaves its bucket's keys out.
+ *   bucket_starts in,  num_buckets int32 in HOST memory, read during the call: ascending (equal
+ *                 starts make an empty bucket), the first one 0; the last bucket is open.
+ *   O             out, [B*H, S, D] of `dtype`, 16-byte aligned; rows without keys are 0.
+ *   lse           out, [B*H, S] float32, 4-byte aligned (16-byte for the backward call), or NULL:
+ *                 the log-sum-exp of z per row, -inf for rows without keys.
+ * Outputs overlap no input and no other output.
+ *
+ * Limits: those of tsa_scheduled_attention, 1 <= num_buckets <= TSA_MAX_BUCKETS,
+ * scale >= 1e-30.  Rows past S are neither read nor written, in no lane.  Errors:
+ * INVALID_ARGUMENT, UNSUPPORTED, NOT_DEVICE_POINTER, DEVICE_MISMATCH, CUDA; on the device
+ * BAD_SCHEDULE (a row is cut at its first bad entry), TIMEOUT.
+ */
+tsa_status tsa_biased_attention_fwd(const void *Q, const void *K, const void *V,
+                                    const int32_t *row_ptr, const int32_t *col_idx, int64_t nnz_cap,
+                                    const void *bias, const int32_t *bucket_starts,
+                                    int64_t num_buckets, void *O, float *lse, tsa_dtype dtype,
+                                    int64_t B, int64_t H, int64_t S, int64_t D, int64_t block,
+                                    float scale, tsa_stream_t stream);
+
+/*
+ * Differential attention over a schedule: the halves of a head's dimension hold two maps,
+ * Q = [q1 | q2] and K = [k1 | k2] of D / 2 each, and
+ *   O = (softmax(scale q1.k1) - lambda softmax(scale q2.k2)) V,
+ *   lambda = exp(<lambda_q1, lambda_k1>) - exp(<lambda_q2, lambda_k2>) + lambda_init,
+ * both maps over the allowed keys of tsa_scheduled_attention, V of the full D.
+ *
+ *   lambda_q1 .. lambda_k2  in, [lambda_heads, D / 2] of `dtype`; lambda_heads is H (a lambda
+ *                 per head) or 1 (one for all).
+ *   O             out, [B*H, S, D] of `dtype`, 16-byte aligned; rows without keys are 0.
+ *   O2            out, the second map's softmax(..) V, shaped as O, or NULL; the backward call
+ *                 needs it.
+ *   lse           out, [2, B*H, S] float32: each map's log-sum-exp, or NULL.
+ * The other arguments, limits and errors are those of tsa_biased_attention_fwd.
+ */
+tsa_status tsa_differential_attention_fwd(const void *Q, const void *K, const void *V,
+                                          const int32_t *row_ptr, const int32_t *col_idx,
+                                          int64_t nnz_cap, const void *lambda_q1,
+                                          const void *lambda_k1, const void *lambda_q2,
+                                          const void *lambda_k2, int64_t lambda_heads,
+                                          float lambda_init, void *O, void *O2, float *lse,
+                                          tsa_dtype dtype, int64_t B, int64_t H, int64_t S,
+                                          int64_t D, int64_t block, float scale,
+                                          tsa_stream_t stream);
 
 /* Size of the device array behind tsa_build_schedule_noalloc: 16 MiB on every device that
  * loads the library, held until the process exits. */

@@ -1,0 +1,79 @@
+"""Refusals of the attentions with learned score terms that need no GPU, and their bucket starts."""
+import ctypes
+
+import pytest
+import torch
+
+import topology_scheduled_gb300 as tsa
+
+F = 1 << 20        # any aligned address: never read on these paths
+M = 1 << 24        # farther apart than a tensor of the calls below is long
+
+
+def _starts(*values):
+    return (ctypes.c_int32 * max(1, len(values)))(*values)
+
+
+def _biased(**change):
+    a = dict(Q=F, K=F + M, V=F + 2 * M, row_ptr=F, col_idx=F, nnz_cap=10, bias=F + 3 * M, starts=_starts(0, 1, 2, 8), n=4,
+             O=F + 4 * M, lse=F + 5 * M, dtype=1, B=1, H=2, S=1024, D=64, block=64, scale=0.125, stream=None)
+    a.update(change)
+    return tsa.lib().tsa_biased_attention_fwd(*a.values())
+
+
+def _diff(**change):
+    a = dict(Q=F, K=F + M, V=F + 2 * M, row_ptr=F, col_idx=F, nnz_cap=10, lq1=F + 3 * M, lk1=F + 3 * M + 512,
+             lq2=F + 3 * M + 1024, lk2=F + 3 * M + 1536, heads=2, init=0.5, O=F + 4 * M, O2=F + 5 * M, lse=F + 6 * M,
+             dtype=1, B=1, H=2, S=1024, D=64, block=64, scale=0.125, stream=None)
+    a.update(change)
+    return tsa.lib().tsa_differential_attention_fwd(*a.values())
+
+
+BOTH = [dict(Q=None), dict(row_ptr=None), dict(O=None), dict(dtype=7), dict(B=0), dict(S=0), dict(nnz_cap=0),
+        dict(scale=0.0), dict(scale=-0.1), dict(scale=float("nan")), dict(Q=F + 8), dict(O=F + 4 * M + 2),
+        dict(lse=F + 5 * M + 2), dict(O=F), dict(lse=F + M + 64), dict(row_ptr=F + 2)]
+
+
+@pytest.mark.parametrize("change", BOTH + [dict(bias=None), dict(starts=None), dict(n=0), dict(starts=_starts(1, 2, 3, 4)),
+                                           dict(starts=_starts(0, 5, 4, 8)), dict(bias=F + 3 * M + 1),
+                                           dict(lse=F + 4 * M)])
+def test_biased_arguments(change):
+    assert _biased(**change) == 1  # TSA_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("change", BOTH + [dict(lq1=None), dict(lk2=None), dict(heads=3), dict(heads=0),
+                                           dict(init=float("inf")), dict(lk1=F + 3), dict(O2=F + 4 * M),
+                                           dict(O2=F + 5 * M + 4)])
+def test_differential_arguments(change):
+    assert _diff(**change) == 1
+
+
+@pytest.mark.parametrize("change", [dict(D=96), dict(block=16), dict(H=70000), dict(S=1 << 31), dict(B=64, S=1 << 25),
+                                    dict(nnz_cap=1 << 30)])
+def test_sizes_that_are_not_supported(change):
+    assert _biased(**change) == 2 and _diff(**change) == 2
+
+
+def test_too_many_buckets():
+    assert _biased(n=257, starts=_starts(*range(257))) == 2
+
+
+def test_bucket_starts():
+    s = tsa.relative_bucket_starts(32, 128)
+    assert s[:17] == list(range(17)) and len(s) == 32 and s[-1] < 128
+    for i in range(16):  # the border of bucket 16 + i, written out: 16 * 8 ** (i / 16)
+        d = s[16 + i]
+        assert d ** 16 >= 16 ** 16 * 8 ** i and (d - 1) ** 16 < 16 ** 16 * 8 ** i
+    assert tsa.relative_bucket_starts(2, 2) == [0, 1]
+    for n, most in ((0, 5), (3, 9), (258, 1000), (32, 16)):
+        with pytest.raises(ValueError):
+            tsa.relative_bucket_starts(n, most)
+
+
+def test_binding_checks_need_no_gpu():
+    x = torch.zeros((1, 1, 64, 64), dtype=torch.float16)
+    rp, ci = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        tsa.tsa_biased_attention(x, x, x, rp, ci, torch.zeros((1, 2), dtype=torch.float16), [0, 1])
+    with pytest.raises(ValueError):
+        tsa.tsa_differential_attention(x, x, x, rp, ci, *(torch.zeros(32, dtype=torch.float16) for _ in range(4)), 0.5)

@@ -59,6 +59,11 @@ SIGNATURES = {
     "tsa_scheduled_attention_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P,
                                                         ctypes.c_int, _I64, _I64, _I64, _I64, _I64,
                                                         ctypes.c_float, _P, _SZ, _P]),
+    "tsa_biased_attention_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_int, _I64,
+                                                _I64, _I64, _I64, _I64, ctypes.c_float, _P]),
+    "tsa_differential_attention_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _I64,
+                                                      ctypes.c_float, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64,
+                                                      _I64, _I64, ctypes.c_float, _P]),
     "tsa_topology_attention_host": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64,
                                                    _I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_float,
                                                    _P, _P, _P, _P, _P, _P, _I64, _P, _SZ, _I64, _P]),

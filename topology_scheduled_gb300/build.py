@@ -21,9 +21,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtsa.so")
 
-SOURCES = ["api.cu", "schedule.cu", "segment.cu", "attention.cu", "backward.cu", "noalloc.cu"]
-HEADERS = [os.path.join(CSRC, "tsa_device.cuh"), os.path.join(CSRC, "tsa_internal.h"),
-           os.path.join(INCLUDE, "tsa.h")]
+SOURCES = ["api.cu", "schedule.cu", "segment.cu", "attention.cu", "attention_biased.cu",
+           "attention_differential.cu", "terms_api.cu", "backward.cu", "noalloc.cu"]
+HEADERS = [os.path.join(CSRC, h) for h in ("attention_kernel.cuh", "score_terms.cuh", "tsa_device.cuh",
+                                           "tsa_internal.h")] + [os.path.join(INCLUDE, "tsa.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -23,6 +23,10 @@ struct DeviceState {
 DeviceState g_devices[kMaxDevices];
 std::mutex g_mutex;
 std::atomic<unsigned> g_epoch{0};
+// Process-wide test hook for the failure path (tsa_debug_set_wait_injection).
+std::atomic<unsigned> g_wait_injection{0u};
+
+}  // namespace
 
 tsa_status current_device(int *dev) {
     // Launch errors are read back with cudaGetLastError after each launch; an error an earlier
@@ -40,9 +44,6 @@ tsa_status current_device(int *dev) {
 }
 
 // Device addresses of the status words (looked up once per device) and a fresh epoch.
-// Process-wide test hook for the failure path (tsa_debug_set_wait_injection).
-std::atomic<unsigned> g_wait_injection{0u};
-
 tsa_status device_flags(int dev, DeviceFlags *f) {
     {
         std::lock_guard<std::mutex> lock(g_mutex);
@@ -81,11 +82,7 @@ tsa_status check_device_ptr(const void *p, int dev) {
     return TSA_OK;
 }
 
-#define TSA_TRY(expr)                       \
-    do {                                    \
-        const tsa_status s_ = (expr);       \
-        if (s_ != TSA_OK) return s_;        \
-    } while (0)
+namespace {
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                    const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -107,6 +104,8 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+}  // namespace
+
 // Row-major [rows, cols] 16-bit matrix; boxes of 64 columns (128 B, 128-byte swizzle) x box_rows.
 bool encode_2d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t rows, uint64_t cols,
                uint32_t box_rows) {
@@ -122,10 +121,26 @@ bool encode_2d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t rows, uint
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_3d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t lanes, uint64_t rows, uint64_t cols,
+               uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cols, rows, lanes};
+    const cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void *>(ptr), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + nb && y < x + na;
 }
+
+namespace {
 
 tsa_status launch_attention_checked(const void *Q, const void *K, const void *V, const int32_t *row_ptr,
                                     const int32_t *col_idx, void *O, float *lse, bool bf16, int64_t lanes,
@@ -431,9 +446,10 @@ tsa_status launch_attention_checked(const void *Q, const void *K, const void *V,
     a.tmQ = &tmQ;
     a.tmK = &tmK;
     a.tmV = &tmV;
-    a.tmO = &tmO;
+    a.tmO = a.tmO2 = &tmO;
     a.row_ptr = row_ptr;
     a.col_idx = col_idx;
+    a.nnz_cap = INT_MAX;
     a.O = static_cast<uint16_t *>(O);
     a.lse = lse;
     a.nb = (int)((S + 63) / 64);  // the kernel works in 64-token blocks
@@ -602,7 +618,10 @@ tsa_status tsa_last_device_status(tsa_stream_t stream) {
     unsigned bits = 0;
     const unsigned zero = 0;
     if (cudaMemcpyFromSymbol(&bits, g_status, sizeof(bits)) != cudaSuccess ||
-        cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) {
+        cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess ||
+        // a launch that gave up and is replayed (a captured graph keeps its epoch) runs again
+        ((bits & kDevTimeout) != 0u &&
+         cudaMemcpyToSymbol(g_abort_epoch, &zero, sizeof(zero)) != cudaSuccess)) {
         cudaGetLastError();
         return TSA_ERR_CUDA;
     }

@@ -115,6 +115,24 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// 3-D tiled load / store: x within a row, y the row within a lane, z the lane.  Rows outside the
+// lane read as zero and are not written, whatever follows the lane in memory.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+
 // Plain bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) from global
 // to shared memory; completes `bytes` on the mbarrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -401,6 +419,13 @@ __device__ __forceinline__ void add_half(float &acc, uint32_t w) {
         asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(acc) : "h"(h));
     else
         asm("add.rn.f32.f16 %0, %1, %0;" : "+f"(acc) : "h"(h));
+}
+
+// One 16-bit float (f16 or bf16), widened exactly.
+template <bool kBF16>
+__device__ __forceinline__ float widen16(uint32_t h16) {
+    if constexpr (kBF16) return __uint_as_float(h16 << 16);
+    else return __half2float(__ushort_as_half((unsigned short)h16));
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,

@@ -7,9 +7,25 @@
 #include <stdint.h>
 
 #include "tsa.h"
+#include "score_terms.cuh"
 #include "tsa_device.cuh"
 
 namespace tsa {
+
+// Host side of every call (api.cu).
+#define TSA_TRY(expr)                       \
+    do {                                    \
+        const tsa_status s_ = (expr);       \
+        if (s_ != TSA_OK) return s_;        \
+    } while (0)
+tsa_status current_device(int *dev);
+tsa_status device_flags(int dev, DeviceFlags *f);
+tsa_status check_device_ptr(const void *p, int dev);
+// Row-major 16-bit tensors [rows, cols] and [lanes, rows, cols]; boxes of 64 columns x box_rows.
+bool encode_2d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t rows, uint64_t cols, uint32_t box_rows);
+bool encode_3d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t lanes, uint64_t rows, uint64_t cols,
+               uint32_t box_rows);
+bool overlaps(const void *a, size_t na, const void *b, size_t nb);
 
 // Dynamic shared memory of the attention kernel.  The D = 128 figure is the largest size at
 // which two CTAs fit on one SM (2 x (115712 + 1024 reserved) = 228 KB); it covers the
@@ -21,8 +37,11 @@ __host__ __device__ constexpr int kAttnSmemBytes() {
 
 struct AttnLaunch {
     const CUtensorMap *tmQ, *tmK, *tmV, *tmO;
+    const CUtensorMap *tmO2;  // differential: the second map's output (otherwise tmO again)
     const int32_t *row_ptr, *col_idx;
-    uint16_t *O;  // the output (a partial last block is written with plain stores)
+    int nnz_cap;  // entries of col_idx (read with score terms only)
+    uint16_t *O;  // the output (a partial last block is written with plain stores); differential:
+                  // the second map's output, null when it is not wanted
     float *lse;  // optional: natural-log log-sum-exp of the scaled scores per query row
     int nb, S, D, lanes;  // nb: 64-token blocks
     bool bf16;
@@ -33,6 +52,8 @@ struct AttnLaunch {
 };
 
 tsa_status launch_scheduled_attention(const AttnLaunch &a);
+tsa_status launch_biased_attention(const AttnLaunch &a, const BiasTerms &terms);
+tsa_status launch_differential_attention(const AttnLaunch &a, const DiffTerms &terms);
 
 // Byte offsets of the backward pass's workspace regions (each 256-byte aligned).
 struct BwdWorkspace {

@@ -1,0 +1,170 @@
+"""Binding of the attentions with learned score terms (include/tsa.h): argument marshalling only.
+
+``tsa_biased_attention*``       -- a learned bias per head and bucket of the distance q - k;
+``tsa_differential_attention*`` -- the difference of two softmax maps, weighted by a learned lambda.
+
+Like the calls of ``binding`` they run in libtsa.so on the current stream (or ``stream``) and
+raise when a call fails; there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from .binding import TsaError, _check, _check_qkv, _dtype_code, _lanes_S_D, _stream, lib
+
+MAX_BUCKETS = 256
+
+
+def relative_bucket_starts(num_buckets: int, max_distance: int) -> list[int]:
+    """Starts of ``num_buckets`` (even) buckets of the distance q - k: one per distance below
+    num_buckets / 2, then borders in geometric steps up to ``max_distance``, the last bucket open.
+    Start h + i is the smallest d with d / h >= (max_distance / h) ** (i / h), h = num_buckets / 2,
+    found in integer arithmetic."""
+    h = num_buckets // 2
+    if num_buckets < 2 or num_buckets % 2 or num_buckets > MAX_BUCKETS or max_distance <= h:
+        raise ValueError(f"num_buckets must be even, 2 to {MAX_BUCKETS}, and max_distance above half of it")
+    starts = list(range(h))
+    d = h
+    for i in range(h):
+        border = max_distance ** i * h ** (h - i)  # d ** h reaches it
+        lo, hi = d, max_distance
+        while lo < hi:
+            mid = (lo + hi) // 2
+            lo, hi = (lo, mid) if mid ** h >= border else (mid + 1, hi)
+        d = lo
+        starts.append(d)
+    return starts
+
+
+def _starts(bucket_starts, bias):
+    """The starts as a host array of int32."""
+    if isinstance(bucket_starts, torch.Tensor):
+        if bucket_starts.is_cuda:
+            raise ValueError("bucket_starts must be host integers")
+        bucket_starts = bucket_starts.tolist()
+    n = len(bucket_starts)
+    if bias.shape[-1] != n:
+        raise ValueError(f"bias has {bias.shape[-1]} buckets, bucket_starts {n}")
+    if any(not 0 <= s < 1 << 31 for s in bucket_starts):
+        raise ValueError("bucket_starts must be distances that fit 32 bits")
+    return (ctypes.c_int32 * max(n, 1))(*bucket_starts), n
+
+
+def _schedule(row_ptr, col_idx, rows, device):
+    """Checks a CSR of `rows` rows; col_idx with at least one entry."""
+    for name, t in (("row_ptr", row_ptr), ("col_idx", col_idx)):
+        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be a contiguous int32 tensor on the inputs' device")
+    if row_ptr.numel() != rows + 1:
+        raise ValueError(f"row_ptr must hold {rows + 1} entries")
+    return col_idx if col_idx.numel() > 0 else torch.zeros(1, dtype=torch.int32, device=device)
+
+
+def _learned(name, t, shape, like):
+    if t.shape != torch.Size(shape) or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(shape)} on {like.device}")
+
+
+def _output(name, t, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _on(stream, *tensors):
+    """The stream's handle; memory made here for another stream than the current one is kept for it."""
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        if s != torch.cuda.current_stream():
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+    return _stream(stream)
+
+
+def _blocks(S, block):
+    return -(-S // block) if block > 0 else 0
+
+
+def _lambda_heads(lambdas, H, D, like):
+    """1 (one lambda for all heads) or H; each vector [D / 2], [1, D / 2] or [H, D / 2]."""
+    heads = 1 if lambdas[0].dim() == 1 else lambdas[0].shape[0]
+    if heads not in (1, H):
+        raise ValueError(f"the lambda vectors must be of one head or of {H}")
+    for name, t in zip(("lambda_q1", "lambda_k1", "lambda_q2", "lambda_k2"), lambdas):
+        _learned(name, t, (D // 2,) if lambdas[0].dim() == 1 else (heads, D // 2), like)
+    return heads
+
+
+def tsa_biased_attention(Q, K, V, row_ptr, col_idx, bias, bucket_starts, scale: float | None = None, *,
+                         out=None, block: int = 64, stream=None):
+    """Scheduled attention with a learned relative position bias: softmax(scale q.k +
+    bias[head, bucket(q - k)]) V over the CSR, in the inputs' type and shape.
+
+    ``bias`` is [H, buckets] of the inputs' type, ``bucket_starts`` the buckets' ascending first
+    distances (host integers, the first one 0; see ``relative_bucket_starts``)."""
+    return tsa_biased_attention_fwd(Q, K, V, row_ptr, col_idx, bias, bucket_starts, scale, out=out, block=block,
+                                    stream=stream, with_lse=False)
+
+
+def tsa_biased_attention_fwd(Q, K, V, row_ptr, col_idx, bias, bucket_starts, scale: float | None = None, *,
+                             out=None, lse=None, block: int = 64, stream=None, with_lse: bool = True):
+    """tsa_biased_attention that also returns the rows' log-sum-exp ([B*H, S] float32) for the backward."""
+    _check_qkv(Q=Q, K=K, V=V)
+    B, H, S, D = _lanes_S_D(Q)
+    dev = Q.device
+    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
+    starts, n = _starts(bucket_starts, bias)
+    _learned("bias", bias, (H, n), Q)
+    out = _output("out", out, Q.shape, Q.dtype, dev)
+    lse = _output("lse", lse, (B * H, S), torch.float32, dev) if with_lse else None
+    _check(lib().tsa_biased_attention_fwd(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(), bias.data_ptr(),
+        starts, n, out.data_ptr(), lse.data_ptr() if with_lse else None, _dtype_code(Q), B, H, S, D, block,
+        1.0 / math.sqrt(D) if scale is None else float(scale), _on(stream, out, lse, ci)), "tsa_biased_attention_fwd")
+    return (out, lse) if with_lse else out
+
+
+def tsa_differential_attention(Q, K, V, row_ptr, col_idx, lambda_q1, lambda_k1, lambda_q2, lambda_k2,
+                               lambda_init: float, scale: float | None = None, *, out=None, block: int = 64,
+                               stream=None):
+    """Differential attention over the CSR: (softmax(scale q1.k1) - lambda softmax(scale q2.k2)) V,
+    in the inputs' type and shape, where q1 | q2 and k1 | k2 are the halves of Q's and K's rows and
+    lambda = exp(lambda_q1.lambda_k1) - exp(lambda_q2.lambda_k2) + lambda_init.
+
+    The lambda vectors are [H, D/2] (a lambda per head), [1, D/2] or [D/2] (one for all heads), of
+    the inputs' type; ``scale`` defaults to (D/2) ** -0.5."""
+    return tsa_differential_attention_fwd(Q, K, V, row_ptr, col_idx, lambda_q1, lambda_k1, lambda_q2, lambda_k2,
+                                          lambda_init, scale, out=out, block=block, stream=stream,
+                                          for_backward=False)
+
+
+def tsa_differential_attention_fwd(Q, K, V, row_ptr, col_idx, lambda_q1, lambda_k1, lambda_q2, lambda_k2,
+                                   lambda_init: float, scale: float | None = None, *, out=None, out2=None, lse=None,
+                                   block: int = 64, stream=None, for_backward: bool = True):
+    """tsa_differential_attention that also returns what its backward pass reads: the second map's
+    output (shaped as the output) and both maps' log-sum-exp ([2, B*H, S] float32)."""
+    _check_qkv(Q=Q, K=K, V=V)
+    B, H, S, D = _lanes_S_D(Q)
+    dev = Q.device
+    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
+    lambdas = (lambda_q1, lambda_k1, lambda_q2, lambda_k2)
+    heads = _lambda_heads(lambdas, H, D, Q)
+    out = _output("out", out, Q.shape, Q.dtype, dev)
+    if for_backward:
+        out2 = _output("out2", out2, Q.shape, Q.dtype, dev)
+        lse = _output("lse", lse, (2, B * H, S), torch.float32, dev)
+    else:
+        out2 = lse = None
+    _check(lib().tsa_differential_attention_fwd(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(),
+        *(t.data_ptr() for t in lambdas), heads, float(lambda_init), out.data_ptr(),
+        out2.data_ptr() if for_backward else None, lse.data_ptr() if for_backward else None, _dtype_code(Q), B, H, S,
+        D, block, (D / 2) ** -0.5 if scale is None else float(scale), _on(stream, out, out2, lse, ci)),
+        "tsa_differential_attention_fwd")
+    return (out, out2, lse) if for_backward else out
