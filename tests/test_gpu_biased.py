@@ -6,6 +6,7 @@ import torch
 import topology_scheduled_gb300 as tsa
 from _terms import U, _close, biased
 from test_gpu_backward import _schedule
+from topology_scheduled_gb300.autograd import biased_attention
 from topology_scheduled_gb300.workloads import random_density_csr
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +121,76 @@ def test_bad_rows_are_reported():
                      ([0, 1, 3, 5, 7], [0, 0, 1, 1, 3, 0, 3])):    # a block after the row's own
         tsa.tsa_biased_attention(q, k, v, *_dev(ptr, idx), bias, STARTS["geometric"])
         assert tsa.tsa_last_device_status() == 8
+
+
+BACKWARD = [(1, 1, 1, 64, torch.float16, 64, "dense", "geometric"), (1, 2, 2, 128, torch.bfloat16, 64, "dense", "steps"),
+            (1, 2, 63, 64, torch.bfloat16, 64, "dense", "geometric"), (3, 2, 65, 128, torch.float16, 128, "dense", "single"),
+            (2, 2, 384, 64, torch.bfloat16, 64, "holes", "geometric"), (1, 2, 640, 128, torch.bfloat16, 64, "random", "far"),
+            (1, 3, 1000, 64, torch.float16, 128, "random", "steps"), (2, 2, 1000, 128, torch.float16, 64, "random", "geometric"),
+            (1, 1, 450, 128, torch.bfloat16, 64, "holes", "empty buckets"), (1, 2, 300, 64, torch.float16, 64, "empty", "geometric"),
+            (1, 1, 700, 64, torch.float16, 64, "diagonal", "fine"), (1, 1, 500, 128, torch.float16, 64, "dense", "fine"),
+            (1, 1, 900, 64, torch.bfloat16, 64, "dense", "far")]
+
+
+@pytest.mark.parametrize("B,H,S,D,dtype,block,kind,starts", BACKWARD)
+def test_backward(B, H, S, D, dtype, block, kind, starts):
+    starts = STARTS[starts]
+    q, k, v, do, bias = _inputs(B, H, S, D, dtype, len(starts), S + D)
+    rp, ci = _csr(kind, S, block, seed=H)
+    ref = biased(q, k, v, rp, ci, block, D ** -0.5, bias, starts, do)
+    rpd, cid = _dev(rp, ci)
+    qd, kd, vd, dod, bd = (x.to(DEV) for x in (q, k, v, do, bias))
+    O, lse = tsa.tsa_biased_attention_fwd(qd, kd, vd, rpd, cid, bd, starts, block=block)
+    N, rows = B * H * S, 64
+    big = [torch.full((N + rows, D), 7.0, dtype=dtype, device=DEV) for _ in range(3)]
+    outs = [x[:N].view(B, H, S, D) for x in big]
+    got = tsa.tsa_biased_attention_backward(qd, kd, vd, O, dod, lse, rpd, cid, bd, starts, block=block, dq=outs[0],
+                                            dk=outs[1], dv=outs[2])
+    assert tsa.tsa_last_device_status() == 0
+    for x in big:  # rows behind the last lane stay as they were
+        assert bool((x[N:] == 7.0).all())
+    for name, x in zip(("dQ", "dK", "dV", "dbias"), got):
+        _close(x, *ref[name], name)
+    if starts[-1] >= S:  # a bucket that no distance reaches
+        assert bool((got[3][:, -1] == 0).all())
+    again = tsa.tsa_biased_attention_backward(qd, kd, vd, O, dod, lse, rpd, cid, bd, starts, block=block)
+    for x, y in zip(got, again):
+        assert torch.equal(x, y)
+
+
+def test_backward_with_buckets_left_out():
+    """Keys whose bucket is left out get no gradient, nor does the bucket, the open last one included."""
+    B, H, S, D = 1, 2, 300, 64
+    starts = [0, 1, 8, 70]
+    q, k, v, do, bias = _inputs(B, H, S, D, torch.bfloat16, 4, 13)
+    bias[0, 3], bias[1, 0], bias[1, 2] = -float("inf"), torch.finfo(torch.bfloat16).min, -1e35
+    rp, ci = _csr("dense", S, 64)
+    ref = biased(q, k, v, rp, ci, 64, D ** -0.5, bias, starts, do)
+    rpd, cid = _dev(rp, ci)
+    qd, kd, vd, dod, bd = (x.to(DEV) for x in (q, k, v, do, bias))
+    O, lse = tsa.tsa_biased_attention_fwd(qd, kd, vd, rpd, cid, bd, starts)
+    got = tsa.tsa_biased_attention_backward(qd, kd, vd, O, dod, lse, rpd, cid, bd, starts)
+    assert tsa.tsa_last_device_status() == 0
+    for name, x in zip(("dQ", "dK", "dV", "dbias"), got):
+        _close(x, *ref[name], name)
+    assert got[3][0, 3] == 0 and got[3][1, 0] == 0 and got[3][1, 2] == 0
+
+
+def test_autograd():
+    B, H, S, D = 2, 2, 200, 64
+    starts = STARTS["geometric"]
+    q, k, v, do, bias = _inputs(B, H, S, D, torch.float16, 32, 21)
+    rp, ci = _csr("random", S, 64, 5)
+    ref = biased(q, k, v, rp, ci, 64, 0.2, bias, starts, do)
+    leaves = [x.to(DEV).requires_grad_(True) for x in (q, k, v, bias)]
+    # strided views of the inputs, an expanded upstream gradient
+    O = biased_attention(leaves[0].transpose(1, 2).contiguous().transpose(1, 2), *leaves[1:3], *_dev(rp, ci), leaves[3],
+                         starts, 0.2)
+    O.backward(do.to(DEV))
+    for name, x in zip(("dQ", "dK", "dV", "dbias"), leaves):
+        _close(x.grad, *ref[name], name)
+    leaves = [x.to(DEV).requires_grad_(True) for x in (q, k, v, bias)]
+    biased_attention(*leaves[:3], *_dev(rp, ci), leaves[3], starts, 0.2).sum().backward()
+    ref = biased(q, k, v, rp, ci, 64, 0.2, bias, starts, torch.ones_like(do))
+    for name, x in zip(("dQ", "dK", "dV", "dbias"), leaves):
+        _close(x.grad, *ref[name], name)

@@ -6,6 +6,7 @@ import torch
 import topology_scheduled_gb300 as tsa
 from _terms import _close, differential
 from test_gpu_biased import DEV, _csr, _dev
+from topology_scheduled_gb300.autograd import differential_attention
 
 pytestmark = pytest.mark.gpu
 INIT = 0.5
@@ -89,3 +90,48 @@ def test_bad_rows_are_reported(block):
                      ([-2, 1, 3, 5, 7], [0, 0, 1, 1, 2, 0, 3]), ([0, 1, 3, 5, 7], [0, 0, 1, 1, 3, 0, 3])):
         tsa.tsa_differential_attention(q, k, v, *_dev(ptr, idx), *lam, INIT, block=block)
         assert tsa.tsa_last_device_status() == 8
+
+
+NAMES = ("dQ", "dK", "dV", "dlq1", "dlk1", "dlq2", "dlk2")
+BACKWARD = [(1, 1, 1, 64, torch.float16, 64, "dense", 1), (1, 2, 2, 128, torch.bfloat16, 64, "dense", 2),
+            (1, 2, 63, 64, torch.bfloat16, 64, "dense", 1), (3, 2, 65, 128, torch.float16, 128, "dense", 2),
+            (2, 2, 384, 64, torch.bfloat16, 64, "holes", 1), (1, 2, 640, 128, torch.bfloat16, 64, "random", 2),
+            (1, 3, 1000, 64, torch.float16, 128, "random", 3), (2, 2, 1000, 128, torch.float16, 64, "random", 1),
+            (1, 1, 450, 128, torch.bfloat16, 64, "holes", 1), (1, 2, 300, 64, torch.float16, 64, "empty", 2),
+            (1, 1, 700, 64, torch.float16, 64, "diagonal", 1)]
+
+
+@pytest.mark.parametrize("B,H,S,D,dtype,block,kind,heads", BACKWARD)
+def test_backward(B, H, S, D, dtype, block, kind, heads):
+    q, k, v, do, lam = _inputs(B, H, S, D, dtype, heads, S + D)
+    rp, ci = _csr(kind, S, block, seed=H)
+    ref = differential(q, k, v, rp, ci, block, (D / 2) ** -0.5, lam, INIT, do)
+    rpd, cid = _dev(rp, ci)
+    qd, kd, vd, dod, *ld = (x.to(DEV) for x in (q, k, v, do, *lam))
+    O, O2, lse = tsa.tsa_differential_attention_fwd(qd, kd, vd, rpd, cid, *ld, INIT, block=block)
+    N, rows = B * H * S, 64
+    big = [torch.full((N + rows, D), 7.0, dtype=dtype, device=DEV) for _ in range(3)]
+    outs = [x[:N].view(B, H, S, D) for x in big]
+    got = tsa.tsa_differential_attention_backward(qd, kd, vd, O, O2, dod, lse, rpd, cid, *ld, INIT, block=block,
+                                                  dq=outs[0], dk=outs[1], dv=outs[2])
+    assert tsa.tsa_last_device_status() == 0
+    for x in big:  # rows behind the last lane stay as they were
+        assert bool((x[N:] == 7.0).all())
+    for name, x in zip(NAMES, got):
+        _close(x, *ref[name], name)
+    again = tsa.tsa_differential_attention_backward(qd, kd, vd, O, O2, dod, lse, rpd, cid, *ld, INIT, block=block)
+    for x, y in zip(got, again):
+        assert torch.equal(x, y)
+
+
+def test_autograd():
+    """Vectors of one dimension: one lambda for all heads."""
+    B, H, S, D = 2, 2, 200, 64
+    q, k, v, do, lam = _inputs(B, H, S, D, torch.float16, 1, 21)
+    rp, ci = _csr("random", S, 64, 5)
+    ref = differential(q, k, v, rp, ci, 64, 0.2, lam, INIT, do)
+    leaves = [x.to(DEV).requires_grad_(True) for x in (q, k, v, *(x[0] for x in lam))]
+    differential_attention(*leaves[:3], *_dev(rp, ci), *leaves[3:], INIT, 0.2).backward(do.to(DEV))
+    for name, x in zip(NAMES, leaves):
+        assert x.grad.shape == x.shape
+        _close(x.grad, *ref[name], name)

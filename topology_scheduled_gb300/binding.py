@@ -61,6 +61,12 @@ SIGNATURES = {
                                                         ctypes.c_float, _P, _SZ, _P]),
     "tsa_biased_attention_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_int, _I64,
                                                 _I64, _I64, _I64, _I64, ctypes.c_float, _P]),
+    "tsa_biased_attention_backward_workspace_bytes": (_SZ, [_I64] * 5),
+    "tsa_biased_attention_backward": (ctypes.c_int, [_P] * 8 + [_I64, _P, _P, _I64] + [_P] * 4 + [ctypes.c_int] +
+                                      [_I64] * 5 + [ctypes.c_float, _P, _SZ, _P]),
+    "tsa_differential_attention_backward_workspace_bytes": (_SZ, [_I64] * 4),
+    "tsa_differential_attention_backward": (ctypes.c_int, [_P] * 9 + [_I64] + [_P] * 4 + [_I64, ctypes.c_float] +
+                                            [_P] * 7 + [ctypes.c_int] + [_I64] * 5 + [ctypes.c_float, _P, _SZ, _P]),
     "tsa_differential_attention_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _I64,
                                                       ctypes.c_float, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64,
                                                       _I64, _I64, ctypes.c_float, _P]),

@@ -584,6 +584,8 @@ tsa_status tsa_scheduled_attention_backward(const void *Q, const void *K, const 
     a.row_ptr = row_ptr;
     a.col_idx = col_idx;
     a.nnz_cap = cap;
+    a.read_cap = LLONG_MAX;
+    a.partial = nullptr;
     a.nb_in = (int)nb_in;
     a.vlen_in = reinterpret_cast<int *>(w + ws.vlen_in);
     a.rp64 = reinterpret_cast<int32_t *>(w + ws.rp64);

@@ -1,0 +1,1179 @@
+// backward_kernels.cuh -- the two gradient kernels of the scheduled causal attention on tcgen05
+// tensor cores (sm_103a), plain or with the score terms of score_terms.cuh.  backward.cu has the
+// mathematics and the launches around them.
+//
+// Bias by buckets.  P is recomputed with the bias, a constant per step or a window per warp as in the
+// forward.  Its gradient sums dS over buckets in bwd_dq_kernel, in binary32 before dS is rounded:
+//  * a step inside one bucket adds each row's sum, kept in registers until the bucket changes;
+//  * near the diagonal a warp lays its 32 x 64 values out in shared memory with rows 65 apart, adds
+//    up the 95 diagonals (one distance each; every read of a warp touches 32 banks) and then, by
+//    shuffles, the distances of each bucket;
+//  * the last, open bucket gets minus the sum of the row's other values, since a row of dS sums to
+//    zero: no work on the far steps, and none of the error that Delta's rounded output leaves in each
+//    of their many values (it is a common shift of a row's dP, which the far keys would add up).
+// No atomics: a warp has its own sums, a CTA writes its tile's, and terms_reduce_bias adds the tiles
+// in order.
+//
+// Differential attention.  As in the forward a CTA takes one block and both maps: Q (or K) block-
+// diagonal, dO (or V) twice, so S and dP of both maps come from the same products.  The second map's
+// dP is -lambda times the first's, folded into the subtraction of Delta.  dQ = dS [k1 | k2] holds
+// each map's gradient in its half of the columns; dV adds the upper and lower rows through shared
+// memory.  lambda's gradient is - sum P2 o dP, summed over a CTA's rows in binary32 from the exact
+// weights, so that a sum over every query keeps the precision that P's rounding would cost.
+#pragma once
+
+#include <climits>
+#include <type_traits>
+
+#include "score_terms.cuh"
+#include "tsa_device.cuh"
+#include "tsa_internal.h"
+
+namespace tsa {
+namespace {
+
+constexpr int kBlock = 64;
+constexpr int kThreads = 192;
+constexpr int kRows = 128;
+constexpr int kProducerWarp = 4;
+constexpr int kMmaWarp = 5;
+constexpr int kStream = 3;     // depth of the ring of streamed blocks
+constexpr int kMetaRing = 4;   // > kStream: a slot is rewritten only after its step is consumed
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ---------------------------------------------------------------- shared helpers
+
+// Two floats rounded to the 16-bit input dtype and packed (first in the low half).
+template <bool kBF16>
+__device__ __forceinline__ uint32_t pack16x2(float a, float b) {
+    if constexpr (kBF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// Union of two ascending index lists (already checked), with membership bits (1: first list,
+// 2: second list); -1 at the end.
+struct ListUnion {
+    const int32_t *a, *b;
+    int ia, ia_end, ib, ib_end;
+
+    __device__ int next(int &flags) {
+        const int ja = ia < ia_end ? __ldg(a + ia) : INT_MAX;
+        const int jb = ib < ib_end ? __ldg(b + ib) : INT_MAX;
+        if (ja == INT_MAX && jb == INT_MAX) {
+            flags = 0;
+            return -1;
+        }
+        const int j = ja < jb ? ja : jb;
+        flags = (ja == j ? 1 : 0) | (jb == j ? 2 : 0);
+        if (ja == j) ++ia;
+        if (jb == j) ++ib;
+        return j;
+    }
+};
+
+// 128 rows of fp32 accumulator in TMEM (this warp's 32 lanes, D columns starting at `col`),
+// times `mul`, rounded and written to a 128-row SW128 staging tile in the layout TMA stores.
+template <int D, bool kBF16>
+__device__ __forceinline__ void stage_rows(uint32_t tmem_row, uint32_t col, bool valid, float mul,
+                                           uint32_t tile, int row) {
+    const uint32_t sw = (uint32_t)(row & 7);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        const uint32_t o_row = tile + c * 16384 + row * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t o[32];
+            if (valid) {
+                tmem_ld32(tmem_row + col + c * 64 + h * 32, o);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 32; ++t) o[t] = 0u;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    w[t] = pack16x2<kBF16>(__uint_as_float(o[q * 8 + 2 * t]) * mul,
+                                           __uint_as_float(o[q * 8 + 2 * t + 1]) * mul);
+                st_shared_v4(o_row + (((uint32_t)(h * 4 + q) ^ sw) << 4), w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+}
+
+// Row `row` (0-127) of a 128-row SW128 staging tile (the layout stage_rows writes: 64-column
+// chunks of 16 KB, 16-byte units of a row permuted by row & 7) copied to a global row of D
+// 16-bit values.
+template <int D>
+__device__ __forceinline__ void copy_staged_row(const uint8_t *tile, int row, uint16_t *dst) {
+    const uint32_t sw = (uint32_t)(row & 7);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        const uint8_t *src = tile + c * 16384 + row * 128;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4 *>(dst + c * 64 + u * 8) =
+                *reinterpret_cast<const uint4 *>(src + (((uint32_t)u ^ sw) << 4));
+    }
+}
+
+// Differential attention: half m's 64 rows x D / 2 columns of an accumulator that starts at `col`
+// (columns m D/2 ..), times `mul`, rounded and written to a 64-row SW128 staging tile.
+template <int D, bool kBF16>
+__device__ __forceinline__ void stage_half_rows(uint32_t tmem_row, uint32_t col, bool valid, float mul,
+                                                uint32_t tile, int half, int row) {
+    const uint32_t sw = (uint32_t)(row & 7);
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {  // 32 columns at a time
+        uint32_t o[32];
+        if (valid) {
+            tmem_ld32(tmem_row + col + half * (D / 2) + h * 32, o);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 32; ++t) o[t] = 0u;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                w[t] = pack16x2<kBF16>(__uint_as_float(o[q * 8 + 2 * t]) * mul,
+                                       __uint_as_float(o[q * 8 + 2 * t + 1]) * mul);
+            const uint32_t unit = D == 128 ? (uint32_t)(h * 4 + q) : (uint32_t)(half * 4 + q);
+            st_shared_v4(tile + (D == 128 ? half * 16384 : 0) + row * 128 + ((unit ^ sw) << 4), w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// Differential attention: the upper 64 rows of an accumulator plus the lower ones (which pass
+// through `passed` in binary32), rounded and written to a 64-row SW128 staging tile.  Called by all
+// 128 elementwise threads; has a barrier.
+template <int D, bool kBF16>
+__device__ __forceinline__ void stage_sum_of_halves(uint32_t tmem_row, uint32_t col, bool valid, uint32_t tile,
+                                                    float4 *passed, int half, int row) {
+    const uint32_t sw = (uint32_t)(row & 7);
+    passed += row;
+    if (half == 0) named_barrier(1, kRows);
+#pragma unroll
+    for (int h = 0; h < D / 32; ++h) {
+        uint32_t o[32];
+        if (valid) {
+            tmem_ld32(tmem_row + col + h * 32, o);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 32; ++t) o[t] = 0u;
+        }
+        if (half) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                passed[(h * 8 + t) * 64] = make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
+                                                       __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 x = passed[(h * 8 + 2 * q) * 64], y = passed[(h * 8 + 2 * q + 1) * 64];
+                const uint32_t *v = o + q * 8;
+                st_shared_v4(tile + (h >> 1) * 16384 + row * 128 + ((((h & 1) * 4 + q) ^ sw) << 4),
+                             pack16x2<kBF16>(__uint_as_float(v[0]) + x.x, __uint_as_float(v[1]) + x.y),
+                             pack16x2<kBF16>(__uint_as_float(v[2]) + x.z, __uint_as_float(v[3]) + x.w),
+                             pack16x2<kBF16>(__uint_as_float(v[4]) + y.x, __uint_as_float(v[5]) + y.y),
+                             pack16x2<kBF16>(__uint_as_float(v[6]) + y.z, __uint_as_float(v[7]) + y.w));
+            }
+        }
+    }
+    if (half) named_barrier(1, kRows);
+}
+
+// Meta area (byte offsets from the meta base), common to both kernels.
+constexpr int kBarTile = 0;                           // resident tile(s) loaded
+constexpr int kBarFull = 8;                           // kStream x 8: streamed block landed
+constexpr int kBarEmpty = kBarFull + 8 * kStream;     // kStream x 8: streamed block released
+constexpr int kBarSFull = kBarEmpty + 8 * kStream;    // 2 x 8: products of a step in TMEM
+constexpr int kBarPFull = kBarSFull + 16;             // 2 x 8: elementwise results of a step in TMEM
+constexpr int kBarDone = kBarPFull + 16;              // accumulation MMA of a step completed
+constexpr int kBarFin = kBarDone + 8;
+constexpr int kBarVFull = kBarFin + 8;                // dQ kernel: kStream x 8, V of a step landed
+constexpr int kBarVEmpty = kBarVFull + 8 * kStream;   // dQ kernel: kStream x 8
+constexpr int kBarDiag = kBarVEmpty + 8 * kStream;    // the resident tile is block-diagonal
+constexpr int kTmemSlot = kBarDiag + 8;
+constexpr int kAbortFlag = kTmemSlot + 4;
+constexpr int kMetaJ = kAbortFlag + 4;                // kMetaRing x 4
+constexpr int kMetaF = kMetaJ + 4 * kMetaRing;        // kMetaRing x 4
+constexpr int kMetaBytes = 256;
+static_assert(kMetaF + 4 * kMetaRing <= kMetaBytes, "meta area");
+
+constexpr uint32_t kTmemCols = 512;  // S0 | S1 | dP0 | dP1 | accumulator(s)
+
+// Each CTA takes all 512 TMEM columns, so a second CTA on the same SM would only wait in its
+// allocation: ask for more than half of the SM's shared memory so that one CTA fits.
+constexpr int smem_bytes_one_cta(int need) { return need > 116 * 1024 ? need : 116 * 1024; }
+__device__ __forceinline__ uint32_t s_col(int b) { return b ? 64u : 0u; }
+__device__ __forceinline__ uint32_t dp_col(int b) { return b ? 192u : 128u; }
+constexpr uint32_t kAccCol = 256;
+
+// ---------------------------------------------------------------- dQ
+// Adds a warp's 32 x 64 values of dS to its bucket sums, but for the last bucket's: row r, column c
+// lies at the distance d_lo + 63 + r - c.  `win` is scratch (96 floats).
+__device__ __forceinline__ void sum_diagonals(float *bins, float *win, const float *diag, const BucketTable &t,
+                                              int top, int last, int d_lo, int d_hi, int lane);
+
+// A warp's 32 x 64 values of dS near the diagonal, rows 65 apart.
+constexpr int kDiagStride = 65;
+constexpr int kDiagBytes = 32 * kDiagStride * 4;
+
+__device__ __forceinline__ void sum_diagonals(float *bins, float *win, const float *diag, const BucketTable &t,
+                                              int top, int last, int d_lo, int d_hi, int lane) {
+    __syncwarp();  // every lane's values are there, and the window has been read
+    // lane's diagonals are the distances d_lo + lane, + 32 and + 64; the first has rows up to `lane`,
+    // the third those after it
+    float a0 = 0.f, a1 = 0.f, a2 = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+        const float *row = diag + r * kDiagStride + r - lane;
+        a1 += row[31];
+        const float x = row[r <= lane ? 63 : -1];
+        if (r <= lane) a0 += x;
+        else a2 += x;
+    }
+    // running sums over the 96 distances that begin anew with each bucket (so that a bucket's sum
+    // holds nothing of another's): where buckets begin, as three words of bits
+    const int least = d_lo > 0 ? d_lo : 0;
+    uint32_t m0 = 0u, m1 = 0u, m2 = 0u;
+    for (int b0 = top; b0 > 0; b0 -= 32) {  // 32 buckets at a time, one per lane
+        const int b = b0 - lane, at = b > 0 ? t.start[b] - d_lo : 0;
+        const bool in = b > 0 && t.start[b] > least;
+        const uint32_t bit = in ? 1u << (at & 31) : 0u;
+        m0 |= __reduce_or_sync(0xffffffffu, at < 32 ? bit : 0u);
+        m1 |= __reduce_or_sync(0xffffffffu, at >= 32 && at < 64 ? bit : 0u);
+        m2 |= __reduce_or_sync(0xffffffffu, at >= 64 ? bit : 0u);
+        if (!__all_sync(0xffffffffu, in)) break;
+    }
+    const uint32_t upto = 0xffffffffu >> (31 - lane);
+    const int p0 = 31 - __clz(m0 & upto), p1 = 31 - __clz(m1 & upto), p2 = 31 - __clz(m2 & upto);  // -1: none
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float x0 = __shfl_up_sync(0xffffffffu, a0, o), x1 = __shfl_up_sync(0xffffffffu, a1, o),
+                    x2 = __shfl_up_sync(0xffffffffu, a2, o);
+        if (lane >= o && lane - o >= p0) a0 += x0;
+        if (lane >= o && lane - o >= p1) a1 += x1;
+        if (lane >= o && lane - o >= p2) a2 += x2;
+    }
+    const float c1 = __shfl_sync(0xffffffffu, a0, 31);
+    if (p1 < 0) a1 += c1;
+    const float c2 = __shfl_sync(0xffffffffu, a1, 31);
+    if (p2 < 0) a2 += c2;
+    win[lane] = a0;
+    win[lane + 32] = a1;
+    win[lane + 64] = a2;
+    __syncwarp();
+    // buckets top, top - 1, .. down to the one that holds the least distance, one per lane
+    for (int b = top - lane; b >= 0; b -= 32) {
+        const int end = b == top ? d_hi + 1 : t.start[b + 1];  // one past the bucket's last distance here
+        if (end <= least) break;
+        if (b != last && end > t.start[b]) bins[b] += win[end - 1 - d_lo];
+    }
+}
+
+template <int D, class Terms>
+struct DqSmem {
+    static constexpr int kChunks = D / 64;
+    static constexpr int kTileBytes = kRows * D * 2;   // Q and dO tiles (128 rows)
+    static constexpr int kKVBytes = kBlock * D * 2;    // one K or V block
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffDO = kOffQ + kTileBytes;
+    static constexpr int kOffK = kOffDO + kTileBytes;
+    static constexpr int kOffV = kOffK + kStream * kKVBytes;
+    static constexpr int kOffMeta = kOffV + kStream * kKVBytes;
+    static constexpr int kOffTable = kOffMeta + kMetaBytes;                      // bias only, up to kOffEnd
+    static constexpr int kOffWin = kOffTable + kBucketTableBytes;                // 4 windows
+    static constexpr int kOffBins = kOffWin + 4 * kWindow * 4;                   // 4 x kMaxBuckets sums
+    static constexpr int kOffDiag = kOffBins + 4 * kMaxBuckets * 4;              // 4 warps' values
+    static constexpr int kEnd = Terms::kBias ? kOffDiag + 4 * kDiagBytes : kOffTable;
+    static constexpr int kBytes = smem_bytes_one_cta(kEnd + 1024);  // + alignment slack
+};
+
+// partial: with a bias the tile's sums of dS per bucket, [lanes, tiles, n]; differential: the tile's
+// part of lambda's gradient, [lanes, tiles].
+template <int D, bool kBF16, class Terms>
+__global__ void __launch_bounds__(kThreads, 1)
+bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+              const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+              const __grid_constant__ CUtensorMap tmdQ, const int32_t *__restrict__ row_ptr,
+              const int32_t *__restrict__ col_idx, const int *__restrict__ vlen,
+              const float *__restrict__ lse, const float *__restrict__ delta, int nb, int S,
+              float scale, float scale_log2, uint16_t *__restrict__ dQ, float *__restrict__ partial,
+              DeviceFlags flags, const __grid_constant__ Terms terms) {
+    constexpr bool kBias = Terms::kBias, kDiff = Terms::kDiff;
+    using L = DqSmem<D, Terms>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_base = smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    if (base - raw_base + L::kEnd > (uint32_t)L::kBytes) {
+        if (threadIdx.x == 0) raise_status(flags, kDevSmemAlign);
+        return;
+    }
+    uint8_t *smem = smem_raw + (base - raw_base);
+    [[maybe_unused]] const BucketTable table{reinterpret_cast<float *>(smem + L::kOffTable),
+                                             reinterpret_cast<int *>(smem + L::kOffTable) + kMaxBuckets};
+    const uint32_t sQ = base + L::kOffQ, sdO = base + L::kOffDO, sK = base + L::kOffK, sV = base + L::kOffV;
+    const uint32_t meta = base + L::kOffMeta;
+    volatile int *meta_j = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaJ);
+    volatile int *meta_f = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kAbortFlag);
+    const uint32_t bar_tile = meta + kBarTile, bar_done = meta + kBarDone, bar_fin = meta + kBarFin;
+#define BAR_K_FULL(s) (meta + kBarFull + 8u * (uint32_t)(s))
+#define BAR_K_EMPTY(s) (meta + kBarEmpty + 8u * (uint32_t)(s))
+#define BAR_V_FULL(s) (meta + kBarVFull + 8u * (uint32_t)(s))
+#define BAR_V_EMPTY(s) (meta + kBarVEmpty + 8u * (uint32_t)(s))
+#define BAR_S_FULL(b) (meta + kBarSFull + 8u * (uint32_t)(b))
+#define BAR_P_FULL(b) (meta + kBarPFull + 8u * (uint32_t)(b))
+
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int lane_id = blockIdx.x;
+    const int tile = (int)gridDim.y - 1 - (int)blockIdx.y;  // two query blocks (kDiff: one, both maps)
+    const int qa = tile * (kDiff ? 1 : 2);                   // longest rows first
+    const bool has_b = !kDiff && qa + 1 < nb;
+    const int row0 = lane_id * S;
+
+    // The first global reads are issued together and waited for at the barrier below: whether
+    // the launch already gave up elsewhere (one thread, so the whole CTA takes the same branch),
+    // and the producer's two CSR rows.
+    const bool gave_up = tid == 0 && *reinterpret_cast<volatile unsigned *>(flags.abort_epoch) == flags.epoch;
+    ListUnion lu;
+    if (tid == kProducerWarp * 32) {
+        lu.a = col_idx + row_ptr[qa];
+        lu.ia = 0;
+        lu.ia_end = vlen[qa];
+        lu.b = has_b ? col_idx + row_ptr[qa + 1] : col_idx;
+        lu.ib = 0;
+        lu.ib_end = has_b ? vlen[qa + 1] : 0;
+    }
+
+    if (tid == 0) {
+        mbar_init(bar_tile, 1);
+        for (int s = 0; s < kStream; ++s) {
+            mbar_init(BAR_K_FULL(s), 1);
+            mbar_init(BAR_K_EMPTY(s), 1);
+            mbar_init(BAR_V_FULL(s), 1);
+            mbar_init(BAR_V_EMPTY(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(BAR_S_FULL(b), 1);
+            mbar_init(BAR_P_FULL(b), kRows);
+        }
+        mbar_init(bar_done, 1);
+        mbar_init(bar_fin, 1);
+        if constexpr (kDiff) mbar_init(meta + kBarDiag, kRows);
+        *abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(meta + kTmemSlot, kTmemCols);
+        tmem_relinquish();
+    }
+    if constexpr (kBias) {
+        table.template load<kBF16>(terms, lane_id % terms.H, tid, kThreads);
+        for (int b = tid; b < 4 * kMaxBuckets; b += kThreads) reinterpret_cast<float *>(smem + L::kOffBins)[b] = 0.f;
+    }
+    tc_fence_before();
+    const bool leave = __syncthreads_or(gave_up);
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kOffMeta + kTmemSlot);
+    if (leave) {  // nothing was issued yet: give the columns back and go
+        if (tid == 0) raise_status(flags, kDevTimeout);  // a replayed launch that gave up once says so again
+        if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
+
+    if (warp == kProducerWarp) {
+        if ((tid & 31) == 0) {
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmdO);
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+            tma_prefetch_desc(&tmdQ);
+            mbar_arrive_expect_tx(bar_tile, 2 * L::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < L::kChunks; ++c) {
+                load_rows<Terms>(sQ + c * 16384, &tmQ, c * 64, row0, qa * kBlock, lane_id, bar_tile);
+                load_rows<Terms>(sdO + c * 16384, &tmdO, c * 64, row0, qa * kBlock, lane_id, bar_tile);
+                if constexpr (kDiff) {  // 64-row boxes: the block again, for the second map
+                    load_rows<Terms>(sQ + c * 16384 + 8192, &tmQ, c * 64, row0, qa * kBlock, lane_id, bar_tile);
+                    load_rows<Terms>(sdO + c * 16384 + 8192, &tmdO, c * 64, row0, qa * kBlock, lane_id, bar_tile);
+                }
+            }
+            bool ok = true;
+            int k_issued = 0, v_issued = 0;
+            for (int v = 0;; ++v) {
+                const int s = v % kStream;
+                const uint32_t par = (uint32_t)((v / kStream) - 1) & 1u;
+                if (v >= kStream && !mbar_wait(BAR_K_EMPTY(s), par, flags)) { ok = false; break; }
+                int f = 0;
+                const int j = lu.next(f);
+                meta_j[v % kMetaRing] = j;
+                meta_f[v % kMetaRing] = f;
+                if (j < 0) {
+                    mbar_arrive(BAR_K_FULL(s));
+                    break;
+                }
+                mbar_arrive_expect_tx(BAR_K_FULL(s), L::kKVBytes);
+#pragma unroll
+                for (int c = 0; c < L::kChunks; ++c)
+                    load_rows<Terms>(sK + s * L::kKVBytes + c * 8192, &tmK, c * 64, row0, j * kBlock, lane_id,
+                                     BAR_K_FULL(s));
+                k_issued = v + 1;
+                if (v >= kStream && !mbar_wait(BAR_V_EMPTY(s), par, flags)) { ok = false; break; }
+                mbar_arrive_expect_tx(BAR_V_FULL(s), L::kKVBytes);
+#pragma unroll
+                for (int c = 0; c < L::kChunks; ++c)
+                    load_rows<Terms>(sV + s * L::kKVBytes + c * 8192, &tmV, c * 64, row0, j * kBlock, lane_id,
+                                     BAR_V_FULL(s));
+                v_issued = v + 1;
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                (void)mbar_wait_timed(bar_tile, 0);
+                for (int w = k_issued - kStream; w < k_issued; ++w)
+                    if (w >= 0) (void)mbar_wait_timed(BAR_K_FULL(w % kStream), (w / kStream) & 1);
+                for (int w = v_issued - kStream; w < v_issued; ++w)
+                    if (w >= 0) (void)mbar_wait_timed(BAR_V_FULL(w % kStream), (w / kStream) & 1);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        if ((tid & 31) == 0) {
+            constexpr uint32_t kIdescS = idesc_f16(kBF16, 128, 64, false);
+            constexpr uint32_t kIdescAcc = idesc_f16(kBF16, 128, D, true);
+            bool ok = mbar_wait(bar_tile, 0, flags);
+            if constexpr (kDiff) ok = ok && mbar_wait(meta + kBarDiag, 0, flags);
+            int u = 0;
+            bool have = false;
+            // products of step uu: S = Q K^T and dP = dO V^T; V's stage is free afterwards
+            auto issue_products = [&](int uu) -> bool {
+                const int s_ = uu % kStream;
+                if (!mbar_wait(BAR_V_FULL(s_), (uu / kStream) & 1, flags)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t koff = (kk >> 2) * 16384 + (kk & 3) * 32;
+                    const uint32_t boff = s_ * L::kKVBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
+                    tc_mma_ss(tmem + s_col(uu & 1), sdesc_sw128(sQ + koff, 16, 1024),
+                              sdesc_sw128(sK + boff, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+                }
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t koff = (kk >> 2) * 16384 + (kk & 3) * 32;
+                    const uint32_t boff = s_ * L::kKVBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
+                    tc_mma_ss(tmem + dp_col(uu & 1), sdesc_sw128(sdO + koff, 16, 1024),
+                              sdesc_sw128(sV + boff, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(BAR_S_FULL(uu & 1));
+                tc_commit(BAR_V_EMPTY(s_));
+                return true;
+            };
+            if (ok) {
+                ok = mbar_wait(BAR_K_FULL(0), 0, flags);
+                if (ok) {
+                    if (meta_j[0] >= 0) {
+                        ok = issue_products(0);
+                        have = ok;
+                    } else {
+                        mbar_arrive(BAR_S_FULL(0));
+                    }
+                }
+            }
+            while (ok && have) {
+                bool next = false;
+                const int s1 = (u + 1) % kStream;
+                ok = mbar_wait(BAR_K_FULL(s1), ((u + 1) / kStream) & 1, flags);
+                if (!ok) break;
+                if (meta_j[(u + 1) % kMetaRing] >= 0) {
+                    ok = issue_products(u + 1);
+                    if (!ok) break;
+                    next = true;
+                } else {
+                    mbar_arrive(BAR_S_FULL((u + 1) & 1));
+                }
+                // dQ += dS_u K_u once the elementwise warps have written dS_u
+                ok = mbar_wait(BAR_P_FULL(u & 1), (u >> 1) & 1, flags);
+                if (!ok) break;
+                const int s = u % kStream;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_ts(tmem + kAccCol, tmem + s_col(u & 1) + kk * 8,
+                              sdesc_sw128(sK + s * L::kKVBytes + kk * 2048, 8192, 1024), kIdescAcc,
+                              (u > 0 || kk > 0) ? 1u : 0u);
+                tc_commit(BAR_K_EMPTY(s));
+                tc_commit(bar_done);
+                have = next;
+                ++u;
+            }
+            if (!ok) *abort_flag = 1;
+            tc_commit(bar_fin);
+            (void)mbar_wait_timed(bar_fin, 0);
+        }
+    } else {
+        // ------------------------------------------------------------ elementwise (warps 0-3)
+        const int half = tid >> 6;
+        const int r_in = tid & 63;
+        const int my_block = kDiff ? qa : qa + half;
+        const bool row_exists = kDiff || half == 0 || has_b;
+        const int member = kDiff ? 0 : half;  // the membership bit of this thread's row
+        const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
+        // the row in the per-lane padded Delta / log-sum-exp arrays (nb * 64 rows per lane)
+        long long grow = ((long long)lane_id * nb + qa) * kBlock + (kDiff ? r_in : tid);
+        if constexpr (kDiff) grow += half * terms.map_rows;
+        const float lse2 = row_exists ? lse[grow] * kLog2e : -INFINITY;
+        float dlt = row_exists ? delta[grow] : 0.f;
+        const bool live = lse2 > -INFINITY;  // a row with keys
+        bool ok = true;
+        // kDiff: the second map's dP is -lambda dO V^T
+        [[maybe_unused]] float mul = 1.f, dot[2] = {0.f, 0.f};  // dot: sum of P o dO V^T over the row
+        if constexpr (kDiff) {
+            const float lam = lambda_of<D / 2, kBF16>(terms, lane_id % terms.H);
+            if (half) mul = -lam;
+            dlt *= mul;
+            ok = mbar_wait(bar_tile, 0, flags);
+            if (ok) {
+                keep_diagonal<D>(sQ, tid);
+                fence_proxy_async_smem();
+                mbar_arrive(meta + kBarDiag);
+            }
+        }
+        // kBias: the bucket of this warp's largest distance, the sum `run` of dS in it so far, and
+        // the sum over the row of what lies before the last bucket
+        [[maybe_unused]] int bucket = 0, run_bucket = 0;
+        [[maybe_unused]] float run = 0.f, others = 0.f;
+        [[maybe_unused]] bool reached = false;  // the row has keys in the last bucket
+        [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
+        [[maybe_unused]] float *bins = reinterpret_cast<float *>(smem + L::kOffBins) + warp * kMaxBuckets;
+        [[maybe_unused]] float *diag = reinterpret_cast<float *>(smem + L::kOffDiag) + warp * (kDiagBytes / 4);
+        [[maybe_unused]] const int wlane = tid & 31;
+        if constexpr (kBias) bucket = run_bucket = terms.n - 1;
+        auto flush_run = [&]() {
+            float s = run;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (wlane == 0) bins[run_bucket] += s;
+            run = 0.f;
+        };
+        int u = 0;
+        for (; ok; ++u) {
+            if (!mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags)) { ok = false; break; }
+            const int j = meta_j[u % kMetaRing];
+            const int fl = meta_f[u % kMetaRing];
+            if (j < 0) break;
+            tc_fence_after();
+            const bool in_row = row_exists && ((fl >> member) & 1);  // warp-uniform
+            uint32_t dsw[32];
+            __syncwarp();
+            if (in_row) {
+                // the bias: one constant for the step, or a window (key c at distance d_lo + 63 + wlane - c)
+                [[maybe_unused]] bool near = false;
+                [[maybe_unused]] int d_lo = 0, d_hi = 0;
+                float shift = -lse2;
+                if constexpr (kBias) {
+                    d_lo = (qa - j) * kBlock + warp * 32 - 63;
+                    d_hi = d_lo + kWindow - 2;
+                    while (bucket > 0 && d_hi < table.start[bucket]) --bucket;  // steps come nearer
+                    near = table.start[bucket] > (d_lo > 0 ? d_lo : 0);
+                    if (near) fill_window(win, table, bucket, d_lo, wlane);
+                    else shift += table.bias[bucket];
+                }
+                [[maybe_unused]] float sum[2] = {0.f, 0.f};
+                // keys up to this one lie in the last bucket
+                [[maybe_unused]] int far_to = -1;
+                if constexpr (kBias) far_to = d_lo + 63 + wlane - table.start[terms.n - 1];
+                auto step = [&](auto is_near) {
+                    constexpr bool kNear = decltype(is_near)::value;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t sr[32], pr[32];
+                        tmem_ld32_pair(tmem + t_lane + s_col(u & 1) + h * 32, sr,
+                                       tmem + t_lane + dp_col(u & 1) + h * 32, pr);
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) {
+                            float ds[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int c = h * 32 + 2 * t + e;
+                                const bool masked = !live || (j == my_block && c > r_in);
+                                const float s = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
+                                float z;
+                                if constexpr (kNear) z = fmaf(s, scale_log2, win[63 + wlane - c]) - lse2;
+                                else z = fmaf(s, scale_log2, shift);
+                                const float p = masked ? 0.f : ex2_approx(z);
+                                if constexpr (kDiff) {
+                                    ds[e] = p * fmaf(dp, mul, -dlt);
+                                    dot[e] = fmaf(p, dp, dot[e]);
+                                } else {
+                                    ds[e] = p * (dp - dlt);
+                                }
+                                if constexpr (kNear) {
+                                    diag[wlane * kDiagStride + c] = ds[e];
+                                    if (c > far_to) sum[e] += ds[e];
+                                } else if constexpr (kBias) {
+                                    sum[e] += ds[e];
+                                }
+                            }
+                            dsw[h * 16 + t] = pack16x2<kBF16>(ds[0], ds[1]);
+                        }
+                    }
+                };
+                if constexpr (kBias) {
+                    if (near) step(std::true_type{});
+                    else step(std::false_type{});
+                } else {
+                    step(std::false_type{});
+                }
+                if constexpr (kBias) {
+                    const int last = terms.n - 1;
+                    if (near) {
+                        others += sum[0] + sum[1];
+                        reached |= far_to >= 0;
+                        sum_diagonals(bins, win, diag, table, bucket, last, d_lo, d_hi, wlane);
+                    } else if (bucket < last) {
+                        if (bucket != run_bucket) {
+                            flush_run();
+                            run_bucket = bucket;
+                        }
+                        run += sum[0] + sum[1];
+                        others += sum[0] + sum[1];
+                    } else {
+                        reached = true;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 32; ++t) dsw[t] = 0u;
+            }
+            __syncwarp();
+            tmem_st32(tmem + t_lane + s_col(u & 1), dsw);  // dS_u over the first 32 columns of S_u
+            tc_fence_before();
+            mbar_arrive(BAR_P_FULL(u & 1));
+        }
+        if (!ok) *abort_flag = 1;
+        bool acc_valid = false;
+        if (ok && u > 0) {
+            acc_valid = mbar_wait(bar_done, (u - 1) & 1, flags);
+            if (!acc_valid) *abort_flag = 1;
+        }
+        // one decision for all elementwise warps (the section below has a barrier of its own)
+        if (!named_barrier_or(1, kRows, *abort_flag != 0)) {
+            tc_fence_after();
+            __syncwarp();
+            // every product that read Q has completed: Q's tile stages dQ
+            if constexpr (kDiff) stage_half_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, half, r_in);
+            else stage_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, tid);
+            if constexpr (kBias) {
+                flush_run();
+                run_bucket = terms.n - 1;
+                // the last bucket, unless its keys are left out
+                run = reached && table.bias[terms.n - 1] > -INFINITY ? -others : 0.f;
+                flush_run();
+            }
+            if constexpr (kDiff) {
+                float s = dot[0] + dot[1];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                // dO's tile is free as well; the two warps of the second map
+                if (half && (tid & 31) == 0) reinterpret_cast<float *>(smem + L::kOffDO)[warp & 1] = s;
+            }
+            fence_proxy_async_smem();
+            named_barrier(1, kRows);
+            if constexpr (kBias) {
+                const float *all = reinterpret_cast<const float *>(smem + L::kOffBins);
+                float *to = partial + ((long long)lane_id * gridDim.y + tile) * terms.n;
+                for (int b = tid; b < terms.n; b += kRows)
+                    to[b] = (all[b] + all[kMaxBuckets + b]) + (all[2 * kMaxBuckets + b] + all[3 * kMaxBuckets + b]);
+            }
+            if constexpr (kDiff) {
+                const float *two = reinterpret_cast<const float *>(smem + L::kOffDO);
+                if (tid == 0) partial[(long long)lane_id * gridDim.y + tile] = -(two[0] + two[1]);
+            }
+            // A partial last block (S not a multiple of 64) is not TMA-stored -- its box would
+            // run into the next lane's rows -- but copied row by row from the staging tile.
+            // (The score terms' kernels store through three dimensions, which cut the box off.)
+            constexpr bool k3D = kBias || kDiff;
+            const bool part_a = !k3D && (qa + 1) * kBlock > S, part_b = !k3D && has_b && (qa + 2) * kBlock > S;
+            if (tid == 0) {
+#pragma unroll
+                for (int c = 0; c < L::kChunks; ++c) {
+                    if constexpr (k3D) {
+                        tma_store_3d(&tmdQ, c * 64, qa * kBlock, lane_id, sQ + c * 16384);
+                        if (has_b) tma_store_3d(&tmdQ, c * 64, (qa + 1) * kBlock, lane_id, sQ + c * 16384 + 8192);
+                        continue;
+                    }
+                    if (!part_a) tma_store_2d(&tmdQ, c * 64, row0 + qa * kBlock, sQ + c * 16384);
+                    if (has_b && !part_b)
+                        tma_store_2d(&tmdQ, c * 64, row0 + (qa + 1) * kBlock, sQ + c * 16384 + 8192);
+                }
+                tma_store_commit();
+                tma_store_wait_read();
+            }
+            if ((half ? part_b : part_a) && qa * kBlock + tid < S)
+                copy_staged_row<D>(smem + (sQ - base), tid, dQ + ((size_t)row0 + qa * kBlock + tid) * D);
+        }
+    }
+#undef BAR_K_FULL
+#undef BAR_K_EMPTY
+#undef BAR_V_FULL
+#undef BAR_V_EMPTY
+#undef BAR_S_FULL
+#undef BAR_P_FULL
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) {
+        raise_status(flags, kDevTimeout);
+        atomicExch(flags.abort_epoch, flags.epoch);
+    }
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- dK, dV
+template <int D, class Terms>
+struct DkvSmem {
+    static constexpr int kRowBytes = Terms::kDiff ? 512 : 256;  // a step's 64 floats, of each map
+    static constexpr int kChunks = D / 64;
+    static constexpr int kTileBytes = kRows * D * 2;   // K and V tiles (128 keys)
+    static constexpr int kQBytes = kBlock * D * 2;     // one Q or dO block
+    static constexpr int kOffK = 0;
+    static constexpr int kOffV = kOffK + kTileBytes;
+    static constexpr int kOffQ = kOffV + kTileBytes;
+    static constexpr int kOffDO = kOffQ + kStream * kQBytes;
+    static constexpr int kOffLse = kOffDO + kStream * kQBytes;     // kStream x 64 floats (kDiff: of each map)
+    static constexpr int kOffDelta = kOffLse + kStream * kRowBytes;
+    static constexpr int kOffMeta = kOffDelta + kStream * kRowBytes;
+    static constexpr int kOffTable = kOffMeta + kMetaBytes;        // bias only
+    static constexpr int kOffWin = kOffTable + kBucketTableBytes;  // 4 windows (bias only)
+    static constexpr int kEnd = Terms::kBias ? kOffWin + 4 * kWindow * 4 : kOffTable;
+    static constexpr int kBytes = smem_bytes_one_cta(kEnd + 1024);
+    // the lower rows' dV passes through the ring of Q blocks
+    static_assert(kStream * kQBytes >= kBlock * D * 4, "exchange");
+};
+
+template <int D, bool kBF16, class Terms>
+__global__ void __launch_bounds__(kThreads, 1)
+bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+               const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+               const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
+               const int *__restrict__ col_ptr, const int32_t *__restrict__ row_idx,
+               const int *__restrict__ pairs, const float *__restrict__ lse,
+               const float *__restrict__ delta, int nb, int S, float scale, float scale_log2,
+               uint16_t *__restrict__ dK, uint16_t *__restrict__ dV, DeviceFlags flags,
+               const __grid_constant__ Terms terms) {
+    constexpr bool kBias = Terms::kBias, kDiff = Terms::kDiff;
+    using L = DkvSmem<D, Terms>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_base = smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    if (base - raw_base + L::kEnd > (uint32_t)L::kBytes) {
+        if (threadIdx.x == 0) raise_status(flags, kDevSmemAlign);
+        return;
+    }
+    uint8_t *smem = smem_raw + (base - raw_base);
+    [[maybe_unused]] const BucketTable table{reinterpret_cast<float *>(smem + L::kOffTable),
+                                             reinterpret_cast<int *>(smem + L::kOffTable) + kMaxBuckets};
+    const uint32_t sK = base + L::kOffK, sV = base + L::kOffV, sQ = base + L::kOffQ, sdO = base + L::kOffDO;
+    const uint32_t sLse = base + L::kOffLse, sDelta = base + L::kOffDelta;
+    const float *lse_s = reinterpret_cast<const float *>(smem + L::kOffLse);
+    const float *delta_s = reinterpret_cast<const float *>(smem + L::kOffDelta);
+    const uint32_t meta = base + L::kOffMeta;
+    volatile int *meta_j = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaJ);
+    volatile int *meta_f = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kAbortFlag);
+    const uint32_t bar_tile = meta + kBarTile, bar_done = meta + kBarDone, bar_fin = meta + kBarFin;
+#define BAR_FULL(s) (meta + kBarFull + 8u * (uint32_t)(s))
+#define BAR_EMPTY(s) (meta + kBarEmpty + 8u * (uint32_t)(s))
+#define BAR_S_FULL(b) (meta + kBarSFull + 8u * (uint32_t)(b))
+#define BAR_P_FULL(b) (meta + kBarPFull + 8u * (uint32_t)(b))
+
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int lane_id = blockIdx.x;
+    // key blocks ka and kb (-1: none) from the pair list, heaviest transposed columns first (kDiff:
+    // one block, both maps)
+    const int ka = __ldg(pairs + (kDiff ? 1 : 2) * blockIdx.y), kb = kDiff ? -1 : __ldg(pairs + 2 * blockIdx.y + 1);
+    const bool has_b = kb >= 0;
+    const int row0 = lane_id * S;
+
+    // As in the dQ kernel: the abort flag and the producer's two transposed columns are read
+    // before the first barrier.
+    const bool gave_up = tid == 0 && *reinterpret_cast<volatile unsigned *>(flags.abort_epoch) == flags.epoch;
+    ListUnion lu;
+    if (tid == kProducerWarp * 32) {
+        lu.a = row_idx + col_ptr[ka];
+        lu.ia = 0;
+        lu.ia_end = col_ptr[ka + 1] - col_ptr[ka];
+        lu.b = has_b ? row_idx + col_ptr[kb] : row_idx;
+        lu.ib = 0;
+        lu.ib_end = has_b ? col_ptr[kb + 1] - col_ptr[kb] : 0;
+    }
+
+    if (tid == 0) {
+        mbar_init(bar_tile, 1);
+        for (int s = 0; s < kStream; ++s) {
+            mbar_init(BAR_FULL(s), 1);
+            mbar_init(BAR_EMPTY(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(BAR_S_FULL(b), 1);
+            mbar_init(BAR_P_FULL(b), kRows);
+        }
+        mbar_init(bar_done, 1);
+        mbar_init(bar_fin, 1);
+        if constexpr (kDiff) mbar_init(meta + kBarDiag, kRows);
+        *abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(meta + kTmemSlot, kTmemCols);
+        tmem_relinquish();
+    }
+    if constexpr (kBias) table.template load<kBF16>(terms, lane_id % terms.H, tid, kThreads);
+    tc_fence_before();
+    const bool leave = __syncthreads_or(gave_up);
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kOffMeta + kTmemSlot);
+    if (leave) {  // nothing was issued yet: give the columns back and go
+        if (tid == 0) raise_status(flags, kDevTimeout);  // a replayed launch that gave up once says so again
+        if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
+    constexpr uint32_t kDVCol = kAccCol, kDKCol = kAccCol + D;
+
+    if (warp == kProducerWarp) {
+        if ((tid & 31) == 0) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmdO);
+            tma_prefetch_desc(&tmdK);
+            tma_prefetch_desc(&tmdV);
+            mbar_arrive_expect_tx(bar_tile, 2 * L::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < L::kChunks; ++c) {
+                load_rows<Terms>(sK + c * 16384, &tmK, c * 64, row0, ka * kBlock, lane_id, bar_tile);
+                load_rows<Terms>(sV + c * 16384, &tmV, c * 64, row0, ka * kBlock, lane_id, bar_tile);
+                // the second block's rows, or the first block's again (masked; kDiff: the second map)
+                const int y2 = (has_b ? kb : ka) * kBlock;
+                load_rows<Terms>(sK + c * 16384 + 8192, &tmK, c * 64, row0, y2, lane_id, bar_tile);
+                load_rows<Terms>(sV + c * 16384 + 8192, &tmV, c * 64, row0, y2, lane_id, bar_tile);
+            }
+            bool ok = true;
+            int issued = 0;
+            for (int v = 0;; ++v) {
+                const int s = v % kStream;
+                const uint32_t par = (uint32_t)((v / kStream) - 1) & 1u;
+                if (v >= kStream && !mbar_wait(BAR_EMPTY(s), par, flags)) { ok = false; break; }
+                int f = 0;
+                const int i = lu.next(f);
+                meta_j[v % kMetaRing] = i;
+                meta_f[v % kMetaRing] = f;
+                if (i < 0) {
+                    mbar_arrive(BAR_FULL(s));
+                    break;
+                }
+                mbar_arrive_expect_tx(BAR_FULL(s), 2 * L::kQBytes + 2 * L::kRowBytes);
+#pragma unroll
+                for (int c = 0; c < L::kChunks; ++c) {
+                    load_rows<Terms>(sQ + s * L::kQBytes + c * 8192, &tmQ, c * 64, row0, i * kBlock, lane_id, BAR_FULL(s));
+                    load_rows<Terms>(sdO + s * L::kQBytes + c * 8192, &tmdO, c * 64, row0, i * kBlock, lane_id, BAR_FULL(s));
+                }
+                const long long py = ((long long)lane_id * nb + i) * kBlock;  // padded row
+                bulk_load(sLse + s * L::kRowBytes, lse + py, 256, BAR_FULL(s));
+                bulk_load(sDelta + s * L::kRowBytes, delta + py, 256, BAR_FULL(s));
+                if constexpr (kDiff) {
+                    bulk_load(sLse + s * L::kRowBytes + 256, lse + terms.map_rows + py, 256, BAR_FULL(s));
+                    bulk_load(sDelta + s * L::kRowBytes + 256, delta + terms.map_rows + py, 256, BAR_FULL(s));
+                }
+                issued = v + 1;
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                (void)mbar_wait_timed(bar_tile, 0);
+                for (int w = issued - kStream; w < issued; ++w)
+                    if (w >= 0) (void)mbar_wait_timed(BAR_FULL(w % kStream), (w / kStream) & 1);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        if ((tid & 31) == 0) {
+            constexpr uint32_t kIdescS = idesc_f16(kBF16, 128, 64, false);
+            constexpr uint32_t kIdescAcc = idesc_f16(kBF16, 128, D, true);
+            bool ok = mbar_wait(bar_tile, 0, flags);
+            if constexpr (kDiff) ok = ok && mbar_wait(meta + kBarDiag, 0, flags);
+            int u = 0;
+            bool have = false;
+            // products of step uu: S^T = K Q^T and dP^T = V dO^T
+            auto issue_products = [&](int uu) {
+                const int s_ = uu % kStream;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
+                    const uint32_t boff = s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
+                    tc_mma_ss(tmem + s_col(uu & 1), sdesc_sw128(sK + aoff, 16, 1024),
+                              sdesc_sw128(sQ + boff, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+                }
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
+                    const uint32_t boff = s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
+                    tc_mma_ss(tmem + dp_col(uu & 1), sdesc_sw128(sV + aoff, 16, 1024),
+                              sdesc_sw128(sdO + boff, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(BAR_S_FULL(uu & 1));
+            };
+            if (ok) {
+                ok = mbar_wait(BAR_FULL(0), 0, flags);
+                if (ok) {
+                    if (meta_j[0] >= 0) {
+                        issue_products(0);
+                        have = true;
+                    } else {
+                        mbar_arrive(BAR_S_FULL(0));
+                    }
+                }
+            }
+            while (ok && have) {
+                bool next = false;
+                const int s1 = (u + 1) % kStream;
+                ok = mbar_wait(BAR_FULL(s1), ((u + 1) / kStream) & 1, flags);
+                if (!ok) break;
+                if (meta_j[(u + 1) % kMetaRing] >= 0) {
+                    issue_products(u + 1);
+                    next = true;
+                } else {
+                    mbar_arrive(BAR_S_FULL((u + 1) & 1));
+                }
+                // dV += P^T_u dO_u and dK += dS^T_u Q_u once the elementwise warps wrote them
+                ok = mbar_wait(BAR_P_FULL(u & 1), (u >> 1) & 1, flags);
+                if (!ok) break;
+                const int s = u % kStream;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_ts(tmem + kDVCol, tmem + s_col(u & 1) + kk * 8,
+                              sdesc_sw128(sdO + s * L::kQBytes + kk * 2048, 8192, 1024), kIdescAcc,
+                              (u > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_ts(tmem + kDKCol, tmem + dp_col(u & 1) + kk * 8,
+                              sdesc_sw128(sQ + s * L::kQBytes + kk * 2048, 8192, 1024), kIdescAcc,
+                              (u > 0 || kk > 0) ? 1u : 0u);
+                tc_commit(BAR_EMPTY(s));
+                tc_commit(bar_done);
+                have = next;
+                ++u;
+            }
+            if (!ok) *abort_flag = 1;
+            tc_commit(bar_fin);
+            (void)mbar_wait_timed(bar_fin, 0);
+        }
+    } else {
+        // ------------------------------------------------------------ elementwise (warps 0-3)
+        const int half = tid >> 6;               // 0: key block ka, 1: key block kb (kDiff: the maps)
+        const int k_in = tid & 63;               // key token within its block
+        const int key_block = half && !kDiff ? kb : ka;
+        const bool row_exists = kDiff || half == 0 || has_b;
+        const int member = kDiff ? 0 : half;
+        const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
+        bool ok = true;
+        // kDiff: the second map's P and dP count -lambda times
+        [[maybe_unused]] float mul = 1.f;
+        if constexpr (kDiff) {
+            const float lam = lambda_of<D / 2, kBF16>(terms, lane_id % terms.H);
+            if (half) mul = -lam;
+            ok = mbar_wait(bar_tile, 0, flags);
+            if (ok) {
+                keep_diagonal<D>(sK, tid);
+                fence_proxy_async_smem();
+                mbar_arrive(meta + kBarDiag);
+            }
+        }
+        [[maybe_unused]] int bucket = 0;  // the bucket of this warp's largest distance of the step
+        [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
+        [[maybe_unused]] const int wlane = tid & 31;
+        int u = 0;
+        for (; ok; ++u) {
+            if (!mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags)) { ok = false; break; }
+            const int i = meta_j[u % kMetaRing];
+            const int fl = meta_f[u % kMetaRing];
+            if (i < 0) break;
+            const int s = u % kStream;
+            // the step's log-sum-exp and Delta rows arrived with its Q and dO blocks
+            if (!mbar_wait(BAR_FULL(s), (u / kStream) & 1, flags)) { ok = false; break; }
+            tc_fence_after();
+            const bool in_col = row_exists && ((fl >> member) & 1);  // warp-uniform
+            uint32_t pw[32], dw[32];
+            __syncwarp();
+            if (in_col) {
+                const float *ls = lse_s + s * (L::kRowBytes / 4) + (kDiff ? half * 64 : 0);
+                const float *dl = delta_s + s * (L::kRowBytes / 4) + (kDiff ? half * 64 : 0);
+                // the bias: one constant for the step, or a window (query c at distance d_lo + 31 + c - wlane)
+                [[maybe_unused]] bool near = false;
+                [[maybe_unused]] float off = 0.f;
+                if constexpr (kBias) {
+                    const int d_lo = (i - key_block) * kBlock - (warp & 1) * 32 - 31, d_hi = d_lo + kWindow - 2;
+                    while (bucket + 1 < terms.n && d_hi >= table.start[bucket + 1]) ++bucket;  // steps go farther
+                    near = table.start[bucket] > (d_lo > 0 ? d_lo : 0);
+                    if (near) fill_window(win, table, bucket, d_lo, wlane);
+                    else off = table.bias[bucket];
+                }
+                auto step = [&](auto is_near) {
+                    constexpr bool kNear = decltype(is_near)::value;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t sr[32], pr[32];
+                        tmem_ld32_pair(tmem + t_lane + s_col(u & 1) + h * 32, sr,
+                                       tmem + t_lane + dp_col(u & 1) + h * 32, pr);
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) {
+                            float p[2], ds[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int c = h * 32 + 2 * t + e;  // query token within block i
+                                const float l2 = ls[c] * kLog2e;
+                                const bool masked = l2 == -INFINITY || (i == key_block && k_in > c);
+                                const float x = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
+                                float z;
+                                if constexpr (kNear) z = fmaf(x, scale_log2, win[31 + c - wlane]) - l2;
+                                else if constexpr (kBias) z = fmaf(x, scale_log2, off - l2);
+                                else z = fmaf(x, scale_log2, -l2);
+                                p[e] = masked ? 0.f : ex2_approx(z);
+                                if constexpr (kDiff) p[e] *= mul;
+                                ds[e] = p[e] * (dp - dl[c]);
+                            }
+                            pw[h * 16 + t] = pack16x2<kBF16>(p[0], p[1]);
+                            dw[h * 16 + t] = pack16x2<kBF16>(ds[0], ds[1]);
+                        }
+                    }
+                };
+                if constexpr (kBias) {
+                    if (near) step(std::true_type{});
+                    else step(std::false_type{});
+                } else {
+                    step(std::false_type{});
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 32; ++t) pw[t] = dw[t] = 0u;
+            }
+            __syncwarp();
+            tmem_st32(tmem + t_lane + s_col(u & 1), pw);   // P^T over the first 32 columns of S^T
+            tmem_st32(tmem + t_lane + dp_col(u & 1), dw);  // dS^T over the first 32 of dP^T
+            tc_fence_before();
+            mbar_arrive(BAR_P_FULL(u & 1));
+        }
+        if (!ok) *abort_flag = 1;
+        bool acc_valid = false;
+        if (ok && u > 0) {
+            acc_valid = mbar_wait(bar_done, (u - 1) & 1, flags);
+            if (!acc_valid) *abort_flag = 1;
+        }
+        // one decision for all elementwise warps (the section below has a barrier of its own)
+        if (!named_barrier_or(1, kRows, *abort_flag != 0)) {
+            tc_fence_after();
+            __syncwarp();
+            // every product that read K and V has completed: their tiles stage dK and dV
+            if constexpr (kDiff) {
+                stage_sum_of_halves<D, kBF16>(tmem + t_lane, kDVCol, acc_valid, sV,
+                                              reinterpret_cast<float4 *>(smem + L::kOffQ), half, k_in);
+                stage_half_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, half, k_in);
+            } else {
+                stage_rows<D, kBF16>(tmem + t_lane, kDVCol, acc_valid, 1.f, sV, tid);
+                stage_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, tid);
+            }
+            fence_proxy_async_smem();
+            named_barrier(1, kRows);
+            // a partial last key block is copied row by row (see the dQ kernel)
+            constexpr bool k3D = kBias || kDiff;
+            const bool part_a = !k3D && (ka + 1) * kBlock > S, part_b = !k3D && has_b && (kb + 1) * kBlock > S;
+            if (tid == 0) {
+#pragma unroll
+                for (int c = 0; c < L::kChunks; ++c) {
+                    if constexpr (k3D) {
+                        tma_store_3d(&tmdV, c * 64, ka * kBlock, lane_id, sV + c * 16384);
+                        tma_store_3d(&tmdK, c * 64, ka * kBlock, lane_id, sK + c * 16384);
+                        if (has_b) {
+                            tma_store_3d(&tmdV, c * 64, kb * kBlock, lane_id, sV + c * 16384 + 8192);
+                            tma_store_3d(&tmdK, c * 64, kb * kBlock, lane_id, sK + c * 16384 + 8192);
+                        }
+                        continue;
+                    }
+                    if (!part_a) {
+                        tma_store_2d(&tmdV, c * 64, row0 + ka * kBlock, sV + c * 16384);
+                        tma_store_2d(&tmdK, c * 64, row0 + ka * kBlock, sK + c * 16384);
+                    }
+                    if (has_b && !part_b) {
+                        tma_store_2d(&tmdV, c * 64, row0 + kb * kBlock, sV + c * 16384 + 8192);
+                        tma_store_2d(&tmdK, c * 64, row0 + kb * kBlock, sK + c * 16384 + 8192);
+                    }
+                }
+                tma_store_commit();
+                tma_store_wait_read();
+            }
+            if ((half ? part_b : part_a) && key_block * kBlock + k_in < S) {
+                const size_t grow_k = ((size_t)row0 + key_block * kBlock + k_in) * D;
+                copy_staged_row<D>(smem + (sV - base), tid, dV + grow_k);
+                copy_staged_row<D>(smem + (sK - base), tid, dK + grow_k);
+            }
+        }
+    }
+#undef BAR_FULL
+#undef BAR_EMPTY
+#undef BAR_S_FULL
+#undef BAR_P_FULL
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) {
+        raise_status(flags, kDevTimeout);
+        atomicExch(flags.abort_epoch, flags.epoch);
+    }
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+
+template <int D, bool kBF16, class Terms>
+tsa_status launch_grad_kernels(const BwdLaunch &a, const Terms &terms) {
+    auto kq = bwd_dq_kernel<D, kBF16, Terms>;
+    auto kkv = bwd_dkv_kernel<D, kBF16, Terms>;
+    constexpr int kDqBytes = DqSmem<D, Terms>::kBytes, kDkvBytes = DkvSmem<D, Terms>::kBytes;
+    if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, kDkvBytes) != cudaSuccess)
+        return TSA_ERR_CUDA;
+    const unsigned tiles = (unsigned)(Terms::kDiff ? a.nb : (a.nb + 1) / 2);
+    const dim3 grid((unsigned)a.lanes, tiles);
+    const float scale_log2 = a.scale * kLog2e;
+    kq<<<grid, kThreads, kDqBytes, a.stream>>>(*a.tmQ128, *a.tmdO128, *a.tmK64, *a.tmV64, *a.tmdQ64, a.row_ptr,
+                                               a.col_idx, a.vlen, a.lse_pad, a.delta, a.nb, a.S, a.scale, scale_log2,
+                                               a.dQ, a.partial, a.flags, terms);
+    kkv<<<grid, kThreads, kDkvBytes, a.stream>>>(*a.tmK64, *a.tmV64, *a.tmQ64, *a.tmdO64, *a.tmdK64, *a.tmdV64,
+                                                 a.col_ptr, a.row_idx, a.pairs, a.lse_pad, a.delta, a.nb, a.S, a.scale,
+                                                 scale_log2, a.dK, a.dV, a.flags, terms);
+    return cudaGetLastError() == cudaSuccess ? TSA_OK : TSA_ERR_CUDA;
+}
+
+template <class Terms>
+tsa_status launch_gradients(const BwdLaunch &a, const Terms &terms) {
+    if (a.D == 64) return a.bf16 ? launch_grad_kernels<64, true>(a, terms) : launch_grad_kernels<64, false>(a, terms);
+    if (a.D == 128)
+        return a.bf16 ? launch_grad_kernels<128, true>(a, terms) : launch_grad_kernels<128, false>(a, terms);
+    return TSA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+}  // namespace tsa

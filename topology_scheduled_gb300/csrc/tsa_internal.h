@@ -74,6 +74,8 @@ struct BwdLaunch {
     const float *lse;
     const int32_t *row_ptr, *col_idx;
     int64_t nnz_cap;
+    long long read_cap;  // entries of col_idx that may be read
+    float *partial;      // score terms: each tile's part of the learned inputs' gradients
     // Delta and the log-sum-exp per lane over nb * 64 rows (rows past S: 0 and -inf), so a
     // partial last block is read like any other
     float *delta, *lse_pad;
@@ -93,6 +95,15 @@ struct BwdLaunch {
 };
 
 tsa_status launch_attention_backward(const BwdLaunch &a);
+// Its first launches: the transposed schedule (a 128-token CSR is replaced by its expansion in *a),
+// and Delta with the log-sum-exp in padded rows.
+tsa_status launch_backward_schedule(BwdLaunch *a);
+tsa_status launch_backward_delta(const BwdLaunch &a);
+
+// Backward passes with score terms.  dbias [H, n]; dlambda: the gradients of lq1, lk1, lq2, lk2.
+tsa_status launch_biased_backward(const BwdLaunch &a, const BiasTerms &terms, uint16_t *dbias);
+tsa_status launch_differential_backward(const BwdLaunch &a, const DiffTerms &terms, const uint16_t *O2,
+                                        uint16_t *const dlambda[4]);
 
 // Largest number of blocks the schedule builder accepts.
 constexpr int64_t kMaxScheduleBlocks = 4096;

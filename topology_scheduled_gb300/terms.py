@@ -168,3 +168,69 @@ def tsa_differential_attention_fwd(Q, K, V, row_ptr, col_idx, lambda_q1, lambda_
         D, block, (D / 2) ** -0.5 if scale is None else float(scale), _on(stream, out, out2, lse, ci)),
         "tsa_differential_attention_fwd")
     return (out, out2, lse) if for_backward else out
+
+
+def _workspace(t, need, device, where):
+    if need == 0:
+        raise TsaError(2, where)
+    if t is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return t
+
+
+def tsa_biased_attention_backward(Q, K, V, O, dO, lse, row_ptr, col_idx, bias, bucket_starts,
+                                  scale: float | None = None, *, block: int = 64, dq=None, dk=None, dv=None,
+                                  dbias=None, workspace=None, stream=None):
+    """dQ, dK, dV, dbias of tsa_biased_attention for the upstream gradient dO, in the inputs' type;
+    O and lse as tsa_biased_attention_fwd returned them."""
+    _check_qkv(Q=Q, K=K, V=V, O=O, dO=dO)
+    B, H, S, D = _lanes_S_D(Q)
+    dev = Q.device
+    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
+    starts, n = _starts(bucket_starts, bias)
+    _learned("bias", bias, (H, n), Q)
+    lse = _output("lse", lse, (B * H, S), torch.float32, dev)
+    L = lib()
+    workspace = _workspace(workspace, int(L.tsa_biased_attention_backward_workspace_bytes(B * H, S, block, ci.numel(), n)),
+                           dev, "tsa_biased_attention_backward_workspace_bytes")
+    dq, dk, dv = (_output(name, t, Q.shape, Q.dtype, dev) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
+    dbias = _output("dbias", dbias, bias.shape, Q.dtype, dev)
+    _check(L.tsa_biased_attention_backward(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), lse.data_ptr(), row_ptr.data_ptr(),
+        ci.data_ptr(), ci.numel(), bias.data_ptr(), starts, n, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        dbias.data_ptr(), _dtype_code(Q), B, H, S, D, block, 1.0 / math.sqrt(D) if scale is None else float(scale),
+        workspace.data_ptr(), workspace.numel(), _on(stream, workspace, dq, dk, dv, dbias, ci)),
+        "tsa_biased_attention_backward")
+    return dq, dk, dv, dbias
+
+
+def tsa_differential_attention_backward(Q, K, V, O, O2, dO, lse, row_ptr, col_idx, lambda_q1, lambda_k1, lambda_q2,
+                                        lambda_k2, lambda_init: float, scale: float | None = None, *,
+                                        block: int = 64, dq=None, dk=None, dv=None, dlambdas=None, workspace=None,
+                                        stream=None):
+    """dQ, dK, dV and the gradients of the four lambda vectors of tsa_differential_attention for the
+    upstream gradient dO, in the inputs' type; O, O2 and lse as tsa_differential_attention_fwd
+    returned them."""
+    _check_qkv(Q=Q, K=K, V=V, O=O, O2=O2, dO=dO)
+    B, H, S, D = _lanes_S_D(Q)
+    dev = Q.device
+    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
+    lambdas = (lambda_q1, lambda_k1, lambda_q2, lambda_k2)
+    heads = _lambda_heads(lambdas, H, D, Q)
+    lse = _output("lse", lse, (2, B * H, S), torch.float32, dev)
+    L = lib()
+    workspace = _workspace(workspace,
+                           int(L.tsa_differential_attention_backward_workspace_bytes(B * H, S, block, ci.numel())), dev,
+                           "tsa_differential_attention_backward_workspace_bytes")
+    dq, dk, dv = (_output(name, t, Q.shape, Q.dtype, dev) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
+    dlambdas = [_output(f"dlambdas[{i}]", None if dlambdas is None else dlambdas[i], t.shape, Q.dtype, dev)
+                for i, t in enumerate(lambdas)]
+    _check(L.tsa_differential_attention_backward(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), O2.data_ptr(), dO.data_ptr(), lse.data_ptr(),
+        row_ptr.data_ptr(), ci.data_ptr(), ci.numel(), *(t.data_ptr() for t in lambdas), heads, float(lambda_init),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *(t.data_ptr() for t in dlambdas), _dtype_code(Q), B, H, S, D,
+        block, (D / 2) ** -0.5 if scale is None else float(scale), workspace.data_ptr(), workspace.numel(),
+        _on(stream, workspace, dq, dk, dv, *dlambdas, ci)), "tsa_differential_attention_backward")
+    return (dq, dk, dv, *dlambdas)
