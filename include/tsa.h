@@ -62,9 +62,6 @@ typedef enum {
     TSA_ERR_DEVICE = 9             /* device: another device-side check failed             */
 } tsa_status;
 
-/* Most buckets of a relative position bias (tsa_biased_attention_fwd). */
-#define TSA_MAX_BUCKETS 256
-
 typedef enum { TSA_F16 = 0, TSA_BF16 = 1 } tsa_dtype;
 
 /* Human-readable name of a status code (static storage; never NULL). */
@@ -306,116 +303,6 @@ tsa_status tsa_scheduled_attention_backward(const void *Q, const void *K, const 
                                             tsa_dtype dtype, int64_t B, int64_t H, int64_t S,
                                             int64_t D, int64_t block, float scale, void *workspace,
                                             size_t workspace_bytes, tsa_stream_t stream);
-
-/*
- * Scheduled attention with a learned relative position bias: for query q and key k of lane l,
- * head h = l mod H,
- *   z = scale * <Q[l][q], K[l][k]> + bias[h][b],   b the last bucket with starts[b] <= q - k,
- * and O = softmax(z over the allowed keys) V, with the allowed keys of tsa_scheduled_attention.
- *
- *   Q, K, V       in,  [B*H, S, D] of `dtype`, 16-byte aligned.
- *   row_ptr, col_idx  the CSR of `block`-token blocks; nnz_cap: entries of col_idx.  A row that
- *                 points outside them is empty and reported, as any bad row.
- *   bias          in,  [H, num_buckets] of `dtype` on the device.  A bias of -1e30 or less (the
- *                 lowest bf16 value, -inf) leaves its bucket's keys out.
- *   bucket_starts in,  num_buckets int32 in HOST memory, read during the call: ascending (equal
- *                 starts make an empty bucket), the first one 0; the last bucket is open.
- *   O             out, [B*H, S, D] of `dtype`, 16-byte aligned; rows without keys are 0.
- *   lse           out, [B*H, S] float32, or NULL: the log-sum-exp of z per row, -inf for rows
- *                 without keys; the backward call needs it.
- * Outputs overlap no input and no other output.
- *
- * Limits: those of tsa_scheduled_attention, 1 <= num_buckets <= TSA_MAX_BUCKETS,
- * scale >= 1e-30.  Rows past S are neither read nor written, in no lane.  Errors:
- * INVALID_ARGUMENT, UNSUPPORTED, NOT_DEVICE_POINTER, DEVICE_MISMATCH, CUDA; on the device
- * BAD_SCHEDULE (a row is cut at its first bad entry), TIMEOUT.
- */
-tsa_status tsa_biased_attention_fwd(const void *Q, const void *K, const void *V,
-                                    const int32_t *row_ptr, const int32_t *col_idx, int64_t nnz_cap,
-                                    const void *bias, const int32_t *bucket_starts,
-                                    int64_t num_buckets, void *O, float *lse, tsa_dtype dtype,
-                                    int64_t B, int64_t H, int64_t S, int64_t D, int64_t block,
-                                    float scale, tsa_stream_t stream);
-
-/*
- * Differential attention over a schedule: the halves of a head's dimension hold two maps,
- * Q = [q1 | q2] and K = [k1 | k2] of D / 2 each, and
- *   O = (softmax(scale q1.k1) - lambda softmax(scale q2.k2)) V,
- *   lambda = exp(<lambda_q1, lambda_k1>) - exp(<lambda_q2, lambda_k2>) + lambda_init,
- * both maps over the allowed keys of tsa_scheduled_attention, V of the full D.
- *
- *   lambda_q1 .. lambda_k2  in, [lambda_heads, D / 2] of `dtype`; lambda_heads is H (a lambda
- *                 per head) or 1 (one for all).
- *   O             out, [B*H, S, D] of `dtype`, 16-byte aligned; rows without keys are 0.
- *   O2            out, the second map's softmax(..) V, shaped as O, or NULL; the backward call
- *                 needs it.
- *   lse           out, [2, B*H, S] float32: each map's log-sum-exp, or NULL.
- * The other arguments, limits and errors are those of tsa_biased_attention_fwd.
- */
-tsa_status tsa_differential_attention_fwd(const void *Q, const void *K, const void *V,
-                                          const int32_t *row_ptr, const int32_t *col_idx,
-                                          int64_t nnz_cap, const void *lambda_q1,
-                                          const void *lambda_k1, const void *lambda_q2,
-                                          const void *lambda_k2, int64_t lambda_heads,
-                                          float lambda_init, void *O, void *O2, float *lse,
-                                          tsa_dtype dtype, int64_t B, int64_t H, int64_t S,
-                                          int64_t D, int64_t block, float scale,
-                                          tsa_stream_t stream);
-
-/*
- * Backward pass of tsa_biased_attention_fwd: with P the softmax of z over the allowed keys,
- *   Delta = rowsum(dO o O),  dS = P o (dO V^T - Delta),  dV = P^T dO,  dQ = scale dS K,
- *   dK = scale dS^T Q,  dbias[h][b] = sum of dS over the batch's lanes of head h and the pairs
- *   whose distance lies in bucket b,
- * in binary32 from the 16-bit inputs, results rounded once.  (A row of dS sums to zero, so the
- * open last bucket gets minus the sum of the row's others, in rows that reach it.)  The result
- * does not depend on the order in which thread blocks run.
- *
- *   O, lse        as the forward call wrote them for the same inputs and CSR.
- *   dO            in,  the upstream gradient, [B*H, S, D] of `dtype`, 16-byte aligned.
- *   dQ, dK, dV    out, [B*H, S, D] of `dtype`, 16-byte aligned.
- *   dbias         out, [H, num_buckets] of `dtype`.
- *   workspace     >= tsa_biased_attention_backward_workspace_bytes(B*H, S, block, nnz_cap,
- *                 num_buckets) bytes, 256-byte aligned; its contents on entry do not matter.
- * Outputs and workspace overlap no input and one another.  Limits: those of the forward call and
- * of tsa_scheduled_attention_backward (blocks of 64 or 128 tokens, ceil(S/64) <= 8192).  Errors
- * as there.
- */
-size_t tsa_biased_attention_backward_workspace_bytes(int64_t lanes, int64_t S, int64_t block,
-                                                     int64_t nnz_cap, int64_t num_buckets);
-tsa_status tsa_biased_attention_backward(const void *Q, const void *K, const void *V, const void *O,
-                                         const void *dO, const float *lse, const int32_t *row_ptr,
-                                         const int32_t *col_idx, int64_t nnz_cap, const void *bias,
-                                         const int32_t *bucket_starts, int64_t num_buckets,
-                                         void *dQ, void *dK, void *dV, void *dbias, tsa_dtype dtype,
-                                         int64_t B, int64_t H, int64_t S, int64_t D, int64_t block,
-                                         float scale, void *workspace, size_t workspace_bytes,
-                                         tsa_stream_t stream);
-
-/*
- * Backward pass of tsa_differential_attention_fwd.  With P1, P2 the two maps' softmax:
- *   dV = (P1 - lambda P2)^T dO,  dS1 = P1 o (dO V^T - rowsum(dO o O1)),
- *   dS2 = -lambda P2 o (dO V^T - rowsum(dO o O2)),  O1 = O + lambda O2,
- *   d[q1 | q2] = scale [dS1 k1 | dS2 k2],  d[k1 | k2] = scale [dS1^T q1 | dS2^T q2],
- *   dlambda = - sum P2 o (dO V^T) over the lanes and rows that share the lambda, and by the chain
- *   rule dlambda_q1 = dlambda exp(<lambda_q1, lambda_k1>) lambda_k1 and so on.
- *
- *   O, O2, lse    as the forward call wrote them for the same inputs and CSR.
- *   dlambda_q1 .. dlambda_k2  out, [lambda_heads, D / 2] of `dtype`.
- *   workspace     >= tsa_differential_attention_backward_workspace_bytes(B*H, S, block, nnz_cap)
- *                 bytes, 256-byte aligned; its contents on entry do not matter.
- * The other arguments, limits and errors are those of tsa_biased_attention_backward.
- */
-size_t tsa_differential_attention_backward_workspace_bytes(int64_t lanes, int64_t S, int64_t block,
-                                                           int64_t nnz_cap);
-tsa_status tsa_differential_attention_backward(
-    const void *Q, const void *K, const void *V, const void *O, const void *O2, const void *dO,
-    const float *lse, const int32_t *row_ptr, const int32_t *col_idx, int64_t nnz_cap,
-    const void *lambda_q1, const void *lambda_k1, const void *lambda_q2, const void *lambda_k2,
-    int64_t lambda_heads, float lambda_init, void *dQ, void *dK, void *dV, void *dlambda_q1,
-    void *dlambda_k1, void *dlambda_q2, void *dlambda_k2, tsa_dtype dtype, int64_t B, int64_t H,
-    int64_t S, int64_t D, int64_t block, float scale, void *workspace, size_t workspace_bytes,
-    tsa_stream_t stream);
 
 /* Size of the device array behind tsa_build_schedule_noalloc: 16 MiB on every device that
  * loads the library, held until the process exits. */

@@ -1,10 +1,13 @@
 """Refusals of the attentions with learned score terms that need no GPU, and their bucket starts."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
 
 import topology_scheduled_gb300 as tsa
+from topology_scheduled_gb300.binding import SIGNATURES
 
 F = 1 << 20        # any aligned address: never read on these paths
 M = 1 << 24        # farther apart than a tensor of the calls below is long
@@ -32,6 +35,15 @@ def _diff(**change):
 BOTH = [dict(Q=None), dict(row_ptr=None), dict(O=None), dict(dtype=7), dict(B=0), dict(S=0), dict(nnz_cap=0),
         dict(scale=0.0), dict(scale=-0.1), dict(scale=float("nan")), dict(Q=F + 8), dict(O=F + 4 * M + 2),
         dict(lse=F + 5 * M + 2), dict(O=F), dict(lse=F + M + 64), dict(row_ptr=F + 2)]
+
+
+def test_every_declared_symbol_is_exported_and_bound():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(root, "include", "tsa_terms.h")).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(tsa_[a-z_0-9]+)\s*\(", text)))
+    assert names == sorted(n for n in SIGNATURES if "biased" in n or "differential" in n)
+    for n in names:
+        assert hasattr(tsa.lib(), n), n
 
 
 @pytest.mark.parametrize("change", BOTH + [dict(bias=None), dict(starts=None), dict(n=0), dict(starts=_starts(1, 2, 3, 4)),

@@ -25,7 +25,7 @@ SOURCES = ["api.cu", "schedule.cu", "segment.cu", "attention.cu", "attention_bia
            "attention_differential.cu", "terms_api.cu", "backward.cu", "backward_biased.cu", "backward_differential.cu",
            "noalloc.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("attention_kernel.cuh", "backward_kernels.cuh", "score_terms.cuh", "tsa_device.cuh",
-                                           "tsa_internal.h")] + [os.path.join(INCLUDE, "tsa.h")]
+                                           "tsa_internal.h")] + [os.path.join(INCLUDE, h) for h in ("tsa.h", "tsa_terms.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -6,8 +6,8 @@
 
 #include <stdint.h>
 
-#include "tsa.h"
 #include "tsa_device.cuh"
+#include "tsa_terms.h"
 
 namespace tsa {
 

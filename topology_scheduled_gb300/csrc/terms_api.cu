@@ -1,10 +1,11 @@
-// terms_api.cu -- C entry points of the attentions with learned score terms (include/tsa.h):
+// terms_api.cu -- C entry points of the attentions with learned score terms (include/tsa_terms.h):
 // host-side validation, tensor maps and launches.  No call allocates or frees memory.
 #include <climits>
 #include <cmath>
 #include <initializer_list>
 
 #include "tsa_internal.h"
+#include "tsa_terms.h"
 
 namespace tsa {
 namespace {

@@ -6,8 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "tsa.h"
 #include "score_terms.cuh"
+#include "tsa.h"
 #include "tsa_device.cuh"
 
 namespace tsa {

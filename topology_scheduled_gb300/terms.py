@@ -1,4 +1,4 @@
-"""Binding of the attentions with learned score terms (include/tsa.h): argument marshalling only.
+"""Binding of the attentions with learned score terms (include/tsa_terms.h): argument marshalling only.
 
 ``tsa_biased_attention*``       -- a learned bias per head and bucket of the distance q - k;
 ``tsa_differential_attention*`` -- the difference of two softmax maps, weighted by a learned lambda.
