@@ -130,6 +130,39 @@ tsa_status tsa_differential_attention_backward(
     int64_t S, int64_t D, int64_t block, float scale, void *workspace, size_t workspace_bytes,
     tsa_stream_t stream);
 
+/*
+ * One new token per sequence against a key/value cache: sequence b holds seq_lens[b] tokens, the
+ * new one last (its key and value are in the cache already), and its query attends to the keys
+ * k < seq_lens[b] of the cache blocks that row b of the schedule lists, with the scores of
+ * tsa_biased_attention_fwd (q = seq_lens[b] - 1) or the two maps of
+ * tsa_differential_attention_fwd.
+ *
+ *   Q             in,  [B*H, D] of `dtype`, 16-byte aligned.
+ *   K, V          in,  the cache, [B*H, capacity, D] of `dtype`, 16-byte aligned; what it holds at
+ *                 and beyond a sequence's length is not read.
+ *   seq_lens      in,  [B] int32 on the device, 0 .. capacity.
+ *   row_ptr, col_idx  [B + 1] and [nnz_cap] int32 on the device: row b's ascending block indices,
+ *                 blocks of `block` tokens of the cache.  Blocks at or beyond the length hold no keys.
+ *   O             out, [B*H, D] of `dtype`, 16-byte aligned, overlapping no input; 0 for a sequence
+ *                 without keys.
+ * One launch, no workspace.  Limits: block in {32, 64, 128}, D in {64, 128}, B*H <= 65535,
+ * capacity < 2^31 - 256 (the cache may pass 2^31 elements), scale >= 1e-30.  Errors as the forward
+ * calls; on the device BAD_SCHEDULE: a row outside col_idx, a length outside [0, capacity] (the
+ * sequence then has no keys), or a block out of order or outside the cache (left out).
+ */
+tsa_status tsa_biased_attention_decode(const void *Q, const void *K, const void *V,
+                                       const int32_t *seq_lens, const int32_t *row_ptr,
+                                       const int32_t *col_idx, int64_t nnz_cap, const void *bias,
+                                       const int32_t *bucket_starts, int64_t num_buckets, void *O,
+                                       tsa_dtype dtype, int64_t B, int64_t H, int64_t capacity,
+                                       int64_t D, int64_t block, float scale, tsa_stream_t stream);
+tsa_status tsa_differential_attention_decode(
+    const void *Q, const void *K, const void *V, const int32_t *seq_lens, const int32_t *row_ptr,
+    const int32_t *col_idx, int64_t nnz_cap, const void *lambda_q1, const void *lambda_k1,
+    const void *lambda_q2, const void *lambda_k2, int64_t lambda_heads, float lambda_init, void *O,
+    tsa_dtype dtype, int64_t B, int64_t H, int64_t capacity, int64_t D, int64_t block, float scale,
+    tsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

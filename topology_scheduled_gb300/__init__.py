@@ -25,5 +25,6 @@ from .binding import (STATUS_NAMES, TIE_RULES, TSA_BF16, TSA_F16, TsaError, lib,
                       tsa_build_schedule_from_sums, tsa_topology_attention_host,
                       tsa_debug_set_wait_injection)
 from .terms import (relative_bucket_starts, tsa_biased_attention, tsa_biased_attention_backward,  # noqa: F401
-                    tsa_biased_attention_fwd, tsa_differential_attention, tsa_differential_attention_backward,
+                    tsa_biased_attention_decode, tsa_biased_attention_fwd, tsa_differential_attention,
+                    tsa_differential_attention_backward, tsa_differential_attention_decode,
                     tsa_differential_attention_fwd)

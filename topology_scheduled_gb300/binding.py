@@ -61,6 +61,11 @@ SIGNATURES = {
                                                         ctypes.c_float, _P, _SZ, _P]),
     "tsa_biased_attention_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_int, _I64,
                                                 _I64, _I64, _I64, _I64, ctypes.c_float, _P]),
+    "tsa_biased_attention_decode": (ctypes.c_int, [_P] * 6 + [_I64, _P, _P, _I64, _P, ctypes.c_int] + [_I64] * 5 +
+                                    [ctypes.c_float, _P]),
+    "tsa_differential_attention_decode": (ctypes.c_int, [_P] * 6 + [_I64] + [_P] * 4 + [_I64, ctypes.c_float, _P,
+                                                                                    ctypes.c_int] + [_I64] * 5 +
+                                          [ctypes.c_float, _P]),
     "tsa_biased_attention_backward_workspace_bytes": (_SZ, [_I64] * 5),
     "tsa_biased_attention_backward": (ctypes.c_int, [_P] * 8 + [_I64, _P, _P, _I64] + [_P] * 4 + [ctypes.c_int] +
                                       [_I64] * 5 + [ctypes.c_float, _P, _SZ, _P]),

@@ -23,7 +23,7 @@ LIB = os.path.join(BUILD, "libtsa.so")
 
 SOURCES = ["api.cu", "schedule.cu", "segment.cu", "attention.cu", "attention_biased.cu",
            "attention_differential.cu", "terms_api.cu", "backward.cu", "backward_biased.cu", "backward_differential.cu",
-           "noalloc.cu"]
+           "decode.cu", "noalloc.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("attention_kernel.cuh", "backward_kernels.cuh", "score_terms.cuh", "tsa_device.cuh",
                                            "tsa_internal.h")] + [os.path.join(INCLUDE, h) for h in ("tsa.h", "tsa_terms.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

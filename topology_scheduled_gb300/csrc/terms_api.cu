@@ -215,6 +215,44 @@ tsa_status backward_launch(const void *Q, const void *K, const void *V, const vo
     return device_flags(dev, &a->flags);
 }
 
+// The decode calls: everything but the learned inputs.
+tsa_status decode_launch(const void *Q, const void *K, const void *V, const int32_t *seq_lens, const int32_t *row_ptr,
+                         const int32_t *col_idx, int64_t nnz_cap, void *O, tsa_dtype dtype, int64_t B, int64_t H,
+                         int64_t capacity, int64_t D, int64_t block, float scale, tsa_stream_t stream,
+                         std::initializer_list<Span> learned, DecodeLaunch *a) {
+    if (!Q || !K || !V || !seq_lens || !row_ptr || !col_idx || !O) return TSA_ERR_INVALID_ARGUMENT;
+    TSA_TRY(check_shape(dtype, B, H, capacity, D, block, scale, nnz_cap));
+    if (capacity > INT_MAX - 256) return TSA_ERR_UNSUPPORTED;
+    TSA_TRY(check_aligned({Q, K, V, O}, 15));
+    TSA_TRY(check_aligned({seq_lens, row_ptr, col_idx}, 3));
+    const int64_t lanes = B * H;
+    const size_t one = (size_t)(lanes * D) * 2, cache = one * (size_t)capacity;
+    if (outputs_overlap({{O, one}}, {{Q, one}, {K, cache}, {V, cache}})) return TSA_ERR_INVALID_ARGUMENT;
+    for (const Span &s : learned)
+        if (overlaps(O, one, s.p, s.bytes)) return TSA_ERR_INVALID_ARGUMENT;
+    int dev;
+    TSA_TRY(current_device(&dev));
+    TSA_TRY(check_device({Q, K, V, seq_lens, row_ptr, col_idx, O}, dev));
+    for (const Span &s : learned) TSA_TRY(check_device_ptr(s.p, dev));
+    a->Q = static_cast<const uint16_t *>(Q);
+    a->K = static_cast<const uint16_t *>(K);
+    a->V = static_cast<const uint16_t *>(V);
+    a->lens = seq_lens;
+    a->row_ptr = row_ptr;
+    a->col_idx = col_idx;
+    a->nnz_cap = (int)nnz_cap;
+    a->O = static_cast<uint16_t *>(O);
+    a->lanes = (int)lanes;
+    a->H = (int)H;
+    a->cap = (int)capacity;
+    a->D = (int)D;
+    a->block = (int)block;
+    a->bf16 = dtype == TSA_BF16;
+    a->scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a->stream = reinterpret_cast<cudaStream_t>(stream);
+    return device_flags(dev, &a->flags);
+}
+
 // Floats of the tiles' parts: a bias's bucket sums per pair of query blocks, a lambda's per block.
 int64_t bias_parts(int64_t lanes, int64_t S, int64_t n) { return lanes * ((S + 127) / 128) * n; }
 int64_t lambda_parts(int64_t lanes, int64_t S) { return lanes * ((S + 63) / 64); }
@@ -372,6 +410,37 @@ tsa_status tsa_differential_attention_backward(const void *Q, const void *K, con
     uint16_t *const dl[4] = {static_cast<uint16_t *>(dlambda_q1), static_cast<uint16_t *>(dlambda_k1),
                              static_cast<uint16_t *>(dlambda_q2), static_cast<uint16_t *>(dlambda_k2)};
     return launch_differential_backward(a, t, static_cast<const uint16_t *>(O2), dl);
+}
+
+tsa_status tsa_biased_attention_decode(const void *Q, const void *K, const void *V, const int32_t *seq_lens,
+                                       const int32_t *row_ptr, const int32_t *col_idx, int64_t nnz_cap,
+                                       const void *bias, const int32_t *bucket_starts, int64_t num_buckets, void *O,
+                                       tsa_dtype dtype, int64_t B, int64_t H, int64_t capacity, int64_t D,
+                                       int64_t block, float scale, tsa_stream_t stream) {
+    BiasTerms t;
+    if (H <= 0 || H > 65535) return H <= 0 ? TSA_ERR_INVALID_ARGUMENT : TSA_ERR_UNSUPPORTED;
+    TSA_TRY(bias_terms(bias, bucket_starts, num_buckets, H, &t));
+    DecodeLaunch a;
+    TSA_TRY(decode_launch(Q, K, V, seq_lens, row_ptr, col_idx, nnz_cap, O, dtype, B, H, capacity, D, block, scale, stream,
+                          {{bias, (size_t)(H * num_buckets) * 2}}, &a));
+    return launch_biased_decode(a, t);
+}
+
+tsa_status tsa_differential_attention_decode(const void *Q, const void *K, const void *V, const int32_t *seq_lens,
+                                             const int32_t *row_ptr, const int32_t *col_idx, int64_t nnz_cap,
+                                             const void *lambda_q1, const void *lambda_k1, const void *lambda_q2,
+                                             const void *lambda_k2, int64_t lambda_heads, float lambda_init, void *O,
+                                             tsa_dtype dtype, int64_t B, int64_t H, int64_t capacity, int64_t D,
+                                             int64_t block, float scale, tsa_stream_t stream) {
+    DiffTerms t;
+    if (H <= 0 || H > 65535) return H <= 0 ? TSA_ERR_INVALID_ARGUMENT : TSA_ERR_UNSUPPORTED;
+    if (D != 64 && D != 128) return D <= 0 ? TSA_ERR_INVALID_ARGUMENT : TSA_ERR_UNSUPPORTED;
+    TSA_TRY(diff_terms(lambda_q1, lambda_k1, lambda_q2, lambda_k2, lambda_heads, lambda_init, H, 0, &t));
+    const size_t lb = (size_t)(lambda_heads * D);
+    DecodeLaunch a;
+    TSA_TRY(decode_launch(Q, K, V, seq_lens, row_ptr, col_idx, nnz_cap, O, dtype, B, H, capacity, D, block, scale, stream,
+                          {{lambda_q1, lb}, {lambda_k1, lb}, {lambda_q2, lb}, {lambda_k2, lb}}, &a));
+    return launch_differential_decode(a, t);
 }
 
 }  // extern "C"

@@ -105,6 +105,22 @@ tsa_status launch_biased_backward(const BwdLaunch &a, const BiasTerms &terms, ui
 tsa_status launch_differential_backward(const BwdLaunch &a, const DiffTerms &terms, const uint16_t *O2,
                                         uint16_t *const dlambda[4]);
 
+// One new token per sequence against a cache [lanes, cap, D], lanes = B * H; row_ptr has B + 1 entries.
+struct DecodeLaunch {
+    const uint16_t *Q, *K, *V;
+    const int32_t *lens, *row_ptr, *col_idx;
+    int nnz_cap;
+    uint16_t *O;
+    int lanes, H, cap, D, block;
+    bool bf16;
+    float scale_log2;
+    DeviceFlags flags;
+    cudaStream_t stream;
+};
+
+tsa_status launch_biased_decode(const DecodeLaunch &a, const BiasTerms &terms);
+tsa_status launch_differential_decode(const DecodeLaunch &a, const DiffTerms &terms);
+
 // Largest number of blocks the schedule builder accepts.
 constexpr int64_t kMaxScheduleBlocks = 4096;
 constexpr int64_t kMaxScheduleDim = 1024;

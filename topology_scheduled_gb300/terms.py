@@ -234,3 +234,53 @@ def tsa_differential_attention_backward(Q, K, V, O, O2, dO, lse, row_ptr, col_id
         block, (D / 2) ** -0.5 if scale is None else float(scale), workspace.data_ptr(), workspace.numel(),
         _on(stream, workspace, dq, dk, dv, *dlambdas, ci)), "tsa_differential_attention_backward")
     return (dq, dk, dv, *dlambdas)
+
+
+def _cache(Q, K, V, seq_lens):
+    """B, H, capacity, D of a decode call's tensors."""
+    if Q.dim() != 3 or not Q.is_cuda or not Q.is_contiguous():
+        raise ValueError("Q must be a contiguous CUDA tensor [B, H, D]")
+    B, H, D = Q.shape
+    for name, t in (("K", K), ("V", V)):
+        if t.dim() != 4 or t.shape != (B, H, K.shape[2], D) or t.dtype != Q.dtype or t.device != Q.device or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [B, H, capacity, D] tensor of Q's type and device")
+    if seq_lens.dtype != torch.int32 or seq_lens.shape != (B,) or seq_lens.device != Q.device or \
+            not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be a contiguous int32 tensor [B] on the inputs' device")
+    return B, H, K.shape[2], D
+
+
+def tsa_biased_attention_decode(Q, K, V, seq_lens, row_ptr, col_idx, bias, bucket_starts, scale: float | None = None,
+                                *, out=None, block: int = 64, stream=None):
+    """One new token per sequence: Q [B, H, D] against the cache K, V [B, H, capacity, D], whose first
+    ``seq_lens[b]`` tokens are sequence b's, the new one last.  Row b of the CSR lists the cache blocks
+    that sequence b's token visits; scores as in tsa_biased_attention.  Returns [B, H, D]."""
+    B, H, cap, D = _cache(Q, K, V, seq_lens)
+    ci = _schedule(row_ptr, col_idx, B, Q.device)
+    starts, n = _starts(bucket_starts, bias)
+    _learned("bias", bias, (H, n), Q)
+    out = _output("out", out, Q.shape, Q.dtype, Q.device)
+    _check(lib().tsa_biased_attention_decode(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(),
+        bias.data_ptr(), starts, n, out.data_ptr(), _dtype_code(Q), B, H, cap, D, block,
+        1.0 / math.sqrt(D) if scale is None else float(scale), _on(stream, out, ci)), "tsa_biased_attention_decode")
+    return out
+
+
+def tsa_differential_attention_decode(Q, K, V, seq_lens, row_ptr, col_idx, lambda_q1, lambda_k1, lambda_q2, lambda_k2,
+                                      lambda_init: float, scale: float | None = None, *, out=None, block: int = 64,
+                                      stream=None):
+    """One new token per sequence, as tsa_biased_attention_decode, with the two maps of
+    tsa_differential_attention."""
+    B, H, cap, D = _cache(Q, K, V, seq_lens)
+    ci = _schedule(row_ptr, col_idx, B, Q.device)
+    lambdas = (lambda_q1, lambda_k1, lambda_q2, lambda_k2)
+    heads = _lambda_heads(lambdas, H, D, Q)
+    out = _output("out", out, Q.shape, Q.dtype, Q.device)
+    _check(lib().tsa_differential_attention_decode(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(),
+        *(t.data_ptr() for t in lambdas), heads, float(lambda_init), out.data_ptr(), _dtype_code(Q), B, H, cap, D,
+        block, (D / 2) ** -0.5 if scale is None else float(scale), _on(stream, out, ci)),
+        "tsa_differential_attention_decode")
+    return out
