@@ -169,7 +169,7 @@ def differential(Q, K, V, rp, ci, block, scale, lambdas, init, dO=None):
             out["lse"][m, l] = lse
             maps.append((P, es))
             O.append(P @ v[l])
-            raw.append((P * (r + 2 * es + n) + eta * M) @ v[l].abs())  # the denominator adds exact weights
+            raw.append((P * (2 * r + 2 * es + n) + eta * M) @ v[l].abs())
         val = O[0] - lam * O[1]
         out["O"][0][l] = val
         out["O"][1][l] = raw[0] + abs(lam) * raw[1] + el * O[1].abs() + r * val.abs() + eta + \

@@ -48,7 +48,7 @@ def test_forward(B, H, S, D, dtype, block, kind, heads):
     got, want = lse.cpu().double(), ref["lse"]
     assert torch.equal(torch.isinf(got), torch.isinf(want))
     fin = torch.isfinite(want)
-    assert not fin.any() or (got - want)[fin].abs().max() <= 2.0 ** -16  # the denominator adds exact weights
+    assert not fin.any() or (got - want)[fin].abs().max() <= 2.0 ** -16  # the log-sum-exp adds exact weights
     # without the backward pass's outputs: the same output
     again = tsa.tsa_differential_attention(q.to(DEV), k.to(DEV), v.to(DEV), *_dev(rp, ci), *lam_d, INIT, block=block)
     assert torch.equal(again, out)

@@ -39,9 +39,10 @@
 //  * Bias by buckets of the distance q - k.  The keys of a step lie in one bucket for all rows of a
 //    warp whenever the step is far enough from the diagonal (the buckets grow with the distance),
 //    and then the bias is one constant, folded into the FMA that subtracts the row maximum: such a
-//    step costs what a plain one does.  Otherwise the warp lays the biases of its 95 distances out
-//    in shared memory and every thread reads its 64, lane by lane consecutive addresses (no bank
-//    conflicts), one FMA per score.
+//    step costs what a plain one does.  Otherwise every thread reads its 64 biases from a table by
+//    distance in shared memory, lane by lane consecutive addresses (no bank conflicts), one FMA per
+//    score.  The softmax warps fill the table (the first 2048 distances at most) while the first
+//    tiles are on their way; beyond it a warp lays out the 95 distances of its step.
 //  * Differential attention.  A CTA takes one query block and both maps: rows 0-63 of the tile are
 //    the block's first map, rows 64-127 its second.  With Q laid out block-diagonally
 //    ([q1 0; 0 q2], zeros written by the softmax warps) the product with the unsplit K rows gives
@@ -389,8 +390,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     volatile int *meta_f = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kAbortFlag);
     [[maybe_unused]] const uint32_t bar_q_diag = meta + kBarQDiag;
-    [[maybe_unused]] const BucketTable table{reinterpret_cast<float *>(smem + L::kOffTable),
-                                             reinterpret_cast<int *>(smem + L::kOffTable) + kMaxBuckets};
+    [[maybe_unused]] const BucketTable table(smem + L::kOffTable);
     const uint32_t bar_q = meta + kBarQ, bar_o_done = meta + kBarODone, bar_fin = meta + kBarFin;
 #define BAR_K_FULL(s) (meta + kBarKFull + 8u * (uint32_t)(s))
 #define BAR_K_EMPTY(s) (meta + kBarKEmpty + 8u * (uint32_t)(s))
@@ -622,6 +622,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         const uint32_t t_lane = (uint32_t)(warp * 32) << 16;  // this warp's TMEM lane quarter
         float m_used = -INFINITY;                // maximum the accumulators are scaled to (log2)
         float l_sum = 0.f;                       // running denominator
+        [[maybe_unused]] float l_exact = 0.f;    // the same from the weights before their rounding
         bool ok = true;
         [[maybe_unused]] float lam = 0.f;
         if constexpr (kDiff) {
@@ -635,7 +636,12 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
             }
         }
         [[maybe_unused]] int bucket = 0;  // the bucket of this warp's largest distance of the step
-        if constexpr (kBias) bucket = terms.n - 1;
+        [[maybe_unused]] int known = 0;   // distances in the table
+        if constexpr (kBias) {
+            bucket = terms.n - 1;
+            known = table.spread(terms.n, (qa + 2) * kBlock, tid, kRows);
+            named_barrier(2, kRows);
+        }
         [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
         int u = 0;
         for (; ok; ++u) {
@@ -665,8 +671,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                     if (table.start[bucket] <= (d_lo > 0 ? d_lo : 0)) {
                         off = table.bias[bucket];
                     } else {
-                        fill_window(win, table, bucket, d_lo, tid & 31);
-                        const float *wp = win + 63 + (tid & 31);
+                        const float *wp = window_at(win, table, known, bucket, d_lo, tid & 31) + 63 + (tid & 31);
 #pragma unroll
                         for (int c = 0; c < 64; ++c) x[c] = fmaf(x[c], scale_log2, wp[-c]);
                         cc1 = 1.f;
@@ -720,6 +725,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                     }
                     if (grow) {
                         l_sum *= alpha;
+                        if constexpr (kDiff) l_exact *= alpha;
                         m_used = mx;
                     }
                 }
@@ -730,6 +736,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 const uint64_t cc = f2_pack(c1, c1);
                 const uint64_t nm = f2_pack(n1, n1);
                 float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                [[maybe_unused]] uint64_t le = f2_pack(0.f, 0.f);
 #pragma unroll
                 for (int t = 0; t < 32; ++t) {
                     float e0, e1;
@@ -744,17 +751,18 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                     }
                     // The denominator sums the rounded P that the PV product uses, so a row
                     // dominated by one key normalizes exactly.
-                    // (The differential form sums P itself: the backward pass weighs its second map
-                    // with the log-sum-exp to find lambda's gradient, one sum over every row.)
-                    if constexpr (kDiff) {
-                        ls[(t & 1) * 2] += p0;
-                        ls[(t & 1) * 2 + 1] += p1;
-                    } else {
-                        add_half<kBF16, false>(ls[(t & 1) * 2], pw[t]);
-                        add_half<kBF16, true>(ls[(t & 1) * 2 + 1], pw[t]);
-                    }
+                    add_half<kBF16, false>(ls[(t & 1) * 2], pw[t]);
+                    add_half<kBF16, true>(ls[(t & 1) * 2 + 1], pw[t]);
+                    // The log-sum-exp of the differential form adds P itself: the backward pass weighs
+                    // its second map with it to find lambda's gradient, one sum over every row.
+                    if constexpr (kDiff) le = f2_add(le, f2_pack(p0, p1));
                 }
                 l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                if constexpr (kDiff) {
+                    float e0, e1;
+                    f2_unpack(le, e0, e1);
+                    l_exact += e0 + e1;
+                }
             } else {
 #pragma unroll
                 for (int t = 0; t < 32; ++t) pw[t] = 0u;
@@ -786,19 +794,59 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
             if (lse_out && tok_ok) {
                 long long at = row0 + tok;
                 if constexpr (kDiff) at += half * terms.map_rows;
-                lse_out[at] = l_sum > 0.f ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+                lse_out[at] = l_sum > 0.f ? (m_used + log2f(kDiff ? l_exact : l_sum)) * 0.6931471805599453f : -INFINITY;
             }
             const uint32_t sw = (uint32_t)(tid & 7);
             __syncwarp();
-            // kDiff: the lower rows' output passes to the upper rows in binary32 through the K ring
-            // (every product that read it has completed), one 16-byte unit of 64 rows after another
-            [[maybe_unused]] float4 *passed = reinterpret_cast<float4 *>(smem + L::kOffK) + (tid & 63);
-#pragma unroll
-            for (int part = 0; part < (kDiff ? 2 : 1); ++part) {
             if constexpr (kDiff) {
-                if (part == 1) named_barrier(1, kRows);
-                if (half == part) continue;  // lower rows first, then upper ones
-            }
+                // The upper rows' threads finish the first half of the columns, the lower rows' the
+                // second: each passes the other's half on in binary32 through the K ring (every
+                // product that read it has completed), one 16-byte unit of 64 rows after another.
+                // The upper staging rows take O, the lower ones the second map's output.
+                constexpr int kW = D / 2;
+                const int row = tid & 63;
+                float4 *area = reinterpret_cast<float4 *>(smem + L::kOffK) + row;
+                auto stage = [&](int col, int to_row, const float (&y)[8]) {
+                    float unused = 0.f;
+                    st_shared_v4(sQ + (col >> 6) * 16384 + to_row * 128 + ((((col & 63) >> 3) ^ sw) << 4),
+                                 pack2<kBF16>(y[0], y[1], unused), pack2<kBF16>(y[2], y[3], unused),
+                                 pack2<kBF16>(y[4], y[5], unused), pack2<kBF16>(y[6], y[7], unused));
+                };
+#pragma unroll
+                for (int own = 0; own < 2; ++own) {  // the columns to pass on, then one's own
+                    if (own) named_barrier(1, kRows);
+                    const int base_col = (half ^ own ^ 1) * kW;
+#pragma unroll
+                    for (int h = 0; h < kW / 32; ++h) {
+                        uint32_t o[32];
+                        if (o_valid) {
+                            tmem_ld32(tmem + t_lane + L::kOCol + base_col + h * 32, o);
+                        } else {
+#pragma unroll
+                            for (int t = 0; t < 32; ++t) o[t] = 0u;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float y[8];
+#pragma unroll
+                            for (int t = 0; t < 8; ++t) y[t] = __uint_as_float(o[q * 8 + t]) * inv;
+                            const int col = base_col + h * 32 + q * 8;
+                            if (half && O != nullptr) stage(col, tid, y);
+                            float4 *at = area + (((half ^ own) ? kW / 4 : 0) + h * 8 + q * 2) * 64;
+                            if (!own) {
+                                at[0] = make_float4(y[0], y[1], y[2], y[3]);
+                                at[64] = make_float4(y[4], y[5], y[6], y[7]);
+                            } else {
+                                const float4 a = at[0], b = at[64];
+                                const float z[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                                for (int t = 0; t < 8; ++t) y[t] = half ? fmaf(-lam, y[t], z[t]) : fmaf(-lam, z[t], y[t]);
+                                stage(col, row, y);
+                            }
+                        }
+                    }
+                }
+            } else {
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c) {
                 const uint32_t o_row = sQ + c * 16384 + tid * 128;
@@ -815,26 +863,10 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                     for (int q = 0; q < 4; ++q) {
                         float unused = 0.f;
                         uint32_t w[4];
-                        float y[8];
 #pragma unroll
-                        for (int t = 0; t < 8; ++t) y[t] = __uint_as_float(o[q * 8 + t]) * inv;
-                        if constexpr (kDiff) {
-#pragma unroll
-                            for (int t = 0; t < 2; ++t) {
-                                float4 *at = passed + (c * 16 + h * 8 + q * 2 + t) * 64;
-                                if (half) {
-                                    *at = make_float4(y[4 * t], y[4 * t + 1], y[4 * t + 2], y[4 * t + 3]);
-                                } else {
-                                    const float4 z = *at;
-                                    y[4 * t] = fmaf(-lam, z.x, y[4 * t]);
-                                    y[4 * t + 1] = fmaf(-lam, z.y, y[4 * t + 1]);
-                                    y[4 * t + 2] = fmaf(-lam, z.z, y[4 * t + 2]);
-                                    y[4 * t + 3] = fmaf(-lam, z.w, y[4 * t + 3]);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) w[t] = pack2<kBF16>(y[2 * t], y[2 * t + 1], unused);
+                        for (int t = 0; t < 4; ++t)
+                            w[t] = pack2<kBF16>(__uint_as_float(o[q * 8 + 2 * t]) * inv,
+                                                __uint_as_float(o[q * 8 + 2 * t + 1]) * inv, unused);
                         const uint32_t chunk16 = (uint32_t)(h * 4 + q);
                         st_shared_v4(o_row + ((chunk16 ^ sw) << 4), w[0], w[1], w[2], w[3]);
                         if (partial && tok_ok)

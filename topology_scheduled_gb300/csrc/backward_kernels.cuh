@@ -319,8 +319,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         return;
     }
     uint8_t *smem = smem_raw + (base - raw_base);
-    [[maybe_unused]] const BucketTable table{reinterpret_cast<float *>(smem + L::kOffTable),
-                                             reinterpret_cast<int *>(smem + L::kOffTable) + kMaxBuckets};
+    [[maybe_unused]] const BucketTable table(smem + L::kOffTable);
     const uint32_t sQ = base + L::kOffQ, sdO = base + L::kOffDO, sK = base + L::kOffK, sV = base + L::kOffV;
     const uint32_t meta = base + L::kOffMeta;
     volatile int *meta_j = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaJ);
@@ -556,7 +555,12 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         [[maybe_unused]] float *bins = reinterpret_cast<float *>(smem + L::kOffBins) + warp * kMaxBuckets;
         [[maybe_unused]] float *diag = reinterpret_cast<float *>(smem + L::kOffDiag) + warp * (kDiagBytes / 4);
         [[maybe_unused]] const int wlane = tid & 31;
-        if constexpr (kBias) bucket = run_bucket = terms.n - 1;
+        [[maybe_unused]] int known = 0;  // distances in the table
+        if constexpr (kBias) {
+            bucket = run_bucket = terms.n - 1;
+            known = table.spread(terms.n, (qa + 2) * kBlock, tid, kRows);
+            named_barrier(2, kRows);
+        }
         auto flush_run = [&]() {
             float s = run;
 #pragma unroll
@@ -579,12 +583,13 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 [[maybe_unused]] bool near = false;
                 [[maybe_unused]] int d_lo = 0, d_hi = 0;
                 float shift = -lse2;
+                [[maybe_unused]] const float *wp = nullptr;
                 if constexpr (kBias) {
                     d_lo = (qa - j) * kBlock + warp * 32 - 63;
                     d_hi = d_lo + kWindow - 2;
                     while (bucket > 0 && d_hi < table.start[bucket]) --bucket;  // steps come nearer
                     near = table.start[bucket] > (d_lo > 0 ? d_lo : 0);
-                    if (near) fill_window(win, table, bucket, d_lo, wlane);
+                    if (near) wp = window_at(win, table, known, bucket, d_lo, wlane) + 63 + wlane;
                     else shift += table.bias[bucket];
                 }
                 [[maybe_unused]] float sum[2] = {0.f, 0.f};
@@ -596,6 +601,12 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t sr[32], pr[32];
+                        // all at once: a load would wait behind the stores of the values below
+                        [[maybe_unused]] float w[kNear ? 32 : 1];
+                        if constexpr (kNear) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) w[c] = wp[-h * 32 - c];
+                        }
                         tmem_ld32_pair(tmem + t_lane + s_col(u & 1) + h * 32, sr,
                                        tmem + t_lane + dp_col(u & 1) + h * 32, pr);
 #pragma unroll
@@ -607,7 +618,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                                 const bool masked = !live || (j == my_block && c > r_in);
                                 const float s = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
                                 float z;
-                                if constexpr (kNear) z = fmaf(s, scale_log2, win[63 + wlane - c]) - lse2;
+                                if constexpr (kNear) z = fmaf(s, scale_log2, w[2 * t + e]) - lse2;
                                 else z = fmaf(s, scale_log2, shift);
                                 const float p = masked ? 0.f : ex2_approx(z);
                                 if constexpr (kDiff) {
@@ -782,8 +793,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         return;
     }
     uint8_t *smem = smem_raw + (base - raw_base);
-    [[maybe_unused]] const BucketTable table{reinterpret_cast<float *>(smem + L::kOffTable),
-                                             reinterpret_cast<int *>(smem + L::kOffTable) + kMaxBuckets};
+    [[maybe_unused]] const BucketTable table(smem + L::kOffTable);
     const uint32_t sK = base + L::kOffK, sV = base + L::kOffV, sQ = base + L::kOffQ, sdO = base + L::kOffDO;
     const uint32_t sLse = base + L::kOffLse, sDelta = base + L::kOffDelta;
     const float *lse_s = reinterpret_cast<const float *>(smem + L::kOffLse);
@@ -1002,6 +1012,11 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             }
         }
         [[maybe_unused]] int bucket = 0;  // the bucket of this warp's largest distance of the step
+        [[maybe_unused]] int known = 0;   // distances in the table
+        if constexpr (kBias) {
+            known = table.spread(terms.n, S, tid, kRows);
+            named_barrier(2, kRows);
+        }
         [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
         [[maybe_unused]] const int wlane = tid & 31;
         int u = 0;
@@ -1023,11 +1038,12 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 // the bias: one constant for the step, or a window (query c at distance d_lo + 31 + c - wlane)
                 [[maybe_unused]] bool near = false;
                 [[maybe_unused]] float off = 0.f;
+                [[maybe_unused]] const float *wp = nullptr;
                 if constexpr (kBias) {
                     const int d_lo = (i - key_block) * kBlock - (warp & 1) * 32 - 31, d_hi = d_lo + kWindow - 2;
                     while (bucket + 1 < terms.n && d_hi >= table.start[bucket + 1]) ++bucket;  // steps go farther
                     near = table.start[bucket] > (d_lo > 0 ? d_lo : 0);
-                    if (near) fill_window(win, table, bucket, d_lo, wlane);
+                    if (near) wp = window_at(win, table, known, bucket, d_lo, wlane) + 31 - wlane;
                     else off = table.bias[bucket];
                 }
                 auto step = [&](auto is_near) {
@@ -1047,7 +1063,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                                 const bool masked = l2 == -INFINITY || (i == key_block && k_in > c);
                                 const float x = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
                                 float z;
-                                if constexpr (kNear) z = fmaf(x, scale_log2, win[31 + c - wlane]) - l2;
+                                if constexpr (kNear) z = fmaf(x, scale_log2, wp[c]) - l2;
                                 else if constexpr (kBias) z = fmaf(x, scale_log2, off - l2);
                                 else z = fmaf(x, scale_log2, -l2);
                                 p[e] = masked ? 0.f : ex2_approx(z);

@@ -116,8 +116,7 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
     __shared__ __align__(16) float warp_acc[kMaps][kWarps][D];
     __shared__ float warp_m[kMaps][kWarps], warp_l[kMaps][kWarps];
     __shared__ float cta_m[kMaps], cta_l[kMaps], cta_acc[kMaps][D];
-    __shared__ float table_bias[kBias ? kMaxBuckets : 1];
-    __shared__ int table_start[kBias ? kMaxBuckets : 1];
+    __shared__ __align__(16) uint8_t table_smem[kBias ? kBucketTableBytes : 16];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
@@ -125,7 +124,7 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
     const int b = (int)(at / H), head = (int)(at % H);
     const int group = lane / kG, li = lane % kG;
 
-    [[maybe_unused]] const BucketTable table{table_bias, table_start};
+    [[maybe_unused]] const BucketTable table(table_smem);
     if constexpr (kBias) {
         table.template load<kBF16>(terms, head, tid, kThreads);
         __syncthreads();

@@ -45,28 +45,60 @@ __device__ __forceinline__ float bias_log2(float b) {
     return b <= kBiasOut ? -INFINITY : b * 1.4426950408889634f;
 }
 
-// The buckets as a kernel keeps them in shared memory: biases in log2 units and starts.
+// The buckets as a kernel keeps them in shared memory: biases in log2 units and starts, and for the
+// first distances the bias of each.
+constexpr int kDistances = 2048;  // 8 KB beside the D = 128 forward's tiles, two thread blocks per SM
+constexpr int kDistFront = 64;    // distances below zero lie behind the causal mask; they may be read
 struct BucketTable {
     float *bias;  // kMaxBuckets
-    int *start;   // kMaxBuckets
+    int *start;   // kMaxBuckets (INT_MAX from n on)
+    float *dist;  // [-kDistFront, kDistances)
+
+    __device__ __forceinline__ explicit BucketTable(uint8_t *smem)
+        : bias(reinterpret_cast<float *>(smem)), start(reinterpret_cast<int *>(smem) + kMaxBuckets),
+          dist(reinterpret_cast<float *>(smem) + 2 * kMaxBuckets + kDistFront) {}
 
     template <bool kBF16>
     __device__ __forceinline__ void load(const BiasTerms &t, int head, int tid, int nthreads) const {
-        for (int b = tid; b < t.n; b += nthreads) {
-            bias[b] = bias_log2(widen16<kBF16>(__ldg(t.bias + (long long)head * t.n + b)));
+        for (int b = tid; b < kMaxBuckets; b += nthreads) {
+            bias[b] = b < t.n ? bias_log2(widen16<kBF16>(__ldg(t.bias + (long long)head * t.n + b))) : 0.f;
             start[b] = t.starts[b];
         }
+        for (int d = tid; d < kDistFront; d += nthreads) dist[d - kDistFront] = 0.f;
+    }
+
+    // After load and a barrier: fills dist up to where a step can still touch two buckets (or to
+    // `limit`), four distances per thread at a time, each by halving.  Returns how many are known;
+    // another barrier before they are read.
+    __device__ __forceinline__ int spread(int n, int limit, int tid, int nthreads) const {
+        int known = min(kDistances, limit);
+        if (start[n - 1] < kDistances - 95) known = min(known, start[n - 1] + 95);
+        const int first = n > 1 ? 1 << (31 - __clz(n - 1)) : 0;
+        for (int d = tid; d < known; d += 4 * nthreads) {
+            int at[4] = {0, 0, 0, 0};
+            for (int s = first; s > 0; s >>= 1)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (start[min(at[x] + s, kMaxBuckets - 1)] <= d + x * nthreads) at[x] += s;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (d + x * nthreads < known) dist[d + x * nthreads] = bias[at[x]];
+        }
+        return known;
     }
 };
-constexpr int kBucketTableBytes = kMaxBuckets * 8;
+constexpr int kBucketTableBytes = (2 * kMaxBuckets + kDistFront + kDistances) * 4;
 
 // One warp's 32 rows x 64 columns of a step hold 95 distances, d_lo .. d_lo + 94 (negative ones
 // lie behind the causal mask).
 constexpr int kWindow = 96;
 
-// Fills win[0 .. 95] with the biases of the distances d_lo + 0 .. 95; `top` is the bucket of the
-// largest one.  Three entries per lane, and a walk down the buckets that is the same in all lanes.
-__device__ __forceinline__ void fill_window(float *win, const BucketTable &t, int top, int d_lo, int lane) {
+// The biases of the distances d_lo + 0 .. 94, where they are not all the same: the table's, or, beyond
+// it, laid out in `win`; `top` is the bucket of the largest one.  Three entries per lane, and a walk
+// down the buckets that is the same in all lanes.
+__device__ __forceinline__ const float *window_at(float *win, const BucketTable &t, int known, int top, int d_lo,
+                                                  int lane) {
+    if (d_lo + kWindow - 2 < known) return t.dist + d_lo;
     const int d0 = d_lo + lane, d1 = d0 + 32, d2 = d0 + 64;
     const int least = d_lo > 0 ? d_lo : 0;
     float w0 = t.bias[top], w1 = w0, w2 = w0;
@@ -81,6 +113,7 @@ __device__ __forceinline__ void fill_window(float *win, const BucketTable &t, in
     win[lane + 32] = w1;
     win[lane + 64] = w2;
     __syncwarp();
+    return win;
 }
 
 // lambda of `head`, by the whole warp: each lane multiplies kW / 32 pairs of each product (kW = D / 2).

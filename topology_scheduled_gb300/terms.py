@@ -8,12 +8,12 @@ raise when a call fails; there is no fallback.
 """
 from __future__ import annotations
 
-import ctypes
 import math
+from array import array
 
 import torch
 
-from .binding import TsaError, _check, _check_qkv, _dtype_code, _lanes_S_D, _stream, lib
+from .binding import TsaError, _check, _check_qkv, _dtype_code, _lanes_S_D, lib
 
 MAX_BUCKETS = 256
 
@@ -40,51 +40,59 @@ def relative_bucket_starts(num_buckets: int, max_distance: int) -> list[int]:
 
 
 def _starts(bucket_starts, bias):
-    """The starts as a host array of int32."""
+    """The starts as a host array of int32 (the library checks their order)."""
     if isinstance(bucket_starts, torch.Tensor):
         if bucket_starts.is_cuda:
             raise ValueError("bucket_starts must be host integers")
         bucket_starts = bucket_starts.tolist()
-    n = len(bucket_starts)
-    if bias.shape[-1] != n:
-        raise ValueError(f"bias has {bias.shape[-1]} buckets, bucket_starts {n}")
-    if any(not 0 <= s < 1 << 31 for s in bucket_starts):
-        raise ValueError("bucket_starts must be distances that fit 32 bits")
-    return (ctypes.c_int32 * max(n, 1))(*bucket_starts), n
+    starts = array("i", bucket_starts)
+    if bias.shape[-1] != len(starts):
+        raise ValueError(f"bias has {bias.shape[-1]} buckets, bucket_starts {len(starts)}")
+    return starts, len(starts)
 
 
 def _schedule(row_ptr, col_idx, rows, device):
     """Checks a CSR of `rows` rows; col_idx with at least one entry."""
-    for name, t in (("row_ptr", row_ptr), ("col_idx", col_idx)):
-        if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name} must be a contiguous int32 tensor on the inputs' device")
+    for t in (row_ptr, col_idx):
+        if t.dtype is not torch.int32 or t.device != device or not t.is_contiguous():
+            raise ValueError("row_ptr and col_idx must be contiguous int32 tensors on the inputs' device")
     if row_ptr.numel() != rows + 1:
         raise ValueError(f"row_ptr must hold {rows + 1} entries")
     return col_idx if col_idx.numel() > 0 else torch.zeros(1, dtype=torch.int32, device=device)
 
 
 def _learned(name, t, shape, like):
-    if t.shape != torch.Size(shape) or t.dtype != like.dtype or t.device != like.device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not like.dtype or t.device != like.device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(shape)} on {like.device}")
 
 
-def _output(name, t, shape, dtype, device):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+def _output(name, t, like):
+    """`t`, or a new tensor shaped as `like`."""
+    return torch.empty_like(like) if t is None else _given(name, t, like.shape, like.dtype, like.device)
+
+
+def _rows_f32(name, t, shape, device):
+    return torch.empty(shape, dtype=torch.float32, device=device) if t is None else \
+        _given(name, t, shape, torch.float32, device)
+
+
+def _given(name, t, shape, dtype, device):
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
 
-def _on(stream, *tensors):
-    """The stream's handle; memory made here for another stream than the current one is kept for it."""
-    if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        if s != torch.cuda.current_stream():
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(s)
-    return _stream(stream)
+def _on(stream, device, *tensors):
+    """The handle of `stream`, or of the device's current stream; memory made here for another stream
+    than the current one is kept until that stream has used it."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
+    if s.cuda_stream != torch._C._cuda_getCurrentRawStream(device.index):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+    return s.cuda_stream
 
 
 def _blocks(S, block):
@@ -121,12 +129,12 @@ def tsa_biased_attention_fwd(Q, K, V, row_ptr, col_idx, bias, bucket_starts, sca
     ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
     starts, n = _starts(bucket_starts, bias)
     _learned("bias", bias, (H, n), Q)
-    out = _output("out", out, Q.shape, Q.dtype, dev)
-    lse = _output("lse", lse, (B * H, S), torch.float32, dev) if with_lse else None
+    out = _output("out", out, Q)
+    lse = _rows_f32("lse", lse, (B * H, S), dev) if with_lse else None
     _check(lib().tsa_biased_attention_fwd(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(), bias.data_ptr(),
-        starts, n, out.data_ptr(), lse.data_ptr() if with_lse else None, _dtype_code(Q), B, H, S, D, block,
-        1.0 / math.sqrt(D) if scale is None else float(scale), _on(stream, out, lse, ci)), "tsa_biased_attention_fwd")
+        starts.buffer_info()[0], n, out.data_ptr(), lse.data_ptr() if with_lse else None, _dtype_code(Q), B, H, S, D, block,
+        1.0 / math.sqrt(D) if scale is None else float(scale), _on(stream, Q.device, out, lse, ci)), "tsa_biased_attention_fwd")
     return (out, lse) if with_lse else out
 
 
@@ -155,17 +163,17 @@ def tsa_differential_attention_fwd(Q, K, V, row_ptr, col_idx, lambda_q1, lambda_
     ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
     lambdas = (lambda_q1, lambda_k1, lambda_q2, lambda_k2)
     heads = _lambda_heads(lambdas, H, D, Q)
-    out = _output("out", out, Q.shape, Q.dtype, dev)
+    out = _output("out", out, Q)
     if for_backward:
-        out2 = _output("out2", out2, Q.shape, Q.dtype, dev)
-        lse = _output("lse", lse, (2, B * H, S), torch.float32, dev)
+        out2 = _output("out2", out2, Q)
+        lse = _rows_f32("lse", lse, (2, B * H, S), dev)
     else:
         out2 = lse = None
     _check(lib().tsa_differential_attention_fwd(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(),
         *(t.data_ptr() for t in lambdas), heads, float(lambda_init), out.data_ptr(),
         out2.data_ptr() if for_backward else None, lse.data_ptr() if for_backward else None, _dtype_code(Q), B, H, S,
-        D, block, (D / 2) ** -0.5 if scale is None else float(scale), _on(stream, out, out2, lse, ci)),
+        D, block, (D / 2) ** -0.5 if scale is None else float(scale), _on(stream, Q.device, out, out2, lse, ci)),
         "tsa_differential_attention_fwd")
     return (out, out2, lse) if for_backward else out
 
@@ -191,17 +199,17 @@ def tsa_biased_attention_backward(Q, K, V, O, dO, lse, row_ptr, col_idx, bias, b
     ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
     starts, n = _starts(bucket_starts, bias)
     _learned("bias", bias, (H, n), Q)
-    lse = _output("lse", lse, (B * H, S), torch.float32, dev)
+    _given("lse", lse, (B * H, S), torch.float32, dev)
     L = lib()
     workspace = _workspace(workspace, int(L.tsa_biased_attention_backward_workspace_bytes(B * H, S, block, ci.numel(), n)),
                            dev, "tsa_biased_attention_backward_workspace_bytes")
-    dq, dk, dv = (_output(name, t, Q.shape, Q.dtype, dev) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
-    dbias = _output("dbias", dbias, bias.shape, Q.dtype, dev)
+    dq, dk, dv = (_output(name, t, Q) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
+    dbias = _output("dbias", dbias, bias)
     _check(L.tsa_biased_attention_backward(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), lse.data_ptr(), row_ptr.data_ptr(),
-        ci.data_ptr(), ci.numel(), bias.data_ptr(), starts, n, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        ci.data_ptr(), ci.numel(), bias.data_ptr(), starts.buffer_info()[0], n, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
         dbias.data_ptr(), _dtype_code(Q), B, H, S, D, block, 1.0 / math.sqrt(D) if scale is None else float(scale),
-        workspace.data_ptr(), workspace.numel(), _on(stream, workspace, dq, dk, dv, dbias, ci)),
+        workspace.data_ptr(), workspace.numel(), _on(stream, Q.device, workspace, dq, dk, dv, dbias, ci)),
         "tsa_biased_attention_backward")
     return dq, dk, dv, dbias
 
@@ -219,20 +227,19 @@ def tsa_differential_attention_backward(Q, K, V, O, O2, dO, lse, row_ptr, col_id
     ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
     lambdas = (lambda_q1, lambda_k1, lambda_q2, lambda_k2)
     heads = _lambda_heads(lambdas, H, D, Q)
-    lse = _output("lse", lse, (2, B * H, S), torch.float32, dev)
+    _given("lse", lse, (2, B * H, S), torch.float32, dev)
     L = lib()
     workspace = _workspace(workspace,
                            int(L.tsa_differential_attention_backward_workspace_bytes(B * H, S, block, ci.numel())), dev,
                            "tsa_differential_attention_backward_workspace_bytes")
-    dq, dk, dv = (_output(name, t, Q.shape, Q.dtype, dev) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
-    dlambdas = [_output(f"dlambdas[{i}]", None if dlambdas is None else dlambdas[i], t.shape, Q.dtype, dev)
-                for i, t in enumerate(lambdas)]
+    dq, dk, dv = (_output(name, t, Q) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
+    dlambdas = [_output("dlambdas", None if dlambdas is None else dlambdas[i], t) for i, t in enumerate(lambdas)]
     _check(L.tsa_differential_attention_backward(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), O2.data_ptr(), dO.data_ptr(), lse.data_ptr(),
         row_ptr.data_ptr(), ci.data_ptr(), ci.numel(), *(t.data_ptr() for t in lambdas), heads, float(lambda_init),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *(t.data_ptr() for t in dlambdas), _dtype_code(Q), B, H, S, D,
         block, (D / 2) ** -0.5 if scale is None else float(scale), workspace.data_ptr(), workspace.numel(),
-        _on(stream, workspace, dq, dk, dv, *dlambdas, ci)), "tsa_differential_attention_backward")
+        _on(stream, Q.device, workspace, dq, dk, dv, *dlambdas, ci)), "tsa_differential_attention_backward")
     return (dq, dk, dv, *dlambdas)
 
 
@@ -260,11 +267,11 @@ def tsa_biased_attention_decode(Q, K, V, seq_lens, row_ptr, col_idx, bias, bucke
     ci = _schedule(row_ptr, col_idx, B, Q.device)
     starts, n = _starts(bucket_starts, bias)
     _learned("bias", bias, (H, n), Q)
-    out = _output("out", out, Q.shape, Q.dtype, Q.device)
+    out = _output("out", out, Q)
     _check(lib().tsa_biased_attention_decode(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(),
-        bias.data_ptr(), starts, n, out.data_ptr(), _dtype_code(Q), B, H, cap, D, block,
-        1.0 / math.sqrt(D) if scale is None else float(scale), _on(stream, out, ci)), "tsa_biased_attention_decode")
+        bias.data_ptr(), starts.buffer_info()[0], n, out.data_ptr(), _dtype_code(Q), B, H, cap, D, block,
+        1.0 / math.sqrt(D) if scale is None else float(scale), _on(stream, Q.device, out, ci)), "tsa_biased_attention_decode")
     return out
 
 
@@ -277,10 +284,10 @@ def tsa_differential_attention_decode(Q, K, V, seq_lens, row_ptr, col_idx, lambd
     ci = _schedule(row_ptr, col_idx, B, Q.device)
     lambdas = (lambda_q1, lambda_k1, lambda_q2, lambda_k2)
     heads = _lambda_heads(lambdas, H, D, Q)
-    out = _output("out", out, Q.shape, Q.dtype, Q.device)
+    out = _output("out", out, Q)
     _check(lib().tsa_differential_attention_decode(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(),
         *(t.data_ptr() for t in lambdas), heads, float(lambda_init), out.data_ptr(), _dtype_code(Q), B, H, cap, D,
-        block, (D / 2) ** -0.5 if scale is None else float(scale), _on(stream, out, ci)),
+        block, (D / 2) ** -0.5 if scale is None else float(scale), _on(stream, Q.device, out, ci)),
         "tsa_differential_attention_decode")
     return out
