@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(1024) bwd_col_pairs(int nb, int pow2, const in
 // Grid: y over lanes, x over a lane's (row, 16-byte chunk) items -- at most 8192 * 64 * 16, so
 // 32-bit indices and shifts -- with four items per thread whose loads are all issued before
 // their arithmetic.  Rows are laid out per lane over Sp = nb * 64 tokens; the tokens past S (a
-// partial last block) get Delta 0 and log-sum-exp -inf, and the given log-sum-exp is copied
-// into the same layout.
+// partial last block) get Delta 0 and log-sum-exp +inf (see padded_lse), and the given log-sum-exp
+// is copied into the same layout.
 constexpr int kDeltaItems = 4;
 template <bool kBF16, int kG>
 __global__ void __launch_bounds__(256) bwd_delta(const uint16_t *__restrict__ O, const uint16_t *__restrict__ dO,
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(256) bwd_delta(const uint16_t *__restrict__ O,
         if (x < per_lane && x % kG == 0) {
             const long long pr = lane * Sp + t;  // padded row
             delta[pr] = acc;
-            lse_pad[pr] = t < S ? __ldg(lse + lane * S + t) : -INFINITY;
+            lse_pad[pr] = t < S ? padded_lse(__ldg(lse + lane * S + t)) : INFINITY;
         }
     }
 }

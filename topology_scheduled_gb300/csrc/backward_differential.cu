@@ -8,7 +8,7 @@ namespace {
 // Delta of both maps per row, <dO, O1> and <dO, O2> in binary32.  The forward stored O = O1 - lambda O2
 // and O2, so the first is <dO, O> + lambda <dO, O2>.  kG = D / 8 threads per row, 16 bytes of each
 // tensor per thread, three loads in flight per item and two items per thread.  Rows are laid out per
-// map and lane over Sp = nb * 64 tokens; tokens past S get Delta 0 and log-sum-exp -inf.
+// map and lane over Sp = nb * 64 tokens; tokens past S get Delta 0 and log-sum-exp +inf.
 constexpr int kItems = 2;
 template <bool kBF16, int kG>
 __global__ void __launch_bounds__(256)
@@ -55,8 +55,8 @@ diff_delta(const uint16_t *__restrict__ O, const uint16_t *__restrict__ O2, cons
             const long long pr = lane * Sp + t, rows = (long long)gridDim.y * S, at = lane * S + t;
             delta[pr] = fmaf(lam, s2, s);
             delta[terms.map_rows + pr] = s2;
-            lse_pad[pr] = t < S ? __ldg(lse + at) : -INFINITY;
-            lse_pad[terms.map_rows + pr] = t < S ? __ldg(lse + rows + at) : -INFINITY;
+            lse_pad[pr] = t < S ? padded_lse(__ldg(lse + at)) : INFINITY;
+            lse_pad[terms.map_rows + pr] = t < S ? padded_lse(__ldg(lse + rows + at)) : INFINITY;
         }
     }
 }

@@ -55,6 +55,10 @@ __device__ __forceinline__ uint32_t pack16x2(float a, float b) {
     }
 }
 
+// The log-sum-exp as the gradient kernels subtract it: log2 units, and +inf for a row without keys,
+// whose weights 2^(z - inf) are then 0 like those of rows past the end.
+__device__ __forceinline__ float padded_lse(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
 // Union of two ascending index lists (already checked), with membership bits (1: first list,
 // 2: second list); -1 at the end.
 struct ListUnion {
@@ -529,9 +533,8 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         // the row in the per-lane padded Delta / log-sum-exp arrays (nb * 64 rows per lane)
         long long grow = ((long long)lane_id * nb + qa) * kBlock + (kDiff ? r_in : tid);
         if constexpr (kDiff) grow += half * terms.map_rows;
-        const float lse2 = row_exists ? lse[grow] * kLog2e : -INFINITY;
+        const float lse2 = row_exists ? lse[grow] : INFINITY;
         float dlt = row_exists ? delta[grow] : 0.f;
-        const bool live = lse2 > -INFINITY;  // a row with keys
         bool ok = true;
         // kDiff: the second map's dP is -lambda dO V^T
         [[maybe_unused]] float mul = 1.f, dot[2] = {0.f, 0.f};  // dot: sum of P o dO V^T over the row
@@ -596,8 +599,9 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 // keys up to this one lie in the last bucket
                 [[maybe_unused]] int far_to = -1;
                 if constexpr (kBias) far_to = d_lo + 63 + wlane - table.start[terms.n - 1];
-                auto step = [&](auto is_near) {
-                    constexpr bool kNear = decltype(is_near)::value;
+                const float zero_at = shift, delta_at = dlt, times = mul;
+                auto step = [&, zero_at, delta_at, times, wp](auto is_near, auto is_diagonal) {
+                    constexpr bool kNear = decltype(is_near)::value, kDiagonal = decltype(is_diagonal)::value;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t sr[32], pr[32];
@@ -615,17 +619,17 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int c = h * 32 + 2 * t + e;
-                                const bool masked = !live || (j == my_block && c > r_in);
                                 const float s = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
                                 float z;
-                                if constexpr (kNear) z = fmaf(s, scale_log2, w[2 * t + e]) - lse2;
-                                else z = fmaf(s, scale_log2, shift);
-                                const float p = masked ? 0.f : ex2_approx(z);
+                                if constexpr (kNear) z = fmaf(s, scale_log2, w[2 * t + e]) + zero_at;
+                                else z = fmaf(s, scale_log2, zero_at);
+                                float p = ex2_approx(z);
+                                if constexpr (kDiagonal) p = c > r_in ? 0.f : p;
                                 if constexpr (kDiff) {
-                                    ds[e] = p * fmaf(dp, mul, -dlt);
+                                    ds[e] = p * fmaf(dp, times, -delta_at);
                                     dot[e] = fmaf(p, dp, dot[e]);
                                 } else {
-                                    ds[e] = p * (dp - dlt);
+                                    ds[e] = p * (dp - delta_at);
                                 }
                                 if constexpr (kNear) {
                                     diag[wlane * kDiagStride + c] = ds[e];
@@ -638,11 +642,14 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         }
                     }
                 };
-                if constexpr (kBias) {
-                    if (near) step(std::true_type{});
-                    else step(std::false_type{});
+                // (the diagonal block, and with a bias the near steps, as loops of their own)
+                if (kBias && near) {
+                    if (j == my_block) step(std::bool_constant<kBias>{}, std::true_type{});
+                    else step(std::bool_constant<kBias>{}, std::false_type{});
+                } else if (j == my_block) {
+                    step(std::false_type{}, std::true_type{});
                 } else {
-                    step(std::false_type{});
+                    step(std::false_type{}, std::false_type{});
                 }
                 if constexpr (kBias) {
                     const int last = terms.n - 1;
@@ -1046,8 +1053,9 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     if (near) wp = window_at(win, table, known, bucket, d_lo, wlane) + 31 - wlane;
                     else off = table.bias[bucket];
                 }
-                auto step = [&](auto is_near) {
-                    constexpr bool kNear = decltype(is_near)::value;
+                const float bias_at = off, times = mul;
+                auto step = [&, bias_at, times, wp, ls, dl](auto is_near, auto is_diagonal) {
+                    constexpr bool kNear = decltype(is_near)::value, kDiagonal = decltype(is_diagonal)::value;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t sr[32], pr[32];
@@ -1059,15 +1067,15 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int c = h * 32 + 2 * t + e;  // query token within block i
-                                const float l2 = ls[c] * kLog2e;
-                                const bool masked = l2 == -INFINITY || (i == key_block && k_in > c);
+                                const float l2 = ls[c];
                                 const float x = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
                                 float z;
                                 if constexpr (kNear) z = fmaf(x, scale_log2, wp[c]) - l2;
-                                else if constexpr (kBias) z = fmaf(x, scale_log2, off - l2);
+                                else if constexpr (kBias) z = fmaf(x, scale_log2, bias_at - l2);
                                 else z = fmaf(x, scale_log2, -l2);
-                                p[e] = masked ? 0.f : ex2_approx(z);
-                                if constexpr (kDiff) p[e] *= mul;
+                                p[e] = ex2_approx(z);
+                                if constexpr (kDiagonal) p[e] = k_in > c ? 0.f : p[e];
+                                if constexpr (kDiff) p[e] *= times;
                                 ds[e] = p[e] * (dp - dl[c]);
                             }
                             pw[h * 16 + t] = pack16x2<kBF16>(p[0], p[1]);
@@ -1075,11 +1083,13 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         }
                     }
                 };
-                if constexpr (kBias) {
-                    if (near) step(std::true_type{});
-                    else step(std::false_type{});
+                if (kBias && near) {
+                    if (i == key_block) step(std::bool_constant<kBias>{}, std::true_type{});
+                    else step(std::bool_constant<kBias>{}, std::false_type{});
+                } else if (i == key_block) {
+                    step(std::false_type{}, std::true_type{});
                 } else {
-                    step(std::false_type{});
+                    step(std::false_type{}, std::false_type{});
                 }
             } else {
 #pragma unroll

@@ -76,8 +76,8 @@ struct BwdLaunch {
     int64_t nnz_cap;
     long long read_cap;  // entries of col_idx that may be read
     float *partial;      // score terms: each tile's part of the learned inputs' gradients
-    // Delta and the log-sum-exp per lane over nb * 64 rows (rows past S: 0 and -inf), so a
-    // partial last block is read like any other
+    // Delta and the log-sum-exp per lane over nb * 64 rows, so a partial last block is read like any
+    // other; the log-sum-exp in log2 units, +inf for rows past S and rows without keys
     float *delta, *lse_pad;
     int *vlen, *cnt, *col_ptr;
     unsigned *bitmap;
