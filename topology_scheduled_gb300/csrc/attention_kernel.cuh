@@ -412,7 +412,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     // the same branch), and the producer's CSR rows.
     const bool gave_up = tid == 0 && *reinterpret_cast<volatile unsigned *>(flags.abort_epoch) == flags.epoch;
     EntryWalk<kGran, kDiff> ruk, ruv;  // the producer's walks of the row union, one per stream
-    if (tid == kProducerWarp * 32) {
+    if (warp == kProducerWarp && elect_one()) {
         ruk.template init<kBias || kDiff>(row_ptr, col_idx, qa, has_b, nb, S, nnz_cap);
         ruv.template init<kBias || kDiff>(row_ptr, col_idx, qa, has_b, nb, S, nnz_cap);
     }
@@ -459,7 +459,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         // v % kKStages as soon as QK(v - kKStages) has freed it, the V tile into V stage
         // v % kVStages as soon as PV(v - kVStages) has; the thread polls both rings, so a K
         // load never waits behind a V stage.
-        if ((tid & 31) == 0) {
+        if (elect_one()) {
             tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
@@ -539,9 +539,11 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
-        if ((tid & 31) == 0) {
+        if (elect_one()) {
             constexpr uint32_t kIdescQK = idesc_f16(kBF16, 128, 64, false);
             constexpr uint32_t kIdescPV = idesc_f16(kBF16, 128, D, true);
+            const uint64_t q_desc = sdesc_sw128(sQ, 16, 1024), k_desc = sdesc_sw128(sK0, 16, 1024),
+                           v_desc = sdesc_sw128(sV0, 8192, 1024);
             bool ok = mbar_wait(bar_q, 0, flags);
             if constexpr (kDiff) ok = ok && mbar_wait(bar_q_diag, 0, flags);
             int u = 0;
@@ -552,9 +554,8 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         const int s_ = (uu) % kKStages;                                                           \
         tc_fence_after();                                                                         \
         _Pragma("unroll") for (int kk = 0; kk < D / 16; ++kk) {                                   \
-            const uint64_t a_ = sdesc_sw128(sQ + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);    \
-            const uint64_t b_ =                                                                   \
-                sdesc_sw128(sK0 + s_ * L::kKVBytes + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024); \
+            const uint64_t a_ = sdesc_at(q_desc, (kk >> 2) * 16384 + (kk & 3) * 32);              \
+            const uint64_t b_ = sdesc_at(k_desc, s_ * L::kKVBytes + (kk >> 2) * 8192 + (kk & 3) * 32); \
             tc_mma_ss(tmem + s_col((uu) & 1), a_, b_, kIdescQK, kk > 0 ? 1u : 0u);               \
         }                                                                                         \
         tc_commit(BAR_S_FULL((uu) & 1));                                                          \
@@ -597,7 +598,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    const uint64_t b = sdesc_sw128(sV0 + s * L::kKVBytes + kk * 2048, 8192, 1024);
+                    const uint64_t b = sdesc_at(v_desc, s * L::kKVBytes + kk * 2048);
                     tc_mma_ts(tmem + L::kOCol, tmem + s_col(u & 1) + kk * 8, b, kIdescPV,
                               (u > 0 || kk > 0) ? 1u : 0u);
                 }

@@ -204,8 +204,8 @@ constexpr int kBarDone = kBarPFull + 16;              // accumulation MMA of a s
 constexpr int kBarFin = kBarDone + 8;
 constexpr int kBarVFull = kBarFin + 8;                // dQ kernel: kStream x 8, V of a step landed
 constexpr int kBarVEmpty = kBarVFull + 8 * kStream;   // dQ kernel: kStream x 8
-constexpr int kBarDiag = kBarVEmpty + 8 * kStream;    // the resident tile is block-diagonal
-constexpr int kTmemSlot = kBarDiag + 8;
+constexpr int kBarReady = kBarVEmpty + 8 * kStream;   // the resident operands are in place
+constexpr int kTmemSlot = kBarReady + 8;
 constexpr int kAbortFlag = kTmemSlot + 4;
 constexpr int kMetaJ = kAbortFlag + 4;                // kMetaRing x 4
 constexpr int kMetaF = kMetaJ + 4 * kMetaRing;        // kMetaRing x 4
@@ -220,6 +220,28 @@ constexpr int smem_bytes_one_cta(int need) { return need > 116 * 1024 ? need : 1
 __device__ __forceinline__ uint32_t s_col(int b) { return b ? 64u : 0u; }
 __device__ __forceinline__ uint32_t dp_col(int b) { return b ? 192u : 128u; }
 constexpr uint32_t kAccCol = 256;
+
+// Row `row` (0-127) of a 128-row SW128 tile into tensor memory as a product's left operand: D / 2
+// columns from `col`, two 16-bit elements per column.  kDiagonal: rows 0-63 keep the first half of
+// their elements, rows 64-127 the second, the others are zero (see keep_diagonal).
+template <int D, bool kDiagonal>
+__device__ __forceinline__ void tile_row_to_tmem(const uint8_t *tile, int row, uint32_t tmem_row, uint32_t col) {
+    const uint32_t sw = (uint32_t)(row & 7);
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(tile + c * 16384 + row * 128 + (((uint32_t)u ^ sw) << 4));
+            const bool keep = !kDiagonal || (D == 128 ? c : u >> 2) == (row >> 6);
+            w[4 * u] = keep ? x.x : 0u;
+            w[4 * u + 1] = keep ? x.y : 0u;
+            w[4 * u + 2] = keep ? x.z : 0u;
+            w[4 * u + 3] = keep ? x.w : 0u;
+        }
+        tmem_st32(tmem_row + col + c * 32, w);
+    }
+}
 
 // ---------------------------------------------------------------- dQ
 // Adds a warp's 32 x 64 values of dS to its bucket sums, but for the last bucket's: row r, column c
@@ -349,7 +371,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     // and the producer's two CSR rows.
     const bool gave_up = tid == 0 && *reinterpret_cast<volatile unsigned *>(flags.abort_epoch) == flags.epoch;
     ListUnion lu;
-    if (tid == kProducerWarp * 32) {
+    if (warp == kProducerWarp && elect_one()) {
         lu.a = col_idx + row_ptr[qa];
         lu.ia = 0;
         lu.ia_end = vlen[qa];
@@ -372,7 +394,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         }
         mbar_init(bar_done, 1);
         mbar_init(bar_fin, 1);
-        if constexpr (kDiff) mbar_init(meta + kBarDiag, kRows);
+        mbar_init(meta + kBarReady, kRows);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -395,8 +417,11 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         return;
     }
 
+    // Q and dO as left operands, behind the accumulator
+    constexpr uint32_t kQCol = kAccCol + D, kDOCol = kQCol + D / 2;
+
     if (warp == kProducerWarp) {
-        if ((tid & 31) == 0) {
+        if (elect_one()) {
             tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(&tmdO);
             tma_prefetch_desc(&tmK);
@@ -450,11 +475,14 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             }
         }
     } else if (warp == kMmaWarp) {
-        if ((tid & 31) == 0) {
+        if (elect_one()) {
             constexpr uint32_t kIdescS = idesc_f16(kBF16, 128, 64, false);
             constexpr uint32_t kIdescAcc = idesc_f16(kBF16, 128, D, true);
+            const uint64_t k_desc = sdesc_sw128(sK, 16, 1024), v_desc = sdesc_sw128(sV, 16, 1024),
+                           kt_desc = sdesc_sw128(sK, 8192, 1024);
             bool ok = mbar_wait(bar_tile, 0, flags);
-            if constexpr (kDiff) ok = ok && mbar_wait(meta + kBarDiag, 0, flags);
+            ok = ok && mbar_wait(meta + kBarReady, 0, flags);
+            tc_fence_after();
             int u = 0;
             bool have = false;
             // products of step uu: S = Q K^T and dP = dO V^T; V's stage is free afterwards
@@ -464,17 +492,15 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t koff = (kk >> 2) * 16384 + (kk & 3) * 32;
                     const uint32_t boff = s_ * L::kKVBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
-                    tc_mma_ss(tmem + s_col(uu & 1), sdesc_sw128(sQ + koff, 16, 1024),
-                              sdesc_sw128(sK + boff, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+                    tc_mma_ts(tmem + s_col(uu & 1), tmem + kQCol + kk * 8, sdesc_at(k_desc, boff), kIdescS,
+                              kk > 0 ? 1u : 0u);
                 }
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t koff = (kk >> 2) * 16384 + (kk & 3) * 32;
                     const uint32_t boff = s_ * L::kKVBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
-                    tc_mma_ss(tmem + dp_col(uu & 1), sdesc_sw128(sdO + koff, 16, 1024),
-                              sdesc_sw128(sV + boff, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+                    tc_mma_ts(tmem + dp_col(uu & 1), tmem + kDOCol + kk * 8, sdesc_at(v_desc, boff), kIdescS,
+                              kk > 0 ? 1u : 0u);
                 }
                 tc_commit(BAR_S_FULL(uu & 1));
                 tc_commit(BAR_V_EMPTY(s_));
@@ -511,7 +537,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     tc_mma_ts(tmem + kAccCol, tmem + s_col(u & 1) + kk * 8,
-                              sdesc_sw128(sK + s * L::kKVBytes + kk * 2048, 8192, 1024), kIdescAcc,
+                              sdesc_at(kt_desc, s * L::kKVBytes + kk * 2048), kIdescAcc,
                               (u > 0 || kk > 0) ? 1u : 0u);
                 tc_commit(BAR_K_EMPTY(s));
                 tc_commit(bar_done);
@@ -542,12 +568,16 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             const float lam = lambda_of<D / 2, kBF16>(terms, lane_id % terms.H);
             if (half) mul = -lam;
             dlt *= mul;
-            ok = mbar_wait(bar_tile, 0, flags);
-            if (ok) {
-                keep_diagonal<D>(sQ, tid);
-                fence_proxy_async_smem();
-                mbar_arrive(meta + kBarDiag);
-            }
+        }
+        ok = mbar_wait(bar_tile, 0, flags);
+        __syncwarp();
+        if (__all_sync(0xffffffffu, ok)) {
+            tile_row_to_tmem<D, kDiff>(smem + L::kOffQ, tid, tmem + t_lane, kQCol);
+            tile_row_to_tmem<D, false>(smem + L::kOffDO, tid, tmem + t_lane, kDOCol);
+            tc_fence_before();
+            mbar_arrive(meta + kBarReady);
+        } else {
+            ok = false;
         }
         // kBias: the bucket of this warp's largest distance, the sum `run` of dS in it so far, and
         // the sum over the row of what lies before the last bucket
@@ -827,7 +857,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     // before the first barrier.
     const bool gave_up = tid == 0 && *reinterpret_cast<volatile unsigned *>(flags.abort_epoch) == flags.epoch;
     ListUnion lu;
-    if (tid == kProducerWarp * 32) {
+    if (warp == kProducerWarp && elect_one()) {
         lu.a = row_idx + col_ptr[ka];
         lu.ia = 0;
         lu.ia_end = col_ptr[ka + 1] - col_ptr[ka];
@@ -848,7 +878,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
         mbar_init(bar_done, 1);
         mbar_init(bar_fin, 1);
-        if constexpr (kDiff) mbar_init(meta + kBarDiag, kRows);
+        if constexpr (kDiff) mbar_init(meta + kBarReady, kRows);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -870,7 +900,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     constexpr uint32_t kDVCol = kAccCol, kDKCol = kAccCol + D;
 
     if (warp == kProducerWarp) {
-        if ((tid & 31) == 0) {
+        if (elect_one()) {
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
             tma_prefetch_desc(&tmQ);
@@ -924,11 +954,14 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             }
         }
     } else if (warp == kMmaWarp) {
-        if ((tid & 31) == 0) {
+        if (elect_one()) {
             constexpr uint32_t kIdescS = idesc_f16(kBF16, 128, 64, false);
             constexpr uint32_t kIdescAcc = idesc_f16(kBF16, 128, D, true);
+            const uint64_t k_desc = sdesc_sw128(sK, 16, 1024), v_desc = sdesc_sw128(sV, 16, 1024),
+                           q_desc = sdesc_sw128(sQ, 16, 1024), do_desc = sdesc_sw128(sdO, 16, 1024),
+                           qt_desc = sdesc_sw128(sQ, 8192, 1024), dot_desc = sdesc_sw128(sdO, 8192, 1024);
             bool ok = mbar_wait(bar_tile, 0, flags);
-            if constexpr (kDiff) ok = ok && mbar_wait(meta + kBarDiag, 0, flags);
+            if constexpr (kDiff) ok = ok && mbar_wait(meta + kBarReady, 0, flags);
             int u = 0;
             bool have = false;
             // products of step uu: S^T = K Q^T and dP^T = V dO^T
@@ -939,15 +972,15 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
                     const uint32_t boff = s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
-                    tc_mma_ss(tmem + s_col(uu & 1), sdesc_sw128(sK + aoff, 16, 1024),
-                              sdesc_sw128(sQ + boff, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+                    tc_mma_ss(tmem + s_col(uu & 1), sdesc_at(k_desc, aoff), sdesc_at(q_desc, boff),
+                              kIdescS, kk > 0 ? 1u : 0u);
                 }
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
                     const uint32_t boff = s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
-                    tc_mma_ss(tmem + dp_col(uu & 1), sdesc_sw128(sV + aoff, 16, 1024),
-                              sdesc_sw128(sdO + boff, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+                    tc_mma_ss(tmem + dp_col(uu & 1), sdesc_at(v_desc, aoff), sdesc_at(do_desc, boff),
+                              kIdescS, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(BAR_S_FULL(uu & 1));
             };
@@ -981,12 +1014,12 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     tc_mma_ts(tmem + kDVCol, tmem + s_col(u & 1) + kk * 8,
-                              sdesc_sw128(sdO + s * L::kQBytes + kk * 2048, 8192, 1024), kIdescAcc,
+                              sdesc_at(dot_desc, s * L::kQBytes + kk * 2048), kIdescAcc,
                               (u > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     tc_mma_ts(tmem + kDKCol, tmem + dp_col(u & 1) + kk * 8,
-                              sdesc_sw128(sQ + s * L::kQBytes + kk * 2048, 8192, 1024), kIdescAcc,
+                              sdesc_at(qt_desc, s * L::kQBytes + kk * 2048), kIdescAcc,
                               (u > 0 || kk > 0) ? 1u : 0u);
                 tc_commit(BAR_EMPTY(s));
                 tc_commit(bar_done);
@@ -1015,7 +1048,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             if (ok) {
                 keep_diagonal<D>(sK, tid);
                 fence_proxy_async_smem();
-                mbar_arrive(meta + kBarDiag);
+                mbar_arrive(meta + kBarReady);
             }
         }
         [[maybe_unused]] int bucket = 0;  // the bucket of this warp's largest distance of the step

@@ -100,6 +100,16 @@ __device__ __forceinline__ bool mbar_wait_timed(uint32_t bar, uint32_t parity) {
     }
 }
 
+// True in one lane of a converged warp, the same one every time.  The single-thread roles branch on
+// it: the compiler then knows that one lane is active and keeps the operands of the tensor-core and
+// copy instructions in uniform registers, where a test of the lane's number makes it move each of
+// them there one by one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -256,6 +266,9 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
+
+// The descriptor of the same layout `bytes` (a multiple of 16) further on.
+__device__ __forceinline__ uint64_t sdesc_at(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 
 // TMEM load: this warp's 32 lanes x 32 consecutive 32-bit columns -> 32 registers per thread.
 // The wait is fused in and takes the registers as operands so no use moves above it.
