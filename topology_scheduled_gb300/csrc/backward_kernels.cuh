@@ -5,9 +5,9 @@
 // Bias by buckets.  P is recomputed with the bias, a constant per step or a window per warp as in the
 // forward.  Its gradient sums dS over buckets in bwd_dq_kernel, in binary32 before dS is rounded:
 //  * a step inside one bucket adds each row's sum, kept in registers until the bucket changes;
-//  * near the diagonal a warp lays its 32 x 64 values out in shared memory with rows 65 apart, adds
-//    up the 95 diagonals (one distance each; every read of a warp touches 32 banks) and then, by
-//    shuffles, the distances of each bucket;
+//  * near the diagonal a warp adds up the 95 diagonals of its 32 x 64 values, one distance each: for
+//    column c every lane takes the value of the row c + 1 lanes on (by a shuffle), which lies on a
+//    diagonal of its own for all columns; then, by shuffles too, the distances of each bucket;
 //  * the last, open bucket gets minus the sum of the row's other values, since a row of dS sums to
 //    zero: no work on the far steps, and none of the error that Delta's rounded output leaves in each
 //    of their many values (it is a common shift of a row's dP, which the far keys would add up).
@@ -37,8 +37,8 @@ constexpr int kThreads = 192;
 constexpr int kRows = 128;
 constexpr int kProducerWarp = 4;
 constexpr int kMmaWarp = 5;
-constexpr int kStream = 3;     // depth of the ring of streamed blocks
-constexpr int kMetaRing = 4;   // > kStream: a slot is rewritten only after its step is consumed
+constexpr int kStream = 4;     // depth of the ring of streamed blocks
+constexpr int kMetaRing = 8;   // > kStream: a slot is rewritten only after its step is consumed
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------- shared helpers
@@ -209,7 +209,7 @@ constexpr int kTmemSlot = kBarReady + 8;
 constexpr int kAbortFlag = kTmemSlot + 4;
 constexpr int kMetaJ = kAbortFlag + 4;                // kMetaRing x 4
 constexpr int kMetaF = kMetaJ + 4 * kMetaRing;        // kMetaRing x 4
-constexpr int kMetaBytes = 256;
+constexpr int kMetaBytes = 512;
 static_assert(kMetaF + 4 * kMetaRing <= kMetaBytes, "meta area");
 
 constexpr uint32_t kTmemCols = 512;  // S0 | S1 | dP0 | dP1 | accumulator(s)
@@ -244,29 +244,11 @@ __device__ __forceinline__ void tile_row_to_tmem(const uint8_t *tile, int row, u
 }
 
 // ---------------------------------------------------------------- dQ
-// Adds a warp's 32 x 64 values of dS to its bucket sums, but for the last bucket's: row r, column c
-// lies at the distance d_lo + 63 + r - c.  `win` is scratch (96 floats).
-__device__ __forceinline__ void sum_diagonals(float *bins, float *win, const float *diag, const BucketTable &t,
-                                              int top, int last, int d_lo, int d_hi, int lane);
-
-// A warp's 32 x 64 values of dS near the diagonal, rows 65 apart.
-constexpr int kDiagStride = 65;
-constexpr int kDiagBytes = 32 * kDiagStride * 4;
-
-__device__ __forceinline__ void sum_diagonals(float *bins, float *win, const float *diag, const BucketTable &t,
-                                              int top, int last, int d_lo, int d_hi, int lane) {
-    __syncwarp();  // every lane's values are there, and the window has been read
-    // lane's diagonals are the distances d_lo + lane, + 32 and + 64; the first has rows up to `lane`,
-    // the third those after it
-    float a0 = 0.f, a1 = 0.f, a2 = 0.f;
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r) {
-        const float *row = diag + r * kDiagStride + r - lane;
-        a1 += row[31];
-        const float x = row[r <= lane ? 63 : -1];
-        if (r <= lane) a0 += x;
-        else a2 += x;
-    }
+// Adds a warp's sums of dS per distance to its bucket sums, but for the last bucket's.  A lane's
+// distances are d_lo + lane (a0), + 32 (a1) and + 64 (a2); `top` is the bucket of d_hi, `win` scratch
+// (96 floats).
+__device__ __forceinline__ void add_distances(float *bins, float *win, float a0, float a1, float a2,
+                                              const BucketTable &t, int top, int last, int d_lo, int d_hi, int lane) {
     // running sums over the 96 distances that begin anew with each bucket (so that a bucket's sum
     // holds nothing of another's): where buckets begin, as three words of bits
     const int least = d_lo > 0 ? d_lo : 0;
@@ -319,8 +301,7 @@ struct DqSmem {
     static constexpr int kOffTable = kOffMeta + kMetaBytes;                      // bias only, up to kOffEnd
     static constexpr int kOffWin = kOffTable + kBucketTableBytes;                // 4 windows
     static constexpr int kOffBins = kOffWin + 4 * kWindow * 4;                   // 4 x kMaxBuckets sums
-    static constexpr int kOffDiag = kOffBins + 4 * kMaxBuckets * 4;              // 4 warps' values
-    static constexpr int kEnd = Terms::kBias ? kOffDiag + 4 * kDiagBytes : kOffTable;
+    static constexpr int kEnd = Terms::kBias ? kOffBins + 4 * kMaxBuckets * 4 : kOffTable;
     static constexpr int kBytes = smem_bytes_one_cta(kEnd + 1024);  // + alignment slack
 };
 
@@ -586,11 +567,12 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         [[maybe_unused]] bool reached = false;  // the row has keys in the last bucket
         [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
         [[maybe_unused]] float *bins = reinterpret_cast<float *>(smem + L::kOffBins) + warp * kMaxBuckets;
-        [[maybe_unused]] float *diag = reinterpret_cast<float *>(smem + L::kOffDiag) + warp * (kDiagBytes / 4);
         [[maybe_unused]] const int wlane = tid & 31;
         [[maybe_unused]] int known = 0;  // distances in the table
+        [[maybe_unused]] int last_bucket = 0, last_start = 0;
         if constexpr (kBias) {
-            bucket = run_bucket = terms.n - 1;
+            bucket = run_bucket = last_bucket = terms.n - 1;
+            last_start = table.start[last_bucket];
             known = table.spread(terms.n, (qa + 2) * kBlock, tid, kRows);
             named_barrier(2, kRows);
         }
@@ -625,22 +607,20 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     if (near) wp = window_at(win, table, known, bucket, d_lo, wlane) + 63 + wlane;
                     else shift += table.bias[bucket];
                 }
-                [[maybe_unused]] float sum[2] = {0.f, 0.f};
+                // sums of dS over the row (without the last bucket's keys) and over the diagonals
+                [[maybe_unused]] float sum[2] = {0.f, 0.f}, a0 = 0.f, a1 = 0.f, a2 = 0.f;
                 // keys up to this one lie in the last bucket
                 [[maybe_unused]] int far_to = -1;
-                if constexpr (kBias) far_to = d_lo + 63 + wlane - table.start[terms.n - 1];
+                if constexpr (kBias) far_to = d_lo + 63 + wlane - last_start;
                 const float zero_at = shift, delta_at = dlt, times = mul;
-                auto step = [&, zero_at, delta_at, times, wp](auto is_near, auto is_diagonal) {
-                    constexpr bool kNear = decltype(is_near)::value, kDiagonal = decltype(is_diagonal)::value;
+                // kSums 0: no bias sums; 1: the row's; 2: near the diagonal, the row's and the diagonals'
+                auto step = [&, zero_at, delta_at, times, wp](auto sums, auto is_diagonal) {
+                    constexpr int kSums = decltype(sums)::value;
+                    constexpr bool kNear = kSums == 2, kDiagonal = decltype(is_diagonal)::value;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t sr[32], pr[32];
-                        // all at once: a load would wait behind the stores of the values below
-                        [[maybe_unused]] float w[kNear ? 32 : 1];
-                        if constexpr (kNear) {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) w[c] = wp[-h * 32 - c];
-                        }
+                        [[maybe_unused]] float kept[kNear ? 32 : 1];
                         tmem_ld32_pair(tmem + t_lane + s_col(u & 1) + h * 32, sr,
                                        tmem + t_lane + dp_col(u & 1) + h * 32, pr);
 #pragma unroll
@@ -651,7 +631,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                                 const int c = h * 32 + 2 * t + e;
                                 const float s = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
                                 float z;
-                                if constexpr (kNear) z = fmaf(s, scale_log2, w[2 * t + e]) + zero_at;
+                                if constexpr (kNear) z = fmaf(s, scale_log2, wp[-c]) + zero_at;
                                 else z = fmaf(s, scale_log2, zero_at);
                                 float p = ex2_approx(z);
                                 if constexpr (kDiagonal) p = c > r_in ? 0.f : p;
@@ -662,32 +642,47 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                                     ds[e] = p * (dp - delta_at);
                                 }
                                 if constexpr (kNear) {
-                                    diag[wlane * kDiagStride + c] = ds[e];
+                                    kept[2 * t + e] = ds[e];
                                     if (c > far_to) sum[e] += ds[e];
-                                } else if constexpr (kBias) {
-                                    sum[e] += ds[e];
                                 }
+                                if constexpr (kSums == 1) sum[e] += ds[e];
                             }
                             dsw[h * 16 + t] = pack16x2<kBF16>(ds[0], ds[1]);
+                        }
+                        if constexpr (kNear) {
+                            // column c of row (lane + c + 1) mod 32: its distance is lane's first (once the
+                            // sum passes 64), second or third one
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const float x = __shfl_sync(0xffffffffu, kept[c], (wlane + c + 1) & 31);
+                                float &below = h ? a1 : a2, &above = h ? a0 : a1;
+                                if (wlane + c + 1 < 32) below += x;
+                                else above += x;
+                            }
                         }
                     }
                 };
                 // (the diagonal block, and with a bias the near steps, as loops of their own)
+                using None = std::integral_constant<int, 0>;
+                using Row = std::integral_constant<int, kBias ? 1 : 0>;
+                using Near = std::integral_constant<int, kBias ? 2 : 0>;
                 if (kBias && near) {
-                    if (j == my_block) step(std::bool_constant<kBias>{}, std::true_type{});
-                    else step(std::bool_constant<kBias>{}, std::false_type{});
+                    if (j == my_block) step(Near{}, std::true_type{});
+                    else step(Near{}, std::false_type{});
                 } else if (j == my_block) {
-                    step(std::false_type{}, std::true_type{});
+                    step(Row{}, std::true_type{});
+                } else if (kBias && bucket < last_bucket) {
+                    step(Row{}, std::false_type{});
                 } else {
-                    step(std::false_type{}, std::false_type{});
+                    step(None{}, std::false_type{});
                 }
                 if constexpr (kBias) {
-                    const int last = terms.n - 1;
                     if (near) {
                         others += sum[0] + sum[1];
                         reached |= far_to >= 0;
-                        sum_diagonals(bins, win, diag, table, bucket, last, d_lo, d_hi, wlane);
-                    } else if (bucket < last) {
+                        __syncwarp();  // the window has been read
+                        add_distances(bins, win, a0, a1, a2, table, bucket, last_bucket, d_lo, d_hi, wlane);
+                    } else if (bucket < last_bucket) {
                         if (bucket != run_bucket) {
                             flush_run();
                             run_bucket = bucket;
