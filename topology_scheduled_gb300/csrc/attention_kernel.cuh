@@ -442,7 +442,6 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         tmem_alloc(meta + kTmemSlot, L::kTmemCols);
         tmem_relinquish();
     }
-    if constexpr (kBias) table.template load<kBF16>(terms, lane_id % terms.H, tid, kThreads);
     tc_fence_before();
     const bool leave = __syncthreads_or(gave_up);
     tc_fence_after();
@@ -640,6 +639,8 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         [[maybe_unused]] int known = 0;   // distances in the table
         if constexpr (kBias) {
             bucket = terms.n - 1;
+            table.template load<kBF16>(terms, lane_id % terms.H, tid, kRows);
+            named_barrier(2, kRows);
             known = table.spread(terms.n, (qa + 2) * kBlock, tid, kRows);
             named_barrier(2, kRows);
         }

@@ -4,10 +4,10 @@
 //
 // Bias by buckets.  P is recomputed with the bias, a constant per step or a window per warp as in the
 // forward.  Its gradient sums dS over buckets in bwd_dq_kernel, in binary32 before dS is rounded:
-//  * a step inside one bucket adds each row's sum, kept in registers until the bucket changes;
-//  * near the diagonal a warp adds up the 95 diagonals of its 32 x 64 values, one distance each: for
+//  * where a step touches a bucket before the last a warp adds up the 95 diagonals of its 32 x 64 values, one distance each: for
 //    column c every lane takes the value of the row c + 1 lanes on (by a shuffle), which lies on a
-//    diagonal of its own for all columns; then, by shuffles too, the distances of each bucket;
+//    diagonal of its own for all columns.  The sums of the first 512 distances wait in shared memory
+//    until the tile is done; farther ones are added up by bucket at once, by shuffles too;
 //  * the last, open bucket gets minus the sum of the row's other values, since a row of dS sums to
 //    zero: no work on the far steps, and none of the error that Delta's rounded output leaves in each
 //    of their many values (it is a common shift of a row's dP, which the far keys would add up).
@@ -288,6 +288,10 @@ __device__ __forceinline__ void add_distances(float *bins, float *win, float a0,
     }
 }
 
+// A warp keeps the sums of dS of the first distances one by one until its tile is done; farther ones go
+// to its bucket sums step by step.
+constexpr int kNearSums = 512;
+
 template <int D, class Terms>
 struct DqSmem {
     static constexpr int kChunks = D / 64;
@@ -301,7 +305,8 @@ struct DqSmem {
     static constexpr int kOffTable = kOffMeta + kMetaBytes;                      // bias only, up to kOffEnd
     static constexpr int kOffWin = kOffTable + kBucketTableBytes;                // 4 windows
     static constexpr int kOffBins = kOffWin + 4 * kWindow * 4;                   // 4 x kMaxBuckets sums
-    static constexpr int kEnd = Terms::kBias ? kOffBins + 4 * kMaxBuckets * 4 : kOffTable;
+    static constexpr int kOffNear = kOffBins + 4 * kMaxBuckets * 4;              // 4 x sums by distance
+    static constexpr int kEnd = Terms::kBias ? kOffNear + 4 * (kDistFront + kNearSums) * 4 : kOffTable;
     static constexpr int kBytes = smem_bytes_one_cta(kEnd + 1024);  // + alignment slack
 };
 
@@ -383,10 +388,6 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     if (warp == kMmaWarp) {
         tmem_alloc(meta + kTmemSlot, kTmemCols);
         tmem_relinquish();
-    }
-    if constexpr (kBias) {
-        table.template load<kBF16>(terms, lane_id % terms.H, tid, kThreads);
-        for (int b = tid; b < 4 * kMaxBuckets; b += kThreads) reinterpret_cast<float *>(smem + L::kOffBins)[b] = 0.f;
     }
     tc_fence_before();
     const bool leave = __syncthreads_or(gave_up);
@@ -550,6 +551,29 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             if (half) mul = -lam;
             dlt *= mul;
         }
+        // kBias: the bucket of this warp's largest distance, and the sum over the row of the dS that lie
+        // before the last bucket
+        [[maybe_unused]] int bucket = 0;
+        [[maybe_unused]] float others = 0.f, last_bias = 0.f;
+        [[maybe_unused]] bool reached = false;  // the row has keys in the last bucket
+        [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
+        [[maybe_unused]] float *bins = reinterpret_cast<float *>(smem + L::kOffBins) + warp * kMaxBuckets;
+        [[maybe_unused]] float *near_sums =
+            reinterpret_cast<float *>(smem + L::kOffNear) + warp * (kDistFront + kNearSums) + kDistFront;
+        [[maybe_unused]] const int wlane = tid & 31;
+        [[maybe_unused]] int known = 0;  // distances in the table
+        [[maybe_unused]] int last_bucket = 0, last_start = 0;
+        if constexpr (kBias) {
+            for (int b = wlane; b < kMaxBuckets; b += 32) bins[b] = 0.f;
+            for (int d = wlane - kDistFront; d < kNearSums; d += 32) near_sums[d] = 0.f;
+            table.template load<kBF16>(terms, lane_id % terms.H, tid, kRows);
+            named_barrier(2, kRows);
+            bucket = last_bucket = terms.n - 1;
+            last_start = table.start[last_bucket];
+            last_bias = table.bias[last_bucket];
+            known = table.spread(terms.n, (qa + 2) * kBlock, tid, kRows);
+            named_barrier(2, kRows);
+        }
         ok = mbar_wait(bar_tile, 0, flags);
         __syncwarp();
         if (__all_sync(0xffffffffu, ok)) {
@@ -560,29 +584,6 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         } else {
             ok = false;
         }
-        // kBias: the bucket of this warp's largest distance, the sum `run` of dS in it so far, and
-        // the sum over the row of what lies before the last bucket
-        [[maybe_unused]] int bucket = 0, run_bucket = 0;
-        [[maybe_unused]] float run = 0.f, others = 0.f;
-        [[maybe_unused]] bool reached = false;  // the row has keys in the last bucket
-        [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
-        [[maybe_unused]] float *bins = reinterpret_cast<float *>(smem + L::kOffBins) + warp * kMaxBuckets;
-        [[maybe_unused]] const int wlane = tid & 31;
-        [[maybe_unused]] int known = 0;  // distances in the table
-        [[maybe_unused]] int last_bucket = 0, last_start = 0;
-        if constexpr (kBias) {
-            bucket = run_bucket = last_bucket = terms.n - 1;
-            last_start = table.start[last_bucket];
-            known = table.spread(terms.n, (qa + 2) * kBlock, tid, kRows);
-            named_barrier(2, kRows);
-        }
-        auto flush_run = [&]() {
-            float s = run;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (wlane == 0) bins[run_bucket] += s;
-            run = 0.f;
-        };
         int u = 0;
         for (; ok; ++u) {
             if (!mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags)) { ok = false; break; }
@@ -597,100 +598,99 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 // the bias: one constant for the step, or a window (key c at distance d_lo + 63 + wlane - c)
                 [[maybe_unused]] bool near = false;
                 [[maybe_unused]] int d_lo = 0, d_hi = 0;
-                float shift = -lse2;
-                [[maybe_unused]] const float *wp = nullptr;
+                float zero_at = -lse2;
                 if constexpr (kBias) {
                     d_lo = (qa - j) * kBlock + warp * 32 - 63;
                     d_hi = d_lo + kWindow - 2;
                     while (bucket > 0 && d_hi < table.start[bucket]) --bucket;  // steps come nearer
-                    near = table.start[bucket] > (d_lo > 0 ? d_lo : 0);
-                    if (near) wp = window_at(win, table, known, bucket, d_lo, wlane) + 63 + wlane;
-                    else shift += table.bias[bucket];
+                    near = bucket < last_bucket || last_start > d_lo || j == my_block;
+                    if (!near) zero_at += last_bias;
                 }
-                // sums of dS over the row (without the last bucket's keys) and over the diagonals
-                [[maybe_unused]] float sum[2] = {0.f, 0.f}, a0 = 0.f, a1 = 0.f, a2 = 0.f;
-                // keys up to this one lie in the last bucket
-                [[maybe_unused]] int far_to = -1;
-                if constexpr (kBias) far_to = d_lo + 63 + wlane - last_start;
-                const float zero_at = shift, delta_at = dlt, times = mul;
-                // kSums 0: no bias sums; 1: the row's; 2: near the diagonal, the row's and the diagonals'
-                auto step = [&, zero_at, delta_at, times, wp](auto sums, auto is_diagonal) {
-                    constexpr int kSums = decltype(sums)::value;
-                    constexpr bool kNear = kSums == 2, kDiagonal = decltype(is_diagonal)::value;
+                if (!near) {
+                    const bool diagonal = !kBias && j == my_block;
+                    const float delta_at = dlt, times = mul;
+                    auto step = [&, zero_at, delta_at, times](auto is_diagonal) {
+                        constexpr bool kDiagonal = decltype(is_diagonal)::value;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t sr[32], pr[32];
+                            tmem_ld32_pair(tmem + t_lane + s_col(u & 1) + h * 32, sr,
+                                           tmem + t_lane + dp_col(u & 1) + h * 32, pr);
+#pragma unroll
+                            for (int t = 0; t < 16; ++t) {
+                                float ds[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float s = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
+                                    float p = ex2_approx(fmaf(s, scale_log2, zero_at));
+                                    if constexpr (kDiagonal) p = h * 32 + 2 * t + e > r_in ? 0.f : p;
+                                    if constexpr (kDiff) {
+                                        ds[e] = p * fmaf(dp, times, -delta_at);
+                                        dot[e] = fmaf(p, dp, dot[e]);
+                                    } else {
+                                        ds[e] = p * (dp - delta_at);
+                                    }
+                                }
+                                dsw[h * 16 + t] = pack16x2<kBF16>(ds[0], ds[1]);
+                            }
+                        }
+                    };
+                    if (diagonal) step(std::true_type{});  // a loop of its own
+                    else step(std::false_type{});
+                    if constexpr (kBias) reached = true;
+                } else if constexpr (kBias) {
+                    // sums of dS over the row (without the last bucket's keys) and over the diagonals
+                    float a0 = 0.f, a1 = 0.f, a2 = 0.f;
+                    const float *wp = window_at(win, table, known, bucket, d_lo, wlane) + 63 + wlane;
+                    const int far_to = d_lo + 63 + wlane - last_start;  // keys up to this one lie in the last bucket
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t sr[32], pr[32];
-                        [[maybe_unused]] float kept[kNear ? 32 : 1];
                         tmem_ld32_pair(tmem + t_lane + s_col(u & 1) + h * 32, sr,
                                        tmem + t_lane + dp_col(u & 1) + h * 32, pr);
+                        float x[32];
 #pragma unroll
-                        for (int t = 0; t < 16; ++t) {
-                            float ds[2];
+                        for (int c = 0; c < 32; ++c)
+                            x[c] = fmaf(__uint_as_float(sr[c]), scale_log2, wp[-h * 32 - c]) + zero_at;
+                        if (j == my_block) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int c = h * 32 + 2 * t + e;
-                                const float s = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
-                                float z;
-                                if constexpr (kNear) z = fmaf(s, scale_log2, wp[-c]) + zero_at;
-                                else z = fmaf(s, scale_log2, zero_at);
-                                float p = ex2_approx(z);
-                                if constexpr (kDiagonal) p = c > r_in ? 0.f : p;
-                                if constexpr (kDiff) {
-                                    ds[e] = p * fmaf(dp, times, -delta_at);
-                                    dot[e] = fmaf(p, dp, dot[e]);
-                                } else {
-                                    ds[e] = p * (dp - delta_at);
-                                }
-                                if constexpr (kNear) {
-                                    kept[2 * t + e] = ds[e];
-                                    if (c > far_to) sum[e] += ds[e];
-                                }
-                                if constexpr (kSums == 1) sum[e] += ds[e];
-                            }
-                            dsw[h * 16 + t] = pack16x2<kBF16>(ds[0], ds[1]);
+                            for (int c = 0; c < 32; ++c) x[c] = h * 32 + c > r_in ? -INFINITY : x[c];
                         }
-                        if constexpr (kNear) {
-                            // column c of row (lane + c + 1) mod 32: its distance is lane's first (once the
-                            // sum passes 64), second or third one
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                const float x = __shfl_sync(0xffffffffu, kept[c], (wlane + c + 1) & 31);
-                                float &below = h ? a1 : a2, &above = h ? a0 : a1;
-                                if (wlane + c + 1 < 32) below += x;
-                                else above += x;
-                            }
+                        for (int c = 0; c < 32; ++c) x[c] = ex2_approx(x[c]) * (__uint_as_float(pr[c]) - dlt);
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) dsw[h * 16 + t] = pack16x2<kBF16>(x[2 * t], x[2 * t + 1]);
+                        if (d_hi < last_start) {
+                            uint64_t two = f2_pack(x[0], x[1]);
+#pragma unroll
+                            for (int t = 1; t < 16; ++t) two = f2_add(two, f2_pack(x[2 * t], x[2 * t + 1]));
+                            float s0, s1;
+                            f2_unpack(two, s0, s1);
+                            others += s0 + s1;
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) others += h * 32 + c > far_to ? x[c] : 0.f;
+                        }
+                        // column c of row (lane + c + 1) mod 32: its distance is lane's first one (once the
+                        // sum passes 64), second or third
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float y = __shfl_sync(0xffffffffu, x[c], (wlane + c + 1) & 31);
+                            float &below = h ? a1 : a2, &above = h ? a0 : a1;
+                            const bool first = wlane + c + 1 < 32;
+                            below += first ? y : 0.f;
+                            above += first ? 0.f : y;
                         }
                     }
-                };
-                // (the diagonal block, and with a bias the near steps, as loops of their own)
-                using None = std::integral_constant<int, 0>;
-                using Row = std::integral_constant<int, kBias ? 1 : 0>;
-                using Near = std::integral_constant<int, kBias ? 2 : 0>;
-                if (kBias && near) {
-                    if (j == my_block) step(Near{}, std::true_type{});
-                    else step(Near{}, std::false_type{});
-                } else if (j == my_block) {
-                    step(Row{}, std::true_type{});
-                } else if (kBias && bucket < last_bucket) {
-                    step(Row{}, std::false_type{});
-                } else {
-                    step(None{}, std::false_type{});
-                }
-                if constexpr (kBias) {
-                    if (near) {
-                        others += sum[0] + sum[1];
-                        reached |= far_to >= 0;
-                        __syncwarp();  // the window has been read
-                        add_distances(bins, win, a0, a1, a2, table, bucket, last_bucket, d_lo, d_hi, wlane);
-                    } else if (bucket < last_bucket) {
-                        if (bucket != run_bucket) {
-                            flush_run();
-                            run_bucket = bucket;
-                        }
-                        run += sum[0] + sum[1];
-                        others += sum[0] + sum[1];
+                    reached |= far_to >= 0;
+                    __syncwarp();  // the window has been read
+                    if (d_hi < kNearSums) {
+                        float *to = near_sums + d_lo + wlane;
+                        to[0] += a0;
+                        to[32] += a1;
+                        to[64] += a2;
                     } else {
-                        reached = true;
+                        add_distances(bins, win, a0, a1, a2, table, bucket, last_bucket, d_lo, d_hi, wlane);
                     }
                 }
             } else {
@@ -716,11 +716,11 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             if constexpr (kDiff) stage_half_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, half, r_in);
             else stage_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, tid);
             if constexpr (kBias) {
-                flush_run();
-                run_bucket = terms.n - 1;
                 // the last bucket, unless its keys are left out
-                run = reached && table.bias[terms.n - 1] > -INFINITY ? -others : 0.f;
-                flush_run();
+                float s = reached && last_bias > -INFINITY ? -others : 0.f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (wlane == 0) bins[last_bucket] = s;
             }
             if constexpr (kDiff) {
                 float s = dot[0] + dot[1];
@@ -732,10 +732,17 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             fence_proxy_async_smem();
             named_barrier(1, kRows);
             if constexpr (kBias) {
+                // the warps' bucket sums and their sums by distance, a thread per bucket
                 const float *all = reinterpret_cast<const float *>(smem + L::kOffBins);
+                const float *by = reinterpret_cast<const float *>(smem + L::kOffNear) + kDistFront;
+                constexpr int kOne = kDistFront + kNearSums;
                 float *to = partial + ((long long)lane_id * gridDim.y + tile) * terms.n;
-                for (int b = tid; b < terms.n; b += kRows)
-                    to[b] = (all[b] + all[kMaxBuckets + b]) + (all[2 * kMaxBuckets + b] + all[3 * kMaxBuckets + b]);
+                for (int b = tid; b < terms.n; b += kRows) {
+                    float s = (all[b] + all[kMaxBuckets + b]) + (all[2 * kMaxBuckets + b] + all[3 * kMaxBuckets + b]);
+                    const int end = b < last_bucket ? min(table.start[b + 1], kNearSums) : 0;
+                    for (int d = table.start[b]; d < end; ++d) s += (by[d] + by[kOne + d]) + (by[2 * kOne + d] + by[3 * kOne + d]);
+                    to[b] = s;
+                }
             }
             if constexpr (kDiff) {
                 const float *two = reinterpret_cast<const float *>(smem + L::kOffDO);
@@ -882,7 +889,6 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         tmem_alloc(meta + kTmemSlot, kTmemCols);
         tmem_relinquish();
     }
-    if constexpr (kBias) table.template load<kBF16>(terms, lane_id % terms.H, tid, kThreads);
     tc_fence_before();
     const bool leave = __syncthreads_or(gave_up);
     tc_fence_after();
@@ -1049,6 +1055,8 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         [[maybe_unused]] int bucket = 0;  // the bucket of this warp's largest distance of the step
         [[maybe_unused]] int known = 0;   // distances in the table
         if constexpr (kBias) {
+            table.template load<kBF16>(terms, lane_id % terms.H, tid, kRows);
+            named_barrier(2, kRows);
             known = table.spread(terms.n, S, tid, kRows);
             named_barrier(2, kRows);
         }
@@ -1077,12 +1085,14 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 if constexpr (kBias) {
                     const int d_lo = (i - key_block) * kBlock - (warp & 1) * 32 - 31, d_hi = d_lo + kWindow - 2;
                     while (bucket + 1 < terms.n && d_hi >= table.start[bucket + 1]) ++bucket;  // steps go farther
-                    near = table.start[bucket] > (d_lo > 0 ? d_lo : 0);
+                    // (the diagonal block goes with the near steps, which mask)
+                    near = i == key_block || table.start[bucket] > (d_lo > 0 ? d_lo : 0);
                     if (near) wp = window_at(win, table, known, bucket, d_lo, wlane) + 31 - wlane;
                     else off = table.bias[bucket];
                 }
                 const float bias_at = off, times = mul;
-                auto step = [&, bias_at, times, wp, ls, dl](auto is_near, auto is_diagonal) {
+                const int hidden = i == key_block ? k_in : 0;  // queries before this one do not see the key
+                auto step = [&, bias_at, times, wp, ls, dl, hidden](auto is_near, auto is_diagonal) {
                     constexpr bool kNear = decltype(is_near)::value, kDiagonal = decltype(is_diagonal)::value;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -1102,7 +1112,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                                 else if constexpr (kBias) z = fmaf(x, scale_log2, bias_at - l2);
                                 else z = fmaf(x, scale_log2, -l2);
                                 p[e] = ex2_approx(z);
-                                if constexpr (kDiagonal) p[e] = k_in > c ? 0.f : p[e];
+                                if constexpr (kDiagonal) p[e] = c < hidden ? 0.f : p[e];
                                 if constexpr (kDiff) p[e] *= times;
                                 ds[e] = p[e] * (dp - dl[c]);
                             }
@@ -1111,13 +1121,12 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         }
                     }
                 };
-                if (kBias && near) {
-                    if (i == key_block) step(std::bool_constant<kBias>{}, std::true_type{});
-                    else step(std::bool_constant<kBias>{}, std::false_type{});
-                } else if (i == key_block) {
-                    step(std::false_type{}, std::true_type{});
+                if constexpr (kBias) {
+                    if (near) step(std::true_type{}, std::true_type{});
+                    else step(std::false_type{}, std::false_type{});
                 } else {
-                    step(std::false_type{}, std::false_type{});
+                    if (i == key_block) step(std::false_type{}, std::true_type{});
+                    else step(std::false_type{}, std::false_type{});
                 }
             } else {
 #pragma unroll
