@@ -36,10 +36,9 @@
 //  * Two CTAs share an SM, so one CTA's softmax also overlaps the other's MMAs.
 //
 // The same kernel carries the score terms of score_terms.cuh:
-//  * Bias by buckets of the distance q - k.  The keys of a step lie in one bucket for all rows of a
-//    warp whenever the step is far enough from the diagonal (the buckets grow with the distance),
-//    and then the bias is one constant, folded into the FMA that subtracts the row maximum: such a
-//    step costs what a plain one does.  Otherwise every thread reads its 64 biases from a table by
+//  * Bias by buckets of the distance q - k.  Far enough from the diagonal all keys of a step lie in the
+//    open last bucket for all rows of a warp, and then the bias is one constant, folded into the FMA
+//    that subtracts the row maximum: such a step costs what a plain one does.  Otherwise every thread reads its 64 biases from a table by
 //    distance in shared memory, lane by lane consecutive addresses (no bank conflicts), one FMA per
 //    score.  The softmax warps fill the table (the first 2048 distances at most) while the first
 //    tiles are on their way; beyond it a warp lays out the 95 distances of its step.
@@ -635,14 +634,15 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 mbar_arrive(bar_q_diag);
             }
         }
-        [[maybe_unused]] int bucket = 0;  // the bucket of this warp's largest distance of the step
-        [[maybe_unused]] int known = 0;   // distances in the table
+        [[maybe_unused]] int known = 0, last_start = 0;  // distances in the table; of the open bucket
+        [[maybe_unused]] float last_bias = 0.f;
         if constexpr (kBias) {
-            bucket = terms.n - 1;
             table.template load<kBF16>(terms, lane_id % terms.H, tid, kRows);
             named_barrier(2, kRows);
             known = table.spread(terms.n, (qa + 2) * kBlock, tid, kRows);
             named_barrier(2, kRows);
+            last_start = table.start[terms.n - 1];
+            last_bias = table.bias[terms.n - 1];
         }
         [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
         int u = 0;
@@ -668,12 +668,11 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 [[maybe_unused]] float cc1 = scale_log2, off = 0.f;
                 if constexpr (kBias) {
                     // key c lies at the distance d_lo + 63 + (tid & 31) - c
-                    const int d_lo = (qa - j) * kBlock + warp * 32 - 63, d_hi = d_lo + kWindow - 2;
-                    while (bucket > 0 && d_hi < table.start[bucket]) --bucket;  // steps come nearer
-                    if (table.start[bucket] <= (d_lo > 0 ? d_lo : 0)) {
-                        off = table.bias[bucket];
+                    const int d_lo = (qa - j) * kBlock + warp * 32 - 63;
+                    if (last_start <= (d_lo > 0 ? d_lo : 0)) {  // all of it in the open last bucket
+                        off = last_bias;
                     } else {
-                        const float *wp = window_at(win, table, known, bucket, d_lo, tid & 31) + 63 + (tid & 31);
+                        const float *wp = window_at(win, table, known, terms.n, d_lo, tid & 31) + 63 + (tid & 31);
 #pragma unroll
                         for (int c = 0; c < 64; ++c) x[c] = fmaf(x[c], scale_log2, wp[-c]);
                         cc1 = 1.f;

@@ -551,9 +551,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             if (half) mul = -lam;
             dlt *= mul;
         }
-        // kBias: the bucket of this warp's largest distance, and the sum over the row of the dS that lie
-        // before the last bucket
-        [[maybe_unused]] int bucket = 0;
+        // kBias: the sum over the row of the dS that lie before the last bucket
         [[maybe_unused]] float others = 0.f, last_bias = 0.f;
         [[maybe_unused]] bool reached = false;  // the row has keys in the last bucket
         [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
@@ -568,7 +566,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             for (int d = wlane - kDistFront; d < kNearSums; d += 32) near_sums[d] = 0.f;
             table.template load<kBF16>(terms, lane_id % terms.H, tid, kRows);
             named_barrier(2, kRows);
-            bucket = last_bucket = terms.n - 1;
+            last_bucket = terms.n - 1;
             last_start = table.start[last_bucket];
             last_bias = table.bias[last_bucket];
             known = table.spread(terms.n, (qa + 2) * kBlock, tid, kRows);
@@ -602,8 +600,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 if constexpr (kBias) {
                     d_lo = (qa - j) * kBlock + warp * 32 - 63;
                     d_hi = d_lo + kWindow - 2;
-                    while (bucket > 0 && d_hi < table.start[bucket]) --bucket;  // steps come nearer
-                    near = bucket < last_bucket || last_start > d_lo || j == my_block;
+                    near = last_start > d_lo || j == my_block;
                     if (!near) zero_at += last_bias;
                 }
                 if (!near) {
@@ -641,7 +638,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 } else if constexpr (kBias) {
                     // sums of dS over the row (without the last bucket's keys) and over the diagonals
                     float a0 = 0.f, a1 = 0.f, a2 = 0.f;
-                    const float *wp = window_at(win, table, known, bucket, d_lo, wlane) + 63 + wlane;
+                    const float *wp = window_at(win, table, known, terms.n, d_lo, wlane) + 63 + wlane;
                     const int far_to = d_lo + 63 + wlane - last_start;  // keys up to this one lie in the last bucket
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -661,11 +658,13 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
                         for (int t = 0; t < 16; ++t) dsw[h * 16 + t] = pack16x2<kBF16>(x[2 * t], x[2 * t + 1]);
                         if (d_hi < last_start) {
-                            uint64_t two = f2_pack(x[0], x[1]);
+                            uint64_t two[4];
 #pragma unroll
-                            for (int t = 1; t < 16; ++t) two = f2_add(two, f2_pack(x[2 * t], x[2 * t + 1]));
+                            for (int t = 0; t < 4; ++t) two[t] = f2_pack(x[2 * t], x[2 * t + 1]);
+#pragma unroll
+                            for (int t = 4; t < 16; ++t) two[t & 3] = f2_add(two[t & 3], f2_pack(x[2 * t], x[2 * t + 1]));
                             float s0, s1;
-                            f2_unpack(two, s0, s1);
+                            f2_unpack(f2_add(f2_add(two[0], two[1]), f2_add(two[2], two[3])), s0, s1);
                             others += s0 + s1;
                         } else {
 #pragma unroll
@@ -690,7 +689,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         to[32] += a1;
                         to[64] += a2;
                     } else {
-                        add_distances(bins, win, a0, a1, a2, table, bucket, last_bucket, d_lo, d_hi, wlane);
+                        add_distances(bins, win, a0, a1, a2, table, table.find(terms.n, d_hi), last_bucket, d_lo, d_hi, wlane);
                     }
                 }
             } else {
@@ -1052,13 +1051,15 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 mbar_arrive(meta + kBarReady);
             }
         }
-        [[maybe_unused]] int bucket = 0;  // the bucket of this warp's largest distance of the step
-        [[maybe_unused]] int known = 0;   // distances in the table
+        [[maybe_unused]] int known = 0, last_start = 0;  // distances in the table; of the open bucket
+        [[maybe_unused]] float last_bias = 0.f;
         if constexpr (kBias) {
             table.template load<kBF16>(terms, lane_id % terms.H, tid, kRows);
             named_barrier(2, kRows);
             known = table.spread(terms.n, S, tid, kRows);
             named_barrier(2, kRows);
+            last_start = table.start[terms.n - 1];
+            last_bias = table.bias[terms.n - 1];
         }
         [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
         [[maybe_unused]] const int wlane = tid & 31;
@@ -1083,12 +1084,11 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 [[maybe_unused]] float off = 0.f;
                 [[maybe_unused]] const float *wp = nullptr;
                 if constexpr (kBias) {
-                    const int d_lo = (i - key_block) * kBlock - (warp & 1) * 32 - 31, d_hi = d_lo + kWindow - 2;
-                    while (bucket + 1 < terms.n && d_hi >= table.start[bucket + 1]) ++bucket;  // steps go farther
+                    const int d_lo = (i - key_block) * kBlock - (warp & 1) * 32 - 31;
                     // (the diagonal block goes with the near steps, which mask)
-                    near = i == key_block || table.start[bucket] > (d_lo > 0 ? d_lo : 0);
-                    if (near) wp = window_at(win, table, known, bucket, d_lo, wlane) + 31 - wlane;
-                    else off = table.bias[bucket];
+                    near = i == key_block || last_start > d_lo;
+                    if (near) wp = window_at(win, table, known, terms.n, d_lo, wlane) + 31 - wlane;
+                    else off = last_bias;
                 }
                 const float bias_at = off, times = mul;
                 const int hidden = i == key_block ? k_in : 0;  // queries before this one do not see the key

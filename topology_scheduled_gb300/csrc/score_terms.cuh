@@ -67,6 +67,14 @@ struct BucketTable {
         for (int d = tid; d < kDistFront; d += nthreads) dist[d - kDistFront] = 0.f;
     }
 
+    // The last of n buckets that starts at or before distance d.
+    __device__ __forceinline__ int find(int n, int d) const {
+        int at = 0;
+        for (int s = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; s > 0; s >>= 1)
+            if (start[min(at + s, kMaxBuckets - 1)] <= d) at += s;
+        return at;
+    }
+
     // After load and a barrier: fills dist up to where a step can still touch two buckets (or to
     // `limit`), four distances per thread at a time, each by halving.  Returns how many are known;
     // another barrier before they are read.
@@ -93,12 +101,13 @@ constexpr int kBucketTableBytes = (2 * kMaxBuckets + kDistFront + kDistances) * 
 // lie behind the causal mask).
 constexpr int kWindow = 96;
 
-// The biases of the distances d_lo + 0 .. 94, where they are not all the same: the table's, or, beyond
-// it, laid out in `win`; `top` is the bucket of the largest one.  Three entries per lane, and a walk
-// down the buckets that is the same in all lanes.
-__device__ __forceinline__ const float *window_at(float *win, const BucketTable &t, int known, int top, int d_lo,
+// The biases of the distances d_lo + 0 .. 94, which may lie in several buckets: the table's, or, beyond
+// it, laid out in `win` (three entries per lane, and a walk down the n buckets that is the same in all
+// lanes).
+__device__ __forceinline__ const float *window_at(float *win, const BucketTable &t, int known, int n, int d_lo,
                                                   int lane) {
     if (d_lo + kWindow - 2 < known) return t.dist + d_lo;
+    const int top = t.find(n, d_lo + kWindow - 2);
     const int d0 = d_lo + lane, d1 = d0 + 32, d2 = d0 + 64;
     const int least = d_lo > 0 ? d_lo : 0;
     float w0 = t.bias[top], w1 = w0, w2 = w0;
