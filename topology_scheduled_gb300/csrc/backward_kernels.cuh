@@ -6,7 +6,7 @@
 // forward.  Its gradient sums dS over buckets in bwd_dq_kernel, in binary32 before dS is rounded:
 //  * where a step touches a bucket before the last a warp adds up the 95 diagonals of its 32 x 64 values, one distance each: for
 //    column c every lane takes the value of the row c + 1 lanes on (by a shuffle), which lies on a
-//    diagonal of its own for all columns.  The sums of the first 512 distances wait in shared memory
+//    diagonal of its own for all columns.  The sums of the first 256 distances wait in shared memory
 //    until the tile is done; farther ones are added up by bucket at once, by shuffles too;
 //  * the last, open bucket gets minus the sum of the row's other values, since a row of dS sums to
 //    zero: no work on the far steps, and none of the error that Delta's rounded output leaves in each
@@ -33,10 +33,12 @@ namespace tsa {
 namespace {
 
 constexpr int kBlock = 64;
-constexpr int kThreads = 192;
 constexpr int kRows = 128;
-constexpr int kProducerWarp = 4;
-constexpr int kMmaWarp = 5;
+constexpr int kEltWarps = 8;                   // elementwise warps: one per 32 rows x 32 columns of a step
+constexpr int kElt = 32 * kEltWarps;
+constexpr int kThreads = kElt + 64;
+constexpr int kProducerWarp = kEltWarps;
+constexpr int kMmaWarp = kEltWarps + 1;
 constexpr int kStream = 4;     // depth of the ring of streamed blocks
 constexpr int kMetaRing = 8;   // > kStream: a slot is rewritten only after its step is consumed
 constexpr float kLog2e = 1.4426950408889634f;
@@ -80,33 +82,34 @@ struct ListUnion {
     }
 };
 
+// The epilogue's columns go 32 at a time; the two warps of a quarter of the rows (group 0 and 1) take
+// half of the column blocks each.
+//
 // 128 rows of fp32 accumulator in TMEM (this warp's 32 lanes, D columns starting at `col`),
 // times `mul`, rounded and written to a 128-row SW128 staging tile in the layout TMA stores.
 template <int D, bool kBF16>
 __device__ __forceinline__ void stage_rows(uint32_t tmem_row, uint32_t col, bool valid, float mul,
-                                           uint32_t tile, int row) {
+                                           uint32_t tile, int row, int group) {
     const uint32_t sw = (uint32_t)(row & 7);
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-        const uint32_t o_row = tile + c * 16384 + row * 128;
+    for (int x = 0; x < D / 64; ++x) {
+        const int h = group * (D / 64) + x;
+        uint32_t o[32];
+        if (valid) {
+            tmem_ld32(tmem_row + col + h * 32, o);
+        } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t o[32];
-            if (valid) {
-                tmem_ld32(tmem_row + col + c * 64 + h * 32, o);
-            } else {
+            for (int t = 0; t < 32; ++t) o[t] = 0u;
+        }
 #pragma unroll
-                for (int t = 0; t < 32; ++t) o[t] = 0u;
-            }
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t w[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    w[t] = pack16x2<kBF16>(__uint_as_float(o[q * 8 + 2 * t]) * mul,
-                                           __uint_as_float(o[q * 8 + 2 * t + 1]) * mul);
-                st_shared_v4(o_row + (((uint32_t)(h * 4 + q) ^ sw) << 4), w[0], w[1], w[2], w[3]);
-            }
+            for (int t = 0; t < 4; ++t)
+                w[t] = pack16x2<kBF16>(__uint_as_float(o[q * 8 + 2 * t]) * mul,
+                                       __uint_as_float(o[q * 8 + 2 * t + 1]) * mul);
+            st_shared_v4(tile + (h >> 1) * 16384 + row * 128 + (((uint32_t)((h & 1) * 4 + q) ^ sw) << 4), w[0], w[1],
+                         w[2], w[3]);
         }
     }
 }
@@ -131,10 +134,10 @@ __device__ __forceinline__ void copy_staged_row(const uint8_t *tile, int row, ui
 // (columns m D/2 ..), times `mul`, rounded and written to a 64-row SW128 staging tile.
 template <int D, bool kBF16>
 __device__ __forceinline__ void stage_half_rows(uint32_t tmem_row, uint32_t col, bool valid, float mul,
-                                                uint32_t tile, int half, int row) {
+                                                uint32_t tile, int half, int row, int group) {
     const uint32_t sw = (uint32_t)(row & 7);
-#pragma unroll
-    for (int h = 0; h < D / 64; ++h) {  // 32 columns at a time
+    if (group < D / 64) {  // 32 columns of D / 2
+        const int h = group;
         uint32_t o[32];
         if (valid) {
             tmem_ld32(tmem_row + col + half * (D / 2) + h * 32, o);
@@ -157,15 +160,16 @@ __device__ __forceinline__ void stage_half_rows(uint32_t tmem_row, uint32_t col,
 
 // Differential attention: the upper 64 rows of an accumulator plus the lower ones (which pass
 // through `passed` in binary32), rounded and written to a 64-row SW128 staging tile.  Called by all
-// 128 elementwise threads; has a barrier.
+// elementwise threads; has a barrier.
 template <int D, bool kBF16>
 __device__ __forceinline__ void stage_sum_of_halves(uint32_t tmem_row, uint32_t col, bool valid, uint32_t tile,
-                                                    float4 *passed, int half, int row) {
+                                                    float4 *passed, int half, int row, int group) {
     const uint32_t sw = (uint32_t)(row & 7);
     passed += row;
-    if (half == 0) named_barrier(1, kRows);
+    if (half == 0) named_barrier(1, kElt);
 #pragma unroll
-    for (int h = 0; h < D / 32; ++h) {
+    for (int x = 0; x < D / 64; ++x) {
+        const int h = group * (D / 64) + x;
         uint32_t o[32];
         if (valid) {
             tmem_ld32(tmem_row + col + h * 32, o);
@@ -181,17 +185,17 @@ __device__ __forceinline__ void stage_sum_of_halves(uint32_t tmem_row, uint32_t 
         } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float4 x = passed[(h * 8 + 2 * q) * 64], y = passed[(h * 8 + 2 * q + 1) * 64];
+                const float4 x0 = passed[(h * 8 + 2 * q) * 64], y0 = passed[(h * 8 + 2 * q + 1) * 64];
                 const uint32_t *v = o + q * 8;
                 st_shared_v4(tile + (h >> 1) * 16384 + row * 128 + ((((h & 1) * 4 + q) ^ sw) << 4),
-                             pack16x2<kBF16>(__uint_as_float(v[0]) + x.x, __uint_as_float(v[1]) + x.y),
-                             pack16x2<kBF16>(__uint_as_float(v[2]) + x.z, __uint_as_float(v[3]) + x.w),
-                             pack16x2<kBF16>(__uint_as_float(v[4]) + y.x, __uint_as_float(v[5]) + y.y),
-                             pack16x2<kBF16>(__uint_as_float(v[6]) + y.z, __uint_as_float(v[7]) + y.w));
+                             pack16x2<kBF16>(__uint_as_float(v[0]) + x0.x, __uint_as_float(v[1]) + x0.y),
+                             pack16x2<kBF16>(__uint_as_float(v[2]) + x0.z, __uint_as_float(v[3]) + x0.w),
+                             pack16x2<kBF16>(__uint_as_float(v[4]) + y0.x, __uint_as_float(v[5]) + y0.y),
+                             pack16x2<kBF16>(__uint_as_float(v[6]) + y0.z, __uint_as_float(v[7]) + y0.w));
             }
         }
     }
-    if (half) named_barrier(1, kRows);
+    if (half) named_barrier(1, kElt);
 }
 
 // Meta area (byte offsets from the meta base), common to both kernels.
@@ -220,6 +224,9 @@ constexpr int smem_bytes_one_cta(int need) { return need > 116 * 1024 ? need : 1
 __device__ __forceinline__ uint32_t s_col(int b) { return b ? 64u : 0u; }
 __device__ __forceinline__ uint32_t dp_col(int b) { return b ? 192u : 128u; }
 constexpr uint32_t kAccCol = 256;
+// Elements 16 kk .. 16 kk + 15 of a step's packed results: each warp writes its 32 over its own 32
+// columns of the products.
+__device__ __forceinline__ constexpr uint32_t packed_col(int kk) { return (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8); }
 
 // Row `row` (0-127) of a 128-row SW128 tile into tensor memory as a product's left operand: D / 2
 // columns from `col`, two 16-bit elements per column.  kDiagonal: rows 0-63 keep the first half of
@@ -290,7 +297,7 @@ __device__ __forceinline__ void add_distances(float *bins, float *win, float a0,
 
 // A warp keeps the sums of dS of the first distances one by one until its tile is done; farther ones go
 // to its bucket sums step by step.
-constexpr int kNearSums = 512;
+constexpr int kNearSums = 256;
 
 template <int D, class Terms>
 struct DqSmem {
@@ -303,10 +310,10 @@ struct DqSmem {
     static constexpr int kOffV = kOffK + kStream * kKVBytes;
     static constexpr int kOffMeta = kOffV + kStream * kKVBytes;
     static constexpr int kOffTable = kOffMeta + kMetaBytes;                      // bias only, up to kOffEnd
-    static constexpr int kOffWin = kOffTable + kBucketTableBytes;                // 4 windows
-    static constexpr int kOffBins = kOffWin + 4 * kWindow * 4;                   // 4 x kMaxBuckets sums
-    static constexpr int kOffNear = kOffBins + 4 * kMaxBuckets * 4;              // 4 x sums by distance
-    static constexpr int kEnd = Terms::kBias ? kOffNear + 4 * (kDistFront + kNearSums) * 4 : kOffTable;
+    static constexpr int kOffWin = kOffTable + kBucketTableBytes;                // a window of each warp
+    static constexpr int kOffBins = kOffWin + kEltWarps * kWindow * 4;           // kMaxBuckets sums of each warp
+    static constexpr int kOffNear = kOffBins + kEltWarps * kMaxBuckets * 4;      // sums by distance of each warp
+    static constexpr int kEnd = Terms::kBias ? kOffNear + kEltWarps * (kDistFront + kNearSums) * 4 : kOffTable;
     static constexpr int kBytes = smem_bytes_one_cta(kEnd + 1024);  // + alignment slack
 };
 
@@ -376,11 +383,11 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(BAR_S_FULL(b), 1);
-            mbar_init(BAR_P_FULL(b), kRows);
+            mbar_init(BAR_P_FULL(b), kElt);
         }
         mbar_init(bar_done, 1);
         mbar_init(bar_fin, 1);
-        mbar_init(meta + kBarReady, kRows);
+        mbar_init(meta + kBarReady, kElt);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -518,7 +525,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_ts(tmem + kAccCol, tmem + s_col(u & 1) + kk * 8,
+                    tc_mma_ts(tmem + kAccCol, tmem + s_col(u & 1) + packed_col(kk),
                               sdesc_at(kt_desc, s * L::kKVBytes + kk * 2048), kIdescAcc,
                               (u > 0 || kk > 0) ? 1u : 0u);
                 tc_commit(BAR_K_EMPTY(s));
@@ -531,15 +538,16 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             (void)mbar_wait_timed(bar_fin, 0);
         }
     } else {
-        // ------------------------------------------------------------ elementwise (warps 0-3)
-        const int half = tid >> 6;
-        const int r_in = tid & 63;
+        // ------------------------------------------------------------ elementwise (warps 0-7)
+        const int row = tid & 127, col0 = (tid >> 7) * 32;  // this thread's row, and first column of a step
+        const int half = row >> 6;
+        const int r_in = row & 63;
         const int my_block = kDiff ? qa : qa + half;
         const bool row_exists = kDiff || half == 0 || has_b;
         const int member = kDiff ? 0 : half;  // the membership bit of this thread's row
-        const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
+        const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
         // the row in the per-lane padded Delta / log-sum-exp arrays (nb * 64 rows per lane)
-        long long grow = ((long long)lane_id * nb + qa) * kBlock + (kDiff ? r_in : tid);
+        long long grow = ((long long)lane_id * nb + qa) * kBlock + (kDiff ? r_in : row);
         if constexpr (kDiff) grow += half * terms.map_rows;
         const float lse2 = row_exists ? lse[grow] : INFINITY;
         float dlt = row_exists ? delta[grow] : 0.f;
@@ -564,19 +572,19 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         if constexpr (kBias) {
             for (int b = wlane; b < kMaxBuckets; b += 32) bins[b] = 0.f;
             for (int d = wlane - kDistFront; d < kNearSums; d += 32) near_sums[d] = 0.f;
-            table.template load<kBF16>(terms, lane_id % terms.H, tid, kRows);
-            named_barrier(2, kRows);
+            table.template load<kBF16>(terms, lane_id % terms.H, tid, kElt);
+            named_barrier(2, kElt);
             last_bucket = terms.n - 1;
             last_start = table.start[last_bucket];
             last_bias = table.bias[last_bucket];
-            known = table.spread(terms.n, (qa + 2) * kBlock, tid, kRows);
-            named_barrier(2, kRows);
+            known = table.spread(terms.n, (qa + 2) * kBlock, tid, kElt);
+            named_barrier(2, kElt);
         }
         ok = mbar_wait(bar_tile, 0, flags);
         __syncwarp();
         if (__all_sync(0xffffffffu, ok)) {
-            tile_row_to_tmem<D, kDiff>(smem + L::kOffQ, tid, tmem + t_lane, kQCol);
-            tile_row_to_tmem<D, false>(smem + L::kOffDO, tid, tmem + t_lane, kDOCol);
+            if (col0 == 0) tile_row_to_tmem<D, kDiff>(smem + L::kOffQ, row, tmem + t_lane, kQCol);
+            else tile_row_to_tmem<D, false>(smem + L::kOffDO, row, tmem + t_lane, kDOCol);
             tc_fence_before();
             mbar_arrive(meta + kBarReady);
         } else {
@@ -590,7 +598,8 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             if (j < 0) break;
             tc_fence_after();
             const bool in_row = row_exists && ((fl >> member) & 1);  // warp-uniform
-            uint32_t dsw[32];
+            const uint32_t s_at = tmem + t_lane + s_col(u & 1) + col0, dp_at = tmem + t_lane + dp_col(u & 1) + col0;
+            uint32_t dsw[16];
             __syncwarp();
             if (in_row) {
                 // the bias: one constant for the step, or a window (key c at distance d_lo + 63 + wlane - c)
@@ -598,7 +607,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 [[maybe_unused]] int d_lo = 0, d_hi = 0;
                 float zero_at = -lse2;
                 if constexpr (kBias) {
-                    d_lo = (qa - j) * kBlock + warp * 32 - 63;
+                    d_lo = (qa - j) * kBlock + (warp & 3) * 32 - 63;
                     d_hi = d_lo + kWindow - 2;
                     near = last_start > d_lo || j == my_block;
                     if (!near) zero_at += last_bias;
@@ -608,96 +617,88 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     const float delta_at = dlt, times = mul;
                     auto step = [&, zero_at, delta_at, times](auto is_diagonal) {
                         constexpr bool kDiagonal = decltype(is_diagonal)::value;
+                        uint32_t sr[32], pr[32];
+                        tmem_ld32_pair(s_at, sr, dp_at, pr);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t sr[32], pr[32];
-                            tmem_ld32_pair(tmem + t_lane + s_col(u & 1) + h * 32, sr,
-                                           tmem + t_lane + dp_col(u & 1) + h * 32, pr);
+                        for (int t = 0; t < 16; ++t) {
+                            float ds[2];
 #pragma unroll
-                            for (int t = 0; t < 16; ++t) {
-                                float ds[2];
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float s = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
-                                    float p = ex2_approx(fmaf(s, scale_log2, zero_at));
-                                    if constexpr (kDiagonal) p = h * 32 + 2 * t + e > r_in ? 0.f : p;
-                                    if constexpr (kDiff) {
-                                        ds[e] = p * fmaf(dp, times, -delta_at);
-                                        dot[e] = fmaf(p, dp, dot[e]);
-                                    } else {
-                                        ds[e] = p * (dp - delta_at);
-                                    }
+                            for (int e = 0; e < 2; ++e) {
+                                const float s = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
+                                float p = ex2_approx(fmaf(s, scale_log2, zero_at));
+                                if constexpr (kDiagonal) p = 2 * t + e > r_in - col0 ? 0.f : p;
+                                if constexpr (kDiff) {
+                                    ds[e] = p * fmaf(dp, times, -delta_at);
+                                    dot[e] = fmaf(p, dp, dot[e]);
+                                } else {
+                                    ds[e] = p * (dp - delta_at);
                                 }
-                                dsw[h * 16 + t] = pack16x2<kBF16>(ds[0], ds[1]);
                             }
+                            dsw[t] = pack16x2<kBF16>(ds[0], ds[1]);
                         }
                     };
                     if (diagonal) step(std::true_type{});  // a loop of its own
                     else step(std::false_type{});
                     if constexpr (kBias) reached = true;
                 } else if constexpr (kBias) {
-                    // sums of dS over the row (without the last bucket's keys) and over the diagonals
-                    float a0 = 0.f, a1 = 0.f, a2 = 0.f;
-                    const float *wp = window_at(win, table, known, terms.n, d_lo, wlane) + 63 + wlane;
-                    const int far_to = d_lo + 63 + wlane - last_start;  // keys up to this one lie in the last bucket
+                    const float *wp = window_at(win, table, known, terms.n, d_lo, wlane) + 63 + wlane - col0;
+                    // columns up to this one lie in the last bucket
+                    const int far_to = d_lo + 63 + wlane - col0 - last_start;
+                    uint32_t sr[32], pr[32];
+                    tmem_ld32_pair(s_at, sr, dp_at, pr);
+                    float x[32];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t sr[32], pr[32];
-                        tmem_ld32_pair(tmem + t_lane + s_col(u & 1) + h * 32, sr,
-                                       tmem + t_lane + dp_col(u & 1) + h * 32, pr);
-                        float x[32];
+                    for (int c = 0; c < 32; ++c) x[c] = fmaf(__uint_as_float(sr[c]), scale_log2, wp[-c]) + zero_at;
+                    if (j == my_block) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            x[c] = fmaf(__uint_as_float(sr[c]), scale_log2, wp[-h * 32 - c]) + zero_at;
-                        if (j == my_block) {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) x[c] = h * 32 + c > r_in ? -INFINITY : x[c];
-                        }
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) x[c] = ex2_approx(x[c]) * (__uint_as_float(pr[c]) - dlt);
-#pragma unroll
-                        for (int t = 0; t < 16; ++t) dsw[h * 16 + t] = pack16x2<kBF16>(x[2 * t], x[2 * t + 1]);
-                        if (d_hi < last_start) {
-                            uint64_t two[4];
-#pragma unroll
-                            for (int t = 0; t < 4; ++t) two[t] = f2_pack(x[2 * t], x[2 * t + 1]);
-#pragma unroll
-                            for (int t = 4; t < 16; ++t) two[t & 3] = f2_add(two[t & 3], f2_pack(x[2 * t], x[2 * t + 1]));
-                            float s0, s1;
-                            f2_unpack(f2_add(f2_add(two[0], two[1]), f2_add(two[2], two[3])), s0, s1);
-                            others += s0 + s1;
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) others += h * 32 + c > far_to ? x[c] : 0.f;
-                        }
-                        // column c of row (lane + c + 1) mod 32: its distance is lane's first one (once the
-                        // sum passes 64), second or third
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float y = __shfl_sync(0xffffffffu, x[c], (wlane + c + 1) & 31);
-                            float &below = h ? a1 : a2, &above = h ? a0 : a1;
-                            const bool first = wlane + c + 1 < 32;
-                            below += first ? y : 0.f;
-                            above += first ? 0.f : y;
-                        }
+                        for (int c = 0; c < 32; ++c) x[c] = c > r_in - col0 ? -INFINITY : x[c];
                     }
-                    reached |= far_to >= 0;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) x[c] = ex2_approx(x[c]) * (__uint_as_float(pr[c]) - dlt);
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) dsw[t] = pack16x2<kBF16>(x[2 * t], x[2 * t + 1]);
+                    // the sum over the row, without the last bucket's keys
+                    if (d_hi < last_start) {
+                        uint64_t two[4];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) two[t] = f2_pack(x[2 * t], x[2 * t + 1]);
+#pragma unroll
+                        for (int t = 4; t < 16; ++t) two[t & 3] = f2_add(two[t & 3], f2_pack(x[2 * t], x[2 * t + 1]));
+                        float s0, s1;
+                        f2_unpack(f2_add(f2_add(two[0], two[1]), f2_add(two[2], two[3])), s0, s1);
+                        others += s0 + s1;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) others += c > far_to ? x[c] : 0.f;
+                        reached |= far_to + col0 >= 0;
+                    }
+                    // the sums over the diagonals: column c of row (lane + c + 1) mod 32 lies at the distance
+                    // d_lo + 64 - col0 + lane, or 32 nearer once the row wraps
+                    float below = 0.f, above = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float y = __shfl_sync(0xffffffffu, x[c], (wlane + c + 1) & 31);
+                        const bool first = wlane + c + 1 < 32;
+                        below += first ? y : 0.f;
+                        above += first ? 0.f : y;
+                    }
                     __syncwarp();  // the window has been read
                     if (d_hi < kNearSums) {
-                        float *to = near_sums + d_lo + wlane;
-                        to[0] += a0;
-                        to[32] += a1;
-                        to[64] += a2;
+                        float *to = near_sums + d_lo + 32 - col0 + wlane;
+                        to[32] += below;
+                        to[0] += above;
                     } else {
-                        add_distances(bins, win, a0, a1, a2, table, table.find(terms.n, d_hi), last_bucket, d_lo, d_hi, wlane);
+                        const bool second = col0 > 0;
+                        add_distances(bins, win, second ? above : 0.f, second ? below : above, second ? 0.f : below, table,
+                                      table.find(terms.n, d_hi), last_bucket, d_lo, d_hi, wlane);
                     }
                 }
             } else {
 #pragma unroll
-                for (int t = 0; t < 32; ++t) dsw[t] = 0u;
+                for (int t = 0; t < 16; ++t) dsw[t] = 0u;
             }
             __syncwarp();
-            tmem_st32(tmem + t_lane + s_col(u & 1), dsw);  // dS_u over the first 32 columns of S_u
+            tmem_st16(s_at, dsw);  // dS_u over the first 16 of this warp's columns of S_u
             tc_fence_before();
             mbar_arrive(BAR_P_FULL(u & 1));
         }
@@ -708,12 +709,12 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             if (!acc_valid) *abort_flag = 1;
         }
         // one decision for all elementwise warps (the section below has a barrier of its own)
-        if (!named_barrier_or(1, kRows, *abort_flag != 0)) {
+        if (!named_barrier_or(1, kElt, *abort_flag != 0)) {
             tc_fence_after();
             __syncwarp();
             // every product that read Q has completed: Q's tile stages dQ
-            if constexpr (kDiff) stage_half_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, half, r_in);
-            else stage_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, tid);
+            if constexpr (kDiff) stage_half_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, half, r_in, tid >> 7);
+            else stage_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, row, tid >> 7);
             if constexpr (kBias) {
                 // the last bucket, unless its keys are left out
                 float s = reached && last_bias > -INFINITY ? -others : 0.f;
@@ -725,27 +726,32 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 float s = dot[0] + dot[1];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                // dO's tile is free as well; the two warps of the second map
-                if (half && (tid & 31) == 0) reinterpret_cast<float *>(smem + L::kOffDO)[warp & 1] = s;
+                // dO's tile is free as well; the four warps of the second map
+                if (half && wlane == 0) reinterpret_cast<float *>(smem + L::kOffDO)[(warp & 1) + 2 * (warp >> 2)] = s;
             }
             fence_proxy_async_smem();
-            named_barrier(1, kRows);
+            named_barrier(1, kElt);
             if constexpr (kBias) {
                 // the warps' bucket sums and their sums by distance, a thread per bucket
                 const float *all = reinterpret_cast<const float *>(smem + L::kOffBins);
                 const float *by = reinterpret_cast<const float *>(smem + L::kOffNear) + kDistFront;
                 constexpr int kOne = kDistFront + kNearSums;
                 float *to = partial + ((long long)lane_id * gridDim.y + tile) * terms.n;
-                for (int b = tid; b < terms.n; b += kRows) {
-                    float s = (all[b] + all[kMaxBuckets + b]) + (all[2 * kMaxBuckets + b] + all[3 * kMaxBuckets + b]);
+                for (int b = tid; b < terms.n; b += kElt) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kEltWarps; ++w) s += all[w * kMaxBuckets + b];
                     const int end = b < last_bucket ? min(table.start[b + 1], kNearSums) : 0;
-                    for (int d = table.start[b]; d < end; ++d) s += (by[d] + by[kOne + d]) + (by[2 * kOne + d] + by[3 * kOne + d]);
+                    for (int d = table.start[b]; d < end; ++d)
+#pragma unroll
+                        for (int w = 0; w < kEltWarps; ++w) s += by[w * kOne + d];
                     to[b] = s;
                 }
             }
             if constexpr (kDiff) {
-                const float *two = reinterpret_cast<const float *>(smem + L::kOffDO);
-                if (tid == 0) partial[(long long)lane_id * gridDim.y + tile] = -(two[0] + two[1]);
+                const float *four = reinterpret_cast<const float *>(smem + L::kOffDO);
+                if (tid == 0)
+                    partial[(long long)lane_id * gridDim.y + tile] = -((four[0] + four[1]) + (four[2] + four[3]));
             }
             // A partial last block (S not a multiple of 64) is not TMA-stored -- its box would
             // run into the next lane's rows -- but copied row by row from the staging tile.
@@ -767,8 +773,8 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 tma_store_commit();
                 tma_store_wait_read();
             }
-            if ((half ? part_b : part_a) && qa * kBlock + tid < S)
-                copy_staged_row<D>(smem + (sQ - base), tid, dQ + ((size_t)row0 + qa * kBlock + tid) * D);
+            if (tid < kRows && (half ? part_b : part_a) && qa * kBlock + row < S)
+                copy_staged_row<D>(smem + (sQ - base), row, dQ + ((size_t)row0 + qa * kBlock + row) * D);
         }
     }
 #undef BAR_K_FULL
@@ -804,8 +810,8 @@ struct DkvSmem {
     static constexpr int kOffDelta = kOffLse + kStream * kRowBytes;
     static constexpr int kOffMeta = kOffDelta + kStream * kRowBytes;
     static constexpr int kOffTable = kOffMeta + kMetaBytes;        // bias only
-    static constexpr int kOffWin = kOffTable + kBucketTableBytes;  // 4 windows (bias only)
-    static constexpr int kEnd = Terms::kBias ? kOffWin + 4 * kWindow * 4 : kOffTable;
+    static constexpr int kOffWin = kOffTable + kBucketTableBytes;  // a window of each warp (bias only)
+    static constexpr int kEnd = Terms::kBias ? kOffWin + kEltWarps * kWindow * 4 : kOffTable;
     static constexpr int kBytes = smem_bytes_one_cta(kEnd + 1024);
     // the lower rows' dV passes through the ring of Q blocks
     static_assert(kStream * kQBytes >= kBlock * D * 4, "exchange");
@@ -875,11 +881,11 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(BAR_S_FULL(b), 1);
-            mbar_init(BAR_P_FULL(b), kRows);
+            mbar_init(BAR_P_FULL(b), kElt);
         }
         mbar_init(bar_done, 1);
         mbar_init(bar_fin, 1);
-        if constexpr (kDiff) mbar_init(meta + kBarReady, kRows);
+        if constexpr (kDiff) mbar_init(meta + kBarReady, kElt);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -1013,12 +1019,12 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_ts(tmem + kDVCol, tmem + s_col(u & 1) + kk * 8,
+                    tc_mma_ts(tmem + kDVCol, tmem + s_col(u & 1) + packed_col(kk),
                               sdesc_at(dot_desc, s * L::kQBytes + kk * 2048), kIdescAcc,
                               (u > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_ts(tmem + kDKCol, tmem + dp_col(u & 1) + kk * 8,
+                    tc_mma_ts(tmem + kDKCol, tmem + dp_col(u & 1) + packed_col(kk),
                               sdesc_at(qt_desc, s * L::kQBytes + kk * 2048), kIdescAcc,
                               (u > 0 || kk > 0) ? 1u : 0u);
                 tc_commit(BAR_EMPTY(s));
@@ -1031,13 +1037,14 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             (void)mbar_wait_timed(bar_fin, 0);
         }
     } else {
-        // ------------------------------------------------------------ elementwise (warps 0-3)
-        const int half = tid >> 6;               // 0: key block ka, 1: key block kb (kDiff: the maps)
-        const int k_in = tid & 63;               // key token within its block
+        // ------------------------------------------------------------ elementwise (warps 0-7)
+        const int row = tid & 127, col0 = (tid >> 7) * 32;  // this thread's row, and first column of a step
+        const int half = row >> 6;               // 0: key block ka, 1: key block kb (kDiff: the maps)
+        const int k_in = row & 63;               // key token within its block
         const int key_block = half && !kDiff ? kb : ka;
         const bool row_exists = kDiff || half == 0 || has_b;
         const int member = kDiff ? 0 : half;
-        const uint32_t t_lane = (uint32_t)(warp * 32) << 16;
+        const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
         // kDiff: the second map's P and dP count -lambda times
         [[maybe_unused]] float mul = 1.f;
@@ -1046,7 +1053,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             if (half) mul = -lam;
             ok = mbar_wait(bar_tile, 0, flags);
             if (ok) {
-                keep_diagonal<D>(sK, tid);
+                if (tid < kRows) keep_diagonal<D>(sK, row);
                 fence_proxy_async_smem();
                 mbar_arrive(meta + kBarReady);
             }
@@ -1054,10 +1061,10 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         [[maybe_unused]] int known = 0, last_start = 0;  // distances in the table; of the open bucket
         [[maybe_unused]] float last_bias = 0.f;
         if constexpr (kBias) {
-            table.template load<kBF16>(terms, lane_id % terms.H, tid, kRows);
-            named_barrier(2, kRows);
-            known = table.spread(terms.n, S, tid, kRows);
-            named_barrier(2, kRows);
+            table.template load<kBF16>(terms, lane_id % terms.H, tid, kElt);
+            named_barrier(2, kElt);
+            known = table.spread(terms.n, S, tid, kElt);
+            named_barrier(2, kElt);
             last_start = table.start[terms.n - 1];
             last_bias = table.bias[terms.n - 1];
         }
@@ -1074,11 +1081,12 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             if (!mbar_wait(BAR_FULL(s), (u / kStream) & 1, flags)) { ok = false; break; }
             tc_fence_after();
             const bool in_col = row_exists && ((fl >> member) & 1);  // warp-uniform
-            uint32_t pw[32], dw[32];
+            const uint32_t s_at = tmem + t_lane + s_col(u & 1) + col0, dp_at = tmem + t_lane + dp_col(u & 1) + col0;
+            uint32_t pw[16], dw[16];
             __syncwarp();
             if (in_col) {
-                const float *ls = lse_s + s * (L::kRowBytes / 4) + (kDiff ? half * 64 : 0);
-                const float *dl = delta_s + s * (L::kRowBytes / 4) + (kDiff ? half * 64 : 0);
+                const float *ls = lse_s + s * (L::kRowBytes / 4) + (kDiff ? half * 64 : 0) + col0;
+                const float *dl = delta_s + s * (L::kRowBytes / 4) + (kDiff ? half * 64 : 0) + col0;
                 // the bias: one constant for the step, or a window (query c at distance d_lo + 31 + c - wlane)
                 [[maybe_unused]] bool near = false;
                 [[maybe_unused]] float off = 0.f;
@@ -1087,24 +1095,22 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     const int d_lo = (i - key_block) * kBlock - (warp & 1) * 32 - 31;
                     // (the diagonal block goes with the near steps, which mask)
                     near = i == key_block || last_start > d_lo;
-                    if (near) wp = window_at(win, table, known, terms.n, d_lo, wlane) + 31 - wlane;
+                    if (near) wp = window_at(win, table, known, terms.n, d_lo, wlane) + 31 - wlane + col0;
                     else off = last_bias;
                 }
                 const float bias_at = off, times = mul;
-                const int hidden = i == key_block ? k_in : 0;  // queries before this one do not see the key
+                const int hidden = i == key_block ? k_in - col0 : 0;  // queries before this one do not see the key
                 auto step = [&, bias_at, times, wp, ls, dl, hidden](auto is_near, auto is_diagonal) {
                     constexpr bool kNear = decltype(is_near)::value, kDiagonal = decltype(is_diagonal)::value;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    {
                         uint32_t sr[32], pr[32];
-                        tmem_ld32_pair(tmem + t_lane + s_col(u & 1) + h * 32, sr,
-                                       tmem + t_lane + dp_col(u & 1) + h * 32, pr);
+                        tmem_ld32_pair(s_at, sr, dp_at, pr);
 #pragma unroll
                         for (int t = 0; t < 16; ++t) {
                             float p[2], ds[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int c = h * 32 + 2 * t + e;  // query token within block i
+                                const int c = 2 * t + e;  // query token within block i, from col0
                                 const float l2 = ls[c];
                                 const float x = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
                                 float z;
@@ -1116,8 +1122,8 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                                 if constexpr (kDiff) p[e] *= times;
                                 ds[e] = p[e] * (dp - dl[c]);
                             }
-                            pw[h * 16 + t] = pack16x2<kBF16>(p[0], p[1]);
-                            dw[h * 16 + t] = pack16x2<kBF16>(ds[0], ds[1]);
+                            pw[t] = pack16x2<kBF16>(p[0], p[1]);
+                            dw[t] = pack16x2<kBF16>(ds[0], ds[1]);
                         }
                     }
                 };
@@ -1130,11 +1136,11 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 }
             } else {
 #pragma unroll
-                for (int t = 0; t < 32; ++t) pw[t] = dw[t] = 0u;
+                for (int t = 0; t < 16; ++t) pw[t] = dw[t] = 0u;
             }
             __syncwarp();
-            tmem_st32(tmem + t_lane + s_col(u & 1), pw);   // P^T over the first 32 columns of S^T
-            tmem_st32(tmem + t_lane + dp_col(u & 1), dw);  // dS^T over the first 32 of dP^T
+            tmem_st16(s_at, pw);   // P^T over the first 16 of this warp's columns of S^T
+            tmem_st16(dp_at, dw);  // dS^T over the first 16 of those of dP^T
             tc_fence_before();
             mbar_arrive(BAR_P_FULL(u & 1));
         }
@@ -1145,20 +1151,20 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             if (!acc_valid) *abort_flag = 1;
         }
         // one decision for all elementwise warps (the section below has a barrier of its own)
-        if (!named_barrier_or(1, kRows, *abort_flag != 0)) {
+        if (!named_barrier_or(1, kElt, *abort_flag != 0)) {
             tc_fence_after();
             __syncwarp();
             // every product that read K and V has completed: their tiles stage dK and dV
             if constexpr (kDiff) {
                 stage_sum_of_halves<D, kBF16>(tmem + t_lane, kDVCol, acc_valid, sV,
-                                              reinterpret_cast<float4 *>(smem + L::kOffQ), half, k_in);
-                stage_half_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, half, k_in);
+                                              reinterpret_cast<float4 *>(smem + L::kOffQ), half, k_in, tid >> 7);
+                stage_half_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, half, k_in, tid >> 7);
             } else {
-                stage_rows<D, kBF16>(tmem + t_lane, kDVCol, acc_valid, 1.f, sV, tid);
-                stage_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, tid);
+                stage_rows<D, kBF16>(tmem + t_lane, kDVCol, acc_valid, 1.f, sV, row, tid >> 7);
+                stage_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, row, tid >> 7);
             }
             fence_proxy_async_smem();
-            named_barrier(1, kRows);
+            named_barrier(1, kElt);
             // a partial last key block is copied row by row (see the dQ kernel)
             constexpr bool k3D = kBias || kDiff;
             const bool part_a = !k3D && (ka + 1) * kBlock > S, part_b = !k3D && has_b && (kb + 1) * kBlock > S;
@@ -1186,10 +1192,10 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 tma_store_commit();
                 tma_store_wait_read();
             }
-            if ((half ? part_b : part_a) && key_block * kBlock + k_in < S) {
+            if (tid < kRows && (half ? part_b : part_a) && key_block * kBlock + k_in < S) {
                 const size_t grow_k = ((size_t)row0 + key_block * kBlock + k_in) * D;
-                copy_staged_row<D>(smem + (sV - base), tid, dV + grow_k);
-                copy_staged_row<D>(smem + (sK - base), tid, dK + grow_k);
+                copy_staged_row<D>(smem + (sV - base), row, dV + grow_k);
+                copy_staged_row<D>(smem + (sK - base), row, dK + grow_k);
             }
         }
     }
