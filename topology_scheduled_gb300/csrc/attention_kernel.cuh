@@ -111,7 +111,7 @@ constexpr int kBarVEmpty = kBarVFull + 8 * kVStages;  // kVStages x 8
 constexpr int kBarSFull = kBarVEmpty + 8 * kVStages;  // 2 x 8
 constexpr int kBarPFull = kBarSFull + 16;             // 2 x 8
 constexpr int kBarODone = kBarPFull + 16;
-constexpr int kBarFin = kBarODone + 8;
+constexpr int kBarFin = kBarODone + 16;               // (o_done: 2 x 8)
 constexpr int kBarQDiag = kBarFin + 8;  // Q is block-diagonal (differential attention)
 constexpr int kTmemSlot = kBarQDiag + 8;
 constexpr int kAbortFlag = kTmemSlot + 4;
@@ -390,13 +390,14 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kAbortFlag);
     [[maybe_unused]] const uint32_t bar_q_diag = meta + kBarQDiag;
     [[maybe_unused]] const BucketTable table(smem + L::kOffTable);
-    const uint32_t bar_q = meta + kBarQ, bar_o_done = meta + kBarODone, bar_fin = meta + kBarFin;
+    const uint32_t bar_q = meta + kBarQ, bar_fin = meta + kBarFin;
 #define BAR_K_FULL(s) (meta + kBarKFull + 8u * (uint32_t)(s))
 #define BAR_K_EMPTY(s) (meta + kBarKEmpty + 8u * (uint32_t)(s))
 #define BAR_V_FULL(s) (meta + kBarVFull + 8u * (uint32_t)(s))
 #define BAR_V_EMPTY(s) (meta + kBarVEmpty + 8u * (uint32_t)(s))
 #define BAR_S_FULL(b) (meta + kBarSFull + 8u * (uint32_t)(b))
 #define BAR_P_FULL(b) (meta + kBarPFull + 8u * (uint32_t)(b))
+#define BAR_O_DONE(b) (meta + kBarODone + 8u * (uint32_t)(b))
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -429,8 +430,8 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         for (int b = 0; b < 2; ++b) {
             mbar_init(BAR_S_FULL(b), 1);
             mbar_init(BAR_P_FULL(b), kRows);
+            mbar_init(BAR_O_DONE(b), 1);
         }
-        mbar_init(bar_o_done, 1);
         mbar_init(bar_fin, 1);
         if constexpr (kDiff) mbar_init(bar_q_diag, kRows);
         *abort_flag = 0;
@@ -601,7 +602,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                               (u > 0 || kk > 0) ? 1u : 0u);
                 }
                 tc_commit(BAR_V_EMPTY(s));
-                tc_commit(bar_o_done);
+                tc_commit(BAR_O_DONE(u & 1));
                 have = next;
                 ++u;
             }
@@ -711,7 +712,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const float alpha = !grow ? 1.f : (m_used == -INFINITY ? 0.f : ex2_approx(m_used - mx));
                     if (u > 0) {
                         // O must be quiescent: PV(u-1) has completed
-                        const bool done = mbar_wait(bar_o_done, (u - 1) & 1, flags);
+                        const bool done = mbar_wait(BAR_O_DONE((u - 1) & 1), ((u - 1) >> 1) & 1, flags);
                         if (__any_sync(0xffffffffu, !done)) { ok = false; break; }
                         tc_fence_after();
                         __syncwarp();
@@ -777,7 +778,9 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         // ---- epilogue: O / l in the input dtype, staged in the Q tile, TMA-stored per block
         bool o_valid = false;
         if (ok && u > 0) {
-            o_valid = mbar_wait(bar_o_done, (u - 1) & 1, flags);
+            // the last two PV products (those before had completed when the last scores did)
+            o_valid = mbar_wait(BAR_O_DONE((u - 1) & 1), ((u - 1) >> 1) & 1, flags) &&
+                      (u < 2 || mbar_wait(BAR_O_DONE(u & 1), ((u - 2) >> 1) & 1, flags));
             if (!o_valid) *abort_flag = 1;
         }
         // one decision for all softmax warps (the section below has a barrier of its own)
@@ -908,6 +911,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
 #undef BAR_V_EMPTY
 #undef BAR_S_FULL
 #undef BAR_P_FULL
+#undef BAR_O_DONE
 
     tc_fence_before();
     __syncthreads();

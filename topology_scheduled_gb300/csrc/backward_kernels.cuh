@@ -204,8 +204,8 @@ constexpr int kBarFull = 8;                           // kStream x 8: streamed b
 constexpr int kBarEmpty = kBarFull + 8 * kStream;     // kStream x 8: streamed block released
 constexpr int kBarSFull = kBarEmpty + 8 * kStream;    // 2 x 8: products of a step in TMEM
 constexpr int kBarPFull = kBarSFull + 16;             // 2 x 8: elementwise results of a step in TMEM
-constexpr int kBarDone = kBarPFull + 16;              // accumulation MMA of a step completed
-constexpr int kBarFin = kBarDone + 8;
+constexpr int kBarDone = kBarPFull + 16;              // 2 x 8: accumulation MMA of a step completed
+constexpr int kBarFin = kBarDone + 16;
 constexpr int kBarVFull = kBarFin + 8;                // dQ kernel: kStream x 8, V of a step landed
 constexpr int kBarVEmpty = kBarVFull + 8 * kStream;   // dQ kernel: kStream x 8
 constexpr int kBarReady = kBarVEmpty + 8 * kStream;   // the resident operands are in place
@@ -344,13 +344,14 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     volatile int *meta_j = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaJ);
     volatile int *meta_f = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kAbortFlag);
-    const uint32_t bar_tile = meta + kBarTile, bar_done = meta + kBarDone, bar_fin = meta + kBarFin;
+    const uint32_t bar_tile = meta + kBarTile, bar_fin = meta + kBarFin;
 #define BAR_K_FULL(s) (meta + kBarFull + 8u * (uint32_t)(s))
 #define BAR_K_EMPTY(s) (meta + kBarEmpty + 8u * (uint32_t)(s))
 #define BAR_V_FULL(s) (meta + kBarVFull + 8u * (uint32_t)(s))
 #define BAR_V_EMPTY(s) (meta + kBarVEmpty + 8u * (uint32_t)(s))
 #define BAR_S_FULL(b) (meta + kBarSFull + 8u * (uint32_t)(b))
 #define BAR_P_FULL(b) (meta + kBarPFull + 8u * (uint32_t)(b))
+#define BAR_DONE(b) (meta + kBarDone + 8u * (uint32_t)(b))
 
     const int tid = threadIdx.x, warp = tid >> 5;
     const int lane_id = blockIdx.x;
@@ -384,8 +385,8 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         for (int b = 0; b < 2; ++b) {
             mbar_init(BAR_S_FULL(b), 1);
             mbar_init(BAR_P_FULL(b), kElt);
+            mbar_init(BAR_DONE(b), 1);
         }
-        mbar_init(bar_done, 1);
         mbar_init(bar_fin, 1);
         mbar_init(meta + kBarReady, kElt);
         *abort_flag = 0;
@@ -529,7 +530,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                               sdesc_at(kt_desc, s * L::kKVBytes + kk * 2048), kIdescAcc,
                               (u > 0 || kk > 0) ? 1u : 0u);
                 tc_commit(BAR_K_EMPTY(s));
-                tc_commit(bar_done);
+                tc_commit(BAR_DONE(u & 1));
                 have = next;
                 ++u;
             }
@@ -705,7 +706,10 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         if (!ok) *abort_flag = 1;
         bool acc_valid = false;
         if (ok && u > 0) {
-            acc_valid = mbar_wait(bar_done, (u - 1) & 1, flags);
+            // the last two steps' accumulations: those before had completed when the last step's
+            // products did
+            acc_valid = mbar_wait(BAR_DONE((u - 1) & 1), ((u - 1) >> 1) & 1, flags) &&
+                        (u < 2 || mbar_wait(BAR_DONE(u & 1), ((u - 2) >> 1) & 1, flags));
             if (!acc_valid) *abort_flag = 1;
         }
         // one decision for all elementwise warps (the section below has a barrier of its own)
@@ -783,6 +787,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #undef BAR_V_EMPTY
 #undef BAR_S_FULL
 #undef BAR_P_FULL
+#undef BAR_DONE
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) {
@@ -846,11 +851,12 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     volatile int *meta_j = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaJ);
     volatile int *meta_f = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kMetaF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kAbortFlag);
-    const uint32_t bar_tile = meta + kBarTile, bar_done = meta + kBarDone, bar_fin = meta + kBarFin;
+    const uint32_t bar_tile = meta + kBarTile, bar_fin = meta + kBarFin;
 #define BAR_FULL(s) (meta + kBarFull + 8u * (uint32_t)(s))
 #define BAR_EMPTY(s) (meta + kBarEmpty + 8u * (uint32_t)(s))
 #define BAR_S_FULL(b) (meta + kBarSFull + 8u * (uint32_t)(b))
 #define BAR_P_FULL(b) (meta + kBarPFull + 8u * (uint32_t)(b))
+#define BAR_DONE(b) (meta + kBarDone + 8u * (uint32_t)(b))
 
     const int tid = threadIdx.x, warp = tid >> 5;
     const int lane_id = blockIdx.x;
@@ -882,8 +888,8 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         for (int b = 0; b < 2; ++b) {
             mbar_init(BAR_S_FULL(b), 1);
             mbar_init(BAR_P_FULL(b), kElt);
+            mbar_init(BAR_DONE(b), 1);
         }
-        mbar_init(bar_done, 1);
         mbar_init(bar_fin, 1);
         if constexpr (kDiff) mbar_init(meta + kBarReady, kElt);
         *abort_flag = 0;
@@ -1028,7 +1034,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                               sdesc_at(qt_desc, s * L::kQBytes + kk * 2048), kIdescAcc,
                               (u > 0 || kk > 0) ? 1u : 0u);
                 tc_commit(BAR_EMPTY(s));
-                tc_commit(bar_done);
+                tc_commit(BAR_DONE(u & 1));
                 have = next;
                 ++u;
             }
@@ -1147,7 +1153,10 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         if (!ok) *abort_flag = 1;
         bool acc_valid = false;
         if (ok && u > 0) {
-            acc_valid = mbar_wait(bar_done, (u - 1) & 1, flags);
+            // the last two steps' accumulations: those before had completed when the last step's
+            // products did
+            acc_valid = mbar_wait(BAR_DONE((u - 1) & 1), ((u - 1) >> 1) & 1, flags) &&
+                        (u < 2 || mbar_wait(BAR_DONE(u & 1), ((u - 2) >> 1) & 1, flags));
             if (!acc_valid) *abort_flag = 1;
         }
         // one decision for all elementwise warps (the section below has a barrier of its own)
@@ -1203,6 +1212,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #undef BAR_EMPTY
 #undef BAR_S_FULL
 #undef BAR_P_FULL
+#undef BAR_DONE
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) {
