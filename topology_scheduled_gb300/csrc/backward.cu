@@ -265,7 +265,12 @@ constexpr int kDeltaItems = 4;
 template <bool kBF16, int kG>
 __global__ void __launch_bounds__(256) bwd_delta(const uint16_t *__restrict__ O, const uint16_t *__restrict__ dO,
                                                  const float *__restrict__ lse, int S, int Sp,
-                                                 float *__restrict__ delta, float *__restrict__ lse_pad) {
+                                                 float *__restrict__ delta, float *__restrict__ lse_pad,
+                                                 const __grid_constant__ SmallSchedule schedule) {
+    if (schedule.nb > 0 && blockIdx.x == gridDim.x - 1) {  // one block more per lane; the first lane's works
+        if (blockIdx.y == 0) build_small_schedule(schedule);
+        return;
+    }
     constexpr int D = kG * 8;
     const long long lane = blockIdx.y;
     const int per_lane = Sp * kG;
@@ -333,8 +338,25 @@ BwdWorkspace backward_workspace_layout(int64_t lanes, int64_t S, int64_t nb, int
     return w;
 }
 
+SmallSchedule small_schedule(const BwdLaunch &a) {
+    SmallSchedule g{};
+    if (a.nb_in > 0 || a.nb > kSmallBlocks) return g;
+    g.nb = a.nb;
+    g.row_ptr = a.row_ptr;
+    g.col_idx = a.col_idx;
+    g.read_cap = a.read_cap;
+    g.cap = a.nnz_cap;
+    g.vlen = a.vlen;
+    g.col_ptr = a.col_ptr;
+    g.pairs = a.pairs;
+    g.row_idx = a.row_idx;
+    g.flags = a.flags;
+    return g;
+}
+
 tsa_status launch_backward_schedule(BwdLaunch *launch) {
     BwdLaunch &a = *launch;
+    if (small_schedule(a).nb > 0) return TSA_OK;  // built beside Delta
     cudaStream_t st = a.stream;
     const int nb = a.nb;
     const int words = (nb + 31) / 32;
@@ -369,13 +391,15 @@ tsa_status launch_backward_delta(const BwdLaunch &a) {
     cudaStream_t st = a.stream;
     const int Sp = a.nb * kBlock;
     const int per_lane = Sp * (a.D / 8);
-    const dim3 grid((unsigned)((per_lane + 256 * kDeltaItems - 1) / (256 * kDeltaItems)), (unsigned)a.lanes);
+    const SmallSchedule g = small_schedule(a);
+    const dim3 grid((unsigned)((per_lane + 256 * kDeltaItems - 1) / (256 * kDeltaItems)) + (g.nb > 0 ? 1u : 0u),
+                    (unsigned)a.lanes);
     if (a.D == 128) {
-        if (a.bf16) bwd_delta<true, 16><<<grid, 256, 0, st>>>(a.O, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad);
-        else bwd_delta<false, 16><<<grid, 256, 0, st>>>(a.O, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad);
+        if (a.bf16) bwd_delta<true, 16><<<grid, 256, 0, st>>>(a.O, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad, g);
+        else bwd_delta<false, 16><<<grid, 256, 0, st>>>(a.O, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad, g);
     } else if (a.D == 64) {
-        if (a.bf16) bwd_delta<true, 8><<<grid, 256, 0, st>>>(a.O, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad);
-        else bwd_delta<false, 8><<<grid, 256, 0, st>>>(a.O, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad);
+        if (a.bf16) bwd_delta<true, 8><<<grid, 256, 0, st>>>(a.O, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad, g);
+        else bwd_delta<false, 8><<<grid, 256, 0, st>>>(a.O, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad, g);
     } else {
         return TSA_ERR_UNSUPPORTED;
     }

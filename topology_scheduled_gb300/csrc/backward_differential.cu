@@ -14,7 +14,11 @@ template <bool kBF16, int kG>
 __global__ void __launch_bounds__(256)
 diff_delta(const uint16_t *__restrict__ O, const uint16_t *__restrict__ O2, const uint16_t *__restrict__ dO,
            const float *__restrict__ lse, int S, int Sp, float *__restrict__ delta, float *__restrict__ lse_pad,
-           const __grid_constant__ DiffTerms terms) {
+           const __grid_constant__ DiffTerms terms, const __grid_constant__ SmallSchedule schedule) {
+    if (schedule.nb > 0 && blockIdx.x == gridDim.x - 1) {  // one block more per lane; the first lane's works
+        if (blockIdx.y == 0) build_small_schedule(schedule);
+        return;
+    }
     constexpr int D = kG * 8;
     const long long lane = blockIdx.y;
     const float lam = lambda_of<D / 2, kBF16>(terms, (int)(lane % terms.H));
@@ -101,8 +105,9 @@ terms_reduce_lambda(const float *__restrict__ partial, int lanes, int tiles, con
 template <int D, bool kBF16>
 tsa_status launch_typed(const BwdLaunch &a, const DiffTerms &terms, const uint16_t *O2, uint16_t *const dlambda[4]) {
     const int Sp = a.nb * kBlock, per_lane = Sp * (D / 8);
-    const dim3 grid((unsigned)((per_lane + 256 * kItems - 1) / (256 * kItems)), (unsigned)a.lanes);
-    diff_delta<kBF16, D / 8><<<grid, 256, 0, a.stream>>>(a.O, O2, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad, terms);
+    const SmallSchedule g = small_schedule(a);
+    const dim3 grid((unsigned)((per_lane + 256 * kItems - 1) / (256 * kItems)) + (g.nb > 0 ? 1u : 0u), (unsigned)a.lanes);
+    diff_delta<kBF16, D / 8><<<grid, 256, 0, a.stream>>>(a.O, O2, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad, terms, g);
     TSA_TRY((launch_grad_kernels<D, kBF16, DiffTerms>(a, terms)));
     terms_reduce_lambda<D / 2, kBF16><<<terms.per_head ? terms.H : 1, 1024, 0, a.stream>>>(
         a.partial, a.lanes, a.nb, terms, dlambda[0], dlambda[1], dlambda[2], dlambda[3]);

@@ -30,6 +30,17 @@
 #include "tsa_internal.h"
 
 namespace tsa {
+
+// Where a short schedule's transpose comes from and goes to (see build_small_schedule).
+struct SmallSchedule {
+    int nb;  // 0: built elsewhere
+    const int32_t *row_ptr, *col_idx;
+    long long read_cap, cap;
+    int *vlen, *col_ptr, *pairs;
+    int32_t *row_idx;
+    DeviceFlags flags;
+};
+
 namespace {
 
 constexpr int kBlock = 64;
@@ -60,6 +71,75 @@ __device__ __forceinline__ uint32_t pack16x2(float a, float b) {
 // The log-sum-exp as the gradient kernels subtract it: log2 units, and +inf for a row without keys,
 // whose weights 2^(z - inf) are then 0 like those of rows past the end.
 __device__ __forceinline__ float padded_lse(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
+// The transposed schedule of a short 64-token CSR (at most kSmallBlocks rows), by one thread block of
+// 256: what bwd_rows, bwd_col_count, bwd_col_scan, bwd_col_fill and bwd_col_pairs (backward.cu) write,
+// with the bitmap in shared memory.  It runs beside the blocks that compute Delta, so a short sequence
+// pays one launch instead of seven ([2, 8, 1000, 64]: 22 us of small launches).  Longer schedules keep
+// the launches of their own: one block would read their rows one after another.
+constexpr int kSmallBlocks = 64;
+__device__ __forceinline__ void build_small_schedule(const SmallSchedule &g) {
+    __shared__ unsigned bits[kSmallBlocks][kSmallBlocks / 32];
+    __shared__ int count[kSmallBlocks], first[kSmallBlocks + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nb = g.nb;
+    for (int x = tid; x < kSmallBlocks * (kSmallBlocks / 32); x += blockDim.x) (&bits[0][0])[x] = 0u;
+    __syncthreads();
+    for (int i = warp; i < nb; i += blockDim.x >> 5) {  // a row per warp, as in bwd_rows
+        const int b = g.row_ptr[i], len = g.row_ptr[i + 1] - b;
+        int valid = 0;
+        if (len >= 0 && len <= i + 1 && b >= 0 && (long long)b + len <= g.read_cap) {
+            valid = len;
+            for (int e0 = 0; e0 < valid; e0 += 32) {
+                const int e = e0 + lane;
+                bool bad = false;
+                int j = 0;
+                if (e < len) {
+                    j = g.col_idx[b + e];
+                    const int prev = e > 0 ? g.col_idx[b + e - 1] : -1;
+                    bad = j < 0 || j > i || j <= prev;
+                }
+                const unsigned m = __ballot_sync(0xffffffffu, bad);
+                if (m) valid = e0 + __ffs(m) - 1;
+                if (e < valid) atomicOr(&bits[j][i >> 5], 1u << (i & 31));
+            }
+        }
+        if (lane == 0) {
+            if (valid != len) raise_status(g.flags, kDevBadSchedule);
+            g.vlen[i] = valid;
+        }
+    }
+    __syncthreads();
+    if (tid < kSmallBlocks) count[tid] = tid < nb ? __popc(bits[tid][0]) + __popc(bits[tid][1]) : 0;
+    __syncthreads();
+    if (warp == 0) {  // exclusive scan, two columns per lane
+        const int a = count[2 * lane], both = a + count[2 * lane + 1];
+        int incl = both;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const bool fits = __shfl_sync(0xffffffffu, incl, 31) <= g.cap;
+        if (lane == 0 && !fits) raise_status(g.flags, kDevCapacity);
+        first[2 * lane] = fits ? incl - both : 0;
+        first[2 * lane + 1] = fits ? incl - both + a : 0;
+        if (lane == 31) first[kSmallBlocks] = fits ? incl : 0;
+    }
+    __syncthreads();
+    for (int j = tid; j < nb; j += blockDim.x) {
+        int at = first[j];
+        const int end = first[j + 1];
+        g.col_ptr[j] = at;
+        if (j == nb - 1) g.col_ptr[nb] = end;
+        for (int w = 0; w < kSmallBlocks / 32; ++w)
+            for (unsigned m = bits[j][w]; m && at < end; m &= m - 1u) g.row_idx[at++] = w * 32 + __ffs(m) - 1;
+        // the column's place by length (longest first), then by index
+        int place = 0;
+        for (int x = 0; x < nb; ++x) place += count[x] > count[j] || (count[x] == count[j] && x < j);
+        g.pairs[place] = j;
+        if (j == 0 && (nb & 1)) g.pairs[nb] = -1;
+    }
+}
 
 // Union of two ascending index lists (already checked), with membership bits (1: first list,
 // 2: second list); -1 at the end.

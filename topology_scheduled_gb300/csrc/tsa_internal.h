@@ -96,7 +96,9 @@ struct BwdLaunch {
 
 tsa_status launch_attention_backward(const BwdLaunch &a);
 // Its first launches: the transposed schedule (a 128-token CSR is replaced by its expansion in *a),
-// and Delta with the log-sum-exp in padded rows.
+// and Delta with the log-sum-exp in padded rows.  A short schedule's transpose is built by the second.
+struct SmallSchedule;
+SmallSchedule small_schedule(const BwdLaunch &a);  // nb 0: the schedule is not short
 tsa_status launch_backward_schedule(BwdLaunch *a);
 tsa_status launch_backward_delta(const BwdLaunch &a);
 
