@@ -110,7 +110,7 @@ tsa_status launch_typed(const BwdLaunch &a, const DiffTerms &terms, const uint16
     diff_delta<kBF16, D / 8><<<grid, 256, 0, a.stream>>>(a.O, O2, a.dO, a.lse, a.S, Sp, a.delta, a.lse_pad, terms, g);
     TSA_TRY((launch_grad_kernels<D, kBF16, DiffTerms>(a, terms)));
     terms_reduce_lambda<D / 2, kBF16><<<terms.per_head ? terms.H : 1, 1024, 0, a.stream>>>(
-        a.partial, a.lanes, a.nb, terms, dlambda[0], dlambda[1], dlambda[2], dlambda[3]);
+        a.partial, a.lanes, (a.nb + 1) / 2, terms, dlambda[0], dlambda[1], dlambda[2], dlambda[3]);
     return cudaGetLastError() == cudaSuccess ? TSA_OK : TSA_ERR_CUDA;
 }
 

@@ -14,12 +14,15 @@
 // No atomics: a warp has its own sums, a CTA writes its tile's, and terms_reduce_bias adds the tiles
 // in order.
 //
-// Differential attention.  As in the forward a CTA takes one block and both maps: Q (or K) block-
-// diagonal, dO (or V) twice, so S and dP of both maps come from the same products.  The second map's
-// dP is -lambda times the first's, folded into the subtraction of Delta.  dQ = dS [k1 | k2] holds
-// each map's gradient in its half of the columns; dV adds the upper and lower rows through shared
-// memory.  lambda's gradient is - sum P2 o dP, summed over a CTA's rows in binary32 from the exact
-// weights, so that a sum over every query keeps the precision that P's rounding would cost.
+// Differential attention.  A CTA takes a pair of blocks as the plain kernels do, and both maps of them:
+// the first half of the score product's K steps goes into one accumulator, the second half into
+// another, so the two maps' scores cost what a plain score does, and dP serves both maps.  The
+// elementwise warps form dS1 and dS2 (= -lambda P2 o (dP - Delta2)); dQ and dK get each map's half of
+// their columns from products of half the width, and dV one product with P1 - lambda P2, combined in
+// binary32 and rounded once.  (Against one block per CTA with both maps in its 128 rows, by block-
+// diagonal operands: 32 lanes of S 32768, topology, backward 3.36 -> 2.45 ms.)  lambda's gradient is
+// - sum P2 o dP, summed over a CTA's rows in binary32 from the exact weights, so that a sum over every
+// query keeps the precision that P's rounding would cost.
 #pragma once
 
 #include <climits>
@@ -210,74 +213,6 @@ __device__ __forceinline__ void copy_staged_row(const uint8_t *tile, int row, ui
     }
 }
 
-// Differential attention: half m's 64 rows x D / 2 columns of an accumulator that starts at `col`
-// (columns m D/2 ..), times `mul`, rounded and written to a 64-row SW128 staging tile.
-template <int D, bool kBF16>
-__device__ __forceinline__ void stage_half_rows(uint32_t tmem_row, uint32_t col, bool valid, float mul,
-                                                uint32_t tile, int half, int row, int group) {
-    const uint32_t sw = (uint32_t)(row & 7);
-    if (group < D / 64) {  // 32 columns of D / 2
-        const int h = group;
-        uint32_t o[32];
-        if (valid) {
-            tmem_ld32(tmem_row + col + half * (D / 2) + h * 32, o);
-        } else {
-#pragma unroll
-            for (int t = 0; t < 32; ++t) o[t] = 0u;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                w[t] = pack16x2<kBF16>(__uint_as_float(o[q * 8 + 2 * t]) * mul,
-                                       __uint_as_float(o[q * 8 + 2 * t + 1]) * mul);
-            const uint32_t unit = D == 128 ? (uint32_t)(h * 4 + q) : (uint32_t)(half * 4 + q);
-            st_shared_v4(tile + (D == 128 ? half * 16384 : 0) + row * 128 + ((unit ^ sw) << 4), w[0], w[1], w[2], w[3]);
-        }
-    }
-}
-
-// Differential attention: the upper 64 rows of an accumulator plus the lower ones (which pass
-// through `passed` in binary32), rounded and written to a 64-row SW128 staging tile.  Called by all
-// elementwise threads; has a barrier.
-template <int D, bool kBF16>
-__device__ __forceinline__ void stage_sum_of_halves(uint32_t tmem_row, uint32_t col, bool valid, uint32_t tile,
-                                                    float4 *passed, int half, int row, int group) {
-    const uint32_t sw = (uint32_t)(row & 7);
-    passed += row;
-    if (half == 0) named_barrier(1, kElt);
-#pragma unroll
-    for (int x = 0; x < D / 64; ++x) {
-        const int h = group * (D / 64) + x;
-        uint32_t o[32];
-        if (valid) {
-            tmem_ld32(tmem_row + col + h * 32, o);
-        } else {
-#pragma unroll
-            for (int t = 0; t < 32; ++t) o[t] = 0u;
-        }
-        if (half) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-                passed[(h * 8 + t) * 64] = make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
-                                                       __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 x0 = passed[(h * 8 + 2 * q) * 64], y0 = passed[(h * 8 + 2 * q + 1) * 64];
-                const uint32_t *v = o + q * 8;
-                st_shared_v4(tile + (h >> 1) * 16384 + row * 128 + ((((h & 1) * 4 + q) ^ sw) << 4),
-                             pack16x2<kBF16>(__uint_as_float(v[0]) + x0.x, __uint_as_float(v[1]) + x0.y),
-                             pack16x2<kBF16>(__uint_as_float(v[2]) + x0.z, __uint_as_float(v[3]) + x0.w),
-                             pack16x2<kBF16>(__uint_as_float(v[4]) + y0.x, __uint_as_float(v[5]) + y0.y),
-                             pack16x2<kBF16>(__uint_as_float(v[6]) + y0.z, __uint_as_float(v[7]) + y0.w));
-            }
-        }
-    }
-    if (half) named_barrier(1, kElt);
-}
-
 // Meta area (byte offsets from the meta base), common to both kernels.
 constexpr int kBarTile = 0;                           // resident tile(s) loaded
 constexpr int kBarFull = 8;                           // kStream x 8: streamed block landed
@@ -288,8 +223,8 @@ constexpr int kBarDone = kBarPFull + 16;              // 2 x 8: accumulation MMA
 constexpr int kBarFin = kBarDone + 16;
 constexpr int kBarVFull = kBarFin + 8;                // dQ kernel: kStream x 8, V of a step landed
 constexpr int kBarVEmpty = kBarVFull + 8 * kStream;   // dQ kernel: kStream x 8
-constexpr int kBarReady = kBarVEmpty + 8 * kStream;   // the resident operands are in place
-constexpr int kTmemSlot = kBarReady + 8;
+constexpr int kBarLoaded = kBarVEmpty + 8 * kStream;  // dK/dV kernel, differential: 2 x 8, a step's products read
+constexpr int kTmemSlot = kBarLoaded + 16;
 constexpr int kAbortFlag = kTmemSlot + 4;
 constexpr int kMetaJ = kAbortFlag + 4;                // kMetaRing x 4
 constexpr int kMetaF = kMetaJ + 4 * kMetaRing;        // kMetaRing x 4
@@ -304,31 +239,15 @@ constexpr int smem_bytes_one_cta(int need) { return need > 116 * 1024 ? need : 1
 __device__ __forceinline__ uint32_t s_col(int b) { return b ? 64u : 0u; }
 __device__ __forceinline__ uint32_t dp_col(int b) { return b ? 192u : 128u; }
 constexpr uint32_t kAccCol = 256;
+// dQ kernel, differential: S1 0 | 1, S2 0 | 1, dP 0 | 1, accumulator
+__device__ __forceinline__ uint32_t s2_col(int b) { return b ? 192u : 128u; }
+__device__ __forceinline__ uint32_t diff_dp_col(int b) { return b ? 320u : 256u; }
+constexpr uint32_t kDiffAccCol = 384;
+// dK/dV kernel, differential: the columns of product x of step u
+__device__ __forceinline__ uint32_t diff_slot(int u, int x) { return (uint32_t)((3 * u + x) & 3) * 64u; }
 // Elements 16 kk .. 16 kk + 15 of a step's packed results: each warp writes its 32 over its own 32
 // columns of the products.
 __device__ __forceinline__ constexpr uint32_t packed_col(int kk) { return (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8); }
-
-// Row `row` (0-127) of a 128-row SW128 tile into tensor memory as a product's left operand: D / 2
-// columns from `col`, two 16-bit elements per column.  kDiagonal: rows 0-63 keep the first half of
-// their elements, rows 64-127 the second, the others are zero (see keep_diagonal).
-template <int D, bool kDiagonal>
-__device__ __forceinline__ void tile_row_to_tmem(const uint8_t *tile, int row, uint32_t tmem_row, uint32_t col) {
-    const uint32_t sw = (uint32_t)(row & 7);
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-        uint32_t w[32];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(tile + c * 16384 + row * 128 + (((uint32_t)u ^ sw) << 4));
-            const bool keep = !kDiagonal || (D == 128 ? c : u >> 2) == (row >> 6);
-            w[4 * u] = keep ? x.x : 0u;
-            w[4 * u + 1] = keep ? x.y : 0u;
-            w[4 * u + 2] = keep ? x.z : 0u;
-            w[4 * u + 3] = keep ? x.w : 0u;
-        }
-        tmem_st32(tmem_row + col + c * 32, w);
-    }
-}
 
 // ---------------------------------------------------------------- dQ
 // Adds a warp's sums of dS per distance to its bucket sums, but for the last bucket's.  A lane's
@@ -435,9 +354,10 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
     const int tid = threadIdx.x, warp = tid >> 5;
     const int lane_id = blockIdx.x;
-    const int tile = (int)gridDim.y - 1 - (int)blockIdx.y;  // two query blocks (kDiff: one, both maps)
-    const int qa = tile * (kDiff ? 1 : 2);                   // longest rows first
-    const bool has_b = !kDiff && qa + 1 < nb;
+    const int tile = (int)gridDim.y - 1 - (int)blockIdx.y;  // two query blocks
+    const int qa = 2 * tile;                                 // longest rows first
+    const bool has_b = qa + 1 < nb;
+    constexpr uint32_t kAcc = kDiff ? kDiffAccCol : kAccCol;
     const int row0 = lane_id * S;
 
     // The first global reads are issued together and waited for at the barrier below: whether
@@ -468,7 +388,6 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             mbar_init(BAR_DONE(b), 1);
         }
         mbar_init(bar_fin, 1);
-        mbar_init(meta + kBarReady, kElt);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -487,9 +406,6 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         return;
     }
 
-    // Q and dO as left operands, behind the accumulator
-    constexpr uint32_t kQCol = kAccCol + D, kDOCol = kQCol + D / 2;
-
     if (warp == kProducerWarp) {
         if (elect_one()) {
             tma_prefetch_desc(&tmQ);
@@ -502,10 +418,6 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             for (int c = 0; c < L::kChunks; ++c) {
                 load_rows<Terms>(sQ + c * 16384, &tmQ, c * 64, row0, qa * kBlock, lane_id, bar_tile);
                 load_rows<Terms>(sdO + c * 16384, &tmdO, c * 64, row0, qa * kBlock, lane_id, bar_tile);
-                if constexpr (kDiff) {  // 64-row boxes: the block again, for the second map
-                    load_rows<Terms>(sQ + c * 16384 + 8192, &tmQ, c * 64, row0, qa * kBlock, lane_id, bar_tile);
-                    load_rows<Terms>(sdO + c * 16384 + 8192, &tmdO, c * 64, row0, qa * kBlock, lane_id, bar_tile);
-                }
             }
             bool ok = true;
             int k_issued = 0, v_issued = 0;
@@ -547,12 +459,11 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     } else if (warp == kMmaWarp) {
         if (elect_one()) {
             constexpr uint32_t kIdescS = idesc_f16(kBF16, 128, 64, false);
-            constexpr uint32_t kIdescAcc = idesc_f16(kBF16, 128, D, true);
-            const uint64_t k_desc = sdesc_sw128(sK, 16, 1024), v_desc = sdesc_sw128(sV, 16, 1024),
+            constexpr uint32_t kIdescAcc = idesc_f16(kBF16, 128, kDiff ? D / 2 : D, true);
+            const uint64_t q_desc = sdesc_sw128(sQ, 16, 1024), do_desc = sdesc_sw128(sdO, 16, 1024),
+                           k_desc = sdesc_sw128(sK, 16, 1024), v_desc = sdesc_sw128(sV, 16, 1024),
                            kt_desc = sdesc_sw128(sK, 8192, 1024);
             bool ok = mbar_wait(bar_tile, 0, flags);
-            ok = ok && mbar_wait(meta + kBarReady, 0, flags);
-            tc_fence_after();
             int u = 0;
             bool have = false;
             // products of step uu: S = Q K^T and dP = dO V^T; V's stage is free afterwards
@@ -562,15 +473,18 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
                     const uint32_t boff = s_ * L::kKVBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
-                    tc_mma_ts(tmem + s_col(uu & 1), tmem + kQCol + kk * 8, sdesc_at(k_desc, boff), kIdescS,
-                              kk > 0 ? 1u : 0u);
+                    const bool second = kDiff && kk >= D / 32;  // the second map's half of the columns
+                    tc_mma_ss(tmem + (second ? s2_col(uu & 1) : s_col(uu & 1)), sdesc_at(q_desc, aoff),
+                              sdesc_at(k_desc, boff), kIdescS, kk % (kDiff ? D / 32 : D / 16) > 0 ? 1u : 0u);
                 }
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
                     const uint32_t boff = s_ * L::kKVBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
-                    tc_mma_ts(tmem + dp_col(uu & 1), tmem + kDOCol + kk * 8, sdesc_at(v_desc, boff), kIdescS,
-                              kk > 0 ? 1u : 0u);
+                    tc_mma_ss(tmem + (kDiff ? diff_dp_col(uu & 1) : dp_col(uu & 1)), sdesc_at(do_desc, aoff),
+                              sdesc_at(v_desc, boff), kIdescS, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(BAR_S_FULL(uu & 1));
                 tc_commit(BAR_V_EMPTY(s_));
@@ -606,9 +520,17 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_ts(tmem + kAccCol, tmem + s_col(u & 1) + packed_col(kk),
+                    tc_mma_ts(tmem + kAcc, tmem + s_col(u & 1) + packed_col(kk),
                               sdesc_at(kt_desc, s * L::kKVBytes + kk * 2048), kIdescAcc,
                               (u > 0 || kk > 0) ? 1u : 0u);
+                if constexpr (kDiff) {  // dS2 with the second half of K's columns
+                    constexpr uint32_t kHalf = D == 128 ? 8192 : 64;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_ts(tmem + kAcc + D / 2, tmem + s2_col(u & 1) + packed_col(kk),
+                                  sdesc_at(kt_desc, s * L::kKVBytes + kk * 2048 + kHalf), kIdescAcc,
+                                  (u > 0 || kk > 0) ? 1u : 0u);
+                }
                 tc_commit(BAR_K_EMPTY(s));
                 tc_commit(BAR_DONE(u & 1));
                 have = next;
@@ -623,22 +545,23 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         const int row = tid & 127, col0 = (tid >> 7) * 32;  // this thread's row, and first column of a step
         const int half = row >> 6;
         const int r_in = row & 63;
-        const int my_block = kDiff ? qa : qa + half;
-        const bool row_exists = kDiff || half == 0 || has_b;
-        const int member = kDiff ? 0 : half;  // the membership bit of this thread's row
+        const int my_block = qa + half;
+        const bool row_exists = half == 0 || has_b;
         const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
         // the row in the per-lane padded Delta / log-sum-exp arrays (nb * 64 rows per lane)
-        long long grow = ((long long)lane_id * nb + qa) * kBlock + (kDiff ? r_in : row);
-        if constexpr (kDiff) grow += half * terms.map_rows;
+        const long long grow = ((long long)lane_id * nb + qa) * kBlock + row;
         const float lse2 = row_exists ? lse[grow] : INFINITY;
-        float dlt = row_exists ? delta[grow] : 0.f;
+        const float dlt = row_exists ? delta[grow] : 0.f;
         bool ok = true;
-        // kDiff: the second map's dP is -lambda dO V^T
-        [[maybe_unused]] float mul = 1.f, dot[2] = {0.f, 0.f};  // dot: sum of P o dO V^T over the row
+        // kDiff: the second map, whose dP is -lambda dO V^T
+        [[maybe_unused]] float lse2_b = INFINITY, dlt_b = 0.f, mul = 0.f;
+        [[maybe_unused]] float dot[2] = {0.f, 0.f};  // the sum of P2 o dO V^T over the row
         if constexpr (kDiff) {
-            const float lam = lambda_of<D / 2, kBF16>(terms, lane_id % terms.H);
-            if (half) mul = -lam;
-            dlt *= mul;
+            mul = -lambda_of<D / 2, kBF16>(terms, lane_id % terms.H);
+            if (row_exists) {
+                lse2_b = lse[terms.map_rows + grow];
+                dlt_b = delta[terms.map_rows + grow] * mul;
+            }
         }
         // kBias: the sum over the row of the dS that lie before the last bucket
         [[maybe_unused]] float others = 0.f, last_bias = 0.f;
@@ -661,16 +584,6 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             known = table.spread(terms.n, (qa + 2) * kBlock, tid, kElt);
             named_barrier(2, kElt);
         }
-        ok = mbar_wait(bar_tile, 0, flags);
-        __syncwarp();
-        if (__all_sync(0xffffffffu, ok)) {
-            if (col0 == 0) tile_row_to_tmem<D, kDiff>(smem + L::kOffQ, row, tmem + t_lane, kQCol);
-            else tile_row_to_tmem<D, false>(smem + L::kOffDO, row, tmem + t_lane, kDOCol);
-            tc_fence_before();
-            mbar_arrive(meta + kBarReady);
-        } else {
-            ok = false;
-        }
         int u = 0;
         for (; ok; ++u) {
             if (!mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags)) { ok = false; break; }
@@ -678,9 +591,12 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             const int fl = meta_f[u % kMetaRing];
             if (j < 0) break;
             tc_fence_after();
-            const bool in_row = row_exists && ((fl >> member) & 1);  // warp-uniform
-            const uint32_t s_at = tmem + t_lane + s_col(u & 1) + col0, dp_at = tmem + t_lane + dp_col(u & 1) + col0;
+            const bool in_row = row_exists && ((fl >> half) & 1);  // warp-uniform
+            const uint32_t s_at = tmem + t_lane + s_col(u & 1) + col0;
+            const uint32_t dp_at = tmem + t_lane + (kDiff ? diff_dp_col(u & 1) : dp_col(u & 1)) + col0;
+            [[maybe_unused]] const uint32_t s2_at = tmem + t_lane + s2_col(u & 1) + col0;
             uint32_t dsw[16];
+            [[maybe_unused]] uint32_t dsw2[16];
             __syncwarp();
             if (in_row) {
                 // the bias: one constant for the step, or a window (key c at distance d_lo + 63 + wlane - c)
@@ -695,27 +611,33 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 }
                 if (!near) {
                     const bool diagonal = !kBias && j == my_block;
-                    const float delta_at = dlt, times = mul;
-                    auto step = [&, zero_at, delta_at, times](auto is_diagonal) {
+                    const float delta_at = dlt;
+                    [[maybe_unused]] const float zero_b = -lse2_b, delta_b = dlt_b, times = mul;
+                    auto step = [&, zero_at, delta_at, zero_b, delta_b, times](auto is_diagonal) {
                         constexpr bool kDiagonal = decltype(is_diagonal)::value;
                         uint32_t sr[32], pr[32];
-                        tmem_ld32_pair(s_at, sr, dp_at, pr);
+                        [[maybe_unused]] uint32_t sr2[32];
+                        if constexpr (kDiff) tmem_ld32_three(s_at, sr, s2_at, sr2, dp_at, pr);
+                        else tmem_ld32_pair(s_at, sr, dp_at, pr);
 #pragma unroll
                         for (int t = 0; t < 16; ++t) {
                             float ds[2];
+                            [[maybe_unused]] float ds2[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const float s = __uint_as_float(sr[2 * t + e]), dp = __uint_as_float(pr[2 * t + e]);
                                 float p = ex2_approx(fmaf(s, scale_log2, zero_at));
                                 if constexpr (kDiagonal) p = 2 * t + e > r_in - col0 ? 0.f : p;
+                                ds[e] = p * (dp - delta_at);
                                 if constexpr (kDiff) {
-                                    ds[e] = p * fmaf(dp, times, -delta_at);
-                                    dot[e] = fmaf(p, dp, dot[e]);
-                                } else {
-                                    ds[e] = p * (dp - delta_at);
+                                    float p2 = ex2_approx(fmaf(__uint_as_float(sr2[2 * t + e]), scale_log2, zero_b));
+                                    if constexpr (kDiagonal) p2 = 2 * t + e > r_in - col0 ? 0.f : p2;
+                                    ds2[e] = p2 * fmaf(dp, times, -delta_b);
+                                    dot[e] = fmaf(p2, dp, dot[e]);
                                 }
                             }
                             dsw[t] = pack16x2<kBF16>(ds[0], ds[1]);
+                            if constexpr (kDiff) dsw2[t] = pack16x2<kBF16>(ds2[0], ds2[1]);
                         }
                     };
                     if (diagonal) step(std::true_type{});  // a loop of its own
@@ -776,10 +698,14 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 }
             } else {
 #pragma unroll
-                for (int t = 0; t < 16; ++t) dsw[t] = 0u;
+                for (int t = 0; t < 16; ++t) {
+                    dsw[t] = 0u;
+                    if constexpr (kDiff) dsw2[t] = 0u;
+                }
             }
             __syncwarp();
             tmem_st16(s_at, dsw);  // dS_u over the first 16 of this warp's columns of S_u
+            if constexpr (kDiff) tmem_st16(s2_at, dsw2);
             tc_fence_before();
             mbar_arrive(BAR_P_FULL(u & 1));
         }
@@ -797,8 +723,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             tc_fence_after();
             __syncwarp();
             // every product that read Q has completed: Q's tile stages dQ
-            if constexpr (kDiff) stage_half_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, half, r_in, tid >> 7);
-            else stage_rows<D, kBF16>(tmem + t_lane, kAccCol, acc_valid, scale, sQ, row, tid >> 7);
+            stage_rows<D, kBF16>(tmem + t_lane, kAcc, acc_valid, scale, sQ, row, tid >> 7);
             if constexpr (kBias) {
                 // the last bucket, unless its keys are left out
                 float s = reached && last_bias > -INFINITY ? -others : 0.f;
@@ -810,8 +735,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 float s = dot[0] + dot[1];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                // dO's tile is free as well; the four warps of the second map
-                if (half && wlane == 0) reinterpret_cast<float *>(smem + L::kOffDO)[(warp & 1) + 2 * (warp >> 2)] = s;
+                if (wlane == 0) reinterpret_cast<float *>(smem + L::kOffDO)[warp] = s;  // dO's tile is free as well
             }
             fence_proxy_async_smem();
             named_barrier(1, kElt);
@@ -833,9 +757,13 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 }
             }
             if constexpr (kDiff) {
-                const float *four = reinterpret_cast<const float *>(smem + L::kOffDO);
-                if (tid == 0)
-                    partial[(long long)lane_id * gridDim.y + tile] = -((four[0] + four[1]) + (four[2] + four[3]));
+                const float *by = reinterpret_cast<const float *>(smem + L::kOffDO);
+                if (tid == 0) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kEltWarps; ++w) s += by[w];
+                    partial[(long long)lane_id * gridDim.y + tile] = -s;
+                }
             }
             // A partial last block (S not a multiple of 64) is not TMA-stored -- its box would
             // run into the next lane's rows -- but copied row by row from the staging tile.
@@ -889,17 +817,18 @@ struct DkvSmem {
     static constexpr int kQBytes = kBlock * D * 2;     // one Q or dO block
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kTileBytes;
+    static constexpr int kRing = Terms::kDiff && D == 128 ? 3 : kStream;  // two tiles of P beside it
     static constexpr int kOffQ = kOffV + kTileBytes;
-    static constexpr int kOffDO = kOffQ + kStream * kQBytes;
-    static constexpr int kOffLse = kOffDO + kStream * kQBytes;     // kStream x 64 floats (kDiff: of each map)
-    static constexpr int kOffDelta = kOffLse + kStream * kRowBytes;
-    static constexpr int kOffMeta = kOffDelta + kStream * kRowBytes;
+    static constexpr int kOffDO = kOffQ + kRing * kQBytes;
+    static constexpr int kOffP = kOffDO + kRing * kQBytes;          // kDiff: P1 - lambda P2 of two steps, transposed
+    static constexpr int kPBytes = kRows * kBlock * 2;
+    static constexpr int kOffLse = kOffP + (Terms::kDiff ? 2 * kPBytes : 0);  // kRing x 64 floats (kDiff: of each map)
+    static constexpr int kOffDelta = kOffLse + kRing * kRowBytes;
+    static constexpr int kOffMeta = kOffDelta + kRing * kRowBytes;
     static constexpr int kOffTable = kOffMeta + kMetaBytes;        // bias only
     static constexpr int kOffWin = kOffTable + kBucketTableBytes;  // a window of each warp (bias only)
     static constexpr int kEnd = Terms::kBias ? kOffWin + kEltWarps * kWindow * 4 : kOffTable;
     static constexpr int kBytes = smem_bytes_one_cta(kEnd + 1024);
-    // the lower rows' dV passes through the ring of Q blocks
-    static_assert(kStream * kQBytes >= kBlock * D * 4, "exchange");
 };
 
 template <int D, bool kBF16, class Terms>
@@ -924,6 +853,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     uint8_t *smem = smem_raw + (base - raw_base);
     [[maybe_unused]] const BucketTable table(smem + L::kOffTable);
     const uint32_t sK = base + L::kOffK, sV = base + L::kOffV, sQ = base + L::kOffQ, sdO = base + L::kOffDO;
+    [[maybe_unused]] const uint32_t sP = base + L::kOffP;
     const uint32_t sLse = base + L::kOffLse, sDelta = base + L::kOffDelta;
     const float *lse_s = reinterpret_cast<const float *>(smem + L::kOffLse);
     const float *delta_s = reinterpret_cast<const float *>(smem + L::kOffDelta);
@@ -937,12 +867,12 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #define BAR_S_FULL(b) (meta + kBarSFull + 8u * (uint32_t)(b))
 #define BAR_P_FULL(b) (meta + kBarPFull + 8u * (uint32_t)(b))
 #define BAR_DONE(b) (meta + kBarDone + 8u * (uint32_t)(b))
+#define BAR_LOADED(b) (meta + kBarLoaded + 8u * (uint32_t)(b))
 
     const int tid = threadIdx.x, warp = tid >> 5;
     const int lane_id = blockIdx.x;
-    // key blocks ka and kb (-1: none) from the pair list, heaviest transposed columns first (kDiff:
-    // one block, both maps)
-    const int ka = __ldg(pairs + (kDiff ? 1 : 2) * blockIdx.y), kb = kDiff ? -1 : __ldg(pairs + 2 * blockIdx.y + 1);
+    // key blocks ka and kb (-1: none) from the pair list, heaviest transposed columns first
+    const int ka = __ldg(pairs + 2 * blockIdx.y), kb = __ldg(pairs + 2 * blockIdx.y + 1);
     const bool has_b = kb >= 0;
     const int row0 = lane_id * S;
 
@@ -961,7 +891,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
     if (tid == 0) {
         mbar_init(bar_tile, 1);
-        for (int s = 0; s < kStream; ++s) {
+        for (int s = 0; s < L::kRing; ++s) {
             mbar_init(BAR_FULL(s), 1);
             mbar_init(BAR_EMPTY(s), 1);
         }
@@ -971,7 +901,8 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             mbar_init(BAR_DONE(b), 1);
         }
         mbar_init(bar_fin, 1);
-        if constexpr (kDiff) mbar_init(meta + kBarReady, kElt);
+        if constexpr (kDiff)
+            for (int b = 0; b < 2; ++b) mbar_init(BAR_LOADED(b), kElt);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -1004,7 +935,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             for (int c = 0; c < L::kChunks; ++c) {
                 load_rows<Terms>(sK + c * 16384, &tmK, c * 64, row0, ka * kBlock, lane_id, bar_tile);
                 load_rows<Terms>(sV + c * 16384, &tmV, c * 64, row0, ka * kBlock, lane_id, bar_tile);
-                // the second block's rows, or the first block's again (masked; kDiff: the second map)
+                // the second block's rows, or the first block's again (masked) if there is none
                 const int y2 = (has_b ? kb : ka) * kBlock;
                 load_rows<Terms>(sK + c * 16384 + 8192, &tmK, c * 64, row0, y2, lane_id, bar_tile);
                 load_rows<Terms>(sV + c * 16384 + 8192, &tmV, c * 64, row0, y2, lane_id, bar_tile);
@@ -1012,9 +943,9 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             bool ok = true;
             int issued = 0;
             for (int v = 0;; ++v) {
-                const int s = v % kStream;
-                const uint32_t par = (uint32_t)((v / kStream) - 1) & 1u;
-                if (v >= kStream && !mbar_wait(BAR_EMPTY(s), par, flags)) { ok = false; break; }
+                const int s = v % L::kRing;
+                const uint32_t par = (uint32_t)((v / L::kRing) - 1) & 1u;
+                if (v >= L::kRing && !mbar_wait(BAR_EMPTY(s), par, flags)) { ok = false; break; }
                 int f = 0;
                 const int i = lu.next(f);
                 meta_j[v % kMetaRing] = i;
@@ -1041,8 +972,8 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             if (!ok) {
                 *abort_flag = 1;
                 (void)mbar_wait_timed(bar_tile, 0);
-                for (int w = issued - kStream; w < issued; ++w)
-                    if (w >= 0) (void)mbar_wait_timed(BAR_FULL(w % kStream), (w / kStream) & 1);
+                for (int w = issued - L::kRing; w < issued; ++w)
+                    if (w >= 0) (void)mbar_wait_timed(BAR_FULL(w % L::kRing), (w / L::kRing) & 1);
             }
         }
     } else if (warp == kMmaWarp) {
@@ -1053,70 +984,148 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                            q_desc = sdesc_sw128(sQ, 16, 1024), do_desc = sdesc_sw128(sdO, 16, 1024),
                            qt_desc = sdesc_sw128(sQ, 8192, 1024), dot_desc = sdesc_sw128(sdO, 8192, 1024);
             bool ok = mbar_wait(bar_tile, 0, flags);
-            if constexpr (kDiff) ok = ok && mbar_wait(meta + kBarReady, 0, flags);
-            int u = 0;
-            bool have = false;
-            // products of step uu: S^T = K Q^T and dP^T = V dO^T
-            auto issue_products = [&](int uu) {
-                const int s_ = uu % kStream;
-                tc_fence_after();
+            if constexpr (kDiff) {
+                // Step u's three products go to the slots 3u, 3u + 1, 3u + 2 (mod 4) of 64 columns, S1^T, S2^T,
+                // dP^T; its dS1^T and dS2^T come back in the third, P^T in shared memory.  So S1 of the next
+                // step has a slot of its own, and S2 and dP can follow as soon as this step's scores are read.
+                constexpr uint32_t kIdescHalf = idesc_f16(kBF16, 128, D / 2, true);
+                constexpr uint32_t kHalf = D == 128 ? 8192 : 64;  // the second half of Q's columns
+                const uint64_t p_desc = sdesc_sw128(sP, 16, 1024);
+                auto issue = [&](int uu, int x) {  // product x of step uu
+                    const int s_ = uu % L::kRing;
+                    const uint32_t to = tmem + diff_slot(uu, x);
+                    if (x < 2) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
-                    const uint32_t boff = s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
-                    tc_mma_ss(tmem + s_col(uu & 1), sdesc_at(k_desc, aoff), sdesc_at(q_desc, boff),
-                              kIdescS, kk > 0 ? 1u : 0u);
-                }
+                        for (int k = 0; k < D / 32; ++k) {
+                            const int kk = k + x * (D / 32);
+                            tc_mma_ss(to, sdesc_at(k_desc, (kk >> 2) * 16384 + (kk & 3) * 32),
+                                      sdesc_at(q_desc, s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32), kIdescS,
+                                      k > 0 ? 1u : 0u);
+                        }
+                    } else {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
-                    const uint32_t boff = s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
-                    tc_mma_ss(tmem + dp_col(uu & 1), sdesc_at(v_desc, aoff), sdesc_at(do_desc, boff),
-                              kIdescS, kk > 0 ? 1u : 0u);
-                }
-                tc_commit(BAR_S_FULL(uu & 1));
-            };
-            if (ok) {
-                ok = mbar_wait(BAR_FULL(0), 0, flags);
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            tc_mma_ss(to, sdesc_at(v_desc, (kk >> 2) * 16384 + (kk & 3) * 32),
+                                      sdesc_at(do_desc, s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32), kIdescS,
+                                      kk > 0 ? 1u : 0u);
+                    }
+                };
+                ok = ok && mbar_wait(BAR_FULL(0), 0, flags);
+                bool have = false;
                 if (ok) {
-                    if (meta_j[0] >= 0) {
-                        issue_products(0);
-                        have = true;
+                    have = meta_j[0] >= 0;
+                    if (have) {
+                        tc_fence_after();
+                        issue(0, 0);
+                        issue(0, 1);
+                        issue(0, 2);
+                        tc_commit(BAR_S_FULL(0));
                     } else {
                         mbar_arrive(BAR_S_FULL(0));
                     }
                 }
-            }
-            while (ok && have) {
-                bool next = false;
-                const int s1 = (u + 1) % kStream;
-                ok = mbar_wait(BAR_FULL(s1), ((u + 1) / kStream) & 1, flags);
-                if (!ok) break;
-                if (meta_j[(u + 1) % kMetaRing] >= 0) {
-                    issue_products(u + 1);
-                    next = true;
-                } else {
-                    mbar_arrive(BAR_S_FULL((u + 1) & 1));
+                for (int u = 0; ok && have; ++u) {
+                    const int s = u % L::kRing, b = u & 1, s1 = (u + 1) % L::kRing;
+                    ok = mbar_wait(BAR_FULL(s1), ((u + 1) / L::kRing) & 1, flags);
+                    if (!ok) break;
+                    const bool next = meta_j[(u + 1) % kMetaRing] >= 0;
+                    if (next) {
+                        tc_fence_after();
+                        issue(u + 1, 0);
+                    }
+                    ok = mbar_wait(BAR_LOADED(b), (u >> 1) & 1, flags);
+                    if (!ok) break;
+                    if (next) {
+                        tc_fence_after();
+                        issue(u + 1, 1);
+                        issue(u + 1, 2);
+                        tc_commit(BAR_S_FULL(b ^ 1));
+                    } else {
+                        mbar_arrive(BAR_S_FULL(b ^ 1));
+                    }
+                    ok = mbar_wait(BAR_P_FULL(b), (u >> 1) & 1, flags);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_ss(tmem + kDVCol, sdesc_at(p_desc, b * L::kPBytes + kk * 32),
+                                  sdesc_at(dot_desc, s * L::kQBytes + kk * 2048), kIdescAcc, (u > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_ts(tmem + kDKCol + m * (D / 2), tmem + diff_slot(u, 2) + m * 16 + packed_col(kk),
+                                      sdesc_at(qt_desc, s * L::kQBytes + kk * 2048 + m * kHalf), kIdescHalf,
+                                      (u > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(BAR_EMPTY(s));
+                    tc_commit(BAR_DONE(b));
+                    have = next;
                 }
-                // dV += P^T_u dO_u and dK += dS^T_u Q_u once the elementwise warps wrote them
-                ok = mbar_wait(BAR_P_FULL(u & 1), (u >> 1) & 1, flags);
-                if (!ok) break;
-                const int s = u % kStream;
-                tc_fence_after();
+            } else {
+                int u = 0;
+                bool have = false;
+                // products of step uu: S^T = K Q^T and dP^T = V dO^T
+                auto issue_products = [&](int uu) {
+                    const int s_ = uu % L::kRing;
+                    tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_ts(tmem + kDVCol, tmem + s_col(u & 1) + packed_col(kk),
-                              sdesc_at(dot_desc, s * L::kQBytes + kk * 2048), kIdescAcc,
-                              (u > 0 || kk > 0) ? 1u : 0u);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
+                        const uint32_t boff = s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
+                        tc_mma_ss(tmem + s_col(uu & 1), sdesc_at(k_desc, aoff), sdesc_at(q_desc, boff),
+                                  kIdescS, kk > 0 ? 1u : 0u);
+                    }
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_ts(tmem + kDKCol, tmem + dp_col(u & 1) + packed_col(kk),
-                              sdesc_at(qt_desc, s * L::kQBytes + kk * 2048), kIdescAcc,
-                              (u > 0 || kk > 0) ? 1u : 0u);
-                tc_commit(BAR_EMPTY(s));
-                tc_commit(BAR_DONE(u & 1));
-                have = next;
-                ++u;
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
+                        const uint32_t boff = s_ * L::kQBytes + (kk >> 2) * 8192 + (kk & 3) * 32;
+                        tc_mma_ss(tmem + dp_col(uu & 1), sdesc_at(v_desc, aoff), sdesc_at(do_desc, boff),
+                                  kIdescS, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(BAR_S_FULL(uu & 1));
+                };
+                if (ok) {
+                    ok = mbar_wait(BAR_FULL(0), 0, flags);
+                    if (ok) {
+                        if (meta_j[0] >= 0) {
+                            issue_products(0);
+                            have = true;
+                        } else {
+                            mbar_arrive(BAR_S_FULL(0));
+                        }
+                    }
+                }
+                while (ok && have) {
+                    bool next = false;
+                    const int s1 = (u + 1) % L::kRing;
+                    ok = mbar_wait(BAR_FULL(s1), ((u + 1) / L::kRing) & 1, flags);
+                    if (!ok) break;
+                    if (meta_j[(u + 1) % kMetaRing] >= 0) {
+                        issue_products(u + 1);
+                        next = true;
+                    } else {
+                        mbar_arrive(BAR_S_FULL((u + 1) & 1));
+                    }
+                    // dV += P^T_u dO_u and dK += dS^T_u Q_u once the elementwise warps wrote them
+                    ok = mbar_wait(BAR_P_FULL(u & 1), (u >> 1) & 1, flags);
+                    if (!ok) break;
+                    const int s = u % L::kRing;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_ts(tmem + kDVCol, tmem + s_col(u & 1) + packed_col(kk),
+                                  sdesc_at(dot_desc, s * L::kQBytes + kk * 2048), kIdescAcc,
+                                  (u > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_ts(tmem + kDKCol, tmem + dp_col(u & 1) + packed_col(kk),
+                                  sdesc_at(qt_desc, s * L::kQBytes + kk * 2048), kIdescAcc,
+                                  (u > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(BAR_EMPTY(s));
+                    tc_commit(BAR_DONE(u & 1));
+                    have = next;
+                    ++u;
+                }
             }
             if (!ok) *abort_flag = 1;
             tc_commit(bar_fin);
@@ -1125,25 +1134,14 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     } else {
         // ------------------------------------------------------------ elementwise (warps 0-7)
         const int row = tid & 127, col0 = (tid >> 7) * 32;  // this thread's row, and first column of a step
-        const int half = row >> 6;               // 0: key block ka, 1: key block kb (kDiff: the maps)
+        const int half = row >> 6;               // 0: key block ka, 1: key block kb
         const int k_in = row & 63;               // key token within its block
-        const int key_block = half && !kDiff ? kb : ka;
-        const bool row_exists = kDiff || half == 0 || has_b;
-        const int member = kDiff ? 0 : half;
+        const int key_block = half ? kb : ka;
+        const bool row_exists = half == 0 || has_b;
         const uint32_t t_lane = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
-        // kDiff: the second map's P and dP count -lambda times
-        [[maybe_unused]] float mul = 1.f;
-        if constexpr (kDiff) {
-            const float lam = lambda_of<D / 2, kBF16>(terms, lane_id % terms.H);
-            if (half) mul = -lam;
-            ok = mbar_wait(bar_tile, 0, flags);
-            if (ok) {
-                if (tid < kRows) keep_diagonal<D>(sK, row);
-                fence_proxy_async_smem();
-                mbar_arrive(meta + kBarReady);
-            }
-        }
+        [[maybe_unused]] float mul = 0.f;  // kDiff: the second map's P and dP count -lambda times
+        if constexpr (kDiff) mul = -lambda_of<D / 2, kBF16>(terms, lane_id % terms.H);
         [[maybe_unused]] int known = 0, last_start = 0;  // distances in the table; of the open bucket
         [[maybe_unused]] float last_bias = 0.f;
         if constexpr (kBias) {
@@ -1162,17 +1160,19 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             const int i = meta_j[u % kMetaRing];
             const int fl = meta_f[u % kMetaRing];
             if (i < 0) break;
-            const int s = u % kStream;
+            const int s = u % L::kRing;
             // the step's log-sum-exp and Delta rows arrived with its Q and dO blocks
-            if (!mbar_wait(BAR_FULL(s), (u / kStream) & 1, flags)) { ok = false; break; }
+            if (!mbar_wait(BAR_FULL(s), (u / L::kRing) & 1, flags)) { ok = false; break; }
             tc_fence_after();
-            const bool in_col = row_exists && ((fl >> member) & 1);  // warp-uniform
-            const uint32_t s_at = tmem + t_lane + s_col(u & 1) + col0, dp_at = tmem + t_lane + dp_col(u & 1) + col0;
+            const bool in_col = row_exists && ((fl >> half) & 1);  // warp-uniform
+            const uint32_t s_at = tmem + t_lane + (kDiff ? diff_slot(u, 0) : s_col(u & 1)) + col0;
+            const uint32_t dp_at = tmem + t_lane + (kDiff ? diff_slot(u, 2) : dp_col(u & 1)) + col0;
             uint32_t pw[16], dw[16];
+            [[maybe_unused]] uint32_t dw2[16];
             __syncwarp();
             if (in_col) {
-                const float *ls = lse_s + s * (L::kRowBytes / 4) + (kDiff ? half * 64 : 0) + col0;
-                const float *dl = delta_s + s * (L::kRowBytes / 4) + (kDiff ? half * 64 : 0) + col0;
+                const float *ls = lse_s + s * (L::kRowBytes / 4) + col0;
+                const float *dl = delta_s + s * (L::kRowBytes / 4) + col0;
                 // the bias: one constant for the step, or a window (query c at distance d_lo + 31 + c - wlane)
                 [[maybe_unused]] bool near = false;
                 [[maybe_unused]] float off = 0.f;
@@ -1188,8 +1188,35 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 const int hidden = i == key_block ? k_in - col0 : 0;  // queries before this one do not see the key
                 auto step = [&, bias_at, times, wp, ls, dl, hidden](auto is_near, auto is_diagonal) {
                     constexpr bool kNear = decltype(is_near)::value, kDiagonal = decltype(is_diagonal)::value;
-                    {
-                        uint32_t sr[32], pr[32];
+                    uint32_t sr[32], pr[32];
+                    if constexpr (kDiff) {
+                        uint32_t sr2[32];
+                        tmem_ld32_three(s_at, sr, tmem + t_lane + diff_slot(u, 1) + col0, sr2, dp_at, pr);
+                        tc_fence_before();
+                        mbar_arrive(BAR_LOADED(u & 1));
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) {
+                            float p[2], ds1[2], ds2[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int c = 2 * t + e;  // query token within block i, from col0
+                                const float dp = __uint_as_float(pr[c]);
+                                float p1 = ex2_approx(fmaf(__uint_as_float(sr[c]), scale_log2, -ls[c]));
+                                float p2 = ex2_approx(fmaf(__uint_as_float(sr2[c]), scale_log2, -ls[64 + c]));
+                                if constexpr (kDiagonal) {
+                                    p1 = c < hidden ? 0.f : p1;
+                                    p2 = c < hidden ? 0.f : p2;
+                                }
+                                p2 *= times;
+                                p[e] = p1 + p2;
+                                ds1[e] = p1 * (dp - dl[c]);
+                                ds2[e] = p2 * (dp - dl[64 + c]);
+                            }
+                            pw[t] = pack16x2<kBF16>(p[0], p[1]);
+                            dw[t] = pack16x2<kBF16>(ds1[0], ds1[1]);
+                            dw2[t] = pack16x2<kBF16>(ds2[0], ds2[1]);
+                        }
+                    } else {
                         tmem_ld32_pair(s_at, sr, dp_at, pr);
 #pragma unroll
                         for (int t = 0; t < 16; ++t) {
@@ -1205,7 +1232,6 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                                 else z = fmaf(x, scale_log2, -l2);
                                 p[e] = ex2_approx(z);
                                 if constexpr (kDiagonal) p[e] = c < hidden ? 0.f : p[e];
-                                if constexpr (kDiff) p[e] *= times;
                                 ds[e] = p[e] * (dp - dl[c]);
                             }
                             pw[t] = pack16x2<kBF16>(p[0], p[1]);
@@ -1222,11 +1248,25 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 }
             } else {
 #pragma unroll
-                for (int t = 0; t < 16; ++t) pw[t] = dw[t] = 0u;
+                for (int t = 0; t < 16; ++t) {
+                    pw[t] = dw[t] = 0u;
+                    if constexpr (kDiff) dw2[t] = 0u;
+                }
+                if constexpr (kDiff) mbar_arrive(BAR_LOADED(u & 1));
             }
             __syncwarp();
-            tmem_st16(s_at, pw);   // P^T over the first 16 of this warp's columns of S^T
-            tmem_st16(dp_at, dw);  // dS^T over the first 16 of those of dP^T
+            tmem_st16(dp_at, dw);  // dS^T over the first 16 of this warp's columns of dP^T
+            if constexpr (kDiff) {
+                tmem_st16(dp_at + 16, dw2);  // dS2^T over its other 16
+                const uint32_t to = sP + (u & 1) * L::kPBytes + row * 128;  // P^T as a left operand, SW128
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    st_shared_v4(to + ((((uint32_t)(col0 >> 3) + q) ^ (uint32_t)(row & 7)) << 4), pw[4 * q], pw[4 * q + 1],
+                                 pw[4 * q + 2], pw[4 * q + 3]);
+                fence_proxy_async_smem();
+            } else {
+                tmem_st16(s_at, pw);  // P^T over the first 16 of those of S^T
+            }
             tc_fence_before();
             mbar_arrive(BAR_P_FULL(u & 1));
         }
@@ -1244,14 +1284,8 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             tc_fence_after();
             __syncwarp();
             // every product that read K and V has completed: their tiles stage dK and dV
-            if constexpr (kDiff) {
-                stage_sum_of_halves<D, kBF16>(tmem + t_lane, kDVCol, acc_valid, sV,
-                                              reinterpret_cast<float4 *>(smem + L::kOffQ), half, k_in, tid >> 7);
-                stage_half_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, half, k_in, tid >> 7);
-            } else {
-                stage_rows<D, kBF16>(tmem + t_lane, kDVCol, acc_valid, 1.f, sV, row, tid >> 7);
-                stage_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, row, tid >> 7);
-            }
+            stage_rows<D, kBF16>(tmem + t_lane, kDVCol, acc_valid, 1.f, sV, row, tid >> 7);
+            stage_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, row, tid >> 7);
             fence_proxy_async_smem();
             named_barrier(1, kElt);
             // a partial last key block is copied row by row (see the dQ kernel)
@@ -1293,6 +1327,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #undef BAR_S_FULL
 #undef BAR_P_FULL
 #undef BAR_DONE
+#undef BAR_LOADED
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *abort_flag) {
@@ -1314,7 +1349,7 @@ tsa_status launch_grad_kernels(const BwdLaunch &a, const Terms &terms) {
     if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqBytes) != cudaSuccess ||
         cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, kDkvBytes) != cudaSuccess)
         return TSA_ERR_CUDA;
-    const unsigned tiles = (unsigned)(Terms::kDiff ? a.nb : (a.nb + 1) / 2);
+    const unsigned tiles = (unsigned)((a.nb + 1) / 2);
     const dim3 grid((unsigned)a.lanes, tiles);
     const float scale_log2 = a.scale * kLog2e;
     kq<<<grid, kThreads, kDqBytes, a.stream>>>(*a.tmQ128, *a.tmdO128, *a.tmK64, *a.tmV64, *a.tmdQ64, a.row_ptr,

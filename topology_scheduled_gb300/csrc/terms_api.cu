@@ -162,11 +162,11 @@ struct BackwardMaps {
 tsa_status backward_launch(const void *Q, const void *K, const void *V, const void *O, const void *dO, const float *lse,
                            const int32_t *row_ptr, const int32_t *col_idx, int64_t nnz_cap, void *dQ, void *dK, void *dV,
                            tsa_dtype dtype, int64_t lanes, int64_t S, int64_t D, int64_t block, float scale,
-                           uint32_t tile_rows, uint8_t *w, const TermsWorkspace &ws, tsa_stream_t stream, int dev,
+                           uint8_t *w, const TermsWorkspace &ws, tsa_stream_t stream, int dev,
                            BackwardMaps *m, BwdLaunch *a) {
     const bool bf16 = dtype == TSA_BF16;
     const uint64_t L = (uint64_t)lanes, R = (uint64_t)S, C = (uint64_t)D;
-    if (!encode_3d(&m->q, Q, bf16, L, R, C, tile_rows) || !encode_3d(&m->dO, dO, bf16, L, R, C, tile_rows) ||
+    if (!encode_3d(&m->q, Q, bf16, L, R, C, 128) || !encode_3d(&m->dO, dO, bf16, L, R, C, 128) ||
         !encode_3d(&m->q64, Q, bf16, L, R, C, 64) || !encode_3d(&m->dO64, dO, bf16, L, R, C, 64) ||
         !encode_3d(&m->k, K, bf16, L, R, C, 64) || !encode_3d(&m->v, V, bf16, L, R, C, 64) ||
         !encode_3d(&m->dq, dQ, bf16, L, R, C, 64) || !encode_3d(&m->dk, dK, bf16, L, R, C, 64) ||
@@ -253,9 +253,9 @@ tsa_status decode_launch(const void *Q, const void *K, const void *V, const int3
     return device_flags(dev, &a->flags);
 }
 
-// Floats of the tiles' parts: a bias's bucket sums per pair of query blocks, a lambda's per block.
+// Floats of the tiles' parts, a tile per pair of query blocks: a bias's bucket sums, a lambda's one.
 int64_t bias_parts(int64_t lanes, int64_t S, int64_t n) { return lanes * ((S + 127) / 128) * n; }
-int64_t lambda_parts(int64_t lanes, int64_t S) { return lanes * ((S + 63) / 64); }
+int64_t lambda_parts(int64_t lanes, int64_t S) { return lanes * ((S + 127) / 128); }
 
 }  // namespace
 }  // namespace tsa
@@ -357,7 +357,7 @@ tsa_status tsa_biased_attention_backward(const void *Q, const void *K, const voi
     BackwardMaps m;
     BwdLaunch a;
     TSA_TRY(backward_launch(Q, K, V, O, dO, lse, row_ptr, col_idx, nnz_cap, dQ, dK, dV, dtype, lanes, S, D, block,
-                            scale, 128, static_cast<uint8_t *>(workspace), ws, stream, dev, &m, &a));
+                            scale, static_cast<uint8_t *>(workspace), ws, stream, dev, &m, &a));
     return launch_biased_backward(a, t, static_cast<uint16_t *>(dbias));
 }
 
@@ -406,7 +406,7 @@ tsa_status tsa_differential_attention_backward(const void *Q, const void *K, con
     BackwardMaps m;
     BwdLaunch a;
     TSA_TRY(backward_launch(Q, K, V, O, dO, lse, row_ptr, col_idx, nnz_cap, dQ, dK, dV, dtype, lanes, S, D, block,
-                            scale, 64, static_cast<uint8_t *>(workspace), ws, stream, dev, &m, &a));
+                            scale, static_cast<uint8_t *>(workspace), ws, stream, dev, &m, &a));
     uint16_t *const dl[4] = {static_cast<uint16_t *>(dlambda_q1), static_cast<uint16_t *>(dlambda_k1),
                              static_cast<uint16_t *>(dlambda_q2), static_cast<uint16_t *>(dlambda_k2)};
     return launch_differential_backward(a, t, static_cast<const uint16_t *>(O2), dl);

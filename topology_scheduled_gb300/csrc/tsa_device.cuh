@@ -331,6 +331,18 @@ __device__ __forceinline__ void tmem_ld32_pair(uint32_t taddr_r, uint32_t (&r)[3
     TSA_LD32(q, taddr_q);
     // the wait names both destinations so that no use or copy of them moves above it
     asm volatile("tcgen05.wait::ld.sync.aligned;" : TSA_HOLD32(r), TSA_HOLD32(q) : : "memory");
+}
+
+// Three 32-column loads under one wait.
+__device__ __forceinline__ void tmem_ld32_three(uint32_t taddr_r, uint32_t (&r)[32], uint32_t taddr_q,
+                                                uint32_t (&q)[32], uint32_t taddr_p, uint32_t (&p)[32]) {
+    TSA_LD32(r, taddr_r);
+    TSA_LD32(q, taddr_q);
+    TSA_LD32(p, taddr_p);
+    // (the empty statements hold the other destinations below the wait)
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : TSA_HOLD32(r) : : "memory");
+    asm volatile("" : TSA_HOLD32(q) : : "memory");
+    asm volatile("" : TSA_HOLD32(p) : : "memory");
 #undef TSA_LD32
 #undef TSA_HOLD32
 }
