@@ -7,8 +7,8 @@
 // 4 D multiply-adds (6 D with two maps), so the arithmetic stays on the FMA pipe.
 //  * A lane of a warp holds 8 of the D dimensions, so D / 8 lanes read a row with one 16-byte load
 //    each and a warp reads 2 (D = 128) or 4 rows per load.  A warp takes a chunk of 8 such loads of K
-//    and 8 of V at a time, all issued before their first use: 8 KB in flight per warp, 128 KB per SM
-//    with the 16 warps that fit.
+//    and 8 of V at a time; the next chunk's K is loaded while this one's V is used, so that 4 KB or
+//    8 KB are in flight per warp at any time, with the 16 warps that fit an SM.
 //  * Every group of D / 8 lanes keeps its own running maximum, denominator and 8 sums, in binary32;
 //    the weights are never rounded.  They are joined at the end: groups by shuffles, warps through
 //    shared memory, thread blocks through the shared memory of their cluster.
@@ -30,7 +30,9 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLoads = 8;  // 16-byte loads of K (and of V) a lane has in flight
+// 16-byte loads of K (and of V) a lane has in flight: with two maps' sums to keep, half as many
+template <class Terms>
+constexpr int kLoadsOf = Terms::kDiff ? 4 : 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -71,7 +73,8 @@ __device__ __forceinline__ void widen8(const uint4 &w, float (&x)[8]) {
 struct Running {
     float m = -INFINITY, l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 
-    // The weights 2^(s - m) of n scores under the new maximum; what was there is rescaled.
+    // The weights 2^(s - m) of the scores under the new maximum; what was there is rescaled.
+    template <int kLoads>
     __device__ __forceinline__ void weigh(const float (&s)[kLoads], float (&p)[kLoads]) {
         float mx = m;
 #pragma unroll
@@ -103,13 +106,13 @@ struct Running {
 };
 
 template <int D, bool kBF16, class Terms>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Terms::kDiff ? 3 : 2)
 decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, const uint16_t *__restrict__ V,
               const int32_t *__restrict__ lens, const int32_t *__restrict__ row_ptr,
               const int32_t *__restrict__ col_idx, int nnz_cap, uint16_t *__restrict__ O, int H, int cap, int block,
               float scale_log2, DeviceFlags flags, const __grid_constant__ Terms terms) {
     constexpr bool kBias = Terms::kBias, kDiff = Terms::kDiff;
-    constexpr int kMaps = kDiff ? 2 : 1;
+    constexpr int kMaps = kDiff ? 2 : 1, kLoads = kLoadsOf<Terms>;
     constexpr int kG = D / 8;            // lanes per row
     constexpr int kPer = 32 / kG;        // rows per load of a warp
     constexpr int kChunk = kLoads * kPer;
@@ -147,24 +150,41 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
 
     Running state[kMaps];
     const int per_block = block / kChunk, chunks = entries * per_block, step = ranks * kWarps;
-    for (int u = rank * kWarps + warp; u < chunks; u += step) {
-        const int e = u / per_block;
-        const int j = __ldg(col_idx + first + e), before = e > 0 ? __ldg(col_idx + first + e - 1) : -1;
-        if (j >= nb || j <= before || j < 0) {  // out of the cache or out of order: left out and reported
-            if (lane == 0) raise_status(flags, kDevBadSchedule);
-            continue;
+    // The block of chunk u and the one listed before it (entries past the end: none).
+    auto entry_of = [&](int u, int &j, int &before) {
+        j = before = -1;
+        if (u < chunks) {
+            const int *at_entry = col_idx + first + u / per_block;
+            j = __ldg(at_entry);
+            if (u >= per_block) before = __ldg(at_entry - 1);
         }
-        const int k0 = j * block + (u - e * per_block) * kChunk;
-        if (k0 >= len) continue;
-        uint4 kr[kLoads], vr[kLoads];
+    };
+    // First key of chunk u; len (a chunk without keys) for a block outside the cache or out of order.
+    auto first_key = [&](int u, int j, int before) {
+        if (u >= chunks) return len;
+        if (j >= nb || j <= before || j < 0) {
+            if (lane == 0) raise_status(flags, kDevBadSchedule);
+            return len;
+        }
+        return j * block + (u % per_block) * kChunk;
+    };
+    auto load = [&](uint4 (&r)[kLoads], const uint16_t *base, int k0) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int k = k0 + i * kPer + group;
-            const bool there = k < len;
-            const long long off = (long long)k * D;
-            kr[i] = there ? __ldg(reinterpret_cast<const uint4 *>(Kl + off)) : make_uint4(0u, 0u, 0u, 0u);
-            vr[i] = there ? __ldg(reinterpret_cast<const uint4 *>(Vl + off)) : make_uint4(0u, 0u, 0u, 0u);
+            r[i] = k < len ? __ldg(reinterpret_cast<const uint4 *>(base + (long long)k * D)) : make_uint4(0u, 0u, 0u, 0u);
         }
+    };
+    // K of a chunk is loaded while the one before is weighed, V while its scores are summed: a warp
+    // always has a chunk's rows in flight.
+    int u = rank * kWarps + warp, j, before;
+    entry_of(u, j, before);
+    int k0 = first_key(u, j, before);
+    uint4 kr[kLoads], vr[kLoads];
+    load(kr, Kl, k0);
+    entry_of(u + step, j, before);
+    for (; u < chunks; u += step) {
+        load(vr, Vl, k0);
         // the bias of chunk key `lane`, or of all of them
         [[maybe_unused]] float mine = 0.f;
         [[maybe_unused]] bool uniform = true;
@@ -205,6 +225,9 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
                 s[0][i] = there ? dot : -INFINITY;
             }
         }
+        const int next = first_key(u + step, j, before);
+        load(kr, Kl, next);
+        entry_of(u + 2 * step, j, before);
         float p[kMaps][kLoads];
 #pragma unroll
         for (int m = 0; m < kMaps; ++m) state[m].weigh(s[m], p[m]);
@@ -217,6 +240,7 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
 #pragma unroll
                 for (int d = 0; d < 8; ++d) state[m].acc[d] = fmaf(p[m][i], x[d], state[m].acc[d]);
         }
+        k0 = next;
     }
     // groups of a warp, then the warps
 #pragma unroll
@@ -283,11 +307,13 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
 template <int D, bool kBF16, class Terms>
 tsa_status launch_one(const DecodeLaunch &a, const Terms &terms) {
     // Thread blocks per (sequence, head): as many as give every warp a chunk when rows are as long as
-    // the cache, up to a cluster of 8, while the grid is below four waves of two blocks per SM.
-    constexpr int kChunk = kLoads * 32 / (D / 8);
+    // the cache, up to a cluster of 8, while the grid is below four blocks per SM.  More blocks would
+    // each pay for their start and their join: 512 heads of 8192 tokens, biased, 232 us with two blocks
+    // each, 239 with four, 268 with eight, 255 with one (ragged lengths leave its last wave short).
+    constexpr int kChunk = kLoadsOf<Terms> * 32 / (D / 8);
     const long long chunks = ((long long)a.cap + kChunk - 1) / kChunk;
     unsigned ranks = 1;
-    while (ranks < 8 && (long long)ranks * kWarps < chunks && (long long)a.lanes * ranks < 4 * 304) ranks *= 2;
+    while (ranks < 8 && (long long)ranks * kWarps < chunks && (long long)a.lanes * ranks < 4 * 152) ranks *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.lanes * ranks);
     cfg.blockDim = dim3(kThreads);
