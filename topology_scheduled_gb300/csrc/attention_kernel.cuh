@@ -737,34 +737,39 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 if constexpr (kBias) n1 = m_used == -INFINITY ? off : off - m_used;  // no key with weight yet
                 const uint64_t cc = f2_pack(c1, c1);
                 const uint64_t nm = f2_pack(n1, n1);
-                float ls[4] = {0.f, 0.f, 0.f, 0.f};
-                [[maybe_unused]] uint64_t le = f2_pack(0.f, 0.f);
+                auto weigh = [&, cc, nm](auto exact_too) {
+                    constexpr bool kExact = decltype(exact_too)::value;
+                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                    [[maybe_unused]] uint64_t le = f2_pack(0.f, 0.f);
 #pragma unroll
-                for (int t = 0; t < 32; ++t) {
-                    float e0, e1;
-                    f2_unpack(f2_fma(f2_pack(x[2 * t], x[2 * t + 1]), cc, nm), e0, e1);
-                    const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
-                    if constexpr (kBF16) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-                        pw[t] = *reinterpret_cast<const uint32_t *>(&h);
-                    } else {
-                        const __half2 h = __floats2half2_rn(p0, p1);
-                        pw[t] = *reinterpret_cast<const uint32_t *>(&h);
+                    for (int t = 0; t < 32; ++t) {
+                        float e0, e1;
+                        f2_unpack(f2_fma(f2_pack(x[2 * t], x[2 * t + 1]), cc, nm), e0, e1);
+                        const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+                        if constexpr (kBF16) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                            pw[t] = *reinterpret_cast<const uint32_t *>(&h);
+                        } else {
+                            const __half2 h = __floats2half2_rn(p0, p1);
+                            pw[t] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        // The denominator sums the rounded P that the PV product uses, so a row
+                        // dominated by one key normalizes exactly.
+                        add_half<kBF16, false>(ls[(t & 1) * 2], pw[t]);
+                        add_half<kBF16, true>(ls[(t & 1) * 2 + 1], pw[t]);
+                        if constexpr (kExact) le = f2_add(le, f2_pack(p0, p1));
                     }
-                    // The denominator sums the rounded P that the PV product uses, so a row
-                    // dominated by one key normalizes exactly.
-                    add_half<kBF16, false>(ls[(t & 1) * 2], pw[t]);
-                    add_half<kBF16, true>(ls[(t & 1) * 2 + 1], pw[t]);
-                    // The log-sum-exp of the differential form adds P itself: the backward pass weighs
-                    // its second map with it to find lambda's gradient, one sum over every row.
-                    if constexpr (kDiff) le = f2_add(le, f2_pack(p0, p1));
-                }
-                l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-                if constexpr (kDiff) {
-                    float e0, e1;
-                    f2_unpack(le, e0, e1);
-                    l_exact += e0 + e1;
-                }
+                    l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    if constexpr (kExact) {
+                        float e0, e1;
+                        f2_unpack(le, e0, e1);
+                        l_exact += e0 + e1;
+                    }
+                };
+                // The log-sum-exp of the differential form adds P itself: the backward pass weighs its
+                // second map with it to find lambda's gradient, one sum over every row.
+                if (kDiff && lse_out) weigh(std::bool_constant<kDiff>{});
+                else weigh(std::false_type{});
             } else {
 #pragma unroll
                 for (int t = 0; t < 32; ++t) pw[t] = 0u;
