@@ -12,8 +12,8 @@ from __future__ import annotations
 import torch
 
 from .binding import tsa_scheduled_attention_backward, tsa_scheduled_attention_fwd
-from .terms import (tsa_biased_attention_backward, tsa_biased_attention_fwd, tsa_differential_attention_backward,
-                    tsa_differential_attention_fwd)
+from .terms import (_starts, tsa_biased_attention_backward, tsa_biased_attention_fwd,
+                    tsa_differential_attention_backward, tsa_differential_attention_fwd)
 
 
 class ScheduledAttention(torch.autograd.Function):
@@ -44,6 +44,7 @@ class BiasedAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, V, row_ptr, col_idx, bias, bucket_starts, scale, block):
         Q, K, V, bias = (t.contiguous() for t in (Q, K, V, bias))
+        bucket_starts, _ = _starts(bucket_starts, bias)  # a copy: the caller's may change before the backward
         O, lse = tsa_biased_attention_fwd(Q, K, V, row_ptr, col_idx, bias, bucket_starts, scale, block=block)
         ctx.save_for_backward(Q, K, V, O, lse, row_ptr, col_idx, bias)
         ctx.settings = bucket_starts, scale, block
