@@ -12,10 +12,10 @@
 //  * Warp roles (192 threads).  Warp 4 produces: one thread TMA-loads Q once and the K and V
 //    tiles of each visited block into two-stage rings of their own (128-byte swizzle), polling
 //    both rings so that neither stream waits behind the other.  Warp 5 issues the MMAs from
-//    one thread: S = Q K^T (M128 N64 K=D, both operands in shared memory) into one of two TMEM
-//    S buffers, and O += P V (M128 N=D K64) with P read from TMEM.  Warps 0-3 run the online
-//    softmax, one row per thread: tcgen05.ld of the S row, exp2 with the scale folded in, the
-//    new P written back over the S buffer in the input dtype with tcgen05.st.
+//    one thread: S = Q K^T (M128 N64 K=D, both operands in shared memory) into a TMEM S buffer
+//    (of two at D = 128), and O += P V (M128 N=D K64) with P read from TMEM.  Warps 0-3 run the
+//    online softmax, one row per thread: tcgen05.ld of the S row, exp2 with the scale folded in,
+//    the new P written in the input dtype with tcgen05.st (over S at D = 128).
 //  * Pipeline.  The MMA warp issues QK(u+1) before PV(u), so the tensor core computes the next
 //    scores while the softmax warps work on the current ones.  K and V have rings of their
 //    own: a K stage is refilled as soon as its QK is done, so the next key tile is already
@@ -33,7 +33,15 @@
 //    weigh: the block is visited only as the diagonal block of the last row, where the causal
 //    mask already drops keys after the query token.  Its query rows past S are computed and
 //    dropped: the block's output is written row by row for the rows that exist.
-//  * Two CTAs share an SM, so one CTA's softmax also overlaps the other's MMAs.
+//  * CTAs share an SM, so one CTA's softmax also overlaps the others' MMAs: two at D = 128, where the
+//    tiles fill the shared memory, three at D = 64.  Three leave 96 registers per thread and 170 TMEM
+//    columns per CTA.  So at D = 64 a softmax thread takes its 64 scores in two parts of 32, the first
+//    one read twice (for the maximum and for the weights, its biases and mask stored back in between),
+//    and there is one S buffer (64 columns), O (64) and P in 32 columns of its own: the next scores are
+//    computed once the softmax warps have read S, and P is written once the product that read the last
+//    one is done.  Measured, 64 heads of 8192 tokens, 13 blocks a row: 160 us, against 170 us with two
+//    CTAs, two S buffers and 64 scores at once (3 CTAs: biased 184 against 189, differential 299
+//    against 326).  One S buffer with P over it, which would need no P columns, took 178 us.
 //
 // The same kernel carries the score terms of score_terms.cuh:
 //  * Bias by buckets of the distance q - k.  Far enough from the diagonal all keys of a step lie in the
@@ -92,11 +100,17 @@ struct AttnSmem {
     static constexpr int kOffTable = kOffMeta + kMetaBytes;           // BucketTable (bias only)
     static constexpr int kOffWin = kOffTable + kBucketTableBytes;     // 4 windows (bias only)
     static constexpr int kEnd = kOffWin + 4 * kWindow * 4;
-    static constexpr int kTmemCols = 256;  // S0 | S1 | O (P_b aliases the first 32 of S_b)
-    static constexpr int kOCol = 128;
-};
+    static constexpr bool kOneS = D == 64;
+    static constexpr int kCtas = kOneS ? 3 : 2;  // per SM, by shared memory (kOneS: and by TMEM)
+    // S0 | S1 | O, P_b over the first 32 columns of S_b; or S | O, and P in 32 columns of its own
+    static constexpr int kTmemCols = kOneS ? 128 : 256;
+    static constexpr int kPCols = 32;
+    static constexpr int kOCol = kOneS ? 64 : 128;
 
-__device__ __forceinline__ uint32_t s_col(int b) { return b ? 64u : 0u; }
+    static constexpr int kPart = kOneS ? 32 : 64;  // keys of a step that a softmax thread holds at a time
+
+    __device__ static __forceinline__ uint32_t s_col(int b) { return !kOneS && b ? 64u : 0u; }
+};
 
 // Meta area layout (byte offsets from kOffMeta).
 // Union entries in flight: the producer writes entry v once QK(v - kKStages) is done, while the
@@ -113,8 +127,9 @@ constexpr int kBarPFull = kBarSFull + 16;             // 2 x 8
 constexpr int kBarODone = kBarPFull + 16;
 constexpr int kBarFin = kBarODone + 16;               // (o_done: 2 x 8)
 constexpr int kBarQDiag = kBarFin + 8;  // Q is block-diagonal (differential attention)
-constexpr int kTmemSlot = kBarQDiag + 8;
-constexpr int kAbortFlag = kTmemSlot + 4;
+constexpr int kBarSRead = kBarQDiag + 8;  // the softmax warps have read S (one buffer)
+constexpr int kTmemSlot = kBarSRead + 8;  // and the one of P
+constexpr int kAbortFlag = kTmemSlot + 8;
 constexpr int kMetaJ = kAbortFlag + 4;                // kMetaRing x 4
 constexpr int kMetaF = kMetaJ + 4 * kMetaRing;        // kMetaRing x 4
 static_assert(kMetaF + 4 * kMetaRing <= 256, "meta area");
@@ -359,7 +374,7 @@ static_assert(AttnSmem<64>::kEnd + 512 <= kAttnSmemBytes<64>(), "smem");
 static_assert(2 * AttnSmem<128>::kKVBytes >= kBlock * 128 * 4 && 2 * AttnSmem<64>::kKVBytes >= kBlock * 64 * 4, "exchange");
 
 template <int D, bool kBF16, int kGran, class Terms>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, AttnSmem<D>::kCtas)
 scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV,
@@ -390,6 +405,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMeta + kAbortFlag);
     [[maybe_unused]] const uint32_t bar_q_diag = meta + kBarQDiag;
     [[maybe_unused]] const BucketTable table(smem + L::kOffTable);
+    [[maybe_unused]] const uint32_t bar_s_read = meta + kBarSRead;
     const uint32_t bar_q = meta + kBarQ, bar_fin = meta + kBarFin;
 #define BAR_K_FULL(s) (meta + kBarKFull + 8u * (uint32_t)(s))
 #define BAR_K_EMPTY(s) (meta + kBarKEmpty + 8u * (uint32_t)(s))
@@ -434,11 +450,15 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         mbar_init(bar_fin, 1);
         if constexpr (kDiff) mbar_init(bar_q_diag, kRows);
+        if constexpr (L::kOneS) mbar_init(bar_s_read, kRows);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
     if (warp == kMmaWarp) {
+        // The small piece first: with at most three CTAs of this kernel on an SM, each holding 32 of the
+        // 512 columns, a gap of 128 always remains, so the second call waits for no CTA that waits.
+        if constexpr (L::kOneS) tmem_alloc(meta + kTmemSlot + 4, L::kPCols);
         tmem_alloc(meta + kTmemSlot, L::kTmemCols);
         tmem_relinquish();
     }
@@ -446,9 +466,14 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     const bool leave = __syncthreads_or(gave_up);
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kOffMeta + kTmemSlot);
+    [[maybe_unused]] const uint32_t tmem_p = *reinterpret_cast<volatile uint32_t *>(smem + L::kOffMeta + kTmemSlot + 4);
+    auto free_tmem = [&] {
+        tmem_dealloc(tmem, L::kTmemCols);
+        if constexpr (L::kOneS) tmem_dealloc(tmem_p, L::kPCols);
+    };
     if (leave) {  // nothing was issued yet: give the columns back and go
         if (tid == 0) raise_status(flags, kDevTimeout);  // a replayed launch that gave up once says so again
-        if (warp == kMmaWarp) tmem_dealloc(tmem, L::kTmemCols);
+        if (warp == kMmaWarp) free_tmem();
         return;
     }
 
@@ -555,7 +580,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         _Pragma("unroll") for (int kk = 0; kk < D / 16; ++kk) {                                   \
             const uint64_t a_ = sdesc_at(q_desc, (kk >> 2) * 16384 + (kk & 3) * 32);              \
             const uint64_t b_ = sdesc_at(k_desc, s_ * L::kKVBytes + (kk >> 2) * 8192 + (kk & 3) * 32); \
-            tc_mma_ss(tmem + s_col((uu) & 1), a_, b_, kIdescQK, kk > 0 ? 1u : 0u);               \
+            tc_mma_ss(tmem + L::s_col((uu) & 1), a_, b_, kIdescQK, kk > 0 ? 1u : 0u);               \
         }                                                                                         \
         tc_commit(BAR_S_FULL((uu) & 1));                                                          \
         tc_commit(BAR_K_EMPTY(s_));                                                               \
@@ -583,6 +608,8 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 ok = mbar_wait(BAR_K_FULL(s1), ((u + 1) / kKStages) & 1, flags);
                 if (!ok) break;
                 if (meta_j[(u + 1) % kMetaRing] >= 0) {
+                    if constexpr (L::kOneS) ok = mbar_wait(bar_s_read, u & 1, flags);
+                    if (!ok) break;
                     ISSUE_QK(u + 1);
                     next = true;
                 } else {
@@ -598,7 +625,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const uint64_t b = sdesc_at(v_desc, s * L::kKVBytes + kk * 2048);
-                    tc_mma_ts(tmem + L::kOCol, tmem + s_col(u & 1) + kk * 8, b, kIdescPV,
+                    tc_mma_ts(tmem + L::kOCol, (L::kOneS ? tmem_p : tmem + L::s_col(u & 1)) + kk * 8, b, kIdescPV,
                               (u > 0 || kk > 0) ? 1u : 0u);
                 }
                 tc_commit(BAR_V_EMPTY(s));
@@ -628,7 +655,8 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         if constexpr (kDiff) {
             // Q's off-diagonal halves become zero once its copy has landed
             lam = lambda_of<D / 2, kBF16>(terms, lane_id % terms.H);
-            ok = mbar_wait(bar_q, 0, flags);
+            const bool landed = mbar_wait(bar_q, 0, flags);
+            ok = __all_sync(0xffffffffu, landed);
             if (ok) {
                 keep_diagonal<D>(sQ, tid);
                 fence_proxy_async_smem();
@@ -646,9 +674,13 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
             last_bias = table.bias[terms.n - 1];
         }
         [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
+        constexpr int kPart = L::kPart;
+        constexpr bool kOneS = L::kOneS;
         int u = 0;
         for (; ok; ++u) {
-            if (!mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags)) { ok = false; break; }
+            // (all lanes together: one whose wait ran out must not leave the others to a warp-wide step)
+            const bool there = mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags);
+            if (!__all_sync(0xffffffffu, there)) { ok = false; break; }
             const int j = meta_j[u % kMetaRing];
             const int fl = meta_f[u % kMetaRing];
             if (j < 0) break;
@@ -656,73 +688,117 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
             // key halves this warp's 32 rows hold (both, with 64- or 128-token blocks)
             const int fq = kFine ? (fl >> (2 * (kDiff ? warp & 1 : warp))) & 3 : ((fl >> member) & 1) * 3;
             const bool in_row = row_exists && fq != 0;  // warp-uniform
-            const uint32_t s_addr = tmem + t_lane + s_col(u & 1);
-            uint32_t pw[32];
+            const uint32_t s_addr = tmem + t_lane + L::s_col(u & 1);
+            auto store_p = [&](int part, const uint32_t (&pw)[kPart / 2]) {
+                if constexpr (kPart == 64) tmem_st32(s_addr, pw);
+                else tmem_st16(tmem_p + t_lane + part * 16, pw);
+            };
+            // PV(u - 1) has completed: O may be rescaled, and P of one buffer be written
+            auto o_done = [&] {
+                const bool done = u == 0 || mbar_wait(BAR_O_DONE((u - 1) & 1), ((u - 1) >> 1) & 1, flags);
+                return __all_sync(0xffffffffu, done);
+            };
             __syncwarp();
             if (in_row) {
-                uint32_t sr[2][32];
-                tmem_ld32x2(s_addr, sr[0], sr[1]);
-                float x[64];  // raw scores q.k
-#pragma unroll
-                for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sr[c >> 5][c & 31]);
+                float x[kPart];  // raw scores q.k of a part of the keys
                 // scores in log2 units are x * cc + off
                 [[maybe_unused]] float cc1 = scale_log2, off = 0.f;
+                [[maybe_unused]] const float *wp = nullptr;  // the biases, where they differ
                 if constexpr (kBias) {
                     // key c lies at the distance d_lo + 63 + (tid & 31) - c
                     const int d_lo = (qa - j) * kBlock + warp * 32 - 63;
                     if (last_start <= (d_lo > 0 ? d_lo : 0)) {  // all of it in the open last bucket
                         off = last_bias;
                     } else {
-                        const float *wp = window_at(win, table, known, terms.n, d_lo, tid & 31) + 63 + (tid & 31);
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) x[c] = fmaf(x[c], scale_log2, wp[-c]);
+                        wp = window_at(win, table, known, terms.n, d_lo, tid & 31) + 63 + (tid & 31);
                         cc1 = 1.f;
                     }
                 }
-                if constexpr (kFine) {
-                    if (fq != 3) {  // a 32-token key half this row does not hold
+                auto load_scores = [&](int part, bool again) {
+                    const int c0 = part * kPart;
+                    if constexpr (kPart == 64) {
+                        uint32_t sr[2][32];
+                        tmem_ld32x2(s_addr, sr[0], sr[1]);
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (!((fq >> (c >> 5)) & 1)) x[c] = -INFINITY;
+                        for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sr[c >> 5][c & 31]);
+                    } else {
+                        uint32_t sr[32];
+                        tmem_ld32(s_addr + c0, sr);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(sr[c]);
                     }
-                    if (j >= qa) {  // near the diagonal: keys after the query token are masked
-                        const int lim = (qa - j) * kBlock + row_in;  // key 64j + c > query 64qa + row_in
+                    if constexpr (kBias) {
+                        if (wp != nullptr) {
+                            if (again) return;  // they came with their biases, masked
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (c > lim) x[c] = -INFINITY;
+                            for (int c = 0; c < kPart; ++c) x[c] = fmaf(x[c], scale_log2, wp[-c0 - c]);
+                        }
                     }
-                } else if (j == my_block) {  // diagonal block: keys after the query token are masked
+                    if constexpr (kFine) {
+                        if (fq != 3) {  // a 32-token key half this row does not hold
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        if (c > (tid & 63)) x[c] = -INFINITY;
+                            for (int c = 0; c < kPart; ++c)
+                                if (!((fq >> ((c0 + c) >> 5)) & 1)) x[c] = -INFINITY;
+                        }
+                        if (j >= qa) {  // near the diagonal: keys after the query token are masked
+                            const int lim = (qa - j) * kBlock + row_in - c0;  // key 64j + c > query 64qa + row_in
+#pragma unroll
+                            for (int c = 0; c < kPart; ++c)
+                                if (c > lim) x[c] = -INFINITY;
+                        }
+                    } else if (j == my_block) {  // diagonal block: keys after the query token are masked
+#pragma unroll
+                        for (int c = 0; c < kPart; ++c)
+                            if (c > (tid & 63) - c0) x[c] = -INFINITY;
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll
+                for (int part = 0; part < 64 / kPart; ++part) {
+                    load_scores(part, false);
+                    if constexpr (kBias && kOneS) {
+                        if (part == 0 && wp != nullptr) {
+                            uint32_t sr[32];
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(x[c]);
+                            __syncwarp();
+                            tmem_st32(s_addr, sr);
+                        }
+                    }
+                    float m[(kPart + 2) / 3];
+#pragma unroll
+                    for (int t = 0; t < kPart / 3; ++t) m[t] = max3f(x[3 * t], x[3 * t + 1], x[3 * t + 2]);
+                    if constexpr (kPart == 64) {
+                        m[21] = x[63];
+                        const float m7a = max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]),
+                                                max3f(m[6], m[7], m[8]));
+                        const float m7b = max3f(max3f(m[9], m[10], m[11]), max3f(m[12], m[13], m[14]),
+                                                max3f(m[15], m[16], m[17]));
+                        mx = max3f(m7a, m7b, max3f(m[18], m[19], fmaxf(m[20], m[21])));
+                    } else {
+                        m[10] = fmaxf(x[30], x[31]);
+                        mx = fmaxf(mx, max3f(max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]),
+                                                   max3f(m[6], m[7], m[8])),
+                                             m[9], m[10]));
+                    }
                 }
-                float m21[22];
-#pragma unroll
-                for (int t = 0; t < 21; ++t) m21[t] = max3f(x[3 * t], x[3 * t + 1], x[3 * t + 2]);
-                m21[21] = x[63];
-                const float m7a = max3f(max3f(m21[0], m21[1], m21[2]), max3f(m21[3], m21[4], m21[5]),
-                                        max3f(m21[6], m21[7], m21[8]));
-                const float m7b = max3f(max3f(m21[9], m21[10], m21[11]), max3f(m21[12], m21[13], m21[14]),
-                                        max3f(m21[15], m21[16], m21[17]));
-                float mx = max3f(m7a, m7b, max3f(m21[18], m21[19], fmaxf(m21[20], m21[21])));
                 if constexpr (kBias) mx = fmaf(mx, cc1, off);
                 else mx *= scale_log2;
+                if (kOneS && !o_done()) { ok = false; break; }
                 const bool grow = mx > m_used + rescale_log2<kBF16>();
                 if (__any_sync(0xffffffffu, grow)) {
                     const float alpha = !grow ? 1.f : (m_used == -INFINITY ? 0.f : ex2_approx(m_used - mx));
                     if (u > 0) {
-                        // O must be quiescent: PV(u-1) has completed
-                        const bool done = mbar_wait(BAR_O_DONE((u - 1) & 1), ((u - 1) >> 1) & 1, flags);
-                        if (__any_sync(0xffffffffu, !done)) { ok = false; break; }
+                        if (!kOneS && !o_done()) { ok = false; break; }
                         tc_fence_after();
                         __syncwarp();
 #pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tmem + t_lane + L::kOCol + c, o);
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tmem + t_lane + L::kOCol + c, o);
 #pragma unroll
-                            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * alpha);
-                            tmem_st32(tmem + t_lane + L::kOCol + c, o);
+                            for (int t = 0; t < 16; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * alpha);
+                            tmem_st16(tmem + t_lane + L::kOCol + c, o);
                         }
                     }
                     if (grow) {
@@ -742,22 +818,35 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                     float ls[4] = {0.f, 0.f, 0.f, 0.f};
                     [[maybe_unused]] uint64_t le = f2_pack(0.f, 0.f);
 #pragma unroll
-                    for (int t = 0; t < 32; ++t) {
-                        float e0, e1;
-                        f2_unpack(f2_fma(f2_pack(x[2 * t], x[2 * t + 1]), cc, nm), e0, e1);
-                        const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
-                        if constexpr (kBF16) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-                            pw[t] = *reinterpret_cast<const uint32_t *>(&h);
-                        } else {
-                            const __half2 h = __floats2half2_rn(p0, p1);
-                            pw[t] = *reinterpret_cast<const uint32_t *>(&h);
+                    for (int part = 64 / kPart - 1; part >= 0; --part) {  // the last one is still here
+                        if (part < 64 / kPart - 1) load_scores(part, true);
+                        if constexpr (kOneS) {
+                            if (part == 0) {
+                                tc_fence_before();
+                                mbar_arrive(bar_s_read);
+                            }
                         }
-                        // The denominator sums the rounded P that the PV product uses, so a row
-                        // dominated by one key normalizes exactly.
-                        add_half<kBF16, false>(ls[(t & 1) * 2], pw[t]);
-                        add_half<kBF16, true>(ls[(t & 1) * 2 + 1], pw[t]);
-                        if constexpr (kExact) le = f2_add(le, f2_pack(p0, p1));
+                        uint32_t pw[kPart / 2];
+#pragma unroll
+                        for (int t = 0; t < kPart / 2; ++t) {
+                            float e0, e1;
+                            f2_unpack(f2_fma(f2_pack(x[2 * t], x[2 * t + 1]), cc, nm), e0, e1);
+                            const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+                            if constexpr (kBF16) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                                pw[t] = *reinterpret_cast<const uint32_t *>(&h);
+                            } else {
+                                const __half2 h = __floats2half2_rn(p0, p1);
+                                pw[t] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                            // The denominator sums the rounded P that the PV product uses, so a row
+                            // dominated by one key normalizes exactly.
+                            add_half<kBF16, false>(ls[(t & 1) * 2], pw[t]);
+                            add_half<kBF16, true>(ls[(t & 1) * 2 + 1], pw[t]);
+                            if constexpr (kExact) le = f2_add(le, f2_pack(p0, p1));
+                        }
+                        __syncwarp();
+                        store_p(part, pw);
                     }
                     l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                     if constexpr (kExact) {
@@ -771,11 +860,14 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 if (kDiff && lse_out) weigh(std::bool_constant<kDiff>{});
                 else weigh(std::false_type{});
             } else {
+                if constexpr (kOneS) {
+                    mbar_arrive(bar_s_read);
+                    if (!o_done()) { ok = false; break; }
+                }
+                const uint32_t pw[kPart / 2] = {};
 #pragma unroll
-                for (int t = 0; t < 32; ++t) pw[t] = 0u;
+                for (int part = 0; part < 64 / kPart; ++part) store_p(part, pw);
             }
-            __syncwarp();
-            tmem_st32(s_addr, pw);  // P_u over the first 32 columns of S_u
             tc_fence_before();
             mbar_arrive(BAR_P_FULL(u & 1));
         }
@@ -926,7 +1018,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     }
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, L::kTmemCols);
+        free_tmem();
     }
 }
 

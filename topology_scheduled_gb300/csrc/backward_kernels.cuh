@@ -586,7 +586,9 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         }
         int u = 0;
         for (; ok; ++u) {
-            if (!mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags)) { ok = false; break; }
+            // (all lanes together: one whose wait ran out must not leave the others to a warp-wide step)
+            const bool there = mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags);
+            if (!__all_sync(0xffffffffu, there)) { ok = false; break; }
             const int j = meta_j[u % kMetaRing];
             const int fl = meta_f[u % kMetaRing];
             if (j < 0) break;
@@ -1156,13 +1158,16 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         [[maybe_unused]] const int wlane = tid & 31;
         int u = 0;
         for (; ok; ++u) {
-            if (!mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags)) { ok = false; break; }
+            // (all lanes together: one whose wait ran out must not leave the others to a warp-wide step)
+            const bool there = mbar_wait(BAR_S_FULL(u & 1), (u >> 1) & 1, flags);
+            if (!__all_sync(0xffffffffu, there)) { ok = false; break; }
             const int i = meta_j[u % kMetaRing];
             const int fl = meta_f[u % kMetaRing];
             if (i < 0) break;
             const int s = u % L::kRing;
             // the step's log-sum-exp and Delta rows arrived with its Q and dO blocks
-            if (!mbar_wait(BAR_FULL(s), (u / L::kRing) & 1, flags)) { ok = false; break; }
+            const bool rows_there = mbar_wait(BAR_FULL(s), (u / L::kRing) & 1, flags);
+            if (!__all_sync(0xffffffffu, rows_there)) { ok = false; break; }
             tc_fence_after();
             const bool in_col = row_exists && ((fl >> half) & 1);  // warp-uniform
             const uint32_t s_at = tmem + t_lane + (kDiff ? diff_slot(u, 0) : s_col(u & 1)) + col0;

@@ -28,8 +28,9 @@ bool encode_3d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t lanes, uin
 bool overlaps(const void *a, size_t na, const void *b, size_t nb);
 
 // Dynamic shared memory of the attention kernel.  The D = 128 figure is the largest size at
-// which two CTAs fit on one SM (2 x (115712 + 1024 reserved) = 228 KB); it covers the
-// 114816 bytes of tiles and barriers plus 896 bytes of alignment slack.
+// which two CTAs fit on one SM (2 x (115712 + 1024 reserved) = 228 KB), the D = 64 one lets three
+// (3 x (66688 + 1024)); both cover the tiles, barriers and biases plus at least 512 bytes of
+// alignment slack.
 template <int D>
 __host__ __device__ constexpr int kAttnSmemBytes() {
     return D == 128 ? 115712 : 66688;
