@@ -1025,9 +1025,8 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
 template <int D, bool kBF16, int kGran, class Terms>
 tsa_status launch_one(const AttnLaunch &a, const Terms &terms) {
     auto kern = scheduled_attention_kernel<D, kBF16, kGran, Terms>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmemBytes<D>()) !=
-        cudaSuccess)
-        return TSA_ERR_CUDA;
+    static std::atomic<unsigned long long> ready{0};
+    if (!allow_smem(ready, reinterpret_cast<const void *>(kern), kAttnSmemBytes<D>())) return TSA_ERR_CUDA;
     const int tiles = Terms::kDiff ? a.nb : (a.nb + 1) / 2;
     dim3 grid((unsigned)tiles, (unsigned)a.lanes);
     kern<<<grid, kThreads, kAttnSmemBytes<D>(), a.stream>>>(*a.tmQ, *a.tmK, *a.tmV, *a.tmO, *a.tmO2, a.row_ptr,

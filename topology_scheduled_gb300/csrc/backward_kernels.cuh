@@ -1351,8 +1351,9 @@ tsa_status launch_grad_kernels(const BwdLaunch &a, const Terms &terms) {
     auto kq = bwd_dq_kernel<D, kBF16, Terms>;
     auto kkv = bwd_dkv_kernel<D, kBF16, Terms>;
     constexpr int kDqBytes = DqSmem<D, Terms>::kBytes, kDkvBytes = DkvSmem<D, Terms>::kBytes;
-    if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, kDkvBytes) != cudaSuccess)
+    static std::atomic<unsigned long long> q_ready{0}, kv_ready{0};
+    if (!allow_smem(q_ready, reinterpret_cast<const void *>(kq), kDqBytes) ||
+        !allow_smem(kv_ready, reinterpret_cast<const void *>(kkv), kDkvBytes))
         return TSA_ERR_CUDA;
     const unsigned tiles = (unsigned)((a.nb + 1) / 2);
     const dim3 grid((unsigned)a.lanes, tiles);

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "score_terms.cuh"
 #include "tsa.h"
 #include "tsa_device.cuh"
@@ -26,6 +28,18 @@ bool encode_2d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t rows, uint
 bool encode_3d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t lanes, uint64_t rows, uint64_t cols,
                uint32_t box_rows);
 bool overlaps(const void *a, size_t na, const void *b, size_t nb);
+
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device.  `done` (one per kernel and
+// size) keeps a bit per device, so only the first call asks the driver, which takes about a microsecond.
+inline bool allow_smem(std::atomic<unsigned long long> &done, const void *kernel, int bytes) {
+    int dev;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 // Dynamic shared memory of the attention kernel.  The D = 128 figure is the largest size at
 // which two CTAs fit on one SM (2 x (115712 + 1024 reserved) = 228 KB), the D = 64 one lets three
