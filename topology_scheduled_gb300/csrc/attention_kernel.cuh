@@ -13,9 +13,9 @@
 //    tiles of each visited block into two-stage rings of their own (128-byte swizzle), polling
 //    both rings so that neither stream waits behind the other.  Warp 5 issues the MMAs from
 //    one thread: S = Q K^T (M128 N64 K=D, both operands in shared memory) into a TMEM S buffer
-//    (of two at D = 128), and O += P V (M128 N=D K64) with P read from TMEM.  Warps 0-3 run the
+//    (one of two; kThree: the only one), and O += P V (M128 N=D K64) with P read from TMEM.  Warps 0-3 run the
 //    online softmax, one row per thread: tcgen05.ld of the S row, exp2 with the scale folded in,
-//    the new P written in the input dtype with tcgen05.st (over S at D = 128).
+//    the new P written in the input dtype with tcgen05.st (over S; kThree: beside it).
 //  * Pipeline.  The MMA warp issues QK(u+1) before PV(u), so the tensor core computes the next
 //    scores while the softmax warps work on the current ones.  K and V have rings of their
 //    own: a K stage is refilled as soon as its QK is done, so the next key tile is already
@@ -33,15 +33,15 @@
 //    weigh: the block is visited only as the diagonal block of the last row, where the causal
 //    mask already drops keys after the query token.  Its query rows past S are computed and
 //    dropped: the block's output is written row by row for the rows that exist.
-//  * CTAs share an SM, so one CTA's softmax also overlaps the others' MMAs: two at D = 128, where the
-//    tiles fill the shared memory, three at D = 64.  Three leave 96 registers per thread and 170 TMEM
-//    columns per CTA.  So at D = 64 a softmax thread takes its 64 scores in two parts of 32, the first
-//    one read twice (for the maximum and for the weights, its biases and mask stored back in between),
-//    and there is one S buffer (64 columns), O (64) and P in 32 columns of its own: the next scores are
-//    computed once the softmax warps have read S, and P is written once the product that read the last
-//    one is done.  Measured, 64 heads of 8192 tokens, 13 blocks a row: 160 us, against 170 us with two
-//    CTAs, two S buffers and 64 scores at once (3 CTAs: biased 184 against 189, differential 299
-//    against 326).  One S buffer with P over it, which would need no P columns, took 178 us.
+//  * Two CTAs share an SM, so one CTA's softmax also overlaps the other's MMAs.
+//  * Three CTAs per SM (kThree: D = 64, many tiles of short rows).  Two leave half of the issue slots
+//    empty there, and D = 64 tiles leave room for a third, with 96 registers per thread and 170 TMEM
+//    columns per CTA.  So a softmax thread takes its 64 scores in two parts of 32, the first one read
+//    twice (for the maximum and for the weights, its biases and mask stored back in between), and there
+//    is one S buffer (64 columns), O (64) and P in 32 columns of its own: the next scores are computed
+//    once the softmax warps have read S, and P is written once the product that read the last one is
+//    done.  One S buffer with P over it, which needs no P columns, lost (64 heads of 8192 tokens, 26
+//    blocks a row: 178 us; with P columns 160 us; two CTAs 170 us).
 //
 // The same kernel carries the score terms of score_terms.cuh:
 //  * Bias by buckets of the distance q - k.  Far enough from the diagonal all keys of a step lie in the
@@ -86,7 +86,8 @@ constexpr int kMmaWarp = 5;
 template <bool kBF16>
 __device__ __forceinline__ constexpr float rescale_log2() { return kBF16 ? 30.0f : 15.0f; }
 
-template <int D>
+// kThree: the layout for three CTAs per SM (D = 64)
+template <int D, bool kThree>
 struct AttnSmem {
     static constexpr int kD = D;
     static constexpr int kChunks = D / 64;            // 64-element (128 B) column chunks
@@ -100,7 +101,7 @@ struct AttnSmem {
     static constexpr int kOffTable = kOffMeta + kMetaBytes;           // BucketTable (bias only)
     static constexpr int kOffWin = kOffTable + kBucketTableBytes;     // 4 windows (bias only)
     static constexpr int kEnd = kOffWin + 4 * kWindow * 4;
-    static constexpr bool kOneS = D == 64;
+    static constexpr bool kOneS = kThree;
     static constexpr int kCtas = kOneS ? 3 : 2;  // per SM, by shared memory (kOneS: and by TMEM)
     // S0 | S1 | O, P_b over the first 32 columns of S_b; or S | O, and P in 32 columns of its own
     static constexpr int kTmemCols = kOneS ? 128 : 256;
@@ -368,13 +369,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, float &sum) {
 
 // The layout leaves at least 512 bytes for aligning the dynamic shared-memory base to 1024
 // (the kernel checks the actual alignment and reports kDevSmemAlign if it does not fit).
-static_assert(AttnSmem<128>::kEnd + 512 <= kAttnSmemBytes<128>(), "smem");
-static_assert(AttnSmem<64>::kEnd + 512 <= kAttnSmemBytes<64>(), "smem");
+static_assert(AttnSmem<128, false>::kEnd + 512 <= kAttnSmemBytes<128>(), "smem");
+static_assert(AttnSmem<64, true>::kEnd + 512 <= kAttnSmemBytes<64>(), "smem");
 // the K ring holds the second map's fp32 output rows in the differential epilogue
-static_assert(2 * AttnSmem<128>::kKVBytes >= kBlock * 128 * 4 && 2 * AttnSmem<64>::kKVBytes >= kBlock * 64 * 4, "exchange");
+static_assert(2 * AttnSmem<128, false>::kKVBytes >= kBlock * 128 * 4 && 2 * AttnSmem<64, true>::kKVBytes >= kBlock * 64 * 4, "exchange");
 
-template <int D, bool kBF16, int kGran, class Terms>
-__global__ void __launch_bounds__(kThreads, AttnSmem<D>::kCtas)
+template <int D, bool kThree, bool kBF16, int kGran, class Terms>
+__global__ void __launch_bounds__(kThreads, AttnSmem<D, kThree>::kCtas)
 scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV,
@@ -385,7 +386,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                            float scale_log2, DeviceFlags flags, const __grid_constant__ Terms terms) {
     constexpr bool kBias = Terms::kBias, kDiff = Terms::kDiff;
     constexpr bool kFine = kGran == 2;  // 32-token blocks: masks per (query quarter, key half)
-    using L = AttnSmem<D>;
+    using L = AttnSmem<D, kThree>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
 
     const uint32_t raw_base = smem_u32(smem_raw);
@@ -1022,9 +1023,9 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     }
 }
 
-template <int D, bool kBF16, int kGran, class Terms>
+template <int D, bool kThree, bool kBF16, int kGran, class Terms>
 tsa_status launch_one(const AttnLaunch &a, const Terms &terms) {
-    auto kern = scheduled_attention_kernel<D, kBF16, kGran, Terms>;
+    auto kern = scheduled_attention_kernel<D, kThree, kBF16, kGran, Terms>;
     static std::atomic<unsigned long long> ready{0};
     if (!allow_smem(ready, reinterpret_cast<const void *>(kern), kAttnSmemBytes<D>())) return TSA_ERR_CUDA;
     const int tiles = Terms::kDiff ? a.nb : (a.nb + 1) / 2;
@@ -1037,10 +1038,22 @@ tsa_status launch_one(const AttnLaunch &a, const Terms &terms) {
 
 template <int kGran, class Terms>
 tsa_status launch_gran(const AttnLaunch &a, const Terms &terms) {
-    if (a.D == 64)
-        return a.bf16 ? launch_one<64, true, kGran>(a, terms) : launch_one<64, false, kGran>(a, terms);
+    if (a.D == 64) {
+        if constexpr (Terms::kBias || Terms::kDiff) {
+            // Three CTAs per SM for many tiles of short rows.  64 heads of 8192 tokens, 15 blocks a row:
+            // biased 109 us with two, 102 with three, differential 184 and 164.  With a tile or two per SM
+            // the longer step of one CTA shows (16 tiles, rows of up to 32 blocks: 21 and 28 us; 1024 tiles
+            // of short rows: 31.6 and 31.8), and with long rows the last, longest tiles (64 heads of 8192
+            // tokens, dense: biased 671 and 712).  The plain calls do not know their rows' lengths.
+            const long long tiles = (long long)(Terms::kDiff ? a.nb : (a.nb + 1) / 2) * a.lanes;
+            const long long blocks = a.gran == 1 ? 4ll * a.nnz_cap : a.gran == 2 ? a.nnz_cap / 4 : a.nnz_cap;  // of 64 tokens
+            if (tiles > 1024 && blocks <= 16ll * a.nb)
+                return a.bf16 ? launch_one<64, true, true, kGran>(a, terms) : launch_one<64, true, false, kGran>(a, terms);
+        }
+        return a.bf16 ? launch_one<64, false, true, kGran>(a, terms) : launch_one<64, false, false, kGran>(a, terms);
+    }
     if (a.D == 128)
-        return a.bf16 ? launch_one<128, true, kGran>(a, terms) : launch_one<128, false, kGran>(a, terms);
+        return a.bf16 ? launch_one<128, false, true, kGran>(a, terms) : launch_one<128, false, false, kGran>(a, terms);
     return TSA_ERR_UNSUPPORTED;
 }
 
