@@ -17,16 +17,17 @@
 //     its first entry that is out of order or out of [0, i], and the status word reports it).
 //   bwd_delta -- Delta per query row from the stored O and dO.
 //   bwd_dq_kernel -- one CTA per pair of query blocks (M = 128), walking the union of the two
-//     CSR rows like the forward: S = Q K^T and dP = dO V^T into TMEM, dS formed by the four
+//     CSR rows like the forward: S = Q K^T and dP = dO V^T into TMEM, dS formed by the
 //     elementwise warps and written back over S in the input dtype, dQ += dS K with dS read
 //     from TMEM.
 //   bwd_dkv_kernel -- one CTA per pair of key blocks (M = 128), walking the union of the two
 //     transposed columns: S^T = K Q^T and dP^T = V dO^T into TMEM, P^T and dS^T written back
 //     over them, dV += P^T dO and dK += dS^T Q.
-// Warp roles are those of the forward: warp 4 produces (TMA), warp 5 issues the MMAs from one
-// thread (the next step's products before the current step's accumulation), warps 0-3 do the
-// elementwise work, one TMEM lane (row) per thread.  Every wait is bounded; on a timeout a CTA
-// records TSA_ERR_TIMEOUT, drains what it issued, frees its TMEM and returns.
+// Warp roles are those of the forward: one warp produces (TMA, rings of four blocks), one issues the
+// MMAs from one thread (the next step's products before the current step's accumulation), and eight do
+// the elementwise work, two per 32 rows with 32 columns of a step each (no value of a row is needed by
+// the other).  Every wait is bounded; on a timeout a CTA records TSA_ERR_TIMEOUT, drains what it
+// issued, frees its TMEM and returns.
 #include "backward_kernels.cuh"
 
 namespace tsa {

@@ -7,8 +7,8 @@
 // 4 D multiply-adds (6 D with two maps), so the arithmetic stays on the FMA pipe.
 //  * A lane of a warp holds 8 of the D dimensions, so D / 8 lanes read a row with one 16-byte load
 //    each and a warp reads 2 (D = 128) or 4 rows per load.  A warp takes a chunk of 8 such loads of K
-//    and 8 of V at a time; the next chunk's K is loaded while this one's V is used, so that 4 KB or
-//    8 KB are in flight per warp at any time, with the 16 warps that fit an SM.
+//    and 8 of V at a time (two maps: 4, to keep both sums in registers with 24 warps on an SM); the next
+//    chunk's K is loaded while this one's V is used, so that 2 to 8 KB are in flight per warp at any time.
 //  * Every group of D / 8 lanes keeps its own running maximum, denominator and 8 sums, in binary32;
 //    the weights are never rounded.  They are joined at the end: groups by shuffles, warps through
 //    shared memory, thread blocks through the shared memory of their cluster.
@@ -18,6 +18,8 @@
 //  * A bias is one constant for a chunk beyond the last bucket's start; otherwise each lane finds the
 //    bucket of one of the chunk's keys and the groups take theirs by a shuffle.
 // Keys at len and beyond are neither read nor counted, so what the cache holds there does not matter.
+// Measured, 16 sequences of 8192 tokens, 32 heads, D = 128, bf16, all blocks listed (2.15 GB): biased 322 us
+// = 6.7 TB/s, differential 339 us = 6.3 TB/s, of 6.8 TB/s that a copy reaches.
 #include <climits>
 #include <type_traits>
 
