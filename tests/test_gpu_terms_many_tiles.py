@@ -1,5 +1,5 @@
-"""The forward of short rows in many tiles, which runs three thread blocks per SM at D = 64: a few of
-its heads against the 64-bit forms, and the rest against calls of few heads."""
+"""Forwards of more than 1024 tiles at D = 64 (differential: three thread blocks per SM): a few of their
+heads against the 64-bit forms."""
 import numpy as np
 import pytest
 import torch
@@ -15,7 +15,7 @@ LOW = torch.finfo(torch.bfloat16).min
 
 
 def _many(S, block):
-    """Heads that make more than 1024 tiles of two 64-token blocks."""
+    """Heads that make more than 1024 tiles, of two 64-token blocks even."""
     return 1024 // ((-(-S // 64) + 1) // 2) + 2
 
 
@@ -53,7 +53,6 @@ def test_biased(S, dtype, block, kind, starts):
     q, k, v, bias, _ = _inputs(H, S, dtype, S, len(starts))
     bias[0, ::3], bias[H - 1, -1] = LOW, -float("inf")
     rp, ci = _csr(kind, S, block, seed=1)
-    assert len(ci) <= 16 * -(-S // 64)
     args = [x.to(DEV) for x in (q, k, v)]
     rpd, cid = _dev(rp, ci)
     rows = 64  # rows behind the last lane stay as they were

@@ -149,3 +149,15 @@ def test_workspace_bytes():
                     (1 << 40, 1 << 30, 64, 1), (1, 1 << 40, 64, 1), (65535, 1 << 16, 64, 1)):
             assert f(*bad) == 0
     assert L.tsa_biased_attention_backward_workspace_bytes(1, 64, 64, 1, 257) == 0
+
+
+@pytest.mark.parametrize("which", ["biased", "differential"])
+def test_outputs_keep_off_the_schedule(which):
+    """(The arrays of a schedule are inputs like any other.)"""
+    at = F + 40 * M
+    first = _biased if which == "biased" else _diff
+    assert first(O=at, row_ptr=at) == 1 and first(O=at, col_idx=at + 16) == 1
+    for change in (dict(dQ=at, row_ptr=at + 4), dict(ws=at, col_idx=at + 64), dict(dV=at, col_idx=at)):
+        assert _back(which, **change) == 1, change
+    for change in (dict(O=at, row_ptr=at), dict(O=at, lens=at + 4), dict(O=at, col_idx=at)):
+        assert _decode(which, **change) == 1, change

@@ -6,6 +6,10 @@ tsa_scheduled_attention_backward (blocks of 64 or 128 tokens).  The CSR is not d
 
 ``biased_attention`` and ``differential_attention`` do the same for the attentions with learned
 score terms; their learned inputs get gradients as well.
+
+Capturing a backward pass into a CUDA graph: PyTorch's accumulation nodes keep the stream they were
+made on, so the captured pass needs leaves of its own (or torch.autograd.grad, which accumulates
+nothing) while an eager graph of the same leaves is alive.
 """
 from __future__ import annotations
 

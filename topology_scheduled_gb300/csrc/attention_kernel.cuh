@@ -12,10 +12,10 @@
 //  * Warp roles (192 threads).  Warp 4 produces: one thread TMA-loads Q once and the K and V
 //    tiles of each visited block into two-stage rings of their own (128-byte swizzle), polling
 //    both rings so that neither stream waits behind the other.  Warp 5 issues the MMAs from
-//    one thread: S = Q K^T (M128 N64 K=D, both operands in shared memory) into a TMEM S buffer
-//    (one of two; kThree: the only one), and O += P V (M128 N=D K64) with P read from TMEM.  Warps 0-3 run the
-//    online softmax, one row per thread: tcgen05.ld of the S row, exp2 with the scale folded in,
-//    the new P written in the input dtype with tcgen05.st (over S; kThree: beside it).
+//    one thread: S = Q K^T (M128 N64 K=D, both operands in shared memory) into one of two TMEM
+//    S buffers, and O += P V (M128 N=D K64) with P read from TMEM.  Warps 0-3 run the online
+//    softmax, one row per thread: tcgen05.ld of the S row, exp2 with the scale folded in, the
+//    new P written back over the S buffer in the input dtype with tcgen05.st.
 //  * Pipeline.  The MMA warp issues QK(u+1) before PV(u), so the tensor core computes the next
 //    scores while the softmax warps work on the current ones.  K and V have rings of their
 //    own: a K stage is refilled as soon as its QK is done, so the next key tile is already
@@ -34,22 +34,15 @@
 //    mask already drops keys after the query token.  Its query rows past S are computed and
 //    dropped: the block's output is written row by row for the rows that exist.
 //  * Two CTAs share an SM, so one CTA's softmax also overlaps the other's MMAs.
-//  * Three CTAs per SM (kThree: D = 64, many tiles of short rows).  Two leave half of the issue slots
-//    empty there, and D = 64 tiles leave room for a third, with 96 registers per thread and 170 TMEM
-//    columns per CTA.  So a softmax thread takes its 64 scores in two parts of 32, the first one read
-//    twice (for the maximum and for the weights, its biases and mask stored back in between), and there
-//    is one S buffer (64 columns), O (64) and P in 32 columns of its own: the next scores are computed
-//    once the softmax warps have read S, and P is written once the product that read the last one is
-//    done.  One S buffer with P over it, which needs no P columns, lost (64 heads of 8192 tokens, 26
-//    blocks a row: 178 us; with P columns 160 us; two CTAs 170 us).
 //
 // The same kernel carries the score terms of score_terms.cuh:
 //  * Bias by buckets of the distance q - k.  Far enough from the diagonal all keys of a step lie in the
 //    open last bucket for all rows of a warp, and then the bias is one constant, folded into the FMA
-//    that subtracts the row maximum: such a step costs what a plain one does.  Otherwise every thread reads its 64 biases from a table by
-//    distance in shared memory, lane by lane consecutive addresses (no bank conflicts), one FMA per
-//    score.  The softmax warps fill the table (the first 2048 distances at most) while the first
-//    tiles are on their way; beyond it a warp lays out the 95 distances of its step.
+//    that subtracts the row maximum: such a step costs what a plain one does.  Otherwise every thread
+//    reads its 64 biases from a table by distance in shared memory, lane by lane consecutive addresses
+//    (no bank conflicts), one FMA per score.  The softmax warps fill the table (the first 2048 distances
+//    at most) while the first tiles are on their way; beyond it a warp lays out the 95 distances of its
+//    step.
 //  * Differential attention.  A CTA takes one query block and both maps: rows 0-63 of the tile are
 //    the block's first map, rows 64-127 its second.  With Q laid out block-diagonally
 //    ([q1 0; 0 q2], zeros written by the softmax warps) the product with the unsplit K rows gives
@@ -57,6 +50,15 @@
 //    what a plain one of the same D does and no row union is needed.  The zeros double the score
 //    product's multiplications, but a 64-row product would run at half the rate: the tensor time
 //    is the same.  The epilogue subtracts the lower rows from the upper through shared memory.
+//    At D = 64 and many tiles three CTAs share an SM (kThree), as two leave half of the issue slots empty.
+//    Three leave 96 registers per thread and 128 TMEM columns per CTA (one allocation, so that no CTA
+//    waits for columns while it holds some).  So a softmax thread takes its 64 scores in two parts of
+//    32, the first one read twice (for the maximum and for the weights); there is one S buffer beside
+//    O, the next scores are computed once the softmax warps have read S, and P goes through 16 KB of
+//    shared memory, written once the product that read the last one is done.  64 heads of 8192 tokens:
+//    184 -> 163 us.  P over the one S buffer, which makes every step run in series, lost (26 blocks a row:
+//    338 us against 326 with two CTAs), and a bias gains nothing (108 us either way), as the steps near
+//    the diagonal then add it twice.
 // Measured at [1, 32, 32768, 128] bf16, 14.5 blocks a row: plain 0.42 ms (1190 TFLOP/s on visited blocks),
 // biased 0.45 ms, differential 0.85 ms, 0.90 ms with what its backward needs (twice the tiles: 1100
 // TFLOP/s executed).  Bound by the softmax warps' chain of a step beside a tensor pipe that is active for
@@ -90,7 +92,7 @@ constexpr int kMmaWarp = 5;
 template <bool kBF16>
 __device__ __forceinline__ constexpr float rescale_log2() { return kBF16 ? 30.0f : 15.0f; }
 
-// kThree: the layout for three CTAs per SM (D = 64)
+// kThree: the layout for three CTAs per SM (differential, D = 64)
 template <int D, bool kThree>
 struct AttnSmem {
     static constexpr int kD = D;
@@ -100,16 +102,23 @@ struct AttnSmem {
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + kQBytes;                // kKStages tiles
     static constexpr int kOffV = kOffK + kKStages * kKVBytes;    // kVStages tiles
-    static constexpr int kOffMeta = kOffV + kVStages * kKVBytes;
+    static constexpr int kOffP = kOffV + kVStages * kKVBytes;    // kOneS: a step's P
+    static constexpr int kOffMeta = kOffP + (kThree ? kRows * kBlock * 2 : 0);
     static constexpr int kMetaBytes = 256;
     static constexpr int kOffTable = kOffMeta + kMetaBytes;           // BucketTable (bias only)
     static constexpr int kOffWin = kOffTable + kBucketTableBytes;     // 4 windows (bias only)
-    static constexpr int kEnd = kOffWin + 4 * kWindow * 4;
+    static constexpr int kEnd = kThree ? kOffTable : kOffWin + 4 * kWindow * 4;
+    // With the 1 KB that each CTA reserves, 228 KB hold two (D = 128) or three of these; at least 512
+    // bytes are left for aligning the dynamic shared-memory base to 1024 (the kernel checks the actual
+    // alignment and reports kDevSmemAlign if it does not fit).
+    static constexpr int kBytes = D == 128 ? 115712 : 66688;
+    static_assert(kEnd + 512 <= kBytes, "smem");
+    // the K ring holds the second map's fp32 output rows in the differential epilogue
+    static_assert(kKStages * kKVBytes >= kBlock * D * 4, "exchange");
     static constexpr bool kOneS = kThree;
-    static constexpr int kCtas = kOneS ? 3 : 2;  // per SM, by shared memory (kOneS: and by TMEM)
-    // S0 | S1 | O, P_b over the first 32 columns of S_b; or S | O, and P in 32 columns of its own
+    static constexpr int kCtas = kOneS ? 3 : 2;  // per SM
+    // S0 | S1 | O, P_b over the first 32 columns of S_b; or S | O, and P in shared memory
     static constexpr int kTmemCols = kOneS ? 128 : 256;
-    static constexpr int kPCols = 32;
     static constexpr int kOCol = kOneS ? 64 : 128;
 
     static constexpr int kPart = kOneS ? 32 : 64;  // keys of a step that a softmax thread holds at a time
@@ -133,8 +142,8 @@ constexpr int kBarODone = kBarPFull + 16;
 constexpr int kBarFin = kBarODone + 16;               // (o_done: 2 x 8)
 constexpr int kBarQDiag = kBarFin + 8;  // Q is block-diagonal (differential attention)
 constexpr int kBarSRead = kBarQDiag + 8;  // the softmax warps have read S (one buffer)
-constexpr int kTmemSlot = kBarSRead + 8;  // and the one of P
-constexpr int kAbortFlag = kTmemSlot + 8;
+constexpr int kTmemSlot = kBarSRead + 8;
+constexpr int kAbortFlag = kTmemSlot + 4;
 constexpr int kMetaJ = kAbortFlag + 4;                // kMetaRing x 4
 constexpr int kMetaF = kMetaJ + 4 * kMetaRing;        // kMetaRing x 4
 static_assert(kMetaF + 4 * kMetaRing <= 256, "meta area");
@@ -371,13 +380,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, float &sum) {
     }
 }
 
-// The layout leaves at least 512 bytes for aligning the dynamic shared-memory base to 1024
-// (the kernel checks the actual alignment and reports kDevSmemAlign if it does not fit).
-static_assert(AttnSmem<128, false>::kEnd + 512 <= kAttnSmemBytes<128>(), "smem");
-static_assert(AttnSmem<64, true>::kEnd + 512 <= kAttnSmemBytes<64>(), "smem");
-// the K ring holds the second map's fp32 output rows in the differential epilogue
-static_assert(2 * AttnSmem<128, false>::kKVBytes >= kBlock * 128 * 4 && 2 * AttnSmem<64, true>::kKVBytes >= kBlock * 64 * 4, "exchange");
-
 template <int D, bool kThree, bool kBF16, int kGran, class Terms>
 __global__ void __launch_bounds__(kThreads, AttnSmem<D, kThree>::kCtas)
 scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -396,7 +398,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
     constexpr uint32_t kUsed = kBias ? L::kEnd : L::kOffMeta + L::kMetaBytes;
-    if (base - raw_base + kUsed > (uint32_t)kAttnSmemBytes<D>()) {
+    if (base - raw_base + kUsed > (uint32_t)L::kBytes) {
         if (threadIdx.x == 0) raise_status(flags, kDevSmemAlign);
         return;
     }
@@ -461,9 +463,6 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         fence_proxy_async_smem();
     }
     if (warp == kMmaWarp) {
-        // The small piece first: with at most three CTAs of this kernel on an SM, each holding 32 of the
-        // 512 columns, a gap of 128 always remains, so the second call waits for no CTA that waits.
-        if constexpr (L::kOneS) tmem_alloc(meta + kTmemSlot + 4, L::kPCols);
         tmem_alloc(meta + kTmemSlot, L::kTmemCols);
         tmem_relinquish();
     }
@@ -471,14 +470,9 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     const bool leave = __syncthreads_or(gave_up);
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kOffMeta + kTmemSlot);
-    [[maybe_unused]] const uint32_t tmem_p = *reinterpret_cast<volatile uint32_t *>(smem + L::kOffMeta + kTmemSlot + 4);
-    auto free_tmem = [&] {
-        tmem_dealloc(tmem, L::kTmemCols);
-        if constexpr (L::kOneS) tmem_dealloc(tmem_p, L::kPCols);
-    };
     if (leave) {  // nothing was issued yet: give the columns back and go
         if (tid == 0) raise_status(flags, kDevTimeout);  // a replayed launch that gave up once says so again
-        if (warp == kMmaWarp) free_tmem();
+        if (warp == kMmaWarp) tmem_dealloc(tmem, L::kTmemCols);
         return;
     }
 
@@ -573,6 +567,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
             constexpr uint32_t kIdescPV = idesc_f16(kBF16, 128, D, true);
             const uint64_t q_desc = sdesc_sw128(sQ, 16, 1024), k_desc = sdesc_sw128(sK0, 16, 1024),
                            v_desc = sdesc_sw128(sV0, 8192, 1024);
+            [[maybe_unused]] const uint64_t p_desc = sdesc_sw128(base + L::kOffP, 16, 1024);
             bool ok = mbar_wait(bar_q, 0, flags);
             if constexpr (kDiff) ok = ok && mbar_wait(bar_q_diag, 0, flags);
             int u = 0;
@@ -630,8 +625,11 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const uint64_t b = sdesc_at(v_desc, s * L::kKVBytes + kk * 2048);
-                    tc_mma_ts(tmem + L::kOCol, (L::kOneS ? tmem_p : tmem + L::s_col(u & 1)) + kk * 8, b, kIdescPV,
-                              (u > 0 || kk > 0) ? 1u : 0u);
+                    if constexpr (L::kOneS)
+                        tc_mma_ss(tmem + L::kOCol, sdesc_at(p_desc, kk * 32), b, kIdescPV, (u > 0 || kk > 0) ? 1u : 0u);
+                    else
+                        tc_mma_ts(tmem + L::kOCol, tmem + L::s_col(u & 1) + kk * 8, b, kIdescPV,
+                                  (u > 0 || kk > 0) ? 1u : 0u);
                 }
                 tc_commit(BAR_V_EMPTY(s));
                 tc_commit(BAR_O_DONE(u & 1));
@@ -696,7 +694,11 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
             const uint32_t s_addr = tmem + t_lane + L::s_col(u & 1);
             auto store_p = [&](int part, const uint32_t (&pw)[kPart / 2]) {
                 if constexpr (kPart == 64) tmem_st32(s_addr, pw);
-                else tmem_st16(tmem_p + t_lane + part * 16, pw);
+                else
+#pragma unroll
+                    for (int q = 0; q < kPart / 8; ++q)  // (rows of 128 bytes, their 16-byte units permuted by row & 7)
+                        st_shared_v4(base + L::kOffP + tid * 128 + (((part * 4 + q) ^ (tid & 7)) << 4), pw[4 * q],
+                                     pw[4 * q + 1], pw[4 * q + 2], pw[4 * q + 3]);
             };
             // PV(u - 1) has completed: O may be rescaled, and P of one buffer be written
             auto o_done = [&] {
@@ -719,7 +721,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                         cc1 = 1.f;
                     }
                 }
-                auto load_scores = [&](int part, bool again) {
+                auto load_scores = [&](int part) {
                     const int c0 = part * kPart;
                     if constexpr (kPart == 64) {
                         uint32_t sr[2][32];
@@ -734,7 +736,6 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                     }
                     if constexpr (kBias) {
                         if (wp != nullptr) {
-                            if (again) return;  // they came with their biases, masked
 #pragma unroll
                             for (int c = 0; c < kPart; ++c) x[c] = fmaf(x[c], scale_log2, wp[-c0 - c]);
                         }
@@ -760,16 +761,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 float mx = -INFINITY;
 #pragma unroll
                 for (int part = 0; part < 64 / kPart; ++part) {
-                    load_scores(part, false);
-                    if constexpr (kBias && kOneS) {
-                        if (part == 0 && wp != nullptr) {
-                            uint32_t sr[32];
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(x[c]);
-                            __syncwarp();
-                            tmem_st32(s_addr, sr);
-                        }
-                    }
+                    load_scores(part);
                     float m[(kPart + 2) / 3];
 #pragma unroll
                     for (int t = 0; t < kPart / 3; ++t) m[t] = max3f(x[3 * t], x[3 * t + 1], x[3 * t + 2]);
@@ -824,7 +816,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                     [[maybe_unused]] uint64_t le = f2_pack(0.f, 0.f);
 #pragma unroll
                     for (int part = 64 / kPart - 1; part >= 0; --part) {  // the last one is still here
-                        if (part < 64 / kPart - 1) load_scores(part, true);
+                        if (part < 64 / kPart - 1) load_scores(part);
                         if constexpr (kOneS) {
                             if (part == 0) {
                                 tc_fence_before();
@@ -873,6 +865,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
                 for (int part = 0; part < 64 / kPart; ++part) store_p(part, pw);
             }
+            if constexpr (kOneS) fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(BAR_P_FULL(u & 1));
         }
@@ -1023,7 +1016,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     }
     if (warp == kMmaWarp) {
         tc_fence_after();
-        free_tmem();
+        tmem_dealloc(tmem, L::kTmemCols);
     }
 }
 
@@ -1031,10 +1024,11 @@ template <int D, bool kThree, bool kBF16, int kGran, class Terms>
 tsa_status launch_one(const AttnLaunch &a, const Terms &terms) {
     auto kern = scheduled_attention_kernel<D, kThree, kBF16, kGran, Terms>;
     static std::atomic<unsigned long long> ready{0};
-    if (!allow_smem(ready, reinterpret_cast<const void *>(kern), kAttnSmemBytes<D>())) return TSA_ERR_CUDA;
+    constexpr int kBytes = AttnSmem<D, kThree>::kBytes;
+    if (!allow_smem(ready, reinterpret_cast<const void *>(kern), kBytes)) return TSA_ERR_CUDA;
     const int tiles = Terms::kDiff ? a.nb : (a.nb + 1) / 2;
     dim3 grid((unsigned)tiles, (unsigned)a.lanes);
-    kern<<<grid, kThreads, kAttnSmemBytes<D>(), a.stream>>>(*a.tmQ, *a.tmK, *a.tmV, *a.tmO, *a.tmO2, a.row_ptr,
+    kern<<<grid, kThreads, kBytes, a.stream>>>(*a.tmQ, *a.tmK, *a.tmV, *a.tmO, *a.tmO2, a.row_ptr,
                                                             a.col_idx, a.nnz_cap, a.O, a.lse, a.nb, a.S,
                                                             a.scale_log2, a.flags, terms);
     return cudaGetLastError() == cudaSuccess ? TSA_OK : TSA_ERR_CUDA;
@@ -1043,15 +1037,11 @@ tsa_status launch_one(const AttnLaunch &a, const Terms &terms) {
 template <int kGran, class Terms>
 tsa_status launch_gran(const AttnLaunch &a, const Terms &terms) {
     if (a.D == 64) {
-        if constexpr (Terms::kBias || Terms::kDiff) {
-            // Three CTAs per SM for many tiles of short rows.  64 heads of 8192 tokens, 15 blocks a row:
-            // biased 109 us with two, 102 with three, differential 184 and 164.  With a tile or two per SM
-            // the longer step of one CTA shows (16 tiles, rows of up to 32 blocks: 21 and 28 us; 1024 tiles
-            // of short rows: 31.6 and 31.8), and with long rows the last, longest tiles (64 heads of 8192
-            // tokens, dense: biased 671 and 712).  The plain calls do not know their rows' lengths.
-            const long long tiles = (long long)(Terms::kDiff ? a.nb : (a.nb + 1) / 2) * a.lanes;
-            const long long blocks = a.gran == 1 ? 4ll * a.nnz_cap : a.gran == 2 ? a.nnz_cap / 4 : a.nnz_cap;  // of 64 tokens
-            if (tiles > 1024 && blocks <= 16ll * a.nb)
+        if constexpr (Terms::kDiff) {
+            // Three CTAs per SM for many tiles: 64 heads of 8192 tokens, 15 blocks a row, 184 us with two and
+            // 163 with three, dense 1265 and 1271.  With a few tiles per SM the longer step of one CTA shows
+            // (16 tiles, rows of up to 32 blocks: 21 and 26 us).
+            if ((long long)a.nb * a.lanes > 1024)
                 return a.bf16 ? launch_one<64, true, true, kGran>(a, terms) : launch_one<64, true, false, kGran>(a, terms);
         }
         return a.bf16 ? launch_one<64, false, true, kGran>(a, terms) : launch_one<64, false, false, kGran>(a, terms);

@@ -35,8 +35,8 @@ namespace {
 
 // ---------------------------------------------------------------- transposed schedule
 
-// One warp per CSR row: the valid prefix length (0 when it does not lie in [0, cap)), and bit i of column j's bitmap words for each
-// valid entry j of row i.
+// One warp per CSR row: the valid prefix length (0 when it does not lie in [0, cap)), and bit i of
+// column j's bitmap words for each valid entry j of row i.
 __global__ void bwd_rows(int nb, const int32_t *__restrict__ row_ptr, const int32_t *__restrict__ col_idx,
                          long long cap, int words, int *__restrict__ vlen, unsigned *__restrict__ bitmap,
                          DeviceFlags flags) {

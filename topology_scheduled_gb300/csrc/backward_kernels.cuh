@@ -4,17 +4,17 @@
 //
 // Bias by buckets.  P is recomputed with the bias, a constant per step or a window per warp as in the
 // forward.  Its gradient sums dS over buckets in bwd_dq_kernel, in binary32 before dS is rounded:
-//  * where a step touches a bucket before the last a warp adds up the 95 diagonals of its 32 x 64 values, one distance each: for
-//    column c every lane takes the value of the row c + 1 lanes on (by a shuffle), which lies on a
-//    diagonal of its own for all columns.  The sums of the first 256 distances wait in shared memory
+//  * where a step touches a bucket before the last a warp adds up the diagonals of its values, one
+//    distance each: for column c every lane takes the value of the row c + 1 lanes on (by a shuffle),
+//    which lies on a diagonal of its own for all columns.  The sums of the first 256 distances wait in shared memory
 //    until the tile is done; farther ones are added up by bucket at once, by shuffles too;
 //  * the last, open bucket gets minus the sum of the row's other values, since a row of dS sums to
 //    zero: no work on the far steps, and none of the error that Delta's rounded output leaves in each
 //    of their many values (it is a common shift of a row's dP, which the far keys would add up).
 // No atomics: a warp has its own sums, a CTA writes its tile's, and terms_reduce_bias adds the tiles
 // in order.  Measured at [1, 32, 32768, 128] bf16, 14.5 blocks a row: dQ 860 us, dK/dV 1035 us (870 and
-// 964 TFLOP/s on the three and four block products each does; plain 0.72 and 0.93 ms at half of its
-// 64 lanes).
+// 964 TFLOP/s on the three and four block products each does; the plain kernels, 64 lanes: 1435 and
+// 1864 us).
 //
 // Differential attention.  A CTA takes a pair of blocks as the plain kernels do, and both maps of them:
 // the first half of the score product's K steps goes into one accumulator, the second half into

@@ -27,6 +27,12 @@ bool outputs_overlap(std::initializer_list<Span> outs, std::initializer_list<Spa
     return false;
 }
 
+// A schedule's arrays: its row starts, and its entries.
+Span rows_of(const int32_t *row_ptr, int64_t S, int64_t block) {
+    return {row_ptr, (size_t)((S + block - 1) / block + 1) * 4};
+}
+Span entries_of(const int32_t *col_idx, int64_t nnz_cap) { return {col_idx, (size_t)nnz_cap * 4}; }
+
 tsa_status check_aligned(std::initializer_list<const void *> ptrs, uintptr_t mask) {
     for (const void *p : ptrs)
         if (p && (reinterpret_cast<uintptr_t>(p) & mask)) return TSA_ERR_INVALID_ARGUMENT;
@@ -227,7 +233,9 @@ tsa_status decode_launch(const void *Q, const void *K, const void *V, const int3
     TSA_TRY(check_aligned({seq_lens, row_ptr, col_idx}, 3));
     const int64_t lanes = B * H;
     const size_t one = (size_t)(lanes * D) * 2, cache = one * (size_t)capacity;
-    if (outputs_overlap({{O, one}}, {{Q, one}, {K, cache}, {V, cache}})) return TSA_ERR_INVALID_ARGUMENT;
+    if (outputs_overlap({{O, one}}, {{Q, one}, {K, cache}, {V, cache}, {seq_lens, (size_t)B * 4}, rows_of(row_ptr, B, 1),
+                                     entries_of(col_idx, nnz_cap)}))
+        return TSA_ERR_INVALID_ARGUMENT;
     for (const Span &s : learned)
         if (overlaps(O, one, s.p, s.bytes)) return TSA_ERR_INVALID_ARGUMENT;
     int dev;
@@ -279,7 +287,8 @@ tsa_status tsa_biased_attention_fwd(const void *Q, const void *K, const void *V,
     TSA_TRY(bias_terms(bias, bucket_starts, num_buckets, H, &t));
     const size_t bytes = (size_t)(lanes * S * D) * 2;
     if (outputs_overlap({{O, bytes}, {lse, (size_t)(lanes * S) * 4}},
-                        {{Q, bytes}, {K, bytes}, {V, bytes}, {bias, (size_t)(H * num_buckets) * 2}}))
+                        {{Q, bytes}, {K, bytes}, {V, bytes}, {bias, (size_t)(H * num_buckets) * 2},
+                         rows_of(row_ptr, S, block), entries_of(col_idx, nnz_cap)}))
         return TSA_ERR_INVALID_ARGUMENT;
     int dev;
     TSA_TRY(current_device(&dev));
@@ -308,7 +317,7 @@ tsa_status tsa_differential_attention_fwd(const void *Q, const void *K, const vo
     const size_t bytes = (size_t)(lanes * S * D) * 2, lb = (size_t)(lambda_heads * D);
     if (outputs_overlap({{O, bytes}, {O2, bytes}, {lse, (size_t)(lanes * S) * 8}},
                         {{Q, bytes}, {K, bytes}, {V, bytes}, {lambda_q1, lb}, {lambda_k1, lb}, {lambda_q2, lb},
-                         {lambda_k2, lb}}))
+                         {lambda_k2, lb}, rows_of(row_ptr, S, block), entries_of(col_idx, nnz_cap)}))
         return TSA_ERR_INVALID_ARGUMENT;
     int dev;
     TSA_TRY(current_device(&dev));
@@ -349,7 +358,7 @@ tsa_status tsa_biased_attention_backward(const void *Q, const void *K, const voi
     const size_t bytes = (size_t)(lanes * S * D) * 2, bb = (size_t)(H * num_buckets) * 2;
     if (outputs_overlap({{dQ, bytes}, {dK, bytes}, {dV, bytes}, {dbias, bb}, {workspace, ws.total}},
                         {{Q, bytes}, {K, bytes}, {V, bytes}, {O, bytes}, {dO, bytes}, {lse, (size_t)(lanes * S) * 4},
-                         {bias, bb}}))
+                         {bias, bb}, rows_of(row_ptr, S, block), entries_of(col_idx, nnz_cap)}))
         return TSA_ERR_INVALID_ARGUMENT;
     int dev;
     TSA_TRY(current_device(&dev));
@@ -397,7 +406,7 @@ tsa_status tsa_differential_attention_backward(const void *Q, const void *K, con
                          {dlambda_k2, lb}, {workspace, ws.total}},
                         {{Q, bytes}, {K, bytes}, {V, bytes}, {O, bytes}, {O2, bytes}, {dO, bytes},
                          {lse, (size_t)(lanes * S) * 8}, {lambda_q1, lb}, {lambda_k1, lb}, {lambda_q2, lb},
-                         {lambda_k2, lb}}))
+                         {lambda_k2, lb}, rows_of(row_ptr, S, block), entries_of(col_idx, nnz_cap)}))
         return TSA_ERR_INVALID_ARGUMENT;
     int dev;
     TSA_TRY(current_device(&dev));

@@ -41,15 +41,6 @@ inline bool allow_smem(std::atomic<unsigned long long> &done, const void *kernel
     return true;
 }
 
-// Dynamic shared memory of the attention kernel.  The D = 128 figure is the largest size at
-// which two CTAs fit on one SM (2 x (115712 + 1024 reserved) = 228 KB), the D = 64 one lets three
-// (3 x (66688 + 1024)); both cover the tiles, barriers and biases plus at least 512 bytes of
-// alignment slack.
-template <int D>
-__host__ __device__ constexpr int kAttnSmemBytes() {
-    return D == 128 ? 115712 : 66688;
-}
-
 struct AttnLaunch {
     const CUtensorMap *tmQ, *tmK, *tmV, *tmO;
     const CUtensorMap *tmO2;  // differential: the second map's output (otherwise tmO again)
