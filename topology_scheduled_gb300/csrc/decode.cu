@@ -20,6 +20,7 @@
 // Keys at len and beyond are neither read nor counted, so what the cache holds there does not matter.
 // Measured, 16 sequences of 8192 tokens, 32 heads, D = 128, bf16, all blocks listed (2.15 GB): biased 322 us
 // = 6.7 TB/s, differential 339 us = 6.3 TB/s, of 6.8 TB/s that a copy reaches.
+#include <algorithm>
 #include <climits>
 #include <type_traits>
 
@@ -308,14 +309,23 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
 
 template <int D, bool kBF16, class Terms>
 tsa_status launch_one(const DecodeLaunch &a, const Terms &terms) {
-    // Thread blocks per (sequence, head): as many as give every warp a chunk when rows are as long as
-    // the cache, up to a cluster of 8, while the grid is below four blocks per SM.  More blocks would
-    // each pay for their start and their join: 512 heads of 8192 tokens, biased, 232 us with two blocks
-    // each, 239 with four, 268 with eight, 255 with one (ragged lengths leave its last wave short).
+    // Thread blocks per (sequence, head), up to a cluster of 8: as many as leave every warp a chunk of an
+    // average row while the GPU holds them all, and beyond that as many as leave it 32 chunks, since each
+    // block pays for its start and its join.  us with 1 / 2 / 4 / 8 blocks (D = 128; biased, differential):
+    // 8 heads, rows of 128 blocks 73 / 40 / 23 / 14 and 115 / 61 / 35 / 21; 128 heads, 13 blocks 11.4 / 10.1
+    // / 13.8 / 21.0 and 15.6 / 13.8 / 17.6 / 23.8; 512 heads, 42 blocks 108 / 116 / 117 / 147 and 148 / 127 /
+    // 128 / 157; 512 heads, ragged to 128 blocks 267 / 247 / 243 / 263 and 330 / 289 / 273 / 302.
     constexpr int kChunk = kLoadsOf<Terms> * 32 / (D / 8);
-    const long long chunks = ((long long)a.cap + kChunk - 1) / kChunk;
+    const long long sequences = a.lanes / a.H;
+    const long long row = std::min((long long)a.cap, ((long long)a.nnz_cap * a.block + sequences - 1) / sequences);
+    const long long chunks = (row + kChunk - 1) / kChunk;
+    const long long slots = 152 * (Terms::kDiff ? 3 : 2);  // thread blocks that run at once
     unsigned ranks = 1;
-    while (ranks < 8 && (long long)ranks * kWarps < chunks && (long long)a.lanes * ranks < 4 * 152) ranks *= 2;
+    while (ranks < 8) {
+        const long long least = 2 * ranks * (long long)a.lanes <= slots ? 1 : 32;
+        if (ranks * kWarps * least >= chunks) break;
+        ranks *= 2;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.lanes * ranks);
     cfg.blockDim = dim3(kThreads);
