@@ -209,10 +209,15 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
         float s[kMaps][kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            float x[8], dot = 0.f;
+            float x[8];
+            uint64_t two = f2_pack(0.f, 0.f);
             widen8<kBF16>(kr[i], x);
 #pragma unroll
-            for (int d = 0; d < 8; ++d) dot = fmaf(q[d], x[d], dot);
+            for (int d = 0; d < 8; d += 2)
+                two = f2_fma(f2_pack(q[d], q[d + 1]), f2_pack(x[d], x[d + 1]), two);
+            float dot, odd;
+            f2_unpack(two, dot, odd);
+            dot += odd;
 #pragma unroll
             for (int o = 1; o < kG / kMaps; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
             const bool there = k0 + i * kPer + group < len;
@@ -241,7 +246,10 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
 #pragma unroll
             for (int m = 0; m < kMaps; ++m)
 #pragma unroll
-                for (int d = 0; d < 8; ++d) state[m].acc[d] = fmaf(p[m][i], x[d], state[m].acc[d]);
+                for (int d = 0; d < 8; d += 2)
+                    f2_unpack(f2_fma(f2_pack(p[m][i], p[m][i]), f2_pack(x[d], x[d + 1]),
+                                     f2_pack(state[m].acc[d], state[m].acc[d + 1])),
+                              state[m].acc[d], state[m].acc[d + 1]);
         }
         k0 = next;
     }
