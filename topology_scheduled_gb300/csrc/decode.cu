@@ -83,17 +83,20 @@ struct Running {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) mx = fmaxf(mx, s[i]);
         const float ref = mx == -INFINITY ? 0.f : mx;  // no key with weight yet
-        const float keep = ex2_approx(m - ref);
+        if (mx > m) {
+            const float keep = ex2_approx(m - ref);
+            l *= keep;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) acc[d] *= keep;
+            m = mx;
+        }
         float t = 0.f;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             p[i] = ex2_approx(s[i] - ref);
             t += p[i];
         }
-        l = fmaf(l, keep, t);
-#pragma unroll
-        for (int d = 0; d < 8; ++d) acc[d] *= keep;
-        m = mx;
+        l += t;
     }
 
     // Joins the state of the lane `off` away.
@@ -318,7 +321,7 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
 template <int D, bool kBF16, class Terms>
 tsa_status launch_one(const DecodeLaunch &a, const Terms &terms) {
     // Thread blocks per (sequence, head), up to a cluster of 8: as many as leave every warp a chunk of an
-    // average row while the GPU holds them all, and beyond that as many as leave it 32 chunks, since each
+    // average row (the host knows no single row's length) while the GPU holds them all, and beyond that as many as leave it 32 chunks, since each
     // block pays for its start and its join.  us with 1 / 2 / 4 / 8 blocks (D = 128; biased, differential):
     // 8 heads, rows of 128 blocks 73 / 40 / 23 / 14 and 115 / 61 / 35 / 21; 128 heads, 13 blocks 11.4 / 10.1
     // / 13.8 / 21.0 and 15.6 / 13.8 / 17.6 / 23.8; 512 heads, 42 blocks 108 / 116 / 117 / 147 and 148 / 127 /
