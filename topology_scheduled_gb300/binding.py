@@ -94,6 +94,8 @@ def library_path() -> str:
 def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     """The loaded libtsa.so (built on first use when nvcc is available)."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _LOCK:
         if _LIB is None:
             path = _build.LIB
@@ -131,13 +133,10 @@ def _stream(stream) -> int | None:
 
 
 def _lanes_S_D(x: torch.Tensor):
-    if x.dim() == 2:
-        return 1, 1, x.shape[0], x.shape[1]
-    if x.dim() == 3:
-        return 1, x.shape[0], x.shape[1], x.shape[2]
-    if x.dim() == 4:
-        return x.shape[0], x.shape[1], x.shape[2], x.shape[3]
-    raise ValueError(f"expected [S, D], [L, S, D] or [B, H, S, D], got shape {tuple(x.shape)}")
+    shape = tuple(x.shape)
+    if 2 <= len(shape) <= 4:
+        return (1, 1, 1, 1)[len(shape):] + shape
+    raise ValueError(f"expected [S, D], [L, S, D] or [B, H, S, D], got shape {shape}")
 
 
 def tsa_schedule_max_nnz(S: int, block: int, sink: int, local_radius: int, topk: int) -> int:
@@ -305,13 +304,14 @@ def tsa_dense_causal_csr(S: int, block: int = 64, device=None, stream=None):
 
 
 def _check_qkv(**tensors):
-    ref = None
+    shape = dtype = None
     for name, t in tensors.items():
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if ref is not None and (t.shape != ref.shape or t.dtype != ref.dtype):
+        if shape is None:
+            shape, dtype = t.shape, t.dtype
+        elif t.shape != shape or t.dtype is not dtype:
             raise ValueError(f"{', '.join(tensors)} must share shape and dtype")
-        ref = t
 
 
 def _check_csr(row_ptr, col_idx):
