@@ -36,7 +36,9 @@ extern "C" {
  *   O             out, [B*H, S, D] of `dtype`, 16-byte aligned; rows without keys are 0.
  *   lse           out, [B*H, S] float32, or NULL: the log-sum-exp of z per row, -inf for rows
  *                 without keys; the backward call needs it.
- * Outputs overlap no input and no other output.
+ * Outputs overlap no input and no other output.  Rows of a listed block that the token mask leaves
+ * out meet weights of 0 in the products, so they must be finite (padding is zeros, not whatever the
+ * memory held); blocks that no row lists are not read.
  *
  * Limits: those of tsa_scheduled_attention, 1 <= num_buckets <= TSA_MAX_BUCKETS,
  * scale >= 1e-30.  Rows past S are neither read nor written, in no lane.  Errors:
@@ -90,6 +92,7 @@ tsa_status tsa_differential_attention_fwd(const void *Q, const void *K, const vo
  *   dbias         out, [H, num_buckets] of `dtype`.
  *   workspace     >= tsa_biased_attention_backward_workspace_bytes(B*H, S, block, nnz_cap,
  *                 num_buckets) bytes, 256-byte aligned; its contents on entry do not matter.
+ *                 Calls that may run at the same time, captured graphs among them, need one each.
  * Outputs and workspace overlap no input and one another.  Limits: those of the forward call and
  * of tsa_scheduled_attention_backward (blocks of 64 or 128 tokens, ceil(S/64) <= 8192).  Errors
  * as there.
