@@ -82,9 +82,10 @@ tsa_status tsa_differential_attention_fwd(const void *Q, const void *K, const vo
  *   Delta = rowsum(dO o O),  dS = P o (dO V^T - Delta),  dV = P^T dO,  dQ = scale dS K,
  *   dK = scale dS^T Q,  dbias[h][b] = sum of dS over the batch's lanes of head h and the pairs
  *   whose distance lies in bucket b,
- * in binary32 from the 16-bit inputs, results rounded once.  (A row of dS sums to zero, so the
- * open last bucket gets minus the sum of the row's others, in rows that reach it.)  The result
- * does not depend on the order in which thread blocks run.
+ * sums in binary32, P and dS rounded to `dtype` for their products (dbias adds dS before its
+ * rounding), results rounded once.  (A row of dS sums to zero, so the open last bucket gets
+ * minus the sum of the row's others, in rows that reach it.)  The result does not depend on
+ * the order in which thread blocks run.
  *
  *   O, lse        as the forward call wrote them for the same inputs and CSR.
  *   dO            in,  the upstream gradient, [B*H, S, D] of `dtype`, 16-byte aligned.

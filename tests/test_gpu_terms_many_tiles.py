@@ -1,6 +1,5 @@
 """Forwards of more than 1024 tiles at D = 64 (differential: three thread blocks per SM): a few of their
 heads against the 64-bit forms."""
-import numpy as np
 import pytest
 import torch
 
@@ -14,7 +13,7 @@ STARTS = dict(STARTS, **{"past the table": [0, 40, 2100, 2130, 2300]})  # the ke
 LOW = torch.finfo(torch.bfloat16).min
 
 
-def _many(S, block):
+def _many(S):
     """Heads that make more than 1024 tiles, of two 64-token blocks even."""
     return 1024 // ((-(-S // 64) + 1) // 2) + 2
 
@@ -49,7 +48,7 @@ def _heads(H):
 @pytest.mark.parametrize("S,dtype,block,kind,starts", CASES)
 def test_biased(S, dtype, block, kind, starts):
     starts = STARTS[starts]
-    H = _many(S, block)
+    H = _many(S)
     q, k, v, bias, _ = _inputs(H, S, dtype, S, len(starts))
     bias[0, ::3], bias[H - 1, -1] = LOW, -float("inf")
     rp, ci = _csr(kind, S, block, seed=1)
@@ -77,7 +76,7 @@ def test_biased(S, dtype, block, kind, starts):
 
 @pytest.mark.parametrize("S,dtype,block,kind,starts", CASES)
 def test_differential(S, dtype, block, kind, starts):
-    H = _many(S, block)
+    H = _many(S)
     q, k, v, _, lam = _inputs(H, S, dtype, S + 1, 1)
     rp, ci = _csr(kind, S, block, seed=2)
     args = [x.to(DEV) for x in (q, k, v)]
@@ -101,7 +100,7 @@ def test_differential(S, dtype, block, kind, starts):
 
 def test_wait_that_runs_out_is_reported():
     S, starts = 700, STARTS["geometric"]
-    H = _many(S, 64)
+    H = _many(S)
     q, k, v, bias, lam = _inputs(H, S, torch.float16, 3, len(starts))
     rp, ci = _dev(*_csr("random", S, 64, seed=1))
     q, k, v, bias, *lam = (x.to(DEV) for x in (q, k, v, bias, *lam))
@@ -119,7 +118,7 @@ def test_wait_that_runs_out_is_reported():
 
 
 def test_bad_rows_are_reported():
-    S, H = 256, _many(256, 64)
+    S, H = 256, _many(256)
     starts = STARTS["geometric"]
     q, k, v, bias, _ = (x.to(DEV) if isinstance(x, torch.Tensor) else x for x in _inputs(H, S, torch.float16, 4, len(starts)))
     for ptr, idx in (([0, 1, 3, 5, 7], [0, 0, 1, 2, 1, 0, 3]), ([0, 1, 3, 5, 9], [0, 0, 1, 1, 2, 0, 3]),
