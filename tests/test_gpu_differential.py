@@ -1,5 +1,4 @@
 """Differential attention over a schedule, against its 64-bit form."""
-import numpy as np
 import pytest
 import torch
 
