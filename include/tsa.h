@@ -242,7 +242,8 @@ tsa_status tsa_dense_causal_csr(int64_t S, int64_t block, int32_t *row_ptr, int3
  *            one the CSR defines at its own block.
  *
  * S need not be a multiple of the block: rows q >= S of a partial last block are neither
- * computed into O nor into lse, and keys k >= S are never weighed.
+ * computed into O nor into lse, and keys k >= S are never weighed.  A lane's results depend on its own
+ * rows alone, whatever the others hold.
  * Limits: block in {32, 64, 128}, D in {64, 128}, B*H <= 65535, B*H*S < 2^31.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (block or D), NOT_DEVICE_POINTER, DEVICE_MISMATCH,
  * CUDA.  Device-side: BAD_SCHEDULE (a row is truncated at its first bad entry), TIMEOUT.
@@ -288,8 +289,8 @@ tsa_status tsa_scheduled_attention_fwd(const void *Q, const void *K, const void 
  * Limits: block in {64, 128} (a CSR of 128-token blocks is first expanded on the GPU into the
  * 64-token CSR with the same allowed keys: rows 2p and 2p+1 hold 64-blocks 2j and 2j+1 of each
  * j < p, plus 2p, and 2p+1 for row 2p+1, when p is in row p; a 32-token CSR is UNSUPPORTED),
- * D in {64, 128}, ceil(S/64) <= 8192 (a partial last block is allowed: its rows are stored one
- * by one, never past the lane's last row), B*H <= 65535,
+ * D in {64, 128}, ceil(S/64) <= 8192 (a partial last block is allowed; nothing past the lane's last
+ * row is read or written), B*H <= 65535,
  * B*H*S < 2^31.  Errors: INVALID_ARGUMENT, UNSUPPORTED, CAPACITY (workspace), NOT_DEVICE_POINTER,
  * DEVICE_MISMATCH, CUDA.  Device-side: BAD_SCHEDULE (a row is cut at its first bad entry, as in
  * the forward), TSA_ERR_DEVICE (nnz above nnz_cap: dK and dV then come out zero), TIMEOUT.

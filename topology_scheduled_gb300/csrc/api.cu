@@ -106,21 +106,7 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-// Row-major [rows, cols] 16-bit matrix; boxes of 64 columns (128 B, 128-byte swizzle) x box_rows.
-bool encode_2d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t rows, uint64_t cols,
-               uint32_t box_rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {cols * 2};
-    const cuuint32_t box[2] = {64, box_rows};
-    const cuuint32_t elem[2] = {1, 1};
-    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-              const_cast<void *>(ptr), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
+// Row-major [lanes, rows, cols] 16-bit tensor; boxes of 64 columns (128 B, 128-byte swizzle) x box_rows.
 bool encode_3d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t lanes, uint64_t rows, uint64_t cols,
                uint32_t box_rows) {
     EncodeTiledFn fn = encode_fn();
@@ -437,10 +423,10 @@ tsa_status launch_attention_checked(const void *Q, const void *K, const void *V,
                                     const int32_t *col_idx, void *O, float *lse, bool bf16, int64_t lanes,
                                     int64_t S, int64_t D, int64_t block, float scale, cudaStream_t stream,
                                     int dev) {
-    const uint64_t rows = (uint64_t)(lanes * S);
+    const uint64_t n = (uint64_t)lanes, rows = (uint64_t)S, cols = (uint64_t)D;
     CUtensorMap tmQ, tmK, tmV, tmO;
-    if (!encode_2d(&tmQ, Q, bf16, rows, (uint64_t)D, 128) || !encode_2d(&tmK, K, bf16, rows, (uint64_t)D, 64) ||
-        !encode_2d(&tmV, V, bf16, rows, (uint64_t)D, 64) || !encode_2d(&tmO, O, bf16, rows, (uint64_t)D, 64))
+    if (!encode_3d(&tmQ, Q, bf16, n, rows, cols, 128) || !encode_3d(&tmK, K, bf16, n, rows, cols, 64) ||
+        !encode_3d(&tmV, V, bf16, n, rows, cols, 64) || !encode_3d(&tmO, O, bf16, n, rows, cols, 64))
         return TSA_ERR_CUDA;
     AttnLaunch a;
     a.tmQ = &tmQ;
@@ -450,7 +436,7 @@ tsa_status launch_attention_checked(const void *Q, const void *K, const void *V,
     a.row_ptr = row_ptr;
     a.col_idx = col_idx;
     a.nnz_cap = INT_MAX;
-    a.O = static_cast<uint16_t *>(O);
+    a.with_o2 = false;
     a.lse = lse;
     a.nb = (int)((S + 63) / 64);  // the kernel works in 64-token blocks
     a.gran = block == 128 ? 1 : block == 32 ? 2 : 0;
@@ -556,13 +542,13 @@ tsa_status tsa_scheduled_attention_backward(const void *Q, const void *K, const 
                           static_cast<const void *>(col_idx), static_cast<const void *>(workspace)})
         TSA_TRY(check_device_ptr(p, dev));
     const bool bf16 = dtype == TSA_BF16;
-    const uint64_t rows = (uint64_t)(lanes * S), cols = (uint64_t)D;
+    const uint64_t n = (uint64_t)lanes, rows = (uint64_t)S, cols = (uint64_t)D;
     CUtensorMap tQ128, tdO128, tQ64, tdO64, tK64, tV64, tdQ64, tdK64, tdV64;
-    if (!encode_2d(&tQ128, Q, bf16, rows, cols, 128) || !encode_2d(&tdO128, dO, bf16, rows, cols, 128) ||
-        !encode_2d(&tQ64, Q, bf16, rows, cols, 64) || !encode_2d(&tdO64, dO, bf16, rows, cols, 64) ||
-        !encode_2d(&tK64, K, bf16, rows, cols, 64) || !encode_2d(&tV64, V, bf16, rows, cols, 64) ||
-        !encode_2d(&tdQ64, dQ, bf16, rows, cols, 64) || !encode_2d(&tdK64, dK, bf16, rows, cols, 64) ||
-        !encode_2d(&tdV64, dV, bf16, rows, cols, 64))
+    if (!encode_3d(&tQ128, Q, bf16, n, rows, cols, 128) || !encode_3d(&tdO128, dO, bf16, n, rows, cols, 128) ||
+        !encode_3d(&tQ64, Q, bf16, n, rows, cols, 64) || !encode_3d(&tdO64, dO, bf16, n, rows, cols, 64) ||
+        !encode_3d(&tK64, K, bf16, n, rows, cols, 64) || !encode_3d(&tV64, V, bf16, n, rows, cols, 64) ||
+        !encode_3d(&tdQ64, dQ, bf16, n, rows, cols, 64) || !encode_3d(&tdK64, dK, bf16, n, rows, cols, 64) ||
+        !encode_3d(&tdV64, dV, bf16, n, rows, cols, 64))
         return TSA_ERR_CUDA;
     uint8_t *w = static_cast<uint8_t *>(workspace);
     BwdLaunch a;
@@ -577,9 +563,6 @@ tsa_status tsa_scheduled_attention_backward(const void *Q, const void *K, const 
     a.tmdV64 = &tdV64;
     a.O = static_cast<const uint16_t *>(O);
     a.dO = static_cast<const uint16_t *>(dO);
-    a.dQ = static_cast<uint16_t *>(dQ);
-    a.dK = static_cast<uint16_t *>(dK);
-    a.dV = static_cast<uint16_t *>(dV);
     a.lse = lse;
     a.row_ptr = row_ptr;
     a.col_idx = col_idx;

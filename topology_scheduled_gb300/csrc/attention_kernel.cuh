@@ -29,10 +29,10 @@
 //    warp rescales when any of its rows must (factor 1 for the others).
 //  * Epilogue.  O / l rounded to the input dtype, staged in the Q tile, TMA-stored per block;
 //    optionally the row's log-sum-exp (m + log l), which the backward pass recomputes P from.
-//  * Partial last block (S not a multiple of 64).  Its key rows past S are read but never
-//    weigh: the block is visited only as the diagonal block of the last row, where the causal
-//    mask already drops keys after the query token.  Its query rows past S are computed and
-//    dropped: the block's output is written row by row for the rows that exist.
+//  * Partial last block (S not a multiple of 64).  The maps see [lanes, S, D] as three dimensions: rows
+//    past a lane's end read as zero, whatever the next lane holds, and are not written.  As keys
+//    they never weigh, since the block is visited only as the diagonal block of the last row, where
+//    the causal mask already drops keys after the query token.
 //  * Two CTAs share an SM, so one CTA's softmax also overlaps the other's MMAs.
 //
 // The same kernel carries the score terms of score_terms.cuh:
@@ -388,7 +388,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                            const __grid_constant__ CUtensorMap tmO,
                            const __grid_constant__ CUtensorMap tmO2,
                            const int32_t *__restrict__ row_ptr, const int32_t *__restrict__ col_idx, int nnz_cap,
-                           uint16_t *__restrict__ O, float *__restrict__ lse_out, int nb, int S,
+                           bool with_o2, float *__restrict__ lse_out, int nb, int S,
                            float scale_log2, DeviceFlags flags, const __grid_constant__ Terms terms) {
     constexpr bool kBias = Terms::kBias, kDiff = Terms::kDiff;
     constexpr bool kFine = kGran == 2;  // 32-token blocks: masks per (query quarter, key half)
@@ -428,7 +428,6 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int last_tile = (int)gridDim.x - 1;        // a tile: two query blocks (kDiff: one, both maps)
     const int qa = (last_tile - (int)blockIdx.x) * (kDiff ? 1 : 2);  // longest rows first
     const bool has_b = !kDiff && qa + 1 < nb;
-    const int row0 = lane_id * S;                    // first row of this lane in [L*S, D]
 
     // The first global reads are issued together and waited for at the barrier below: whether
     // the launch already gave up elsewhere (one thread reads the flag, so the whole CTA takes
@@ -490,9 +489,9 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
             mbar_arrive_expect_tx(bar_q, L::kQBytes);
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c) {
-                load_rows<Terms>(sQ + c * 16384, &tmQ, c * 64, row0, qa * kBlock, lane_id, bar_q);
+                tma_load_3d(sQ + c * 16384, &tmQ, c * 64, qa * kBlock, lane_id, bar_q);
                 if constexpr (kDiff)  // 64-row boxes: the block again, for the second map
-                    load_rows<Terms>(sQ + c * 16384 + 8192, &tmQ, c * 64, row0, qa * kBlock, lane_id, bar_q);
+                    tma_load_3d(sQ + c * 16384 + 8192, &tmQ, c * 64, qa * kBlock, lane_id, bar_q);
             }
             bool ok = true, k_done = false, v_done = false;
             int kv = 0, vv = 0;  // next union entry of each stream
@@ -513,7 +512,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                         mbar_arrive_expect_tx(BAR_K_FULL(s), L::kKVBytes);
 #pragma unroll
                         for (int c = 0; c < L::kChunks; ++c)
-                            load_rows<Terms>(sK0 + s * L::kKVBytes + c * 8192, &tmK, c * 64, row0, j * kBlock, lane_id,
+                            tma_load_3d(sK0 + s * L::kKVBytes + c * 8192, &tmK, c * 64, j * kBlock, lane_id,
                                              BAR_K_FULL(s));
                         ++kv;
                     }
@@ -530,7 +529,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                         mbar_arrive_expect_tx(BAR_V_FULL(s), L::kKVBytes);
 #pragma unroll
                         for (int c = 0; c < L::kChunks; ++c)
-                            load_rows<Terms>(sV0 + s * L::kKVBytes + c * 8192, &tmV, c * 64, row0, j * kBlock, lane_id,
+                            tma_load_3d(sV0 + s * L::kKVBytes + c * 8192, &tmV, c * 64, j * kBlock, lane_id,
                                              BAR_V_FULL(s));
                         ++vv;
                     }
@@ -882,16 +881,11 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         if (!named_barrier_or(1, kRows, *abort_flag != 0)) {
             tc_fence_after();
             const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
-            // A partial last query block (S not a multiple of 64) is not TMA-stored -- its box
-            // would run into the next lane's rows -- but written row by row from registers.
-            // (The score terms' kernels store through three dimensions, which cut the box off.)
-            constexpr bool k3D = kBias || kDiff;
             const int tok = qa * kBlock + row_in;  // this thread's token (rows of both halves)
-            const bool partial = !k3D && (my_block + 1) * kBlock > S;
             const bool tok_ok = row_exists && tok < S;
             // log-sum-exp of the scaled scores in natural-log units, for the backward pass
             if (lse_out && tok_ok) {
-                long long at = row0 + tok;
+                long long at = (long long)lane_id * S + tok;
                 if constexpr (kDiff) at += half * terms.map_rows;
                 lse_out[at] = l_sum > 0.f ? (m_used + log2f(kDiff ? l_exact : l_sum)) * 0.6931471805599453f : -INFINITY;
             }
@@ -930,7 +924,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
                             for (int t = 0; t < 8; ++t) y[t] = __uint_as_float(o[q * 8 + t]) * inv;
                             const int col = base_col + h * 32 + q * 8;
-                            if (half && O != nullptr) stage(col, tid, y);
+                            if (half && with_o2) stage(col, tid, y);
                             float4 *at = area + (((half ^ own) ? kW / 4 : 0) + h * 8 + q * 2) * 64;
                             if (!own) {
                                 at[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -968,9 +962,6 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                                                 __uint_as_float(o[q * 8 + 2 * t + 1]) * inv, unused);
                         const uint32_t chunk16 = (uint32_t)(h * 4 + q);
                         st_shared_v4(o_row + ((chunk16 ^ sw) << 4), w[0], w[1], w[2], w[3]);
-                        if (partial && tok_ok)
-                            *reinterpret_cast<uint4 *>(O + ((size_t)row0 + tok) * L::kD + c * 64 + chunk16 * 8) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
@@ -980,20 +971,13 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
             if (tid == 0) {
 #pragma unroll
                 for (int c = 0; c < L::kChunks; ++c) {
+                    tma_store_3d(&tmO, c * 64, qa * kBlock, lane_id, sQ + c * 16384);
                     if constexpr (kDiff) {
-                        tma_store_3d(&tmO, c * 64, qa * kBlock, lane_id, sQ + c * 16384);
-                        if (O != nullptr)  // the second map's output, for the backward pass
+                        if (with_o2)  // the second map's output, for the backward pass
                             tma_store_3d(&tmO2, c * 64, qa * kBlock, lane_id, sQ + c * 16384 + 8192);
-                        continue;
+                    } else if (has_b) {
+                        tma_store_3d(&tmO, c * 64, (qa + 1) * kBlock, lane_id, sQ + c * 16384 + 8192);
                     }
-                    if constexpr (kBias) {
-                        tma_store_3d(&tmO, c * 64, qa * kBlock, lane_id, sQ + c * 16384);
-                        if (has_b) tma_store_3d(&tmO, c * 64, (qa + 1) * kBlock, lane_id, sQ + c * 16384 + 8192);
-                        continue;
-                    }
-                    if ((qa + 1) * kBlock <= S) tma_store_2d(&tmO, c * 64, row0 + qa * kBlock, sQ + c * 16384);
-                    if (has_b && (qa + 2) * kBlock <= S)
-                        tma_store_2d(&tmO, c * 64, row0 + (qa + 1) * kBlock, sQ + c * 16384 + 8192);
                 }
                 tma_store_commit();
                 tma_store_wait_read();
@@ -1029,7 +1013,7 @@ tsa_status launch_one(const AttnLaunch &a, const Terms &terms) {
     const int tiles = Terms::kDiff ? a.nb : (a.nb + 1) / 2;
     dim3 grid((unsigned)tiles, (unsigned)a.lanes);
     kern<<<grid, kThreads, kBytes, a.stream>>>(*a.tmQ, *a.tmK, *a.tmV, *a.tmO, *a.tmO2, a.row_ptr,
-                                                            a.col_idx, a.nnz_cap, a.O, a.lse, a.nb, a.S,
+                                                            a.col_idx, a.nnz_cap, a.with_o2, a.lse, a.nb, a.S,
                                                             a.scale_log2, a.flags, terms);
     return cudaGetLastError() == cudaSuccess ? TSA_OK : TSA_ERR_CUDA;
 }

@@ -26,7 +26,9 @@
 // Warp roles are those of the forward: one warp produces (TMA, rings of four blocks), one issues the
 // MMAs from one thread (the next step's products before the current step's accumulation), and eight do
 // the elementwise work, two per 32 rows with 32 columns of a step each (no value of a row is needed by
-// the other).  Every wait is bounded; on a timeout a CTA records TSA_ERR_TIMEOUT, drains what it
+// the other).  A partial last block (S not a multiple of 64) needs no code of its own: the maps see
+// [lanes, S, D] as three dimensions, so rows past a lane's end read as zero, whatever the next lane
+// holds, and are not written.  Every wait is bounded; on a timeout a CTA records TSA_ERR_TIMEOUT, drains what it
 // issued, frees its TMEM and returns.
 #include "backward_kernels.cuh"
 

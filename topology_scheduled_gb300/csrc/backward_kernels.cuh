@@ -206,22 +206,6 @@ __device__ __forceinline__ void stage_rows(uint32_t tmem_row, uint32_t col, bool
     }
 }
 
-// Row `row` (0-127) of a 128-row SW128 staging tile (the layout stage_rows writes: 64-column
-// chunks of 16 KB, 16-byte units of a row permuted by row & 7) copied to a global row of D
-// 16-bit values.
-template <int D>
-__device__ __forceinline__ void copy_staged_row(const uint8_t *tile, int row, uint16_t *dst) {
-    const uint32_t sw = (uint32_t)(row & 7);
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-        const uint8_t *src = tile + c * 16384 + row * 128;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4 *>(dst + c * 64 + u * 8) =
-                *reinterpret_cast<const uint4 *>(src + (((uint32_t)u ^ sw) << 4));
-    }
-}
-
 // Meta area (byte offsets from the meta base), common to both kernels.
 constexpr int kBarTile = 0;                           // resident tile(s) loaded
 constexpr int kBarFull = 8;                           // kStream x 8: streamed block landed
@@ -333,8 +317,8 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
               const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ CUtensorMap tmdQ, const int32_t *__restrict__ row_ptr,
               const int32_t *__restrict__ col_idx, const int *__restrict__ vlen,
-              const float *__restrict__ lse, const float *__restrict__ delta, int nb, int S,
-              float scale, float scale_log2, uint16_t *__restrict__ dQ, float *__restrict__ partial,
+              const float *__restrict__ lse, const float *__restrict__ delta, int nb, float scale,
+              float scale_log2, float *__restrict__ partial,
               DeviceFlags flags, const __grid_constant__ Terms terms) {
     constexpr bool kBias = Terms::kBias, kDiff = Terms::kDiff;
     using L = DqSmem<D, Terms>;
@@ -367,7 +351,6 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     const int qa = 2 * tile;                                 // longest rows first
     const bool has_b = qa + 1 < nb;
     constexpr uint32_t kAcc = kDiff ? kDiffAccCol : kAccCol;
-    const int row0 = lane_id * S;
 
     // The first global reads are issued together and waited for at the barrier below: whether
     // the launch already gave up elsewhere (one thread, so the whole CTA takes the same branch),
@@ -425,8 +408,8 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             mbar_arrive_expect_tx(bar_tile, 2 * L::kTileBytes);
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c) {
-                load_rows<Terms>(sQ + c * 16384, &tmQ, c * 64, row0, qa * kBlock, lane_id, bar_tile);
-                load_rows<Terms>(sdO + c * 16384, &tmdO, c * 64, row0, qa * kBlock, lane_id, bar_tile);
+                tma_load_3d(sQ + c * 16384, &tmQ, c * 64, qa * kBlock, lane_id, bar_tile);
+                tma_load_3d(sdO + c * 16384, &tmdO, c * 64, qa * kBlock, lane_id, bar_tile);
             }
             bool ok = true;
             int k_issued = 0, v_issued = 0;
@@ -445,14 +428,14 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 mbar_arrive_expect_tx(BAR_K_FULL(s), L::kKVBytes);
 #pragma unroll
                 for (int c = 0; c < L::kChunks; ++c)
-                    load_rows<Terms>(sK + s * L::kKVBytes + c * 8192, &tmK, c * 64, row0, j * kBlock, lane_id,
+                    tma_load_3d(sK + s * L::kKVBytes + c * 8192, &tmK, c * 64, j * kBlock, lane_id,
                                      BAR_K_FULL(s));
                 k_issued = v + 1;
                 if (v >= kStream && !mbar_wait(BAR_V_EMPTY(s), par, flags)) { ok = false; break; }
                 mbar_arrive_expect_tx(BAR_V_FULL(s), L::kKVBytes);
 #pragma unroll
                 for (int c = 0; c < L::kChunks; ++c)
-                    load_rows<Terms>(sV + s * L::kKVBytes + c * 8192, &tmV, c * 64, row0, j * kBlock, lane_id,
+                    tma_load_3d(sV + s * L::kKVBytes + c * 8192, &tmV, c * 64, j * kBlock, lane_id,
                                      BAR_V_FULL(s));
                 v_issued = v + 1;
             }
@@ -776,28 +759,15 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     partial[(long long)lane_id * gridDim.y + tile] = -s;
                 }
             }
-            // A partial last block (S not a multiple of 64) is not TMA-stored -- its box would
-            // run into the next lane's rows -- but copied row by row from the staging tile.
-            // (The score terms' kernels store through three dimensions, which cut the box off.)
-            constexpr bool k3D = kBias || kDiff;
-            const bool part_a = !k3D && (qa + 1) * kBlock > S, part_b = !k3D && has_b && (qa + 2) * kBlock > S;
             if (tid == 0) {
 #pragma unroll
                 for (int c = 0; c < L::kChunks; ++c) {
-                    if constexpr (k3D) {
-                        tma_store_3d(&tmdQ, c * 64, qa * kBlock, lane_id, sQ + c * 16384);
-                        if (has_b) tma_store_3d(&tmdQ, c * 64, (qa + 1) * kBlock, lane_id, sQ + c * 16384 + 8192);
-                        continue;
-                    }
-                    if (!part_a) tma_store_2d(&tmdQ, c * 64, row0 + qa * kBlock, sQ + c * 16384);
-                    if (has_b && !part_b)
-                        tma_store_2d(&tmdQ, c * 64, row0 + (qa + 1) * kBlock, sQ + c * 16384 + 8192);
+                    tma_store_3d(&tmdQ, c * 64, qa * kBlock, lane_id, sQ + c * 16384);
+                    if (has_b) tma_store_3d(&tmdQ, c * 64, (qa + 1) * kBlock, lane_id, sQ + c * 16384 + 8192);
                 }
                 tma_store_commit();
                 tma_store_wait_read();
             }
-            if (tid < kRows && (half ? part_b : part_a) && qa * kBlock + row < S)
-                copy_staged_row<D>(smem + (sQ - base), row, dQ + ((size_t)row0 + qa * kBlock + row) * D);
         }
     }
 #undef BAR_K_FULL
@@ -850,8 +820,7 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                const int *__restrict__ col_ptr, const int32_t *__restrict__ row_idx,
                const int *__restrict__ pairs, const float *__restrict__ lse,
                const float *__restrict__ delta, int nb, int S, float scale, float scale_log2,
-               uint16_t *__restrict__ dK, uint16_t *__restrict__ dV, DeviceFlags flags,
-               const __grid_constant__ Terms terms) {
+               DeviceFlags flags, const __grid_constant__ Terms terms) {
     constexpr bool kBias = Terms::kBias, kDiff = Terms::kDiff;
     using L = DkvSmem<D, Terms>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -885,7 +854,6 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     // key blocks ka and kb (-1: none) from the pair list, heaviest transposed columns first
     const int ka = __ldg(pairs + 2 * blockIdx.y), kb = __ldg(pairs + 2 * blockIdx.y + 1);
     const bool has_b = kb >= 0;
-    const int row0 = lane_id * S;
 
     // As in the dQ kernel: the abort flag and the producer's two transposed columns are read
     // before the first barrier.
@@ -944,12 +912,12 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             mbar_arrive_expect_tx(bar_tile, 2 * L::kTileBytes);
 #pragma unroll
             for (int c = 0; c < L::kChunks; ++c) {
-                load_rows<Terms>(sK + c * 16384, &tmK, c * 64, row0, ka * kBlock, lane_id, bar_tile);
-                load_rows<Terms>(sV + c * 16384, &tmV, c * 64, row0, ka * kBlock, lane_id, bar_tile);
+                tma_load_3d(sK + c * 16384, &tmK, c * 64, ka * kBlock, lane_id, bar_tile);
+                tma_load_3d(sV + c * 16384, &tmV, c * 64, ka * kBlock, lane_id, bar_tile);
                 // the second block's rows, or the first block's again (masked) if there is none
                 const int y2 = (has_b ? kb : ka) * kBlock;
-                load_rows<Terms>(sK + c * 16384 + 8192, &tmK, c * 64, row0, y2, lane_id, bar_tile);
-                load_rows<Terms>(sV + c * 16384 + 8192, &tmV, c * 64, row0, y2, lane_id, bar_tile);
+                tma_load_3d(sK + c * 16384 + 8192, &tmK, c * 64, y2, lane_id, bar_tile);
+                tma_load_3d(sV + c * 16384 + 8192, &tmV, c * 64, y2, lane_id, bar_tile);
             }
             bool ok = true;
             int issued = 0;
@@ -968,8 +936,8 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 mbar_arrive_expect_tx(BAR_FULL(s), 2 * L::kQBytes + 2 * L::kRowBytes);
 #pragma unroll
                 for (int c = 0; c < L::kChunks; ++c) {
-                    load_rows<Terms>(sQ + s * L::kQBytes + c * 8192, &tmQ, c * 64, row0, i * kBlock, lane_id, BAR_FULL(s));
-                    load_rows<Terms>(sdO + s * L::kQBytes + c * 8192, &tmdO, c * 64, row0, i * kBlock, lane_id, BAR_FULL(s));
+                    tma_load_3d(sQ + s * L::kQBytes + c * 8192, &tmQ, c * 64, i * kBlock, lane_id, BAR_FULL(s));
+                    tma_load_3d(sdO + s * L::kQBytes + c * 8192, &tmdO, c * 64, i * kBlock, lane_id, BAR_FULL(s));
                 }
                 const long long py = ((long long)lane_id * nb + i) * kBlock;  // padded row
                 bulk_load(sLse + s * L::kRowBytes, lse + py, 256, BAR_FULL(s));
@@ -1302,37 +1270,18 @@ bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             stage_rows<D, kBF16>(tmem + t_lane, kDKCol, acc_valid, scale, sK, row, tid >> 7);
             fence_proxy_async_smem();
             named_barrier(1, kElt);
-            // a partial last key block is copied row by row (see the dQ kernel)
-            constexpr bool k3D = kBias || kDiff;
-            const bool part_a = !k3D && (ka + 1) * kBlock > S, part_b = !k3D && has_b && (kb + 1) * kBlock > S;
             if (tid == 0) {
 #pragma unroll
                 for (int c = 0; c < L::kChunks; ++c) {
-                    if constexpr (k3D) {
-                        tma_store_3d(&tmdV, c * 64, ka * kBlock, lane_id, sV + c * 16384);
-                        tma_store_3d(&tmdK, c * 64, ka * kBlock, lane_id, sK + c * 16384);
-                        if (has_b) {
-                            tma_store_3d(&tmdV, c * 64, kb * kBlock, lane_id, sV + c * 16384 + 8192);
-                            tma_store_3d(&tmdK, c * 64, kb * kBlock, lane_id, sK + c * 16384 + 8192);
-                        }
-                        continue;
-                    }
-                    if (!part_a) {
-                        tma_store_2d(&tmdV, c * 64, row0 + ka * kBlock, sV + c * 16384);
-                        tma_store_2d(&tmdK, c * 64, row0 + ka * kBlock, sK + c * 16384);
-                    }
-                    if (has_b && !part_b) {
-                        tma_store_2d(&tmdV, c * 64, row0 + kb * kBlock, sV + c * 16384 + 8192);
-                        tma_store_2d(&tmdK, c * 64, row0 + kb * kBlock, sK + c * 16384 + 8192);
+                    tma_store_3d(&tmdV, c * 64, ka * kBlock, lane_id, sV + c * 16384);
+                    tma_store_3d(&tmdK, c * 64, ka * kBlock, lane_id, sK + c * 16384);
+                    if (has_b) {
+                        tma_store_3d(&tmdV, c * 64, kb * kBlock, lane_id, sV + c * 16384 + 8192);
+                        tma_store_3d(&tmdK, c * 64, kb * kBlock, lane_id, sK + c * 16384 + 8192);
                     }
                 }
                 tma_store_commit();
                 tma_store_wait_read();
-            }
-            if (tid < kRows && (half ? part_b : part_a) && key_block * kBlock + k_in < S) {
-                const size_t grow_k = ((size_t)row0 + key_block * kBlock + k_in) * D;
-                copy_staged_row<D>(smem + (sV - base), row, dV + grow_k);
-                copy_staged_row<D>(smem + (sK - base), row, dK + grow_k);
             }
         }
     }
@@ -1368,11 +1317,11 @@ tsa_status launch_grad_kernels(const BwdLaunch &a, const Terms &terms) {
     const dim3 grid((unsigned)a.lanes, tiles);
     const float scale_log2 = a.scale * kLog2e;
     kq<<<grid, kThreads, kDqBytes, a.stream>>>(*a.tmQ128, *a.tmdO128, *a.tmK64, *a.tmV64, *a.tmdQ64, a.row_ptr,
-                                               a.col_idx, a.vlen, a.lse_pad, a.delta, a.nb, a.S, a.scale, scale_log2,
-                                               a.dQ, a.partial, a.flags, terms);
+                                               a.col_idx, a.vlen, a.lse_pad, a.delta, a.nb, a.scale, scale_log2,
+                                               a.partial, a.flags, terms);
     kkv<<<grid, kThreads, kDkvBytes, a.stream>>>(*a.tmK64, *a.tmV64, *a.tmQ64, *a.tmdO64, *a.tmdK64, *a.tmdV64,
                                                  a.col_ptr, a.row_idx, a.pairs, a.lse_pad, a.delta, a.nb, a.S, a.scale,
-                                                 scale_log2, a.dK, a.dV, a.flags, terms);
+                                                 scale_log2, a.flags, terms);
     return cudaGetLastError() == cudaSuccess ? TSA_OK : TSA_ERR_CUDA;
 }
 

@@ -146,15 +146,6 @@ __device__ __forceinline__ float lambda_of(const DiffTerms &t, int head, float *
     return e1 - e2 + t.init;
 }
 
-// Loads and stores of a box of rows: a term's kernels see [lanes, S, D] as three dimensions, so
-// that rows past a lane's end read as zero and are never written; the plain kernels keep theirs.
-template <class Terms>
-__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, int x, int row0, int y, int lane,
-                                          uint32_t bar) {
-    if constexpr (Terms::kBias || Terms::kDiff) tma_load_3d(dst, map, x, y, lane, bar);
-    else tma_load_2d(dst, map, x, row0 + y, bar);
-}
-
 // Makes a 128-row tile of two copies of the same 64 rows block-diagonal: rows 0-63 keep the first
 // half of their columns, rows 64-127 the second, so that one product with [x1 | x2] gives x1 in
 // the upper and x2 in the lower rows.  `row` is the calling thread's (0-127); SW128 layout.

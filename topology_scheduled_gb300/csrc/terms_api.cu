@@ -114,7 +114,7 @@ tsa_status forward_launch(const void *Q, const void *K, const void *V, const int
     a->row_ptr = row_ptr;
     a->col_idx = col_idx;
     a->nnz_cap = (int)nnz_cap;
-    a->O = static_cast<uint16_t *>(O2);
+    a->with_o2 = O2 != nullptr;
     a->lse = lse;
     a->nb = (int)((S + 63) / 64);
     a->gran = block == 128 ? 1 : block == 32 ? 2 : 0;
@@ -189,9 +189,6 @@ tsa_status backward_launch(const void *Q, const void *K, const void *V, const vo
     a->tmdV64 = &m->dv;
     a->O = static_cast<const uint16_t *>(O);
     a->dO = static_cast<const uint16_t *>(dO);
-    a->dQ = static_cast<uint16_t *>(dQ);
-    a->dK = static_cast<uint16_t *>(dK);
-    a->dV = static_cast<uint16_t *>(dV);
     a->lse = lse;
     a->row_ptr = row_ptr;
     a->col_idx = col_idx;

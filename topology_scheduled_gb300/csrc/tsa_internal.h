@@ -23,8 +23,7 @@ namespace tsa {
 tsa_status current_device(int *dev);
 tsa_status device_flags(int dev, DeviceFlags *f);
 tsa_status check_device_ptr(const void *p, int dev);
-// Row-major 16-bit tensors [rows, cols] and [lanes, rows, cols]; boxes of 64 columns x box_rows.
-bool encode_2d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// Row-major 16-bit tensor [lanes, rows, cols]; boxes of 64 columns x box_rows, cut off at a lane's end.
 bool encode_3d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t lanes, uint64_t rows, uint64_t cols,
                uint32_t box_rows);
 bool overlaps(const void *a, size_t na, const void *b, size_t nb);
@@ -46,8 +45,7 @@ struct AttnLaunch {
     const CUtensorMap *tmO2;  // differential: the second map's output (otherwise tmO again)
     const int32_t *row_ptr, *col_idx;
     int nnz_cap;  // entries of col_idx (read with score terms only)
-    uint16_t *O;  // the output (a partial last block is written with plain stores); differential:
-                  // the second map's output, null when it is not wanted
+    bool with_o2;  // differential: the second map's output is wanted
     float *lse;  // optional: natural-log log-sum-exp of the scaled scores per query row
     int nb, S, D, lanes;  // nb: 64-token blocks
     bool bf16;
@@ -76,7 +74,6 @@ struct BwdLaunch {
     const CUtensorMap *tmQ128, *tmdO128;
     const CUtensorMap *tmQ64, *tmdO64, *tmK64, *tmV64, *tmdQ64, *tmdK64, *tmdV64;
     const uint16_t *O, *dO;
-    uint16_t *dQ, *dK, *dV;  // for the row stores of a partial last block
     const float *lse;
     const int32_t *row_ptr, *col_idx;
     int64_t nnz_cap;
