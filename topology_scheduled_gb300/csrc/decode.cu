@@ -308,7 +308,7 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
                 a = a * f + a2 * f2;
                 mx = mn;
             }
-            o[m] = l > 0.f ? a / l : 0.f;
+            o[m] = l == 0.f ? 0.f : a / l;  // (a NaN among the scores is the answer's, too)
         }
         float y = o[0];
         if constexpr (kDiff) y = fmaf(-lam, o[1], o[0]);
