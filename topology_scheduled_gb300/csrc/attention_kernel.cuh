@@ -887,7 +887,8 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
             if (lse_out && tok_ok) {
                 long long at = (long long)lane_id * S + tok;
                 if constexpr (kDiff) at += half * terms.map_rows;
-                lse_out[at] = l_sum > 0.f ? (m_used + log2f(kDiff ? l_exact : l_sum)) * 0.6931471805599453f : -INFINITY;
+                // (of a row with a NaN score it is NaN, and so are the weights that the backward pass forms)
+                lse_out[at] = l_sum == 0.f ? -INFINITY : (m_used + log2f(kDiff ? l_exact : l_sum)) * 0.6931471805599453f;
             }
             const uint32_t sw = (uint32_t)(tid & 7);
             __syncwarp();
