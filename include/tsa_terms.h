@@ -65,6 +65,9 @@ tsa_status tsa_biased_attention_fwd(const void *Q, const void *K, const void *V,
  *   O2            out, the second map's softmax(..) V, shaped as O, or NULL; the backward call
  *                 needs it.
  *   lse           out, [2, B*H, S] float32: each map's log-sum-exp, or NULL.
+ * The maps share their products with K (zeros stand in for the other map's half of Q), so what is not
+ * finite in either half of a key makes both maps of the rows that see it NaN; K must be finite, also
+ * where an infinity should leave a key out.
  * The other arguments, limits and errors are those of tsa_biased_attention_fwd.
  */
 tsa_status tsa_differential_attention_fwd(const void *Q, const void *K, const void *V,

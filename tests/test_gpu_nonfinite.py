@@ -91,3 +91,31 @@ def test_training(which, bad, S, D, dtype):
     if which == "differential":
         for x, w in zip(grads[3:], grads0[3:]):
             assert bool(torch.isnan(x[1]).all()) and torch.equal(x[others], w[others])
+
+
+@pytest.mark.parametrize("which,low", [("plain", -float("inf")), ("biased", -float("inf")), ("plain", -3e38), ("biased", -3e38),
+                                       ("differential", -3e38)])  # (a differential form's keys are finite)
+@pytest.mark.parametrize("H,S,D,dtype", [(2, 300, 64, torch.float16), (1, 250, 128, torch.bfloat16), (260, 256, 64, torch.bfloat16)])
+def test_scores_of_minus_infinity(which, low, H, S, D, dtype):
+    """A first block whose scores are all -inf, of infinite keys or by overflow, weighs as one that no row
+    lists.  (260 heads: the differential form's layout for many tiles.)"""
+    if dtype == torch.float16 and low > -float("inf"):
+        low = -65504.0  # (no overflow in f16: weights that are 0 beside any other)
+    g = torch.Generator().manual_seed(S)
+    q, k, v = (torch.randn((1, H, S, D), generator=g).to(dtype).to(DEV) for _ in range(3))
+    q = q.abs() + 0.25
+    k[:, :, :64] = low
+    bias, lam = _learned(H, D, dtype)
+    fwd, _, extra = _calls(which, bias, lam)
+    nb = -(-S // 64)
+    rows = [list(range(i + 1)) for i in range(nb)]
+    got = fwd(q, k, v, *_lists(rows), *extra)
+    want = fwd(q, k, v, *_lists([r[1:] for r in rows]), *extra)
+    assert tsa.tsa_last_device_status() == 0
+    first = 64 if low == -65504.0 else 0  # (rows of that block have no other keys)
+    for x, w in zip(got[:-1], want[:-1]):
+        assert torch.equal(x[:, :, first:], w[:, :, first:])
+    lse, wanted = (x[-1].reshape(-1, H, S) for x in (got, want))
+    assert torch.equal(lse[..., first:], wanted[..., first:])
+    if not first:
+        assert bool((got[0][:, :, :64] == 0).all()) and bool((lse[..., :64] == -float("inf")).all())

@@ -805,8 +805,8 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 }
                 // p = 2^(x * scale * log2(e) - m): one packed FMA per pair, exp2 on the MUFU
                 const float c1 = kBias ? cc1 : scale_log2;
-                float n1 = -m_used;
-                if constexpr (kBias) n1 = m_used == -INFINITY ? off : off - m_used;  // no key with weight yet
+                float n1 = m_used == -INFINITY ? 0.f : -m_used;  // (no key with weight yet: all scores are -inf)
+                if constexpr (kBias) n1 += off;
                 const uint64_t cc = f2_pack(c1, c1);
                 const uint64_t nm = f2_pack(n1, n1);
                 auto weigh = [&, cc, nm](auto exact_too) {
