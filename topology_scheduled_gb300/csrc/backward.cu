@@ -382,9 +382,12 @@ tsa_status launch_backward_schedule(BwdLaunch *launch) {
     {
         int pow2 = 1;
         while (pow2 < nb) pow2 <<= 1;
-        const size_t smem = sizeof(unsigned long long) * (size_t)pow2;  // <= 64 KB (nb <= 8192)
-        if (cudaFuncSetAttribute(bwd_col_pairs, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-            return TSA_ERR_CUDA;
+        const size_t smem = sizeof(unsigned long long) * (size_t)pow2;
+        // (the limit is the kernel's, not the call's: always the most that any call needs, so that no call
+        // on another thread lowers it before this launch)
+        static std::atomic<unsigned long long> ready{0};
+        constexpr int kMost = (int)(sizeof(unsigned long long) * kMaxBackwardBlocks);
+        if (!allow_smem(ready, reinterpret_cast<const void *>(bwd_col_pairs), kMost)) return TSA_ERR_CUDA;
         bwd_col_pairs<<<1, 1024, smem, st>>>(nb, pow2, a.cnt, a.pairs);
     }
     return cudaGetLastError() == cudaSuccess ? TSA_OK : TSA_ERR_CUDA;
