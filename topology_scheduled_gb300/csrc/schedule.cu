@@ -1338,10 +1338,19 @@ int next_pow2(int n) {
     return p;
 }
 
-template <typename K>
-bool set_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
-           cudaSuccess;
+constexpr int kGraphThreads = 512;
+
+// Dynamic shared memory of schedule_graph_kernel: the largest of its phases, and from *xs_offset on the
+// threads' scratch.
+size_t graph_smem(int nb, size_t *xs_offset) {
+    const int pow2 = next_pow2(nb), words = (nb + 31) / 32;
+    const size_t merge = (size_t)nb * (8 + 8 + 4 + 4);
+    const size_t elder = (size_t)pow2 * 16 + (size_t)nb * 16;  // edges, sizes, parents, 2 claims
+    const size_t topk = (size_t)pow2 * 20 + (size_t)(kGraphThreads / 32) * words * 4;
+    size_t most = merge > elder ? merge : elder;
+    if (topk > most) most = topk;
+    *xs_offset = (most + 15) & ~(size_t)15;
+    return *xs_offset + (size_t)kGraphThreads * 16;
 }
 
 }  // namespace
@@ -1482,16 +1491,14 @@ tsa_status launch_schedule_from_sums(const ScheduleLaunch &a, const double *sums
     int rounds = 0;
     while ((1 << rounds) < nb) ++rounds;
     const int pow2 = next_pow2(nb);
-    const int words = (nb + 31) / 32;
-    constexpr int kGraphThreads = 512;
-    const size_t merge_smem = (size_t)nb * (8 + 8 + 4 + 4);
-    const size_t elder_smem = (size_t)pow2 * 16 + (size_t)nb * 16;  // edges, sizes, parents, 2 claims
-    const size_t topk_smem = (size_t)pow2 * 20 + (size_t)(kGraphThreads / 32) * words * 4;
-    size_t smem = merge_smem > elder_smem ? merge_smem : elder_smem;
-    if (topk_smem > smem) smem = topk_smem;
-    const size_t xs_offset = (smem + 15) & ~(size_t)15;
-    smem = xs_offset + (size_t)kGraphThreads * 16;
-    if (!set_smem(schedule_graph_kernel, smem)) return TSA_ERR_CUDA;
+    size_t xs_offset, unused;
+    const size_t smem = graph_smem(nb, &xs_offset);
+    // (the limit is the kernel's, not the call's: always the most that any call needs, so that no call on
+    // another thread lowers it before this launch)
+    static std::atomic<unsigned long long> ready{0};
+    if (!allow_smem(ready, reinterpret_cast<const void *>(schedule_graph_kernel),
+                    (int)graph_smem((int)kMaxScheduleBlocks, &unused)))
+        return TSA_ERR_CUDA;
     int dev = 0, sms = 0, per_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
