@@ -290,6 +290,9 @@ __device__ __forceinline__ void add_distances(float *bins, float *win, float a0,
 // A warp keeps the sums of dS of the first distances one by one until its tile is done; farther ones go
 // to its bucket sums step by step.
 constexpr int kNearSums = 256;
+// A warp's row of them: distances below zero lie behind the mask, and a step whose farthest distance is the
+// last one kept has its last lane add a 0 one place on.
+constexpr int kNearRow = kDistFront + kNearSums + 1;
 
 template <int D, class Terms>
 struct DqSmem {
@@ -305,7 +308,7 @@ struct DqSmem {
     static constexpr int kOffWin = kOffTable + kBucketTableBytes;                // a window of each warp
     static constexpr int kOffBins = kOffWin + kEltWarps * kWindow * 4;           // kMaxBuckets sums of each warp
     static constexpr int kOffNear = kOffBins + kEltWarps * kMaxBuckets * 4;      // sums by distance of each warp
-    static constexpr int kEnd = Terms::kBias ? kOffNear + kEltWarps * (kDistFront + kNearSums) * 4 : kOffTable;
+    static constexpr int kEnd = Terms::kBias ? kOffNear + kEltWarps * kNearRow * 4 : kOffTable;
     static constexpr int kBytes = smem_bytes_one_cta(kEnd + 1024);  // + alignment slack
 };
 
@@ -561,13 +564,13 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
         [[maybe_unused]] float *bins = reinterpret_cast<float *>(smem + L::kOffBins) + warp * kMaxBuckets;
         [[maybe_unused]] float *near_sums =
-            reinterpret_cast<float *>(smem + L::kOffNear) + warp * (kDistFront + kNearSums) + kDistFront;
+            reinterpret_cast<float *>(smem + L::kOffNear) + warp * kNearRow + kDistFront;
         [[maybe_unused]] const int wlane = tid & 31;
         [[maybe_unused]] int known = 0;  // distances in the table
         [[maybe_unused]] int last_bucket = 0, last_start = 0;
         if constexpr (kBias) {
             for (int b = wlane; b < kMaxBuckets; b += 32) bins[b] = 0.f;
-            for (int d = wlane - kDistFront; d < kNearSums; d += 32) near_sums[d] = 0.f;
+            for (int d = wlane - kDistFront; d < kNearRow - kDistFront; d += 32) near_sums[d] = 0.f;
             table.template load<kBF16>(terms, lane_id % terms.H, tid, kElt);
             named_barrier(2, kElt);
             last_bucket = terms.n - 1;
@@ -737,7 +740,6 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 // the warps' bucket sums and their sums by distance, a thread per bucket
                 const float *all = reinterpret_cast<const float *>(smem + L::kOffBins);
                 const float *by = reinterpret_cast<const float *>(smem + L::kOffNear) + kDistFront;
-                constexpr int kOne = kDistFront + kNearSums;
                 float *to = partial + ((long long)lane_id * gridDim.y + tile) * terms.n;
                 for (int b = tid; b < terms.n; b += kElt) {
                     float s = 0.f;
@@ -746,7 +748,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     const int end = b < last_bucket ? min(table.start[b + 1], kNearSums) : 0;
                     for (int d = table.start[b]; d < end; ++d)
 #pragma unroll
-                        for (int w = 0; w < kEltWarps; ++w) s += by[w * kOne + d];
+                        for (int w = 0; w < kEltWarps; ++w) s += by[w * kNearRow + d];
                     to[b] = s;
                 }
             }
