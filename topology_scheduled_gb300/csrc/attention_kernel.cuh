@@ -50,15 +50,14 @@
 //    what a plain one of the same D does and no row union is needed.  The zeros double the score
 //    product's multiplications, but a 64-row product would run at half the rate: the tensor time
 //    is the same.  The epilogue subtracts the lower rows from the upper through shared memory.
-//    At D = 64 and many tiles three CTAs share an SM (kThree), as two leave half of the issue slots empty.
+//    At D = 64, many tiles and short rows three CTAs share an SM (kThree), as two leave half of the issue slots empty.
 //    Three leave 96 registers per thread and 128 TMEM columns per CTA (one allocation, so that no CTA
 //    waits for columns while it holds some).  So a softmax thread takes its 64 scores in two parts of
 //    32, the first one read twice (for the maximum and for the weights); there is one S buffer beside
 //    O, the next scores are computed once the softmax warps have read S, and P goes through 16 KB of
-//    shared memory, written once the product that read the last one is done.  64 heads of 8192 tokens:
-//    184 -> 163 us.  P over the one S buffer, which makes every step run in series, lost (26 blocks a row:
-//    338 us against 326 with two CTAs), and a bias gains nothing (108 us either way), as the steps near
-//    the diagonal then add it twice.
+//    shared memory, written once the product that read the last one is done (figures at launch_gran).  P
+//    over the one S buffer, which makes every step run in series, lost to two CTAs, and a bias gains
+//    nothing, as the steps near the diagonal then add it twice.
 // Measured at [1, 32, 32768, 128] bf16, 14.5 blocks a row: plain 0.42 ms (1190 TFLOP/s on visited blocks),
 // biased 0.45 ms, differential 0.85 ms, 0.90 ms with what its backward needs (twice the tiles: 1100
 // TFLOP/s executed).  Bound by the softmax warps' chain of a step beside a tensor pipe that is active for
@@ -1023,10 +1022,20 @@ template <int kGran, class Terms>
 tsa_status launch_gran(const AttnLaunch &a, const Terms &terms) {
     if (a.D == 64) {
         if constexpr (Terms::kDiff) {
-            // Three CTAs per SM for many tiles: 64 heads of 8192 tokens, 15 blocks a row, 184 us with two and
-            // 163 with three, dense 1265 and 1271.  With a few tiles per SM the longer step of one CTA shows
-            // (16 tiles, rows of up to 32 blocks: 21 and 26 us).
-            if ((long long)a.nb * a.lanes > 1024)
+            // Three CTAs per SM hide more of a tile's start and end, two take less time for a step.  So three for
+            // more tiles than run at once, a few times over, and short rows.  us with two / three (f16, rows of
+            // random blocks, times without the host's):
+            //   blocks a row       2              4              8             16             32             64
+            //    512 tiles   11.0 / 11.6    13.8 / 15.4    19.0 / 22.3    28.9 / 30.3    48.9 / 45.4    65.6 / 67.2
+            //   1024         19.3 / 17.4    24.6 / 23.2    34.5 / 34.6    51.1 / 51.7    76.6 / 80.5   107.3 / 118.8
+            //   2048         33.8 / 29.2    43.4 / 39.6    60.9 / 58.7    92.5 / 92.4   141.6 / 146.1  189.8 / 199.7
+            //   8192        134.7 / 109.4  169.3 / 146.8  233.2 / 212.9  349.6 / 335.6  531.0 / 528.8  690.6 / 696.7
+            // (64 blocks a head; 16, 32, 128 and 256 differ by a few percent).  The average row is that of the
+            // capacity of col_idx, as the host knows no other.
+            const int rows = a.gran == 1 ? (a.nb + 1) / 2 : a.gran == 2 ? (a.S + 31) / 32 : a.nb;
+            const int block = a.gran == 1 ? 128 : a.gran == 2 ? 32 : 64;
+            const bool short_rows = (long long)a.nnz_cap * block <= 16ll * 64 * rows;
+            if ((long long)a.nb * a.lanes > 1024 && short_rows)
                 return a.bf16 ? launch_one<64, true, true, kGran>(a, terms) : launch_one<64, true, false, kGran>(a, terms);
         }
         return a.bf16 ? launch_one<64, false, true, kGran>(a, terms) : launch_one<64, false, false, kGran>(a, terms);
