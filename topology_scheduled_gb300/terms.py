@@ -51,14 +51,14 @@ def _starts(bucket_starts, bias):
     return starts, len(starts)
 
 
-def _schedule(row_ptr, col_idx, rows, device):
+def _schedule(row_ptr, col_idx, rows, device, other):
     """Checks a CSR of `rows` rows; col_idx with at least one entry."""
     for t in (row_ptr, col_idx):
         if t.dtype is not torch.int32 or t.device != device or not t.is_contiguous():
             raise ValueError("row_ptr and col_idx must be contiguous int32 tensors on the inputs' device")
     if row_ptr.numel() != rows + 1:
         raise ValueError(f"row_ptr must hold {rows + 1} entries")
-    return col_idx if col_idx.numel() > 0 else torch.zeros(1, dtype=torch.int32, device=device)
+    return col_idx if col_idx.numel() > 0 else _made(other, torch.zeros, 1, dtype=torch.int32, device=device)
 
 
 def _learned(name, t, shape, like):
@@ -66,13 +66,13 @@ def _learned(name, t, shape, like):
         raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(shape)} on {like.device}")
 
 
-def _output(name, t, like):
+def _output(name, t, like, other):
     """`t`, or a new tensor shaped as `like`."""
-    return torch.empty_like(like) if t is None else _given(name, t, like.shape, like.dtype, like.device)
+    return _made(other, torch.empty_like, like) if t is None else _given(name, t, like.shape, like.dtype, like.device)
 
 
-def _rows_f32(name, t, shape, device):
-    return torch.empty(shape, dtype=torch.float32, device=device) if t is None else \
+def _rows_f32(name, t, shape, device, other):
+    return _made(other, torch.empty, shape, dtype=torch.float32, device=device) if t is None else \
         _given(name, t, shape, torch.float32, device)
 
 
@@ -82,17 +82,26 @@ def _given(name, t, shape, dtype, device):
     return t
 
 
-def _on(stream, device, *tensors):
-    """The handle of `stream`, or of the device's current stream; memory made here for another stream
-    than the current one is kept until that stream has used it."""
+def _on(stream, device):
+    """The handle of `stream`, or of the device's current stream, and `stream` itself if it is another."""
+    current = torch._C._cuda_getCurrentRawStream(device.index)
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return current, None
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
-    if s.cuda_stream != torch._C._cuda_getCurrentRawStream(device.index):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
-    return s.cuda_stream
+    return s.cuda_stream, None if s.cuda_stream == current else s
+
+
+def _made(other, make, *args, **kw):
+    """make(..), for use by a call on the stream `other` (None: on the current one).  Its memory is then that
+    stream's own, which nothing that the current stream still runs has a hand in, and is not given away before
+    the current stream has done what it is asked to do with it."""
+    if other is None:
+        return make(*args, **kw)
+    here = torch.cuda.current_stream(other.device)
+    with torch.cuda.stream(other):
+        t = make(*args, **kw)
+    t.record_stream(here)
+    return t
 
 
 def _blocks(S, block):
@@ -126,15 +135,16 @@ def tsa_biased_attention_fwd(Q, K, V, row_ptr, col_idx, bias, bucket_starts, sca
     _check_qkv(Q=Q, K=K, V=V)
     B, H, S, D = _lanes_S_D(Q)
     dev = Q.device
-    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
+    handle, other = _on(stream, dev)
+    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev, other)
     starts, n = _starts(bucket_starts, bias)
     _learned("bias", bias, (H, n), Q)
-    out = _output("out", out, Q)
-    lse = _rows_f32("lse", lse, (B * H, S), dev) if with_lse else None
+    out = _output("out", out, Q, other)
+    lse = _rows_f32("lse", lse, (B * H, S), dev, other) if with_lse else None
     _check(lib().tsa_biased_attention_fwd(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(), bias.data_ptr(),
         starts.buffer_info()[0], n, out.data_ptr(), lse.data_ptr() if with_lse else None, _dtype_code(Q), B, H, S, D, block,
-        1.0 / math.sqrt(D) if scale is None else float(scale), _on(stream, Q.device, out, lse, ci)), "tsa_biased_attention_fwd")
+        1.0 / math.sqrt(D) if scale is None else float(scale), handle), "tsa_biased_attention_fwd")
     return (out, lse) if with_lse else out
 
 
@@ -160,29 +170,30 @@ def tsa_differential_attention_fwd(Q, K, V, row_ptr, col_idx, lambda_q1, lambda_
     _check_qkv(Q=Q, K=K, V=V)
     B, H, S, D = _lanes_S_D(Q)
     dev = Q.device
-    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
+    handle, other = _on(stream, dev)
+    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev, other)
     lambdas = (lambda_q1, lambda_k1, lambda_q2, lambda_k2)
     heads = _lambda_heads(lambdas, H, D, Q)
-    out = _output("out", out, Q)
+    out = _output("out", out, Q, other)
     if for_backward:
-        out2 = _output("out2", out2, Q)
-        lse = _rows_f32("lse", lse, (2, B * H, S), dev)
+        out2 = _output("out2", out2, Q, other)
+        lse = _rows_f32("lse", lse, (2, B * H, S), dev, other)
     else:
         out2 = lse = None
     _check(lib().tsa_differential_attention_fwd(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(),
         *(t.data_ptr() for t in lambdas), heads, float(lambda_init), out.data_ptr(),
         out2.data_ptr() if for_backward else None, lse.data_ptr() if for_backward else None, _dtype_code(Q), B, H, S,
-        D, block, (D / 2) ** -0.5 if scale is None else float(scale), _on(stream, Q.device, out, out2, lse, ci)),
+        D, block, (D / 2) ** -0.5 if scale is None else float(scale), handle),
         "tsa_differential_attention_fwd")
     return (out, out2, lse) if for_backward else out
 
 
-def _workspace(t, need, device, where):
+def _workspace(t, need, device, where, other):
     if need == 0:
         raise TsaError(2, where)
     if t is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return _made(other, torch.empty, need, dtype=torch.uint8, device=device)
     if t.dtype != torch.uint8 or t.device != device or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
     return t
@@ -196,20 +207,21 @@ def tsa_biased_attention_backward(Q, K, V, O, dO, lse, row_ptr, col_idx, bias, b
     _check_qkv(Q=Q, K=K, V=V, O=O, dO=dO)
     B, H, S, D = _lanes_S_D(Q)
     dev = Q.device
-    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
+    handle, other = _on(stream, dev)
+    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev, other)
     starts, n = _starts(bucket_starts, bias)
     _learned("bias", bias, (H, n), Q)
     _given("lse", lse, (B * H, S), torch.float32, dev)
     L = lib()
     workspace = _workspace(workspace, int(L.tsa_biased_attention_backward_workspace_bytes(B * H, S, block, ci.numel(), n)),
-                           dev, "tsa_biased_attention_backward_workspace_bytes")
-    dq, dk, dv = (_output(name, t, Q) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
-    dbias = _output("dbias", dbias, bias)
+                           dev, "tsa_biased_attention_backward_workspace_bytes", other)
+    dq, dk, dv = (_output(name, t, Q, other) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
+    dbias = _output("dbias", dbias, bias, other)
     _check(L.tsa_biased_attention_backward(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), lse.data_ptr(), row_ptr.data_ptr(),
         ci.data_ptr(), ci.numel(), bias.data_ptr(), starts.buffer_info()[0], n, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
         dbias.data_ptr(), _dtype_code(Q), B, H, S, D, block, 1.0 / math.sqrt(D) if scale is None else float(scale),
-        workspace.data_ptr(), workspace.numel(), _on(stream, Q.device, workspace, dq, dk, dv, dbias, ci)),
+        workspace.data_ptr(), workspace.numel(), handle),
         "tsa_biased_attention_backward")
     return dq, dk, dv, dbias
 
@@ -224,22 +236,23 @@ def tsa_differential_attention_backward(Q, K, V, O, O2, dO, lse, row_ptr, col_id
     _check_qkv(Q=Q, K=K, V=V, O=O, O2=O2, dO=dO)
     B, H, S, D = _lanes_S_D(Q)
     dev = Q.device
-    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev)
+    handle, other = _on(stream, dev)
+    ci = _schedule(row_ptr, col_idx, _blocks(S, block), dev, other)
     lambdas = (lambda_q1, lambda_k1, lambda_q2, lambda_k2)
     heads = _lambda_heads(lambdas, H, D, Q)
     _given("lse", lse, (2, B * H, S), torch.float32, dev)
     L = lib()
     workspace = _workspace(workspace,
                            int(L.tsa_differential_attention_backward_workspace_bytes(B * H, S, block, ci.numel())), dev,
-                           "tsa_differential_attention_backward_workspace_bytes")
-    dq, dk, dv = (_output(name, t, Q) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
-    dlambdas = [_output("dlambdas", None if dlambdas is None else dlambdas[i], t) for i, t in enumerate(lambdas)]
+                           "tsa_differential_attention_backward_workspace_bytes", other)
+    dq, dk, dv = (_output(name, t, Q, other) for name, t in (("dq", dq), ("dk", dk), ("dv", dv)))
+    dlambdas = [_output("dlambdas", None if dlambdas is None else dlambdas[i], t, other) for i, t in enumerate(lambdas)]
     _check(L.tsa_differential_attention_backward(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), O2.data_ptr(), dO.data_ptr(), lse.data_ptr(),
         row_ptr.data_ptr(), ci.data_ptr(), ci.numel(), *(t.data_ptr() for t in lambdas), heads, float(lambda_init),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *(t.data_ptr() for t in dlambdas), _dtype_code(Q), B, H, S, D,
         block, (D / 2) ** -0.5 if scale is None else float(scale), workspace.data_ptr(), workspace.numel(),
-        _on(stream, Q.device, workspace, dq, dk, dv, *dlambdas, ci)), "tsa_differential_attention_backward")
+        handle), "tsa_differential_attention_backward")
     return (dq, dk, dv, *dlambdas)
 
 
@@ -264,14 +277,15 @@ def tsa_biased_attention_decode(Q, K, V, seq_lens, row_ptr, col_idx, bias, bucke
     ``seq_lens[b]`` tokens are sequence b's, the new one last.  Row b of the CSR lists the cache blocks
     that sequence b's token visits; scores as in tsa_biased_attention.  Returns [B, H, D]."""
     B, H, cap, D = _cache(Q, K, V, seq_lens)
-    ci = _schedule(row_ptr, col_idx, B, Q.device)
+    handle, other = _on(stream, Q.device)
+    ci = _schedule(row_ptr, col_idx, B, Q.device, other)
     starts, n = _starts(bucket_starts, bias)
     _learned("bias", bias, (H, n), Q)
-    out = _output("out", out, Q)
+    out = _output("out", out, Q, other)
     _check(lib().tsa_biased_attention_decode(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(),
         bias.data_ptr(), starts.buffer_info()[0], n, out.data_ptr(), _dtype_code(Q), B, H, cap, D, block,
-        1.0 / math.sqrt(D) if scale is None else float(scale), _on(stream, Q.device, out, ci)), "tsa_biased_attention_decode")
+        1.0 / math.sqrt(D) if scale is None else float(scale), handle), "tsa_biased_attention_decode")
     return out
 
 
@@ -281,13 +295,14 @@ def tsa_differential_attention_decode(Q, K, V, seq_lens, row_ptr, col_idx, lambd
     """One new token per sequence, as tsa_biased_attention_decode, with the two maps of
     tsa_differential_attention."""
     B, H, cap, D = _cache(Q, K, V, seq_lens)
-    ci = _schedule(row_ptr, col_idx, B, Q.device)
+    handle, other = _on(stream, Q.device)
+    ci = _schedule(row_ptr, col_idx, B, Q.device, other)
     lambdas = (lambda_q1, lambda_k1, lambda_q2, lambda_k2)
     heads = _lambda_heads(lambdas, H, D, Q)
-    out = _output("out", out, Q)
+    out = _output("out", out, Q, other)
     _check(lib().tsa_differential_attention_decode(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), seq_lens.data_ptr(), row_ptr.data_ptr(), ci.data_ptr(), ci.numel(),
         *(t.data_ptr() for t in lambdas), heads, float(lambda_init), out.data_ptr(), _dtype_code(Q), B, H, cap, D,
-        block, (D / 2) ** -0.5 if scale is None else float(scale), _on(stream, Q.device, out, ci)),
+        block, (D / 2) ** -0.5 if scale is None else float(scale), handle),
         "tsa_differential_attention_decode")
     return out
