@@ -132,6 +132,29 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on(stream, device):
+    """The handle of `stream`, or of the device's current stream, and `stream` itself if it is another."""
+    current = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
+    if stream is None:
+        return current, None
+    s = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device)
+    return s.cuda_stream, None if s.cuda_stream == current else s
+
+
+def _made(other, make, *args, **kw):
+    """make(..), for use by a call on the stream `other` (None: on the current one).  Its memory is then that
+    stream's own, which nothing that the current stream still runs has a hand in, and is not given away before
+    the current stream has done what it is asked to do with it."""
+    if other is None:
+        return make(*args, **kw)
+    here = torch.cuda.current_stream(other.device)
+    with torch.cuda.stream(other):
+        t = make(*args, **kw)
+    t.record_stream(here)
+    return t
+
+
 def _lanes_S_D(x: torch.Tensor):
     shape = tuple(x.shape)
     if 2 <= len(shape) <= 4:
@@ -173,18 +196,19 @@ def tsa_build_schedule(K: torch.Tensor, block: int = 64, sink: int = 1, local_ra
     if ws_bytes == 0:
         raise TsaError(2, "tsa_build_schedule_workspace_bytes")
     dev = K.device
+    handle, other = _on(stream, dev)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _made(other, torch.empty, ws_bytes, dtype=torch.uint8, device=dev)
     if row_ptr is None:
-        row_ptr = torch.empty(nb + 1, dtype=torch.int32, device=dev)
+        row_ptr = _made(other, torch.empty, nb + 1, dtype=torch.int32, device=dev)
     if col_idx is None:
-        col_idx = torch.empty(max(cap, 1), dtype=torch.int32, device=dev)
-    sal = torch.empty(nb, dtype=torch.float64, device=dev) if salience else None
+        col_idx = _made(other, torch.empty, max(cap, 1), dtype=torch.int32, device=dev)
+    sal = _made(other, torch.empty, nb, dtype=torch.float64, device=dev) if salience else None
     _check(L.tsa_build_schedule_ex(K.data_ptr(), _dtype_code(K), lanes, S, D, block, sink,
                                    local_radius, topk, TIE_RULES[tie_break], row_ptr.data_ptr(),
                                    col_idx.data_ptr(), col_idx.numel(),
                                    sal.data_ptr() if sal is not None else None,
-                                   workspace.data_ptr(), workspace.numel(), _stream(stream)),
+                                   workspace.data_ptr(), workspace.numel(), handle),
            "tsa_build_schedule_ex")
     return (row_ptr, col_idx, sal) if salience else (row_ptr, col_idx)
 
@@ -196,12 +220,13 @@ def tsa_block_sums(K: torch.Tensor, block: int = 64, *, out: torch.Tensor | None
     B, H, S, D = _lanes_S_D(K)
     lanes = B * H
     nb = -(-S // block) if block > 0 else 0  # a partial last block counts
+    handle, other = _on(stream, K.device)
     if out is None:
-        out = torch.empty((lanes, nb, D), dtype=torch.float64, device=K.device)
+        out = _made(other, torch.empty, (lanes, nb, D), dtype=torch.float64, device=K.device)
     elif out.dtype != torch.float64 or not out.is_contiguous() or out.numel() != lanes * nb * D:
         raise ValueError("out must be a contiguous float64 tensor of lanes * S/block * D elements")
     _check(lib().tsa_block_sums(K.data_ptr(), _dtype_code(K), lanes, S, D, block, out.data_ptr(),
-                                _stream(stream)), "tsa_block_sums")
+                                handle), "tsa_block_sums")
     return out
 
 
@@ -232,22 +257,23 @@ def tsa_build_schedule_from_sums(sums: torch.Tensor, block: int = 64, sink: int 
     if ws_bytes == 0:
         raise TsaError(2, "tsa_build_schedule_workspace_bytes")
     dev = sums.device
+    handle, other = _on(stream, dev)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _made(other, torch.empty, ws_bytes, dtype=torch.uint8, device=dev)
     if row_ptr is None:
-        row_ptr = torch.empty(nb + 1, dtype=torch.int32, device=dev)
+        row_ptr = _made(other, torch.empty, nb + 1, dtype=torch.int32, device=dev)
     if col_idx is None:
-        col_idx = torch.empty(max(cap, 1), dtype=torch.int32, device=dev)
+        col_idx = _made(other, torch.empty, max(cap, 1), dtype=torch.int32, device=dev)
     for t in (row_ptr, col_idx):
         if t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
             raise ValueError("row_ptr / col_idx must be contiguous int32 tensors on the sums' device")
     if row_ptr.numel() != nb + 1:
         raise ValueError("row_ptr must hold nb + 1 entries")
-    sal = torch.empty(nb, dtype=torch.float64, device=dev) if salience else None
+    sal = _made(other, torch.empty, nb, dtype=torch.float64, device=dev) if salience else None
     _check(L.tsa_build_schedule_from_sums(sums.data_ptr(), lanes, S, D, block, sink, local_radius, topk,
                                           TIE_RULES[tie_break], row_ptr.data_ptr(), col_idx.data_ptr(),
                                           col_idx.numel(), sal.data_ptr() if sal is not None else None,
-                                          workspace.data_ptr(), workspace.numel(), _stream(stream)),
+                                          workspace.data_ptr(), workspace.numel(), handle),
            "tsa_build_schedule_from_sums")
     return (row_ptr, col_idx, sal) if salience else (row_ptr, col_idx)
 
@@ -260,13 +286,14 @@ def tsa_fixed_segment_csr(S: int, block: int, segment_tokens: int, device=None, 
     """CSR of fixed segments of ``segment_tokens`` tokens, as int32 device tensors."""
     nb = S // block if block > 0 else 0
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    handle, other = _on(stream, dev)
     nnz = tsa_fixed_segment_nnz(S, block, segment_tokens)
     if nnz < 0:
         raise TsaError(1, "tsa_fixed_segment_nnz")
-    row_ptr = torch.empty(nb + 1, dtype=torch.int32, device=dev)
-    col_idx = torch.empty(max(nnz, 1), dtype=torch.int32, device=dev)
+    row_ptr = _made(other, torch.empty, nb + 1, dtype=torch.int32, device=dev)
+    col_idx = _made(other, torch.empty, max(nnz, 1), dtype=torch.int32, device=dev)
     _check(lib().tsa_fixed_segment_csr(S, block, segment_tokens, row_ptr.data_ptr(),
-                                       col_idx.data_ptr(), col_idx.numel(), _stream(stream)),
+                                       col_idx.data_ptr(), col_idx.numel(), handle),
            "tsa_fixed_segment_csr")
     return row_ptr, col_idx[:nnz]
 
@@ -283,11 +310,12 @@ def tsa_segment_csr(S: int, block: int, starts: torch.Tensor, *, col_cap: int | 
     nb = S // block if block > 0 else 0
     if col_cap is None:
         col_cap = max(nb * (nb + 1) // 2, 1)
-    row_ptr = torch.empty(nb + 1, dtype=torch.int32, device=starts.device)
-    col_idx = torch.empty(col_cap, dtype=torch.int32, device=starts.device)
+    handle, other = _on(stream, starts.device)
+    row_ptr = _made(other, torch.empty, nb + 1, dtype=torch.int32, device=starts.device)
+    col_idx = _made(other, torch.empty, col_cap, dtype=torch.int32, device=starts.device)
     _check(lib().tsa_segment_csr(S, block, starts.data_ptr() if starts.numel() else None,
                                  starts.numel(), row_ptr.data_ptr(), col_idx.data_ptr(), col_cap,
-                                 _stream(stream)), "tsa_segment_csr")
+                                 handle), "tsa_segment_csr")
     return row_ptr, col_idx
 
 
@@ -295,11 +323,12 @@ def tsa_dense_causal_csr(S: int, block: int = 64, device=None, stream=None):
     """Dense causal CSR (row i = blocks 0..i) as int32 device tensors."""
     nb = -(-S // block) if block > 0 else 0  # a partial last block counts
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-    row_ptr = torch.empty(nb + 1, dtype=torch.int32, device=dev)
+    handle, other = _on(stream, dev)
+    row_ptr = _made(other, torch.empty, nb + 1, dtype=torch.int32, device=dev)
     nnz = nb * (nb + 1) // 2
-    col_idx = torch.empty(max(nnz, 1), dtype=torch.int32, device=dev)
+    col_idx = _made(other, torch.empty, max(nnz, 1), dtype=torch.int32, device=dev)
     _check(lib().tsa_dense_causal_csr(S, block, row_ptr.data_ptr(), col_idx.data_ptr(),
-                                      col_idx.numel(), _stream(stream)), "tsa_dense_causal_csr")
+                                      col_idx.numel(), handle), "tsa_dense_causal_csr")
     return row_ptr, col_idx[:nnz] if nnz > 0 else col_idx[:0]
 
 
@@ -335,20 +364,21 @@ def tsa_scheduled_attention_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tenso
     _check_qkv(Q=Q, K=K, V=V)
     _check_csr(row_ptr, col_idx)
     B, H, S, D = _lanes_S_D(Q)
+    handle, other = _on(stream, Q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_like(Q)
+        out = _made(other, torch.empty_like, Q)
     elif out.shape != Q.shape or out.dtype != Q.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor with Q's shape and dtype")
     if with_lse and lse is None:
-        lse = torch.empty((B * H, S), dtype=torch.float32, device=Q.device)
-    ci = col_idx if col_idx.numel() > 0 else torch.zeros(1, dtype=torch.int32, device=Q.device)
+        lse = _made(other, torch.empty, (B * H, S), dtype=torch.float32, device=Q.device)
+    ci = col_idx if col_idx.numel() > 0 else _made(other, torch.zeros, 1, dtype=torch.int32, device=Q.device)
     _check(lib().tsa_scheduled_attention_fwd(Q.data_ptr(), K.data_ptr(), V.data_ptr(),
                                              row_ptr.data_ptr(), ci.data_ptr(), out.data_ptr(),
                                              lse.data_ptr() if with_lse else None,
                                              _dtype_code(Q), B, H, S, D, block, float(scale),
-                                             _stream(stream)), "tsa_scheduled_attention_fwd")
+                                             handle), "tsa_scheduled_attention_fwd")
     return (out, lse) if with_lse else out
 
 
@@ -363,25 +393,26 @@ def tsa_scheduled_attention_backward(Q, K, V, O, dO, lse, row_ptr, col_idx, scal
     _check_qkv(Q=Q, K=K, V=V, O=O, dO=dO)
     _check_csr(row_ptr, col_idx)
     B, H, S, D = _lanes_S_D(Q)
+    handle, other = _on(stream, Q.device)
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.numel() != B * H * S:
         raise ValueError("lse must be a contiguous float32 tensor of B*H*S elements")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    ci = col_idx if col_idx.numel() > 0 else torch.zeros(1, dtype=torch.int32, device=Q.device)
+    ci = col_idx if col_idx.numel() > 0 else _made(other, torch.zeros, 1, dtype=torch.int32, device=Q.device)
     nnz_cap = ci.numel()
     ws = tsa_attention_backward_workspace_bytes(B * H, S, block, nnz_cap)
     if ws == 0:
         raise TsaError(2, "tsa_attention_backward_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(ws, dtype=torch.uint8, device=Q.device)
-    dq = torch.empty_like(Q) if dq is None else dq
-    dk = torch.empty_like(K) if dk is None else dk
-    dv = torch.empty_like(V) if dv is None else dv
+        workspace = _made(other, torch.empty, ws, dtype=torch.uint8, device=Q.device)
+    dq = _made(other, torch.empty_like, Q) if dq is None else dq
+    dk = _made(other, torch.empty_like, K) if dk is None else dk
+    dv = _made(other, torch.empty_like, V) if dv is None else dv
     _check(lib().tsa_scheduled_attention_backward(
         Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), dO.data_ptr(), lse.data_ptr(),
         row_ptr.data_ptr(), ci.data_ptr(), nnz_cap, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
         _dtype_code(Q), B, H, S, D, block, float(scale), workspace.data_ptr(), workspace.numel(),
-        _stream(stream)), "tsa_scheduled_attention_backward")
+        handle), "tsa_scheduled_attention_backward")
     return dq, dk, dv
 
 
@@ -420,6 +451,7 @@ def tsa_topology_attention_host(hQ: torch.Tensor, hK: torch.Tensor, hV: torch.Te
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    handle, other = _on(stream, dev)
     L = lib()
     nb = -(-S // block) if block > 0 else 0
     cap = int(L.tsa_schedule_max_nnz(S, block, sink, local_radius, topk))
@@ -429,13 +461,13 @@ def tsa_topology_attention_host(hQ: torch.Tensor, hK: torch.Tensor, hV: torch.Te
     if ws_bytes == 0:
         raise TsaError(2, "tsa_build_schedule_workspace_bytes")
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _made(other, torch.empty, ws_bytes, dtype=torch.uint8, device=dev)
     if row_ptr is None:
-        row_ptr = torch.empty(nb + 1, dtype=torch.int32, device=dev)
+        row_ptr = _made(other, torch.empty, nb + 1, dtype=torch.int32, device=dev)
     if col_idx is None:
-        col_idx = torch.empty(max(cap, 1), dtype=torch.int32, device=dev)
+        col_idx = _made(other, torch.empty, max(cap, 1), dtype=torch.int32, device=dev)
     if device_buffers is None:
-        device_buffers = tuple(torch.empty(hQ.shape, dtype=hQ.dtype, device=dev) for _ in range(4))
+        device_buffers = tuple(_made(other, torch.empty, hQ.shape, dtype=hQ.dtype, device=dev) for _ in range(4))
     if out is None:
         out = torch.empty(hQ.shape, dtype=hQ.dtype, pin_memory=True)
     dq, dk, dv, do = device_buffers
@@ -444,5 +476,5 @@ def tsa_topology_attention_host(hQ: torch.Tensor, hK: torch.Tensor, hV: torch.Te
                                          TIE_RULES[tie_break], float(scale), dq.data_ptr(), dk.data_ptr(),
                                          dv.data_ptr(), do.data_ptr(), row_ptr.data_ptr(), col_idx.data_ptr(),
                                          col_idx.numel(), workspace.data_ptr(), workspace.numel(), int(lane_chunk),
-                                         _stream(stream)), "tsa_topology_attention_host")
+                                         handle), "tsa_topology_attention_host")
     return out, row_ptr, col_idx

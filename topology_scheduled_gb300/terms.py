@@ -13,7 +13,7 @@ from array import array
 
 import torch
 
-from .binding import TsaError, _check, _check_qkv, _dtype_code, _lanes_S_D, lib
+from .binding import TsaError, _check, _check_qkv, _dtype_code, _lanes_S_D, _made, _on, lib
 
 MAX_BUCKETS = 256
 
@@ -79,28 +79,6 @@ def _rows_f32(name, t, shape, device, other):
 def _given(name, t, shape, dtype, device):
     if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return t
-
-
-def _on(stream, device):
-    """The handle of `stream`, or of the device's current stream, and `stream` itself if it is another."""
-    current = torch._C._cuda_getCurrentRawStream(device.index)
-    if stream is None:
-        return current, None
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
-    return s.cuda_stream, None if s.cuda_stream == current else s
-
-
-def _made(other, make, *args, **kw):
-    """make(..), for use by a call on the stream `other` (None: on the current one).  Its memory is then that
-    stream's own, which nothing that the current stream still runs has a hand in, and is not given away before
-    the current stream has done what it is asked to do with it."""
-    if other is None:
-        return make(*args, **kw)
-    here = torch.cuda.current_stream(other.device)
-    with torch.cuda.stream(other):
-        t = make(*args, **kw)
-    t.record_stream(here)
     return t
 
 
