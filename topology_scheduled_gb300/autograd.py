@@ -20,10 +20,17 @@ from .terms import (_starts, tsa_biased_attention_backward, tsa_biased_attention
                     tsa_differential_attention_backward, tsa_differential_attention_fwd)
 
 
+def _dense(t):
+    """`t` as the kernels read it: contiguous, from a 16-byte boundary on.  (The gradient that reaches a
+    backward pass may be a slice of another, at any element.)"""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class ScheduledAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, V, row_ptr, col_idx, scale, block):
-        Q, K, V = (t.contiguous() for t in (Q, K, V))
+        Q, K, V = (_dense(t) for t in (Q, K, V))
         O, lse = tsa_scheduled_attention_fwd(Q, K, V, row_ptr, col_idx, scale, block=block)
         ctx.save_for_backward(Q, K, V, O, lse, row_ptr, col_idx)
         ctx.scale = scale
@@ -33,7 +40,7 @@ class ScheduledAttention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dO):
         Q, K, V, O, lse, row_ptr, col_idx = ctx.saved_tensors
-        dQ, dK, dV = tsa_scheduled_attention_backward(Q, K, V, O, dO.contiguous(), lse, row_ptr, col_idx,
+        dQ, dK, dV = tsa_scheduled_attention_backward(Q, K, V, O, _dense(dO), lse, row_ptr, col_idx,
                                                       ctx.scale, block=ctx.block)
         return dQ, dK, dV, None, None, None, None
 
@@ -47,7 +54,7 @@ def scheduled_attention(Q, K, V, row_ptr, col_idx, scale: float | None = None, b
 class BiasedAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, V, row_ptr, col_idx, bias, bucket_starts, scale, block):
-        Q, K, V, bias = (t.contiguous() for t in (Q, K, V, bias))
+        Q, K, V, bias = _dense(Q), _dense(K), _dense(V), bias.contiguous()
         bucket_starts, _ = _starts(bucket_starts, bias)  # a copy: the caller's may change before the backward
         O, lse = tsa_biased_attention_fwd(Q, K, V, row_ptr, col_idx, bias, bucket_starts, scale, block=block)
         ctx.save_for_backward(Q, K, V, O, lse, row_ptr, col_idx, bias)
@@ -59,7 +66,7 @@ class BiasedAttention(torch.autograd.Function):
     def backward(ctx, dO):
         Q, K, V, O, lse, row_ptr, col_idx, bias = ctx.saved_tensors
         bucket_starts, scale, block = ctx.settings
-        dQ, dK, dV, dbias = tsa_biased_attention_backward(Q, K, V, O, dO.contiguous(), lse, row_ptr, col_idx, bias,
+        dQ, dK, dV, dbias = tsa_biased_attention_backward(Q, K, V, O, _dense(dO), lse, row_ptr, col_idx, bias,
                                                           bucket_starts, scale, block=block)
         return dQ, dK, dV, None, None, dbias, None, None, None
 
@@ -72,7 +79,7 @@ def biased_attention(Q, K, V, row_ptr, col_idx, bias, bucket_starts, scale: floa
 class DifferentialAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, V, row_ptr, col_idx, lambda_q1, lambda_k1, lambda_q2, lambda_k2, lambda_init, scale, block):
-        Q, K, V = (t.contiguous() for t in (Q, K, V))
+        Q, K, V = (_dense(t) for t in (Q, K, V))
         lambdas = [t.contiguous() for t in (lambda_q1, lambda_k1, lambda_q2, lambda_k2)]
         O, O2, lse = tsa_differential_attention_fwd(Q, K, V, row_ptr, col_idx, *lambdas, lambda_init, scale, block=block)
         ctx.save_for_backward(Q, K, V, O, O2, lse, row_ptr, col_idx, *lambdas)
@@ -84,7 +91,7 @@ class DifferentialAttention(torch.autograd.Function):
     def backward(ctx, dO):
         Q, K, V, O, O2, lse, row_ptr, col_idx, *lambdas = ctx.saved_tensors
         lambda_init, scale, block = ctx.settings
-        grads = tsa_differential_attention_backward(Q, K, V, O, O2, dO.contiguous(), lse, row_ptr, col_idx, *lambdas,
+        grads = tsa_differential_attention_backward(Q, K, V, O, O2, _dense(dO), lse, row_ptr, col_idx, *lambdas,
                                                     lambda_init, scale, block=block)
         return (*grads[:3], None, None, *grads[3:], None, None, None)
 
