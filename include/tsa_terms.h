@@ -87,8 +87,9 @@ tsa_status tsa_differential_attention_fwd(const void *Q, const void *K, const vo
  *   whose distance lies in bucket b,
  * sums in binary32, P and dS rounded to `dtype` for their products (dbias adds dS before its
  * rounding), results rounded once.  (A row of dS sums to zero, so the open last bucket gets
- * minus the sum of the row's others, in rows that reach it.)  The result does not depend on
- * the order in which thread blocks run.
+ * minus the sum of the row's others, in rows where any of its own dS is not 0.  It carries
+ * their error: Delta's, from the rounded O, times their weights.)  The result does not depend on
+ * the order in which thread blocks run.  A gradient beyond the range of `dtype` is an infinity.
  *
  *   O, lse        as the forward call wrote them for the same inputs and CSR.
  *   dO            in,  the upstream gradient, [B*H, S, D] of `dtype`, 16-byte aligned.

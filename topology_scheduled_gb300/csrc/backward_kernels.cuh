@@ -9,8 +9,9 @@
 //    which lies on a diagonal of its own for all columns.  The sums of the first 256 distances wait in shared memory
 //    until the tile is done; farther ones are added up by bucket at once, by shuffles too;
 //  * the last, open bucket gets minus the sum of the row's other values, since a row of dS sums to
-//    zero: no work on the far steps, and none of the error that Delta's rounded output leaves in each
-//    of their many values (it is a common shift of a row's dP, which the far keys would add up).
+//    zero: almost no work on the far steps, and none of the error that Delta's rounded output leaves in
+//    each of their many values (it is a common shift of a row's dP, which the far keys would add up).
+//    In a row where every dS of the bucket is 0 (its bias a finite mask) it gets nothing.
 // No atomics: a warp has its own sums, a CTA writes its tile's, and terms_reduce_bias adds the tiles
 // in order.  Measured at [1, 32, 32768, 128] bf16, 14.5 blocks a row: dQ 860 us, dK/dV 1035 us (870 and
 // 964 TFLOP/s on the three and four block products each does; the plain kernels, 64 lanes: 1435 and
@@ -560,7 +561,7 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         }
         // kBias: the sum over the row of the dS that lie before the last bucket
         [[maybe_unused]] float others = 0.f, last_bias = 0.f;
-        [[maybe_unused]] bool reached = false;  // the row has keys in the last bucket
+        [[maybe_unused]] uint32_t reached = 0u;  // the bits of the last bucket's dS: their sign aside 0 if all of them are 0
         [[maybe_unused]] float *win = reinterpret_cast<float *>(smem + L::kOffWin) + warp * kWindow;
         [[maybe_unused]] float *bins = reinterpret_cast<float *>(smem + L::kOffBins) + warp * kMaxBuckets;
         [[maybe_unused]] float *near_sums =
@@ -639,7 +640,10 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     };
                     if (diagonal) step(std::true_type{});  // a loop of its own
                     else step(std::false_type{});
-                    if constexpr (kBias) reached = true;
+                    if constexpr (kBias) {
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) reached |= dsw[t];
+                    }
                 } else if constexpr (kBias) {
                     const float *wp = window_at(win, table, known, terms.n, d_lo, wlane) + 63 + wlane - col0;
                     // columns up to this one lie in the last bucket
@@ -669,8 +673,10 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         others += s0 + s1;
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) others += c > far_to ? x[c] : 0.f;
-                        reached |= far_to + col0 >= 0;
+                        for (int c = 0; c < 32; ++c) {
+                            others += c > far_to ? x[c] : 0.f;
+                            reached |= c <= far_to && x[c] != 0.f ? 1u : 0u;
+                        }
                     }
                     // the sums over the diagonals: column c of row (lane + c + 1) mod 32 lies at the distance
                     // d_lo + 64 - col0 + lane, or 32 nearer once the row wraps
@@ -715,6 +721,10 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         (u < 2 || mbar_wait(BAR_DONE(u & 1), ((u - 2) >> 1) & 1, flags));
             if (!acc_valid) *abort_flag = 1;
         }
+        if constexpr (kBias) {  // for the warp with the row's other columns; the window has been read
+            __syncwarp();
+            win[wlane] = __uint_as_float(reached);
+        }
         // one decision for all elementwise warps (the section below has a barrier of its own)
         if (!named_barrier_or(1, kElt, *abort_flag != 0)) {
             tc_fence_after();
@@ -722,8 +732,9 @@ bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             // every product that read Q has completed: Q's tile stages dQ
             stage_rows<D, kBF16>(tmem + t_lane, kAcc, acc_valid, scale, sQ, row, tid >> 7);
             if constexpr (kBias) {
-                // the last bucket, unless its keys are left out
-                float s = reached && last_bias > -INFINITY ? -others : 0.f;
+                // the last bucket, unless none of its keys has any weight in the row
+                reached |= __float_as_uint(win[((warp ^ 4) - warp) * kWindow + wlane]);
+                float s = (reached & 0x7FFF7FFFu) != 0u ? -others : 0.f;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
                 if (wlane == 0) bins[last_bucket] = s;
