@@ -19,6 +19,7 @@ struct DeviceState {
     bool ready = false;
     unsigned *status = nullptr;
     unsigned *abort_epoch = nullptr;
+    std::atomic<int> sms{0};
 };
 DeviceState g_devices[kMaxDevices];
 std::mutex g_mutex;
@@ -66,6 +67,19 @@ tsa_status device_flags(int dev, DeviceFlags *f) {
     } while (e == 0u || e == ~0u);
     f->epoch = e;
     f->inject = g_wait_injection.load();
+    return TSA_OK;
+}
+
+// The device's number of multiprocessors (asked for once).
+tsa_status multiprocessors(int dev, int *sms) {
+    std::atomic<int> &kept = g_devices[dev].sms;
+    *sms = kept.load(std::memory_order_relaxed);
+    if (*sms > 0) return TSA_OK;
+    if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return TSA_ERR_CUDA;
+    }
+    kept.store(*sms, std::memory_order_relaxed);
     return TSA_OK;
 }
 

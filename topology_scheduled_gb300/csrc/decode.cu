@@ -4,7 +4,7 @@
 // that row b of the schedule lists, z and the difference of maps as in the forward kernels.
 //
 // Bound by memory: each listed key and value row is read once, 4 D bytes per key and head, against
-// 4 D multiply-adds (6 D with two maps), so the arithmetic stays on the FMA pipe.
+// 2 D multiply-adds (3 D with two maps), so the arithmetic stays on the FMA pipe.
 //  * A lane of a warp holds 8 of the D dimensions, so D / 8 lanes read a row with one 16-byte load
 //    each and a warp reads 2 (D = 128) or 4 rows per load.  A warp takes a chunk of 8 such loads of K
 //    and 8 of V at a time (two maps: 4, to keep both sums in registers with 24 warps on an SM); the next
@@ -125,7 +125,7 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
     __shared__ __align__(16) float warp_acc[kMaps][kWarps][D];
     __shared__ float warp_m[kMaps][kWarps], warp_l[kMaps][kWarps];
     __shared__ float cta_m[kMaps], cta_l[kMaps], cta_acc[kMaps][D];
-    __shared__ __align__(16) uint8_t table_smem[kBias ? kBucketTableBytes : 16];
+    __shared__ __align__(16) uint8_t table_smem[kBias ? kBucketBytes : 16];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
@@ -321,16 +321,17 @@ decode_kernel(const uint16_t *__restrict__ Q, const uint16_t *__restrict__ K, co
 template <int D, bool kBF16, class Terms>
 tsa_status launch_one(const DecodeLaunch &a, const Terms &terms) {
     // Thread blocks per (sequence, head), up to a cluster of 8: as many as leave every warp a chunk of an
-    // average row (the host knows no single row's length) while the GPU holds them all, and beyond that as many as leave it 32 chunks, since each
-    // block pays for its start and its join.  us with 1 / 2 / 4 / 8 blocks (D = 128; biased, differential):
-    // 8 heads, rows of 128 blocks 73 / 40 / 23 / 14 and 115 / 61 / 35 / 21; 128 heads, 13 blocks 11.4 / 10.1
-    // / 13.8 / 21.0 and 15.6 / 13.8 / 17.6 / 23.8; 512 heads, 42 blocks 108 / 116 / 117 / 147 and 148 / 127 /
-    // 128 / 157; 512 heads, ragged to 128 blocks 267 / 247 / 243 / 263 and 330 / 289 / 273 / 302.
+    // average row (the host knows no single row's length) while the GPU holds them all, and beyond that as
+    // many as leave it 32 chunks, since each block pays for its start and its join.  us with 1 / 2 / 4 / 8
+    // blocks (D = 128; biased, differential): 8 heads, rows of 128 blocks 73 / 40 / 23 / 14 and 115 / 61 / 35 /
+    // 21; 128 heads, 13 blocks 11.4 / 10.1 / 13.8 / 21.0 and 15.6 / 13.8 / 17.6 / 23.8; 512 heads, 42 blocks
+    // 108 / 116 / 117 / 147 and 148 / 127 / 128 / 157; 512 heads, ragged to 128 blocks 267 / 247 / 243 / 263
+    // and 330 / 289 / 273 / 302.
     constexpr int kChunk = kLoadsOf<Terms> * 32 / (D / 8);
     const long long sequences = a.lanes / a.H;
     const long long row = std::min((long long)a.cap, ((long long)a.nnz_cap * a.block + sequences - 1) / sequences);
     const long long chunks = (row + kChunk - 1) / kChunk;
-    const long long slots = 152 * (Terms::kDiff ? 3 : 2);  // thread blocks that run at once
+    const long long slots = (long long)a.sms * (Terms::kDiff ? 3 : 2);  // thread blocks that run at once
     unsigned ranks = 1;
     while (ranks < 8) {
         const long long least = 2 * ranks * (long long)a.lanes <= slots ? 1 : 32;

@@ -45,8 +45,8 @@ __device__ __forceinline__ float bias_log2(float b) {
     return b <= kBiasOut ? -INFINITY : b * 1.4426950408889634f;
 }
 
-// The buckets as a kernel keeps them in shared memory: biases in log2 units and starts, and for the
-// first distances the bias of each.
+// The buckets as a kernel keeps them in shared memory: biases in log2 units and starts, and, for kernels
+// that call spread, the bias of each of the first distances.
 constexpr int kDistances = 2048;  // 8 KB beside the D = 128 forward's tiles, two thread blocks per SM
 constexpr int kDistFront = 64;    // distances below zero lie behind the causal mask; they may be read
 struct BucketTable {
@@ -64,7 +64,6 @@ struct BucketTable {
             bias[b] = b < t.n ? bias_log2(widen16<kBF16>(__ldg(t.bias + (long long)head * t.n + b))) : 0.f;
             start[b] = t.starts[b];
         }
-        for (int d = tid; d < kDistFront; d += nthreads) dist[d - kDistFront] = 0.f;
     }
 
     // The last of n buckets that starts at or before distance d.
@@ -79,6 +78,7 @@ struct BucketTable {
     // `limit`), four distances per thread at a time, each by halving.  Returns how many are known;
     // another barrier before they are read.
     __device__ __forceinline__ int spread(int n, int limit, int tid, int nthreads) const {
+        for (int d = tid; d < kDistFront; d += nthreads) dist[d - kDistFront] = 0.f;
         int known = min(kDistances, limit);
         if (start[n - 1] < kDistances - 95) known = min(known, start[n - 1] + 95);
         const int first = n > 1 ? 1 << (31 - __clz(n - 1)) : 0;
@@ -95,7 +95,8 @@ struct BucketTable {
         return known;
     }
 };
-constexpr int kBucketTableBytes = (2 * kMaxBuckets + kDistFront + kDistances) * 4;
+constexpr int kBucketBytes = 2 * kMaxBuckets * 4;  // without the distances
+constexpr int kBucketTableBytes = kBucketBytes + (kDistFront + kDistances) * 4;
 
 // One warp's 32 rows x 64 columns of a step hold 95 distances, d_lo .. d_lo + 94 (negative ones
 // lie behind the causal mask).

@@ -252,6 +252,7 @@ tsa_status decode_launch(const void *Q, const void *K, const void *V, const int3
     a->cap = (int)capacity;
     a->D = (int)D;
     a->block = (int)block;
+    TSA_TRY(multiprocessors(dev, &a->sms));
     a->bf16 = dtype == TSA_BF16;
     a->scale_log2 = (float)((double)scale * 1.4426950408889634);
     a->stream = reinterpret_cast<cudaStream_t>(stream);

@@ -23,6 +23,7 @@ namespace tsa {
 tsa_status current_device(int *dev);
 tsa_status device_flags(int dev, DeviceFlags *f);
 tsa_status check_device_ptr(const void *p, int dev);
+tsa_status multiprocessors(int dev, int *sms);
 // Row-major 16-bit tensor [lanes, rows, cols]; boxes of 64 columns x box_rows, cut off at a lane's end.
 bool encode_3d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t lanes, uint64_t rows, uint64_t cols,
                uint32_t box_rows);
@@ -116,7 +117,7 @@ struct DecodeLaunch {
     const int32_t *lens, *row_ptr, *col_idx;
     int nnz_cap;
     uint16_t *O;
-    int lanes, H, cap, D, block;
+    int lanes, H, cap, D, block, sms;
     bool bf16;
     float scale_log2;
     DeviceFlags flags;
