@@ -24,6 +24,9 @@
  *   - Every pointer argument except `salience_sq` is required.  Buffers are DEVICE memory
  *     of the current CUDA device, allocated and owned by the caller; the library never
  *     allocates or frees and keeps no pointer after a call returns.
+ *   - What the library knows of a device (its own status words there, its kernels' attributes) it
+ *     looks up once in a process: a device that has been reset (cudaDeviceReset) cannot be used
+ *     with it again in that process.
  *   - Calls are asynchronous and stream-ordered on `stream` (a cudaStream_t; NULL is the
  *     legacy default stream).  The return value reports only what the host can check
  *     before launch.  Problems met on the device (an out-of-range or unsorted col_idx, a

@@ -27,6 +27,9 @@
 //    than 2^30 (bf16) or 2^15 (f16); the final O / l uses the same stale maximum, so the result
 //    is unchanged.  The decision is per row but TMEM loads/stores are warp-collective, so a
 //    warp rescales when any of its rows must (factor 1 for the others).
+//  * Precision.  Scores, maxima, denominators and O are binary32.  P is rounded to the input dtype for its
+//    product with V: tcgen05 multiplies 16-bit operands at twice the rate of the 32-bit ones, which keep 10
+//    bits.  An output is off by at most that rounding of the weights and its own.
 //  * Epilogue.  O / l rounded to the input dtype, staged in the Q tile, TMA-stored per block;
 //    optionally the row's log-sum-exp (m + log l), which the backward pass recomputes P from.
 //  * Partial last block (S not a multiple of 64).  The maps see [lanes, S, D] as three dimensions: rows

