@@ -84,3 +84,29 @@ def test_memory_for_another_stream(which, raw):
             assert torch.equal(_written(which, x, copies), _written(which, y, want))
         del more
     assert tsa.tsa_last_device_status() == 0
+
+
+def test_another_stream_within_a_capture():
+    """Calls on a stream that forks from the captured one, their memory the graph's; replayed with other work
+    between the replays."""
+    calls = _calls()
+    names = ["plain backward", "biased", "biased backward", "differential", "differential backward", "biased decode"]
+    want = {n: [x.clone() for x in calls[n](None)] for n in names}
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st.wait_stream(torch.cuda.current_stream())
+        got = {n: calls[n](st) for n in names}
+        torch.cuda.current_stream().wait_stream(st)
+    for _ in range(3):
+        for x in sum((list(v) for v in got.values()), []):
+            x.fill_(7.0)
+        g.replay()
+        rubbish = [torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        torch.cuda.synchronize()
+        for n in names:
+            for x, y in zip(got[n], want[n]):
+                assert torch.equal(x, y), n
+        del rubbish
+    assert tsa.tsa_last_device_status() == 0
