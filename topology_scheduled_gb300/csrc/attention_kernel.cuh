@@ -69,6 +69,7 @@
 // in-flight copies and MMAs (bounded), frees TMEM and returns.
 #pragma once
 
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -651,7 +652,9 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
         const int member = kDiff ? 0 : half;     // the membership bit of this thread's row
         const int row_in = kDiff ? tid & 63 : tid;  // this thread's token, from the tile's first
         const uint32_t t_lane = (uint32_t)(warp * 32) << 16;  // this warp's TMEM lane quarter
-        float m_used = -INFINITY;                // maximum the accumulators are scaled to (log2)
+        // maximum the accumulators are scaled to (log2).  Below any finite score, but finite: where all scores so
+        // far are -inf their weights are 2^(-inf + FLT_MAX) = 0
+        float m_used = -FLT_MAX;
         float l_sum = 0.f;                       // running denominator
         [[maybe_unused]] float l_exact = 0.f;    // the same from the weights before their rounding
         bool ok = true;
@@ -785,7 +788,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 if (kOneS && !o_done()) { ok = false; break; }
                 const bool grow = mx > m_used + rescale_log2<kBF16>();
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float alpha = !grow ? 1.f : (m_used == -INFINITY ? 0.f : ex2_approx(m_used - mx));
+                    const float alpha = !grow ? 1.f : ex2_approx(m_used - mx);
                     if (u > 0) {
                         if (!kOneS && !o_done()) { ok = false; break; }
                         tc_fence_after();
@@ -807,7 +810,7 @@ scheduled_attention_kernel(const __grid_constant__ CUtensorMap tmQ,
                 }
                 // p = 2^(x * scale * log2(e) - m): one packed FMA per pair, exp2 on the MUFU
                 const float c1 = kBias ? cc1 : scale_log2;
-                float n1 = m_used == -INFINITY ? 0.f : -m_used;  // (no key with weight yet: all scores are -inf)
+                float n1 = -m_used;
                 if constexpr (kBias) n1 += off;
                 const uint64_t cc = f2_pack(c1, c1);
                 const uint64_t nm = f2_pack(n1, n1);
