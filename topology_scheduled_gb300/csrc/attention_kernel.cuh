@@ -62,7 +62,7 @@
 //    over the one S buffer, which makes every step run in series, lost to two CTAs, and a bias gains
 //    nothing, as the steps near the diagonal then add it twice.
 // Measured at [1, 32, 32768, 128] bf16, 14.5 blocks a row: plain 0.42 ms (1190 TFLOP/s on visited blocks),
-// biased 0.45 ms, differential 0.85 ms, 0.90 ms with what its backward needs (twice the tiles: 1100
+// biased 0.44 ms, differential 0.85 ms, 0.90 ms with what its backward needs (twice the tiles: 1100
 // TFLOP/s executed).  Bound by the softmax warps' chain of a step beside a tensor pipe that is active for
 // 44 to 53 % of the time: the 64-column score product runs at 2/3 of the full rate.
 // Every mbarrier wait is bounded; on a timeout the CTA records TSA_ERR_TIMEOUT, drains its

@@ -6,16 +6,16 @@
 // forward.  Its gradient sums dS over buckets in bwd_dq_kernel, in binary32 before dS is rounded:
 //  * where a step touches a bucket before the last a warp adds up the diagonals of its values, one
 //    distance each: for column c every lane takes the value of the row c + 1 lanes on (by a shuffle),
-//    which lies on a diagonal of its own for all columns.  The sums of the first 256 distances wait in shared memory
-//    until the tile is done; farther ones are added up by bucket at once, by shuffles too;
+//    which lies on a diagonal of its own for all columns.  The sums of the first 256 distances wait in
+//    shared memory until the tile is done; farther ones are added up by bucket at once, by shuffles too;
 //  * the last, open bucket gets minus the sum of the row's other values, since a row of dS sums to
 //    zero: almost no work on the far steps, and none of the error that Delta's rounded output leaves in
 //    each of their many values (it is a common shift of a row's dP, which the far keys would add up).
 //    In a row where every dS of the bucket is 0 (its bias a finite mask) it gets nothing.
 // No atomics: a warp has its own sums, a CTA writes its tile's, and terms_reduce_bias adds the tiles
-// in order.  Measured at [1, 32, 32768, 128] bf16, 14.5 blocks a row: dQ 860 us, dK/dV 1035 us (870 and
-// 964 TFLOP/s on the three and four block products each does; the plain kernels, 64 lanes: 1435 and
-// 1864 us).
+// in order.  Measured at [1, 32, 32768, 128] bf16, 14.5 blocks a row: dQ 880 us, dK/dV 1044 us (850 and
+// 954 TFLOP/s on the three and four block products each does; the plain kernels, 64 lanes: 1435 and
+// 1864 us).  Leaving a bucket without weight alone took the whole pass from 2036 to 2047 us.
 //
 // Differential attention.  A CTA takes a pair of blocks as the plain kernels do, and both maps of them:
 // the first half of the score product's K steps goes into one accumulator, the second half into
@@ -25,7 +25,7 @@
 // binary32 and rounded once.  (Against one block per CTA with both maps in its 128 rows, by block-
 // diagonal operands: 32 lanes of S 32768, topology, backward 3.36 -> 2.45 ms.)  lambda's gradient is
 // - sum P2 o dP, summed over a CTA's rows in binary32 from the exact weights, so that a sum over every
-// query keeps the precision that P's rounding would cost.  Measured there: dQ 879 us, dK/dV 1334 us (its
+// query keeps the precision that P's rounding would cost.  Measured there: dQ 885 us, dK/dV 1339 us (its
 // dV product takes P from shared memory, as three accumulators and a step's products fill TMEM).
 //
 // What bounds the kernels: the tensor pipe is active for 22 to 37 % of the time and issue slots for 35 to
