@@ -10,41 +10,6 @@
 namespace tsa {
 namespace {
 
-struct Span {
-    const void *p;
-    size_t bytes;
-};
-
-// No output may overlap an input or another output.
-bool outputs_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-    for (const Span *o = outs.begin(); o != outs.end(); ++o) {
-        if (!o->p) continue;
-        for (const Span &i : ins)
-            if (i.p && overlaps(o->p, o->bytes, i.p, i.bytes)) return true;
-        for (const Span *q = o + 1; q != outs.end(); ++q)
-            if (q->p && overlaps(o->p, o->bytes, q->p, q->bytes)) return true;
-    }
-    return false;
-}
-
-// A schedule's arrays: its row starts, and its entries.
-Span rows_of(const int32_t *row_ptr, int64_t S, int64_t block) {
-    return {row_ptr, (size_t)((S + block - 1) / block + 1) * 4};
-}
-Span entries_of(const int32_t *col_idx, int64_t nnz_cap) { return {col_idx, (size_t)nnz_cap * 4}; }
-
-tsa_status check_aligned(std::initializer_list<const void *> ptrs, uintptr_t mask) {
-    for (const void *p : ptrs)
-        if (p && (reinterpret_cast<uintptr_t>(p) & mask)) return TSA_ERR_INVALID_ARGUMENT;
-    return TSA_OK;
-}
-
-tsa_status check_device(std::initializer_list<const void *> ptrs, int dev) {
-    for (const void *p : ptrs)
-        if (p) TSA_TRY(check_device_ptr(p, dev));
-    return TSA_OK;
-}
-
 // Sizes every form shares.  (A scale of zero or below would turn the masked scores' -inf around.)
 tsa_status check_shape(tsa_dtype dtype, int64_t B, int64_t H, int64_t S, int64_t D, int64_t block, float scale,
                        int64_t nnz_cap) {

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 
 #include "score_terms.cuh"
 #include "tsa.h"
@@ -28,6 +29,41 @@ tsa_status multiprocessors(int dev, int *sms);
 bool encode_3d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t lanes, uint64_t rows, uint64_t cols,
                uint32_t box_rows);
 bool overlaps(const void *a, size_t na, const void *b, size_t nb);
+
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+
+// No output may overlap an input or another output.
+inline bool outputs_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->p) continue;
+        for (const Span &i : ins)
+            if (i.p && overlaps(o->p, o->bytes, i.p, i.bytes)) return true;
+        for (const Span *q = o + 1; q != outs.end(); ++q)
+            if (q->p && overlaps(o->p, o->bytes, q->p, q->bytes)) return true;
+    }
+    return false;
+}
+
+// A schedule's arrays: its row starts, and its entries.
+inline Span rows_of(const int32_t *row_ptr, int64_t S, int64_t block) {
+    return {row_ptr, (size_t)((S + block - 1) / block + 1) * 4};
+}
+inline Span entries_of(const int32_t *col_idx, int64_t nnz_cap) { return {col_idx, (size_t)nnz_cap * 4}; }
+
+inline tsa_status check_aligned(std::initializer_list<const void *> ptrs, uintptr_t mask) {
+    for (const void *p : ptrs)
+        if (p && (reinterpret_cast<uintptr_t>(p) & mask)) return TSA_ERR_INVALID_ARGUMENT;
+    return TSA_OK;
+}
+
+inline tsa_status check_device(std::initializer_list<const void *> ptrs, int dev) {
+    for (const void *p : ptrs)
+        if (p) TSA_TRY(check_device_ptr(p, dev));
+    return TSA_OK;
+}
 
 // Lets `kernel` have `bytes` of dynamic shared memory on the current device.  `done` (one per kernel and
 // size) keeps a bit per device, so only the first call asks the driver, which takes about a microsecond.
