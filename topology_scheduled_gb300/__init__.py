@@ -14,7 +14,10 @@ its operations with the same names:
 * ``tsa_block_sums`` / ``tsa_build_schedule_from_sums`` -- the build in two halves, for keys
   whose lanes are spread over several GPUs (``distributed.build_schedule_lane_sharded``);
 * ``tsa_topology_attention_host`` -- one forward step (schedule + attention) from host
-  tensors, the host<->device copies overlapped with the work.
+  tensors, the host<->device copies overlapped with the work;
+* ``tsa_biased_attention*`` / ``tsa_differential_attention*`` -- attentions with learned score terms;
+* ``tsa_rotary``, ``tsa_paged_append``, ``tsa_paged_attention_decode`` -- rotary positions, a paged
+  key/value cache, and the attention of one new token over it.
 """
 from .binding import (STATUS_NAMES, TIE_RULES, TSA_BF16, TSA_F16, TsaError, lib,  # noqa: F401
                       library_path, tsa_build_schedule, tsa_build_schedule_workspace_bytes,
@@ -28,3 +31,5 @@ from .terms import (relative_bucket_starts, tsa_biased_attention, tsa_biased_att
                     tsa_biased_attention_decode, tsa_biased_attention_fwd, tsa_differential_attention,
                     tsa_differential_attention_backward, tsa_differential_attention_decode,
                     tsa_differential_attention_fwd)
+from .cache import (rotary_frequencies, rotary_magnitude, tsa_paged_append, tsa_paged_attention_decode,  # noqa: F401
+                    tsa_paged_attention_decode_workspace_bytes, tsa_rotary)

@@ -5,7 +5,8 @@ tsa_scheduled_attention_fwd and keeps its log-sum-exp; its backward runs
 tsa_scheduled_attention_backward (blocks of 64 or 128 tokens).  The CSR is not differentiable.
 
 ``biased_attention`` and ``differential_attention`` do the same for the attentions with learned
-score terms; their learned inputs get gradients as well.
+score terms; their learned inputs get gradients as well.  ``rotary`` rotates Q and K by their
+positions, and their gradients back.
 
 Capturing a backward pass into a CUDA graph: PyTorch's accumulation nodes keep the stream they were
 made on, so the captured pass needs leaves of its own (or torch.autograd.grad, which accumulates
@@ -16,6 +17,7 @@ from __future__ import annotations
 import torch
 
 from .binding import tsa_scheduled_attention_backward, tsa_scheduled_attention_fwd
+from .cache import _frequencies, tsa_rotary
 from .terms import (_starts, tsa_biased_attention_backward, tsa_biased_attention_fwd,
                     tsa_differential_attention_backward, tsa_differential_attention_fwd)
 
@@ -102,3 +104,43 @@ def differential_attention(Q, K, V, row_ptr, col_idx, lambda_q1, lambda_k1, lamb
     64 or 128 tokens)."""
     return DifferentialAttention.apply(Q, K, V, row_ptr, col_idx, lambda_q1, lambda_k1, lambda_q2, lambda_k2,
                                        float(lambda_init), scale, int(block))
+
+
+def _strided(t):
+    """`t` as the rotation reads it: whole rows, 16 bytes apart and from such a boundary on.  (The gradient that
+    reaches a backward pass may be any view, an expanded one too.)"""
+    fine = t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and all(x % 8 == 0 for x, n in zip(t.stride()[:-1], t.shape) if n > 1)
+    return t if fine else t.clone(memory_format=torch.contiguous_format)
+
+
+class Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, Q, K, frequencies, positions, interleaved, magnitude):
+        frequencies = _frequencies(frequencies)[:]  # a copy: the caller's may change before the backward
+        ctx.settings = frequencies, interleaved, magnitude
+        # the gradients take their inputs' layout
+        ctx.strides = [None if t is None else torch.empty_like(t, device="meta").stride() for t in (Q, K)]
+        ctx.save_for_backward(positions)
+        ctx.set_materialize_grads(False)
+        return tsa_rotary(_strided(Q), None if K is None else _strided(K), frequencies, positions,
+                          interleaved=interleaved, magnitude=magnitude)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dQ, dK=None):
+        frequencies, interleaved, magnitude = ctx.settings
+        positions, = ctx.saved_tensors
+        grads = [_strided(g) if g is not None and need else None for g, need in zip((dQ, dK), ctx.needs_input_grad)]
+        outs = [None if g is None else torch.empty_strided(g.shape, st, dtype=g.dtype, device=g.device)
+                for g, st in zip(grads, ctx.strides)]
+        wanted = [(g, o) for g, o in zip(grads, outs) if g is not None]
+        if wanted:
+            (g, o), (g2, o2) = (*wanted, (None, None))[:2]
+            tsa_rotary(g, g2, frequencies, positions, interleaved=interleaved, magnitude=magnitude, inverse=True, out=o,
+                       out_k=o2)
+        return (*outs, None, None, None, None)
+
+
+def rotary(Q, K, frequencies, positions=None, interleaved: bool = False, magnitude: float = 1.0):
+    """tsa_rotary of Q and K (or of Q alone, K None) with gradients for both, in their layouts."""
+    return Rotary.apply(Q, K, frequencies, positions, bool(interleaved), float(magnitude))

@@ -31,7 +31,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 
-# name -> (restype, argtypes), mirroring include/tsa.h
+# name -> (restype, argtypes), mirroring include/tsa.h, tsa_terms.h and tsa_cache.h
 SIGNATURES = {
     "tsa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "tsa_schedule_max_nnz": (_I64, [_I64, _I64, _I64, _I64, _I64]),
@@ -75,6 +75,13 @@ SIGNATURES = {
     "tsa_differential_attention_fwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _I64,
                                                       ctypes.c_float, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64,
                                                       _I64, _I64, ctypes.c_float, _P]),
+    "tsa_rotary": (ctypes.c_int, [_P] * 4 + [_I64, _P, _I64, ctypes.c_int, ctypes.c_float, ctypes.c_int, _P, _P,
+                                             ctypes.c_int] + [_I64] * 5 + [_P]),
+    "tsa_paged_append": (ctypes.c_int, [_P] * 6 + [_I64] * 4 + [_P, _I64, _P, _P, _P, _I64, ctypes.c_int, ctypes.c_float,
+                                                            _P, ctypes.c_int] + [_I64] * 5 + [_P]),
+    "tsa_paged_attention_decode_workspace_bytes": (_SZ, [_I64] * 8),
+    "tsa_paged_attention_decode": (ctypes.c_int, [_P] * 3 + [_I64] * 4 + [_P, _I64, _P, _P, _P, _I64, _P, ctypes.c_int] +
+                                   [_I64] * 5 + [ctypes.c_float, _P, _SZ, _P]),
     "tsa_topology_attention_host": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64,
                                                    _I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_float,
                                                    _P, _P, _P, _P, _P, _P, _I64, _P, _SZ, _I64, _P]),

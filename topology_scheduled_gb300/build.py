@@ -23,9 +23,9 @@ LIB = os.path.join(BUILD, "libtsa.so")
 
 SOURCES = ["api.cu", "schedule.cu", "segment.cu", "attention.cu", "attention_biased.cu",
            "attention_differential.cu", "terms_api.cu", "backward.cu", "backward_biased.cu", "backward_differential.cu",
-           "decode.cu", "noalloc.cu"]
+           "decode.cu", "rotary.cu", "paged_decode.cu", "cache_api.cu", "noalloc.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("attention_kernel.cuh", "backward_kernels.cuh", "score_terms.cuh", "tsa_device.cuh",
-                                           "tsa_internal.h")] + [os.path.join(INCLUDE, h) for h in ("tsa.h", "tsa_terms.h")]
+                                           "tsa_internal.h")] + [os.path.join(INCLUDE, h) for h in ("tsa.h", "tsa_terms.h", "tsa_cache.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

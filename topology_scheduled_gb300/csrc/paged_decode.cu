@@ -1,0 +1,456 @@
+// paged_decode.cu -- one new token per sequence against a paged key/value cache (include/tsa_cache.h):
+// o = softmax(scale q.k) V over the sequence's keys, or those of the blocks its row of a schedule lists.
+//
+// Bound by memory: 4 D bytes per key and key head.  A key head's queries share them, so the arithmetic,
+// 4 D multiply-adds per key and query, goes to the tensor cores once several queries share a key; the
+// products are small enough for mma.sync (m16n8k16), which works on registers that hold rows as they were
+// loaded, with no shared memory on the way:
+//  * a warp takes 16 keys at a time for up to 8 (or 16) queries.  Scores are S^T = K Q^T, keys as rows.  The
+//    order of a contraction is free, so a lane's 16-byte piece of a key serves as two k16 steps' fragment and
+//    the same piece of a query as their other operand;
+//  * O^T = V^T P^T, dimensions as rows.  A lane loads the same 8 dimensions of four keys, and a byte permute
+//    pairs two keys' elements: that is V^T's fragment.  P^T's is the scores' fragment, transposed (movmatrix);
+//  * a weight is the sum of two numbers of the inputs' type, each with a product of its own, so weights keep
+//    16 (bf16) or 22 bits; in f16 they are scaled by 2^14 beforehand, so that none above 2^-38 of the largest
+//    vanishes.  Sums, maxima and denominators are binary32;
+//  * the next 16 keys' K is loaded while this one's weights are found, V at the start of its step: 4 to 8 KB
+//    per warp in flight.
+// A (sequence, key head, group of queries) is split over the warps of a cluster of thread blocks, whose sums
+// are joined through shared memory in a fixed order; where eight blocks a row cannot fill the GPU, several
+// clusters share a row, leave their sums in the workspace, and a second kernel joins them.
+// Keys at the length and beyond are neither read nor counted.
+#include <algorithm>
+#include <climits>
+#include <type_traits>
+
+#include "tsa_device.cuh"
+#include "tsa_internal.h"
+
+namespace tsa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+
+__device__ __forceinline__ uint4 load_row(const uint16_t *p) {
+    return __ldg(reinterpret_cast<const uint4 *>(p));
+}
+
+template <bool kBF16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if constexpr (kBF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit elements, two per lane, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Elements `i` (0..7) of two vectors, in one word.
+template <int i>
+__device__ __forceinline__ uint32_t pair_of(const uint4 &x, const uint4 &y) {
+    const uint32_t u = i / 2 == 0 ? x.x : i / 2 == 1 ? x.y : i / 2 == 2 ? x.z : x.w;
+    const uint32_t v = i / 2 == 0 ? y.x : i / 2 == 1 ? y.y : i / 2 == 2 ? y.z : y.w;
+    return __byte_perm(u, v, i % 2 == 0 ? 0x5410 : 0x7632);
+}
+
+// Two weights as a word of their roundings to the inputs' type and a word of what those leave.
+template <bool kBF16>
+__device__ __forceinline__ void two_parts(float a, float b, uint32_t &hi, uint32_t &lo) {
+    if constexpr (kBF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        lo = *reinterpret_cast<const uint32_t *>(&l);
+    }
+}
+
+template <bool kBF16>
+__device__ __forceinline__ void store16(uint16_t *p, float y) {
+    if constexpr (kBF16) *p = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+    else *p = __half_as_ushort(__float2half_rn(y));
+}
+
+// A reference for exponents: the maximum, or 0 where there is no key with weight yet.
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
+
+// Queries per thread block are 8 kGroups; a warp's step takes 16 kSub keys (4 KB of K either way).
+template <int D, bool kBF16, int kGroups>
+__global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
+paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
+    constexpr int kSub = D == 64 ? 2 : 1;
+    constexpr int kVec = D / 32;   // 16-byte pieces of a key that a lane holds
+    constexpr int kV = D / 64;     // .. of a value row
+    constexpr int kTiles = D / 16; // m16 tiles of the output's dimensions
+    constexpr int kQ = 8 * kGroups;
+    constexpr int kBatch = 32 / kSub;  // a warp's steps whose places it looks up at once
+    constexpr float kLift = kBF16 ? 0.f : 14.f;
+    __shared__ __align__(16) float sum[kWarps][kQ][D];
+    __shared__ float warp_m[kWarps][kQ], warp_l[kWarps][kQ], cta_m[kQ], cta_l[kQ];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int share = a.H / a.HK, chunks = (share + kQ - 1) / kQ;
+    const int rank = blockIdx.x % a.ranks, part = blockIdx.x / a.ranks % a.parts;
+    const int row = blockIdx.x / a.ranks / a.parts;  // (sequence, key head, chunk of queries)
+    const int chunk = row % chunks, kvh = row / chunks % a.HK, b = row / chunks / a.HK;
+    const int first_q = kvh * share + chunk * kQ, queries = min(kQ, share - chunk * kQ);
+
+    int len = __ldg(a.lens + b);
+    int n16 = 0, first = 0;  // groups of 16 keys to visit
+    const int per_block = a.block / 16, cap = a.max_pages << a.page_shift;
+    if (len < 0 || len > cap) {
+        if (tid == 0) raise_status(a.flags, kDevBadSchedule);
+        len = 0;
+    }
+    const int nb = (cap + a.block - 1) / a.block;
+    if (a.row_ptr) {
+        first = __ldg(a.row_ptr + b);
+        int entries = __ldg(a.row_ptr + b + 1) - first;
+        if (first < 0 || entries < 0 || entries > nb || first > a.nnz_cap - entries) {
+            if (tid == 0) raise_status(a.flags, kDevBadSchedule);
+            entries = 0;
+        }
+        n16 = len > 0 ? entries * per_block : 0;
+    } else {
+        n16 = (len + 15) / 16;
+    }
+    const int workers = a.ranks * a.parts * kWarps, worker = (part * a.ranks + rank) * kWarps + warp;
+    const int steps = (n16 + kSub - 1) / kSub;  // of all workers, dealt out in turn
+
+    // Where group u of 16 keys begins, and its page; len (no keys) for what is not there.
+    auto place = [&](int u, int &k0, int &page) {
+        k0 = len;
+        page = 0;
+        if (u >= n16) return;
+        int k = u * 16;
+        if (a.row_ptr) {
+            const int e = u / per_block, *entry = a.col_idx + first + e;
+            const int j = __ldg(entry), before = e > 0 ? __ldg(entry - 1) : -1;
+            if (j < 0 || j >= nb || j <= before) {
+                raise_status(a.flags, kDevBadSchedule);
+                return;
+            }
+            k = j * a.block + (u % per_block) * 16;
+        }
+        if (k >= len) return;
+        const int p = __ldg(a.page_table + (long long)b * a.max_pages + (k >> a.page_shift));
+        if (p < 0 || p >= a.num_pages) {
+            raise_status(a.flags, kDevBadSchedule);
+            return;
+        }
+        k0 = k;
+        page = p;
+    };
+    // Lane i looks up group i % kSub of the warp's step kBatch * batch + i / kSub.
+    auto places = [&](int batch, int &k0, int &page) {
+        const long long step = worker + ((long long)batch * kBatch + lane / kSub) * workers;
+        place(step < steps ? (int)step * kSub + lane % kSub : INT_MAX, k0, page);
+    };
+    const int mask = (1 << a.page_shift) - 1;
+    const long long head_at = (long long)kvh << a.page_shift;
+    auto row_at = [&](int k0, int page, int64_t page_stride) { return page * page_stride + (head_at + (k0 & mask)) * D; };
+
+    uint4 kr[kSub][2][kVec], vr[kSub][4][kV];
+    auto load_k = [&](int sub, int k0, int page) {
+        const uint16_t *base = a.K + row_at(k0, page, a.k_page_stride) + t * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < kVec; ++c)
+                kr[sub][h][c] = k0 + g + 8 * h < len ? load_row(base + (g + 8 * h) * D + 32 * c) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    auto load_v = [&](int sub, int k0, int page) {
+        const uint16_t *base = a.V + row_at(k0, page, a.v_page_stride) + g * 8;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int k = 2 * t + (r & 1) + 8 * (r >> 1);
+#pragma unroll
+            for (int c = 0; c < kV; ++c)
+                vr[sub][r][c] = k0 + k < len ? load_row(base + k * D + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+
+    int k0_now, page_now, k0_next, page_next;  // of this batch of steps, and the one after
+    places(0, k0_now, page_now);
+    uint4 q[kGroups][kVec];
+#pragma unroll
+    for (int m = 0; m < kGroups; ++m)
+#pragma unroll
+        for (int c = 0; c < kVec; ++c)
+            q[m][c] = 8 * m + g < queries
+                          ? load_row(a.Q + ((long long)b * a.H + first_q + 8 * m + g) * D + t * 8 + 32 * c)
+                          : make_uint4(0u, 0u, 0u, 0u);
+    int k0[kSub], page[kSub];
+#pragma unroll
+    for (int s = 0; s < kSub; ++s) {
+        k0[s] = __shfl_sync(0xffffffffu, k0_now, s);
+        page[s] = __shfl_sync(0xffffffffu, page_now, s);
+        load_k(s, k0[s], page[s]);
+    }
+    places(1, k0_next, page_next);
+
+    float m[kGroups][2], l[kGroups][2], acc[kGroups][kTiles][4];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        m[i][0] = m[i][1] = -INFINITY;
+        l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
+    }
+
+    for (int n = 0, step = worker; step < steps; ++n, step += workers) {
+#pragma unroll
+        for (int s = 0; s < kSub; ++s) load_v(s, k0[s], page[s]);
+        float sc[kGroups][kSub][4];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+            for (int s = 0; s < kSub; ++s) {
+                float (&c)[4] = sc[i][s];
+                c[0] = c[1] = c[2] = c[3] = 0.f;
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) {
+                    const uint4 &x = kr[s][0][v], &y = kr[s][1][v], &z = q[i][v];
+                    mma<kBF16>(c, x.x, y.x, x.y, y.y, z.x, z.y);
+                    mma<kBF16>(c, x.z, y.z, x.w, y.w, z.z, z.w);
+                }
+                const bool there = k0[s] + g < len, there8 = k0[s] + g + 8 < len;
+                c[0] = there ? c[0] * a.scale_log2 : -INFINITY;
+                c[1] = there ? c[1] * a.scale_log2 : -INFINITY;
+                c[2] = there8 ? c[2] * a.scale_log2 : -INFINITY;
+                c[3] = there8 ? c[3] * a.scale_log2 : -INFINITY;
+            }
+        // the next step's K
+        const int at = (n + 1) % kBatch;
+        if (at == 0) {
+            k0_now = k0_next;
+            page_now = page_next;
+            places((n + 1) / kBatch + 1, k0_next, page_next);
+        }
+#pragma unroll
+        for (int s = 0; s < kSub; ++s) {
+            k0[s] = __shfl_sync(0xffffffffu, k0_now, at * kSub + s);
+            page[s] = __shfl_sync(0xffffffffu, page_now, at * kSub + s);
+            load_k(s, k0[s], page[s]);
+        }
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            uint32_t hi[kSub][2], lo[kSub][2];
+            float p[kSub][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // queries 2 t and 2 t + 1
+                float top = m[i][e];
+#pragma unroll
+                for (int s = 0; s < kSub; ++s) top = fmaxf(top, fmaxf(sc[i][s][e], sc[i][s][e + 2]));
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float ref = reference(top) - kLift;
+                if (top > m[i][e]) {  // (of all of the query's lanes)
+                    const float keep = ex2_approx(m[i][e] - reference(top));
+                    l[i][e] *= keep;
+#pragma unroll
+                    for (int j = 0; j < kTiles; ++j) {
+                        acc[i][j][e] *= keep;
+                        acc[i][j][e + 2] *= keep;
+                    }
+                    m[i][e] = top;
+                }
+#pragma unroll
+                for (int s = 0; s < kSub; ++s) {
+                    p[s][e] = ex2_approx(sc[i][s][e] - ref);
+                    p[s][e + 2] = ex2_approx(sc[i][s][e + 2] - ref);
+                    l[i][e] += p[s][e] + p[s][e + 2];
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < kSub; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    two_parts<kBF16>(p[s][2 * h], p[s][2 * h + 1], hi[s][h], lo[s][h]);
+                    hi[s][h] = transpose8(hi[s][h]);
+                    lo[s][h] = transpose8(lo[s][h]);
+                }
+#pragma unroll
+            for (int s = 0; s < kSub; ++s) {
+                auto tile = [&](auto index) {
+                    constexpr int j = decltype(index)::value, other = D == 64 ? j + 4 : j;
+                    const uint32_t a0 = pair_of<j>(vr[s][0][0], vr[s][1][0]), a2 = pair_of<j>(vr[s][2][0], vr[s][3][0]);
+                    const uint32_t a1 = pair_of<other>(vr[s][0][kV - 1], vr[s][1][kV - 1]);
+                    const uint32_t a3 = pair_of<other>(vr[s][2][kV - 1], vr[s][3][kV - 1]);
+                    mma<kBF16>(acc[i][j], a0, a1, a2, a3, hi[s][0], hi[s][1]);
+                    mma<kBF16>(acc[i][j], a0, a1, a2, a3, lo[s][0], lo[s][1]);
+                };
+                tile(std::integral_constant<int, 0>());
+                tile(std::integral_constant<int, 1>());
+                tile(std::integral_constant<int, 2>());
+                tile(std::integral_constant<int, 3>());
+                if constexpr (D == 128) {
+                    tile(std::integral_constant<int, 4>());
+                    tile(std::integral_constant<int, 5>());
+                    tile(std::integral_constant<int, 6>());
+                    tile(std::integral_constant<int, 7>());
+                }
+            }
+        }
+    }
+
+    // the warps' sums, then the cluster's
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int query = 8 * i + 2 * t + e;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], o);
+            if (g == 0) {
+                warp_m[warp][query] = m[i][e];
+                warp_l[warp][query] = l[i][e];
+            }
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+                sum[warp][query][8 * g + j] = acc[i][j][e];
+                sum[warp][query][(D == 64 ? 8 * g + 4 : 64 + 8 * g) + j] = acc[i][j][e + 2];
+            }
+        }
+    __syncthreads();
+    for (int at = tid; at < queries * D; at += kThreads) {
+        const int query = at / D, d = at % D;
+        float top = warp_m[0][query];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, warp_m[w][query]);
+        float total = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2_approx(warp_m[w][query] - reference(top));
+            total = fmaf(warp_l[w][query], f, total);
+            y = fmaf(sum[w][query][d], f, y);
+        }
+        sum[0][query][d] = y;  // read by this thread alone so far
+        if (d == 0) {
+            cta_m[query] = top;
+            cta_l[query] = total;
+        }
+    }
+    if (a.ranks > 1) cluster_sync();
+    else __syncthreads();
+    for (int at = rank * kThreads + tid; at < queries * D; at += a.ranks * kThreads) {
+        const int query = at / D, d = at % D;
+        float top = -INFINITY, total = 0.f, y = 0.f;
+        for (int r = 0; r < a.ranks; ++r) {
+            const float m2 = a.ranks > 1 ? load_remote(&cta_m[query], r) : cta_m[query];
+            const float l2 = a.ranks > 1 ? load_remote(&cta_l[query], r) : cta_l[query];
+            const float y2 = a.ranks > 1 ? load_remote(&sum[0][query][d], r) : sum[0][query][d];
+            const float mn = fmaxf(top, m2), f = ex2_approx(top - reference(mn)), f2 = ex2_approx(m2 - reference(mn));
+            total = total * f + l2 * f2;
+            y = y * f + y2 * f2;
+            top = mn;
+        }
+        if (a.parts == 1) {
+            // (a NaN among the scores is the answer's, too)
+            store16<kBF16>(a.O + ((long long)b * a.H + first_q + query) * D + d, total == 0.f ? 0.f : y / total);
+        } else {
+            float *to = a.partial + (((long long)b * a.H + first_q + query) * a.parts + part) * (D + 2);
+            to[d] = y;
+            if (d == 0) {
+                to[D] = top;
+                to[D + 1] = total;
+            }
+        }
+    }
+    if (a.ranks > 1) cluster_sync();  // no thread block leaves while its shared memory may be read
+}
+
+// Joins the parts' sums of one query, D dimensions.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(D) join_parts_kernel(const float *__restrict__ partial, uint16_t *__restrict__ O, int parts) {
+    const long long row = blockIdx.x;
+    const int d = threadIdx.x;
+    const float *from = partial + row * parts * (D + 2);
+    float top = -INFINITY, total = 0.f, y = 0.f;
+    for (int p = 0; p < parts; ++p, from += D + 2) {
+        const float m2 = from[D], mn = fmaxf(top, m2);
+        const float f = ex2_approx(top - reference(mn)), f2 = ex2_approx(m2 - reference(mn));
+        total = total * f + from[D + 1] * f2;
+        y = y * f + from[d] * f2;
+        top = mn;
+    }
+    store16<kBF16>(O + row * D + d, total == 0.f ? 0.f : y / total);
+}
+
+int groups_of(const PagedDecodeLaunch &a) { return a.H / a.HK > 8 ? 2 : 1; }
+
+template <int D, bool kBF16, int kGroups>
+tsa_status launch_one(const PagedDecodeLaunch &a) {
+    const int share = a.H / a.HK, chunks = (share + 8 * kGroups - 1) / (8 * kGroups);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)a.B * a.HK * chunks * a.parts * a.ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = a.stream;
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = (unsigned)a.ranks;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, kBF16, kGroups>, a) != cudaSuccess) return TSA_ERR_CUDA;
+    if (a.parts > 1) {
+        join_parts_kernel<D, kBF16><<<(unsigned)(a.B * a.H), D, 0, a.stream>>>(a.partial, a.O, a.parts);
+        if (cudaGetLastError() != cudaSuccess) return TSA_ERR_CUDA;
+    }
+    return TSA_OK;
+}
+
+template <int D, bool kBF16>
+tsa_status launch_groups(const PagedDecodeLaunch &a) {
+    return groups_of(a) == 1 ? launch_one<D, kBF16, 1>(a) : launch_one<D, kBF16, 2>(a);
+}
+
+}  // namespace
+
+void split_paged_decode(PagedDecodeLaunch *a) {
+    const int per = 8 * groups_of(*a), share = a->H / a->HK;
+    const long long rows = (long long)a->B * a->HK * ((share + per - 1) / per);
+    const long long cap = (long long)a->max_pages << a->page_shift;
+    const long long keys = a->nnz_cap > 0 ? std::min(cap, ((long long)a->nnz_cap * a->block + a->B - 1) / a->B) : cap;
+    const long long steps = (keys + 31) / 32;
+    const long long slots = 152 * 3;
+    int ranks = 1, parts = 1;
+    while (ranks < 8) {
+        const long long least = 2 * ranks * rows <= slots ? 1 : 32;
+        if (ranks * kWarps * least >= steps) break;
+        ranks *= 2;
+    }
+    if (ranks == 8) {
+        while (parts < 32 && 2 * parts * ranks * rows <= slots && 2ll * parts * ranks * kWarps * 8 <= steps) parts *= 2;
+    }
+    a->ranks = ranks;
+    a->parts = parts;
+}
+
+size_t paged_decode_workspace(const PagedDecodeLaunch &a) {
+    return a.parts == 1 ? 0 : (size_t)a.B * a.H * a.parts * (a.D + 2) * sizeof(float);
+}
+
+tsa_status launch_paged_decode(const PagedDecodeLaunch &a) {
+    if (a.D == 64) return a.bf16 ? launch_groups<64, true>(a) : launch_groups<64, false>(a);
+    return a.bf16 ? launch_groups<128, true>(a) : launch_groups<128, false>(a);
+}
+
+}  // namespace tsa

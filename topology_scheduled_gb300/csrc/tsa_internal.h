@@ -163,6 +163,55 @@ struct DecodeLaunch {
 tsa_status launch_biased_decode(const DecodeLaunch &a, const BiasTerms &terms);
 tsa_status launch_differential_decode(const DecodeLaunch &a, const DiffTerms &terms);
 
+// Rows that rows_kernel moves: `heads` heads of a tensor, strides in elements; to the pages of a cache where
+// page_stride > 0 (to_head is then a head's distance in a page).
+struct RowsPart {
+    const uint16_t *from;
+    uint16_t *to;
+    int64_t from_batch, from_head, from_token, to_batch, to_head, to_token, page_stride;
+    int heads;
+    bool rotated;
+};
+
+constexpr int kMaxRotaryDim = 256;
+
+struct RowsLaunch {
+    RowsPart part[3];  // heads 0: unused
+    const int32_t *positions;  // [position_rows, S], or null: 0 .. S - 1
+    const int32_t *page_table, *seq_lens, *counts;  // seq_lens not null: new tokens for a cache
+    int64_t num_pages;
+    int position_rows, max_pages, page_shift;
+    int B, S, D, R, heads_per_cta;
+    float magnitude;
+    bool bf16, interleaved;
+    DeviceFlags flags;
+    cudaStream_t stream;
+    uint64_t step[kMaxRotaryDim / 2];  // each pair's turns per position, times 2^64 (modulo whole turns)
+};
+
+tsa_status launch_rows(RowsLaunch *a, int sms);
+
+// One new token per sequence against a paged cache.
+struct PagedDecodeLaunch {
+    const uint16_t *Q, *K, *V;
+    const int32_t *page_table, *lens, *row_ptr, *col_idx;  // row_ptr null: every key
+    int64_t k_page_stride, v_page_stride;  // elements
+    uint16_t *O;
+    float *partial;  // joined afterwards where parts > 1
+    int nnz_cap, num_pages, max_pages, page_shift;
+    int B, H, HK, D, block;
+    int ranks, parts;  // thread blocks per cluster, clusters per row
+    bool bf16;
+    float scale_log2;
+    DeviceFlags flags;
+    cudaStream_t stream;
+};
+
+// How the keys of a (sequence, key head, group of queries) are split, and what that needs.
+void split_paged_decode(PagedDecodeLaunch *a);
+size_t paged_decode_workspace(const PagedDecodeLaunch &a);
+tsa_status launch_paged_decode(const PagedDecodeLaunch &a);
+
 // Largest number of blocks the schedule builder accepts.
 constexpr int64_t kMaxScheduleBlocks = 4096;
 constexpr int64_t kMaxScheduleDim = 1024;
