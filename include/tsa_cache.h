@@ -11,12 +11,13 @@
  *
  * A paged cache is two arrays K_cache, V_cache of num_pages pages; a page holds page_size tokens of every
  * key/value head, [HK, page_size, D] contiguous, and page p begins p * page_stride elements into its array
- * (page_stride >= HK * page_size * D: both arrays may be slices of one).  page_table[b][i] is the page of
+ * (page_stride >= HK * page_size * D, any for one page: both arrays may be slices of one).  page_table[b][i] is the page of
  * sequence b's tokens [i * page_size, (i + 1) * page_size); entries that no token reaches are not read.
  *
  * Rows of Q, K, V and of the rotated outputs are D contiguous elements; `strides` (int64 in HOST memory,
  * read during the call) gives, for each tensor in the order stated, the elements from one batch, head and
- * token to the next: not negative, multiples of 8.  NULL: all are contiguous [B, heads, tokens, D].
+ * token to the next: not negative, multiples of 8 (along an axis of one, any).  NULL: all are contiguous
+ * [B, heads, tokens, D].
  */
 #ifndef TSA_CACHE_H
 #define TSA_CACHE_H

@@ -166,3 +166,17 @@ def test_positions_changed_before_the_backward_are_noticed():
     pos += 1
     with pytest.raises(RuntimeError):
         out.sum().backward()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_second_gradients(interleaved):
+    """The backward pass is a rotation, and has a gradient of its own: <v, dQ(g)> has the gradient R v by g."""
+    f = tsa.rotary_frequencies(64)
+    q = _normal(1, 2, 6, 64, dtype=torch.float16, seed=1).to(DEV).requires_grad_()
+    g = _normal(1, 2, 6, 64, dtype=torch.float16, seed=2).to(DEV).requires_grad_()
+    v = _normal(1, 2, 6, 64, dtype=torch.float16, seed=3).to(DEV)
+    out = autograd.rotary(q, None, f, None, interleaved, 1.5)
+    dq, = torch.autograd.grad(out, [q], g, create_graph=True)
+    dg, = torch.autograd.grad(dq, [g], v)
+    close(dq, *rotated(g, range(6), f, interleaved, 1.5, inverse=True))
+    close(dg, *rotated(v, range(6), f, interleaved, 1.5))

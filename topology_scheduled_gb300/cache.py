@@ -18,7 +18,7 @@ import torch
 from .binding import _check, _dtype_code, _made, _on, lib
 from .terms import _given, _output, _schedule, _workspace
 
-_ZERO = (0, 0, 0)
+_NONE = (0, 0, 0)
 
 
 def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
@@ -69,28 +69,24 @@ def _frequencies(frequencies):
 def _rows(name, t, like=None):
     """Checks a tensor [B, heads, tokens, D] whose rows are contiguous, on `like`'s device and of its type, batch,
     tokens and D."""
-    if t.dim() != 4 or not t.is_cuda or (t.stride(3) != 1 and t.shape[3] > 1):
+    shape = t.shape
+    if len(shape) != 4 or not t.is_cuda or t.stride(3) != 1:
         raise ValueError(f"{name} must be a CUDA tensor [B, heads, tokens, D] with contiguous rows")
-    if like is not None and (t.dtype is not like.dtype or t.device != like.device or t.shape[0] != like.shape[0] or
-                             t.shape[2:] != like.shape[2:]):
-        raise ValueError(f"{name} must have the type, device, batch, tokens and row length of the others")
-    return t
+    if like is not None:
+        other = like.shape
+        if t.dtype is not like.dtype or t.device != like.device or shape[0] != other[0] or shape[2] != other[2] or \
+                shape[3] != other[3]:
+            raise ValueError(f"{name} must have the type, device, batch, tokens and row length of the others")
 
 
 def _rotated(name, t, like, other):
     """`t`, or a new contiguous tensor shaped as `like`."""
     if t is None:
-        return _made(other, torch.empty, like.shape, dtype=like.dtype, device=like.device)
+        return _made(other, torch.empty_like, like, memory_format=torch.contiguous_format)
     _rows(name, t, like)
     if t.shape != like.shape:
         raise ValueError(f"{name} must have the shape {tuple(like.shape)}")
     return t
-
-
-def _strides(*tensors):
-    """12 strides: batch, head and token of each tensor, 0 for none.  (An axis of one row has no stride.)"""
-    return array("q", [v for t in tensors for v in (
-        _ZERO if t is None else [x if n > 1 else 0 for x, n in zip(t.stride()[:3], t.shape)])])
 
 
 def tsa_rotary(Q, K, frequencies, positions=None, *, interleaved: bool = False, magnitude: float = 1.0,
@@ -119,30 +115,35 @@ def tsa_rotary(Q, K, frequencies, positions=None, *, interleaved: bool = False, 
     out = _rotated("out", out, Q, other)
     if K is not None:
         out_k = _rotated("out_k", out_k, K, other)
-    strides = _strides(Q, K, out, out_k)
+    at, rows = (None, 1) if positions is None else (positions.data_ptr(), 1 if positions.dim() == 1 else B)
+    if K is None:
+        strides = array("q", Q.stride()[:3] + _NONE + out.stride()[:3] + _NONE)
+        _check(lib().tsa_rotary(
+            Q.data_ptr(), None, strides.buffer_info()[0], at, rows, f.buffer_info()[0], 2 * len(f), interleaved, magnitude,
+            inverse, out.data_ptr(), None, _dtype_code(Q), B, H, 0, S, D, handle), "tsa_rotary")
+        return out
+    strides = array("q", Q.stride()[:3] + K.stride()[:3] + out.stride()[:3] + out_k.stride()[:3])
     _check(lib().tsa_rotary(
-        Q.data_ptr(), None if K is None else K.data_ptr(), strides.buffer_info()[0],
-        None if positions is None else positions.data_ptr(), 1 if positions is None or positions.dim() == 1 else B,
-        f.buffer_info()[0], 2 * len(f), interleaved, magnitude, inverse, out.data_ptr(),
-        None if K is None else out_k.data_ptr(), _dtype_code(Q), B, H, 0 if K is None else K.shape[1], S, D, handle),
-        "tsa_rotary")
-    return out if K is None else (out, out_k)
+        Q.data_ptr(), K.data_ptr(), strides.buffer_info()[0], at, rows, f.buffer_info()[0], 2 * len(f), interleaved,
+        magnitude, inverse, out.data_ptr(), out_k.data_ptr(), _dtype_code(Q), B, H, K.shape[1], S, D, handle), "tsa_rotary")
+    return out, out_k
 
 
 def _pages(K_cache, V_cache, page_table, seq_lens, B, HK, D, like):
     """Checks a paged cache [pages, HK, page_size, D] and its lists; page counts, sizes and strides."""
+    shape = K_cache.shape
+    if len(shape) != 4 or shape[1] != HK or shape[3] != D:
+        raise ValueError(f"K_cache must be [pages, {HK}, page_size, {D}]")
+    inner = (shape[2] * D, D, 1)
     for name, t in (("K_cache", K_cache), ("V_cache", V_cache)):
-        if t.dim() != 4 or t.shape != K_cache.shape or t.shape[1] != HK or t.shape[3] != D or t.dtype is not like.dtype or \
-                t.device != like.device or t.stride()[1:] != (t.shape[2] * D, D, 1):
+        if t.shape != shape or t.dtype is not like.dtype or t.device != like.device or t.stride()[1:] != inner:
             raise ValueError(f"{name} must be a [pages, HK, page_size, D] tensor of the inputs' type and device, "
                              "its pages contiguous")
-    for name, t, shape in (("page_table", page_table, (B, page_table.shape[-1])), ("seq_lens", seq_lens, (B,))):
-        if t.dtype is not torch.int32 or t.shape != shape or t.device != like.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor {'[B, pages]' if t is page_table else '[B]'} "
-                             "on the inputs' device")
-    pages, size = K_cache.shape[0], K_cache.shape[2]
-    dense = HK * size * D
-    return pages, size, K_cache.stride(0) if pages > 1 else dense, V_cache.stride(0) if pages > 1 else dense
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype is not torch.int32 or \
+            page_table.device != like.device or not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous int32 tensor [B, pages] on the inputs' device")
+    _given("seq_lens", seq_lens, (B,), torch.int32, like.device)
+    return shape[0], shape[2], K_cache.stride(0), V_cache.stride(0)
 
 
 def tsa_paged_append(Q, K, V, K_cache, V_cache, page_table, seq_lens, counts=None, frequencies=None, *,
@@ -172,7 +173,8 @@ def tsa_paged_append(Q, K, V, K_cache, V_cache, page_table, seq_lens, counts=Non
     if counts is not None:
         _given("counts", counts, (B,), torch.int32, K.device)
     f = None if frequencies is None else _frequencies(frequencies)
-    strides = _strides(Q, K, V, out)
+    strides = array("q", (_NONE if Q is None else Q.stride()[:3]) + K.stride()[:3] + V.stride()[:3] +
+                    (_NONE if Q is None else out.stride()[:3]))
     _check(lib().tsa_paged_append(
         None if Q is None else Q.data_ptr(), K.data_ptr(), V.data_ptr(), strides.buffer_info()[0], K_cache.data_ptr(),
         V_cache.data_ptr(), num, size, k_stride, v_stride, page_table.data_ptr(), page_table.shape[1],

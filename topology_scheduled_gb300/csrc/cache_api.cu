@@ -82,7 +82,7 @@ tsa_status rows_in(const void *p, const int64_t *strides, int64_t B, int64_t hea
     r->heads = heads;
     const int64_t dense[3] = {heads * S * D, S * D, D}, n[3] = {B, heads, S};
     for (int i = 0; i < 3; ++i) {
-        r->stride[i] = strides ? strides[i] : dense[i];
+        r->stride[i] = n[i] == 1 ? 0 : strides ? strides[i] : dense[i];
         if (r->stride[i] < 0 || r->stride[i] % 8 || r->stride[i] > kMaxExtent) return TSA_ERR_INVALID_ARGUMENT;
     }
     TSA_TRY(check_aligned({p}, 15));
@@ -177,10 +177,10 @@ tsa_status pages_in(const void *K_cache, const void *V_cache, int64_t num_pages,
     for (int i = 0; i < 2; ++i) {
         f[i]->p = p[i];
         f[i]->n[0] = num_pages;
-        f[i]->stride[0] = stride[i];
         f[i]->inner = HK * page_size * D;
+        f[i]->stride[0] = num_pages == 1 ? f[i]->inner : stride[i];
         int64_t e;
-        if (stride[i] % 8 || stride[i] < f[i]->inner || stride[i] > kMaxExtent || !extent(*f[i], &e))
+        if (f[i]->stride[0] % 8 || f[i]->stride[0] < f[i]->inner || f[i]->stride[0] > kMaxExtent || !extent(*f[i], &e))
             return TSA_ERR_INVALID_ARGUMENT;
     }
     return TSA_OK;
@@ -299,9 +299,9 @@ tsa_status tsa_paged_append(const void *Q, const void *K, const void *V, const i
     const Rows kc = {K_cache, HK, {0, head, 0}}, vc = {V_cache, HK, {0, head, 0}};
     if (Q) a.part[0] = part_of(q, qo, true);
     a.part[1] = part_of(k, kc, frequencies != nullptr);
-    a.part[1].page_stride = k_page_stride;
+    a.part[1].page_stride = c.k.stride[0];
     a.part[2] = part_of(v, vc, false);
-    a.part[2].page_stride = v_page_stride;
+    a.part[2].page_stride = c.v.stride[0];
     a.page_table = page_table;
     a.seq_lens = seq_lens;
     a.counts = counts;
@@ -355,8 +355,8 @@ tsa_status tsa_paged_attention_decode(const void *Q, const void *K_cache, const 
     a.lens = seq_lens;
     a.row_ptr = row_ptr;
     a.col_idx = col_idx;
-    a.k_page_stride = k_page_stride;
-    a.v_page_stride = v_page_stride;
+    a.k_page_stride = c.k.stride[0];
+    a.v_page_stride = c.v.stride[0];
     a.O = static_cast<uint16_t *>(O);
     a.partial = static_cast<float *>(workspace);
     a.num_pages = (int)num_pages;
