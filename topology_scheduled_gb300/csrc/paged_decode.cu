@@ -3,8 +3,7 @@
 //
 // Bound by memory: 4 D bytes per key and key head.  A key head's queries share them, so the arithmetic,
 // 4 D multiply-adds per key and query, goes to the tensor cores once several queries share a key; the
-// products are small enough for mma.sync (m16n8k16), which works on registers that hold rows as they were
-// loaded, with no shared memory on the way:
+// products are small enough for mma.sync (m16n8k16), whose fragments are plain 16-byte pieces of rows:
 //  * a warp takes 16 keys at a time for up to 8 (or 16) queries.  Scores are S^T = K Q^T, keys as rows.  The
 //    order of a contraction is free, so a lane's 16-byte piece of a key serves as two k16 steps' fragment and
 //    the same piece of a query as their other operand;
@@ -13,13 +12,16 @@
 //  * a weight is the sum of two numbers of the inputs' type, each with a product of its own, so weights keep
 //    16 (bf16) or 22 bits; in f16 they are scaled by 2^14 beforehand, so that none above 2^-38 of the largest
 //    vanishes.  Sums, maxima and denominators are binary32;
-//  * the next 16 keys' K is loaded while this one's weights are found, V at the start of its step: 4 to 8 KB
-//    per warp in flight.
+//  * a warp copies its keys and values to a ring of its own in shared memory (cp.async), two steps ahead of
+//    the one it works on: up to 24 KB in flight per warp, whatever the registers hold.  16 keys of a page are
+//    one contiguous 2 D x 16 byte piece; its 16-byte pieces are stored with the row's bits exclusive-ored into
+//    their place, so that the reads of eight lanes meet all banks once.
 // A (sequence, key head, group of queries) is split over the warps of a cluster of thread blocks, whose sums
 // are joined through shared memory in a fixed order; where eight blocks a row cannot fill the GPU, several
 // clusters share a row, leave their sums in the workspace, and a second kernel joins them.
 // Keys at the length and beyond are neither read nor counted.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -32,8 +34,26 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 
-__device__ __forceinline__ uint4 load_row(const uint16_t *p) {
-    return __ldg(reinterpret_cast<const uint4 *>(p));
+constexpr int kStages = 3;                     // of a warp's ring
+constexpr int kHalf = 4096;                    // bytes of a step's keys, and of its values
+constexpr int kRing = kStages * 2 * kHalf;     // bytes per warp
+constexpr int kSmem = kWarps * kRing;
+
+// 16 bytes to shared memory, or 16 zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const uint16_t *from, bool there) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_begun() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_done() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ uint4 load_piece(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
 }
 
 template <bool kBF16>
@@ -93,7 +113,7 @@ __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.
 
 // Queries per thread block are 8 kGroups; a warp's step takes 16 kSub keys (4 KB of K either way).
 template <int D, bool kBF16, int kGroups>
-__global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     constexpr int kSub = D == 64 ? 2 : 1;
     constexpr int kVec = D / 32;   // 16-byte pieces of a key that a lane holds
@@ -102,7 +122,9 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     constexpr int kQ = 8 * kGroups;
     constexpr int kBatch = 32 / kSub;  // a warp's steps whose places it looks up at once
     constexpr float kLift = kBF16 ? 0.f : 14.f;
-    __shared__ __align__(16) float sum[kWarps][kQ][D];
+    extern __shared__ __align__(128) uint8_t smem[];
+    auto sum = reinterpret_cast<float (*)[kQ][D]>(smem);  // [kWarps][kQ][D], once the rings are done with
+    static_assert(kWarps * kQ * D * 4 <= kSmem, "the sums fit where the rings were");
     __shared__ float warp_m[kWarps][kQ], warp_l[kWarps][kQ], cta_m[kQ], cta_l[kQ];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -167,26 +189,6 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     const long long head_at = (long long)kvh << a.page_shift;
     auto row_at = [&](int k0, int page, int64_t page_stride) { return page * page_stride + (head_at + (k0 & mask)) * D; };
 
-    uint4 kr[kSub][2][kVec], vr[kSub][4][kV];
-    auto load_k = [&](int sub, int k0, int page) {
-        const uint16_t *base = a.K + row_at(k0, page, a.k_page_stride) + t * 8;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < kVec; ++c)
-                kr[sub][h][c] = k0 + g + 8 * h < len ? load_row(base + (g + 8 * h) * D + 32 * c) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto load_v = [&](int sub, int k0, int page) {
-        const uint16_t *base = a.V + row_at(k0, page, a.v_page_stride) + g * 8;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int k = 2 * t + (r & 1) + 8 * (r >> 1);
-#pragma unroll
-            for (int c = 0; c < kV; ++c)
-                vr[sub][r][c] = k0 + k < len ? load_row(base + k * D + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-
     int k0_now, page_now, k0_next, page_next;  // of this batch of steps, and the one after
     places(0, k0_now, page_now);
     uint4 q[kGroups][kVec];
@@ -194,17 +196,54 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     for (int m = 0; m < kGroups; ++m)
 #pragma unroll
         for (int c = 0; c < kVec; ++c)
-            q[m][c] = 8 * m + g < queries
-                          ? load_row(a.Q + ((long long)b * a.H + first_q + 8 * m + g) * D + t * 8 + 32 * c)
-                          : make_uint4(0u, 0u, 0u, 0u);
-    int k0[kSub], page[kSub];
+            q[m][c] = 8 * m + g < queries ? __ldg(reinterpret_cast<const uint4 *>(
+                                                a.Q + ((long long)b * a.H + first_q + 8 * m + g) * D + t * 8 + 32 * c))
+                                          : make_uint4(0u, 0u, 0u, 0u);
+
+    // The copies of step n, 16 keys and then 16 values at a time, a group of copies in any case.
+    const uint32_t ring = smem_u32(smem) + warp * kRing;
+    constexpr int kPieces = D / 8, kRows = 32 / kPieces;  // pieces per row, rows that a warp's copy takes
+    const int piece = lane % kPieces, row_in = lane / kPieces;
+    auto copy_step = [&](int n, int batch) {
+        const int at = n % kBatch;
+        const bool now = n / kBatch == batch;
+        const uint32_t to = ring + n % kStages * 2 * kHalf;
 #pragma unroll
-    for (int s = 0; s < kSub; ++s) {
-        k0[s] = __shfl_sync(0xffffffffu, k0_now, s);
-        page[s] = __shfl_sync(0xffffffffu, page_now, s);
-        load_k(s, k0[s], page[s]);
+        for (int s = 0; s < kSub; ++s) {
+            const int k0 = __shfl_sync(0xffffffffu, now ? k0_now : k0_next, at * kSub + s);
+            const int page = __shfl_sync(0xffffffffu, now ? page_now : page_next, at * kSub + s);
+            if (k0 >= len) {
+#pragma unroll
+                for (int i = 0; i < 16 / kRows; ++i) {
+                    copy16(to + s * 2048 + i * 512 + lane * 16, a.K, false);
+                    copy16(to + kHalf + s * 2048 + i * 512 + lane * 16, a.V, false);
+                }
+                continue;
+            }
+            const uint16_t *k = a.K + row_at(k0, page, a.k_page_stride) + lane * 8;
+            const uint16_t *v = a.V + row_at(k0, page, a.v_page_stride) + lane * 8;
+#pragma unroll
+            for (int i = 0; i < 16 / kRows; ++i) {
+                const int r = i * kRows + row_in;
+                copy16(to + s * 2048 + r * 2 * D + ((piece ^ ((r & 1) << 2)) << 4), k + i * 256, k0 + r < len);
+            }
+#pragma unroll
+            for (int i = 0; i < 16 / kRows; ++i) {
+                const int r = i * kRows + row_in;
+                copy16(to + kHalf + s * 2048 + r * 2 * D + ((piece ^ ((r & 6))) << 4), v + i * 256, k0 + r < len);
+            }
+        }
+    };
+    const int mine = steps > worker ? (steps - worker + workers - 1) / workers : 0;  // this warp's steps
+#pragma unroll
+    for (int n = 0; n < kStages - 1; ++n) {
+        if (n < mine) copy_step(n, 0);
+        copies_begun();
     }
     places(1, k0_next, page_next);
+    // a lane's pieces of a step's keys (rows g and g + 8) and values (rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9)
+    const uint32_t k_even = ring + g * 2 * D + ((t ^ ((g & 1) << 2)) << 4), k_odd = k_even ^ 64;
+    const uint32_t v_at = ring + kHalf + 2 * t * 2 * D + ((g ^ (t << 1)) << 4);
 
     float m[kGroups][2], l[kGroups][2], acc[kGroups][kTiles][4];
 #pragma unroll
@@ -215,44 +254,48 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
         for (int j = 0; j < kTiles; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
     }
 
-    for (int n = 0, step = worker; step < steps; ++n, step += workers) {
-#pragma unroll
-        for (int s = 0; s < kSub; ++s) load_v(s, k0[s], page[s]);
+    for (int n = 0; n < mine; ++n) {
+        const int batch = n / kBatch;
+        if (n > 0 && n % kBatch == 0) {
+            k0_now = k0_next;
+            page_now = page_next;
+            places(batch + 1, k0_next, page_next);
+        }
+        if (n + kStages - 1 < mine) copy_step(n + kStages - 1, batch);
+        copies_begun();
+        copies_done<kStages - 1>();
+        __syncwarp();
+        const uint32_t stage = n % kStages * 2 * kHalf;
         float sc[kGroups][kSub][4];
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i)
+        for (int s = 0; s < kSub; ++s) {
 #pragma unroll
-            for (int s = 0; s < kSub; ++s) {
-                float (&c)[4] = sc[i][s];
-                c[0] = c[1] = c[2] = c[3] = 0.f;
+            for (int i = 0; i < kGroups; ++i) sc[i][s][0] = sc[i][s][1] = sc[i][s][2] = sc[i][s][3] = 0.f;
 #pragma unroll
-                for (int v = 0; v < kVec; ++v) {
-                    const uint4 &x = kr[s][0][v], &y = kr[s][1][v], &z = q[i][v];
-                    mma<kBF16>(c, x.x, y.x, x.y, y.y, z.x, z.y);
-                    mma<kBF16>(c, x.z, y.z, x.w, y.w, z.z, z.w);
+            for (int v = 0; v < kVec; ++v) {
+                const uint32_t at = (v & 1 ? k_odd : k_even) + stage + s * 2048 + v / 2 * 128;
+                const uint4 x = load_piece(at), y = load_piece(at + 8 * 2 * D);
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) {
+                    const uint4 &z = q[i][v];
+                    mma<kBF16>(sc[i][s], x.x, y.x, x.y, y.y, z.x, z.y);
+                    mma<kBF16>(sc[i][s], x.z, y.z, x.w, y.w, z.z, z.w);
                 }
-                const bool there = k0[s] + g < len, there8 = k0[s] + g + 8 < len;
+            }
+            const int k0 = __shfl_sync(0xffffffffu, k0_now, n % kBatch * kSub + s);
+            const bool there = k0 + g < len, there8 = k0 + g + 8 < len;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                float (&c)[4] = sc[i][s];
                 c[0] = there ? c[0] * a.scale_log2 : -INFINITY;
                 c[1] = there ? c[1] * a.scale_log2 : -INFINITY;
                 c[2] = there8 ? c[2] * a.scale_log2 : -INFINITY;
                 c[3] = there8 ? c[3] * a.scale_log2 : -INFINITY;
             }
-        // the next step's K
-        const int at = (n + 1) % kBatch;
-        if (at == 0) {
-            k0_now = k0_next;
-            page_now = page_next;
-            places((n + 1) / kBatch + 1, k0_next, page_next);
         }
-#pragma unroll
-        for (int s = 0; s < kSub; ++s) {
-            k0[s] = __shfl_sync(0xffffffffu, k0_now, at * kSub + s);
-            page[s] = __shfl_sync(0xffffffffu, page_now, at * kSub + s);
-            load_k(s, k0[s], page[s]);
-        }
+        uint32_t hi[kGroups][kSub][2], lo[kGroups][kSub][2];
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            uint32_t hi[kSub][2], lo[kSub][2];
             float p[kSub][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {  // queries 2 t and 2 t + 1
@@ -283,35 +326,47 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
             for (int s = 0; s < kSub; ++s)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    two_parts<kBF16>(p[s][2 * h], p[s][2 * h + 1], hi[s][h], lo[s][h]);
-                    hi[s][h] = transpose8(hi[s][h]);
-                    lo[s][h] = transpose8(lo[s][h]);
+                    two_parts<kBF16>(p[s][2 * h], p[s][2 * h + 1], hi[i][s][h], lo[i][s][h]);
+                    hi[i][s][h] = transpose8(hi[i][s][h]);
+                    lo[i][s][h] = transpose8(lo[i][s][h]);
                 }
+        }
 #pragma unroll
-            for (int s = 0; s < kSub; ++s) {
-                auto tile = [&](auto index) {
-                    constexpr int j = decltype(index)::value, other = D == 64 ? j + 4 : j;
-                    const uint32_t a0 = pair_of<j>(vr[s][0][0], vr[s][1][0]), a2 = pair_of<j>(vr[s][2][0], vr[s][3][0]);
-                    const uint32_t a1 = pair_of<other>(vr[s][0][kV - 1], vr[s][1][kV - 1]);
-                    const uint32_t a3 = pair_of<other>(vr[s][2][kV - 1], vr[s][3][kV - 1]);
-                    mma<kBF16>(acc[i][j], a0, a1, a2, a3, hi[s][0], hi[s][1]);
-                    mma<kBF16>(acc[i][j], a0, a1, a2, a3, lo[s][0], lo[s][1]);
-                };
-                tile(std::integral_constant<int, 0>());
-                tile(std::integral_constant<int, 1>());
-                tile(std::integral_constant<int, 2>());
-                tile(std::integral_constant<int, 3>());
-                if constexpr (D == 128) {
-                    tile(std::integral_constant<int, 4>());
-                    tile(std::integral_constant<int, 5>());
-                    tile(std::integral_constant<int, 6>());
-                    tile(std::integral_constant<int, 7>());
+        for (int s = 0; s < kSub; ++s) {
+            uint4 vr[4][kV];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < kV; ++c)
+                    vr[r][c] = load_piece(v_at + stage + s * 2048 + ((r & 1) + 8 * (r >> 1)) * 2 * D + 128 * c);
+            auto tile = [&](auto index) {
+                constexpr int j = decltype(index)::value, other = D == 64 ? j + 4 : j;
+                const uint32_t a0 = pair_of<j>(vr[0][0], vr[1][0]), a2 = pair_of<j>(vr[2][0], vr[3][0]);
+                const uint32_t a1 = pair_of<other>(vr[0][kV - 1], vr[1][kV - 1]);
+                const uint32_t a3 = pair_of<other>(vr[2][kV - 1], vr[3][kV - 1]);
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) {
+                    mma<kBF16>(acc[i][j], a0, a1, a2, a3, hi[i][s][0], hi[i][s][1]);
+                    mma<kBF16>(acc[i][j], a0, a1, a2, a3, lo[i][s][0], lo[i][s][1]);
                 }
+            };
+            tile(std::integral_constant<int, 0>());
+            tile(std::integral_constant<int, 1>());
+            tile(std::integral_constant<int, 2>());
+            tile(std::integral_constant<int, 3>());
+            if constexpr (D == 128) {
+                tile(std::integral_constant<int, 4>());
+                tile(std::integral_constant<int, 5>());
+                tile(std::integral_constant<int, 6>());
+                tile(std::integral_constant<int, 7>());
             }
         }
+        __syncwarp();  // the stage may be written again
     }
 
     // the warps' sums, then the cluster's
+    copies_done<0>();
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < kGroups; ++i)
 #pragma unroll
@@ -402,7 +457,10 @@ tsa_status launch_one(const PagedDecodeLaunch &a) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)a.B * a.HK * chunks * a.parts * a.ranks));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = a.stream;
+    static std::atomic<unsigned long long> allowed{0};
+    if (!allow_smem(allowed, reinterpret_cast<const void *>(paged_decode_kernel<D, kBF16, kGroups>), kSmem)) return TSA_ERR_CUDA;
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
     cluster.val.clusterDim.x = (unsigned)a.ranks;
@@ -430,7 +488,7 @@ void split_paged_decode(PagedDecodeLaunch *a) {
     const long long cap = (long long)a->max_pages << a->page_shift;
     const long long keys = a->nnz_cap > 0 ? std::min(cap, ((long long)a->nnz_cap * a->block + a->B - 1) / a->B) : cap;
     const long long steps = (keys + 31) / 32;
-    const long long slots = 152 * 3;
+    const long long slots = 152 * 2;
     int ranks = 1, parts = 1;
     while (ranks < 8) {
         const long long least = 2 * ranks * rows <= slots ? 1 : 32;
