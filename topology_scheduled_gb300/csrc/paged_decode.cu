@@ -121,7 +121,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     constexpr int kTiles = D / 16; // m16 tiles of the output's dimensions
     constexpr int kQ = 8 * kGroups;
     constexpr int kBatch = 32 / kSub;  // a warp's steps whose places it looks up at once
-    constexpr float kLift = kBF16 ? 0.f : 14.f;
+    // A weight is at most 2^(kLift + kSlack) as it is rounded: 2^15 in f16, whose weights are lifted.
+    constexpr float kLift = kBF16 ? 0.f : 14.f, kSlack = kBF16 ? 8.f : 1.f;
     extern __shared__ __align__(128) uint8_t smem[];
     auto sum = reinterpret_cast<float (*)[kQ][D]>(smem);  // [kWarps][kQ][D], once the rings are done with
     static_assert(kWarps * kQ * D * 4 <= kSmem, "the sums fit where the rings were");
@@ -133,6 +134,15 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     const int row = blockIdx.x / a.ranks / a.parts;  // (sequence, key head, chunk of queries)
     const int chunk = row % chunks, kvh = row / chunks % a.HK, b = row / chunks / a.HK;
     const int first_q = kvh * share + chunk * kQ, queries = min(kQ, share - chunk * kQ);
+
+    uint4 q[kGroups][kVec];
+#pragma unroll
+    for (int m = 0; m < kGroups; ++m)
+#pragma unroll
+        for (int c = 0; c < kVec; ++c)
+            q[m][c] = 8 * m + g < queries ? __ldg(reinterpret_cast<const uint4 *>(
+                                                a.Q + ((long long)b * a.H + first_q + 8 * m + g) * D + t * 8 + 32 * c))
+                                          : make_uint4(0u, 0u, 0u, 0u);
 
     int len = __ldg(a.lens + b);
     int n16 = 0, first = 0;  // groups of 16 keys to visit
@@ -156,34 +166,36 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     const int workers = a.ranks * a.parts * kWarps, worker = (part * a.ranks + rank) * kWarps + warp;
     const int steps = (n16 + kSub - 1) / kSub;  // of all workers, dealt out in turn
 
-    // Where group u of 16 keys begins, and its page; len (no keys) for what is not there.
-    auto place = [&](int u, int &k0, int &page) {
+    // Where group u of 16 keys begins, and its page; len (no keys) for what is not there.  (The page is asked
+    // for before the length is known to reach it: a table's row has entries for all of `cap`.)
+    auto place = [&](long long u, int &k0, int &page) {
         k0 = len;
         page = 0;
-        if (u >= n16) return;
-        int k = u * 16;
+        long long k = u * 16;
         if (a.row_ptr) {
-            const int e = u / per_block, *entry = a.col_idx + first + e;
+            if (u >= n16) return;
+            const int e = (int)u / per_block, *entry = a.col_idx + first + e;
             const int j = __ldg(entry), before = e > 0 ? __ldg(entry - 1) : -1;
             if (j < 0 || j >= nb || j <= before) {
                 raise_status(a.flags, kDevBadSchedule);
                 return;
             }
-            k = j * a.block + (u % per_block) * 16;
+            k = (long long)j * a.block + u % per_block * 16;
         }
-        if (k >= len) return;
+        if (k >= cap) return;
         const int p = __ldg(a.page_table + (long long)b * a.max_pages + (k >> a.page_shift));
+        if (k >= len) return;
         if (p < 0 || p >= a.num_pages) {
             raise_status(a.flags, kDevBadSchedule);
             return;
         }
-        k0 = k;
+        k0 = (int)k;
         page = p;
     };
     // Lane i looks up group i % kSub of the warp's step kBatch * batch + i / kSub.
     auto places = [&](int batch, int &k0, int &page) {
         const long long step = worker + ((long long)batch * kBatch + lane / kSub) * workers;
-        place(step < steps ? (int)step * kSub + lane % kSub : INT_MAX, k0, page);
+        place(step * kSub + lane % kSub, k0, page);
     };
     const int mask = (1 << a.page_shift) - 1;
     const long long head_at = (long long)kvh << a.page_shift;
@@ -191,15 +203,6 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
 
     int k0_now, page_now, k0_next, page_next;  // of this batch of steps, and the one after
     places(0, k0_now, page_now);
-    uint4 q[kGroups][kVec];
-#pragma unroll
-    for (int m = 0; m < kGroups; ++m)
-#pragma unroll
-        for (int c = 0; c < kVec; ++c)
-            q[m][c] = 8 * m + g < queries ? __ldg(reinterpret_cast<const uint4 *>(
-                                                a.Q + ((long long)b * a.H + first_q + 8 * m + g) * D + t * 8 + 32 * c))
-                                          : make_uint4(0u, 0u, 0u, 0u);
-
     // The copies of step n, 16 keys and then 16 values at a time, a group of copies in any case.
     const uint32_t ring = smem_u32(smem) + warp * kRing;
     constexpr int kPieces = D / 8, kRows = 32 / kPieces;  // pieces per row, rows that a warp's copy takes
@@ -269,8 +272,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
         float sc[kGroups][kSub][4];
 #pragma unroll
         for (int s = 0; s < kSub; ++s) {
+            float other[kGroups][4];  // half of the dimensions: two chains of products
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i) sc[i][s][0] = sc[i][s][1] = sc[i][s][2] = sc[i][s][3] = 0.f;
+            for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[i][s][e] = other[i][e] = 0.f;
 #pragma unroll
             for (int v = 0; v < kVec; ++v) {
                 const uint32_t at = (v & 1 ? k_odd : k_even) + stage + s * 2048 + v / 2 * 128;
@@ -279,7 +285,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
                 for (int i = 0; i < kGroups; ++i) {
                     const uint4 &z = q[i][v];
                     mma<kBF16>(sc[i][s], x.x, y.x, x.y, y.y, z.x, z.y);
-                    mma<kBF16>(sc[i][s], x.z, y.z, x.w, y.w, z.z, z.w);
+                    mma<kBF16>(other[i], x.z, y.z, x.w, y.w, z.z, z.w);
                 }
             }
             const int k0 = __shfl_sync(0xffffffffu, k0_now, n % kBatch * kSub + s);
@@ -287,34 +293,49 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 float (&c)[4] = sc[i][s];
-                c[0] = there ? c[0] * a.scale_log2 : -INFINITY;
-                c[1] = there ? c[1] * a.scale_log2 : -INFINITY;
-                c[2] = there8 ? c[2] * a.scale_log2 : -INFINITY;
-                c[3] = there8 ? c[3] * a.scale_log2 : -INFINITY;
+                c[0] = there ? (c[0] + other[i][0]) * a.scale_log2 : -INFINITY;
+                c[1] = there ? (c[1] + other[i][1]) * a.scale_log2 : -INFINITY;
+                c[2] = there8 ? (c[2] + other[i][2]) * a.scale_log2 : -INFINITY;
+                c[3] = there8 ? (c[3] + other[i][3]) * a.scale_log2 : -INFINITY;
             }
         }
-        uint32_t hi[kGroups][kSub][2], lo[kGroups][kSub][2];
+        // The reference of a query's weights follows its maximum only once a score is kSlack above it.
+        bool grown = false;
+        float top[kGroups][2];
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-            float p[kSub][4];
+        for (int i = 0; i < kGroups; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {  // queries 2 t and 2 t + 1
-                float top = m[i][e];
+                top[i][e] = fmaxf(sc[i][0][e], sc[i][0][e + 2]);
 #pragma unroll
-                for (int s = 0; s < kSub; ++s) top = fmaxf(top, fmaxf(sc[i][s][e], sc[i][s][e + 2]));
+                for (int s = 1; s < kSub; ++s) top[i][e] = fmaxf(top[i][e], fmaxf(sc[i][s][e], sc[i][s][e + 2]));
+                grown |= top[i][e] > m[i][e] + kSlack;
+            }
+        if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float ref = reference(top) - kLift;
-                if (top > m[i][e]) {  // (of all of the query's lanes)
-                    const float keep = ex2_approx(m[i][e] - reference(top));
+            for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float to = fmaxf(m[i][e], top[i][e]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, o));
+                    const float keep = ex2_approx(m[i][e] - reference(to));
                     l[i][e] *= keep;
 #pragma unroll
                     for (int j = 0; j < kTiles; ++j) {
                         acc[i][j][e] *= keep;
                         acc[i][j][e + 2] *= keep;
                     }
-                    m[i][e] = top;
+                    m[i][e] = to;
                 }
+        }
+        uint32_t hi[kGroups][kSub][2], lo[kGroups][kSub][2];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            float p[kSub][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float ref = reference(m[i][e]) - kLift;
 #pragma unroll
                 for (int s = 0; s < kSub; ++s) {
                     p[s][e] = ex2_approx(sc[i][s][e] - ref);
@@ -483,23 +504,26 @@ tsa_status launch_groups(const PagedDecodeLaunch &a) {
 }  // namespace
 
 void split_paged_decode(PagedDecodeLaunch *a) {
-    const int per = 8 * groups_of(*a), share = a->H / a->HK;
+    const int per = 8 * groups_of(*a), share = a->H / a->HK, kStep = a->D == 64 ? 32 : 16;
     const long long rows = (long long)a->B * a->HK * ((share + per - 1) / per);
     const long long cap = (long long)a->max_pages << a->page_shift;
     const long long keys = a->nnz_cap > 0 ? std::min(cap, ((long long)a->nnz_cap * a->block + a->B - 1) / a->B) : cap;
-    const long long steps = (keys + 31) / 32;
-    const long long slots = 152 * 2;
-    int ranks = 1, parts = 1;
-    while (ranks < 8) {
-        const long long least = 2 * ranks * rows <= slots ? 1 : 32;
-        if (ranks * kWarps * least >= steps) break;
-        ranks *= 2;
-    }
-    if (ranks == 8) {
-        while (parts < 32 && 2 * parts * ranks * rows <= slots && 2ll * parts * ranks * kWarps * 8 <= steps) parts *= 2;
-    }
-    a->ranks = ranks;
-    a->parts = parts;
+    const long long steps = (keys + kStep - 1) / kStep;  // of a row
+    // Thread blocks per row.  As many as the GPU holds at once (two per multiprocessor, 32 clusters of eight)
+    // while every warp has a step, clusters first: us with 1 / 2 / 4 / 8 of them, 16 rows of 32 steps 8.1 / 6.3 /
+    // 5.0 / 4.9; 128 rows of 86 steps 19.4 / 17.3 / 22.1 / 30.2; with 1 / 4 clusters of eight, 8 rows of 8192 steps
+    // 161 / 85, of 256 steps 9.6 / 8.6.  Four times as many where each warp is left 24 steps and the blocks would
+    // not fill their last wave, so that short and long rows even out: 256 ragged rows of 384 steps 119 -> 111, 32
+    // of 6000 steps 212 -> 191; but 512 rows of 512 steps 290 -> 296, 256 of 250 steps 76 -> 78.
+    const long long slots = 2 * 152, clusters = 32;
+    long long ranks = 1, parts = 1;
+    while (ranks < 8 && 2 * ranks * rows <= slots && ranks * kWarps < steps) ranks *= 2;
+    if (ranks == 8) parts = std::max(1ll, std::min(clusters / rows, steps / (8 * kWarps * 2)));
+    const long long blocks = rows * ranks * parts;
+    if ((blocks <= slots || blocks % slots < slots / 2) && blocks < 4 * slots && steps >= 4 * ranks * parts * kWarps * 24)
+        for (int i = 0; i < 2; ++i) (ranks < 8 ? ranks : parts) *= 2;
+    a->ranks = (int)ranks;
+    a->parts = (int)parts;
 }
 
 size_t paged_decode_workspace(const PagedDecodeLaunch &a) {
