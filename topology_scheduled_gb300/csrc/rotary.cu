@@ -154,9 +154,12 @@ tsa_status launch_rows(RowsLaunch *a, int sms) {
     const long long tiles = ((long long)a->B * a->S + per_cta - 1) / per_cta;
     int heads = 0;
     for (const RowsPart &p : a->part) heads += p.heads;
-    // Heads per thread block: as many as leave the GPU four blocks per multiprocessor, 16 at most.
-    int per = 16;
-    while (per > 1 && tiles * ((heads + per - 1) / per) < 4ll * sms) per /= 2;
+    // Heads per thread block: 8, or as many as leave half of the multiprocessors a block.  A block's angles cost
+    // as much as two to three heads' rows, but one block's heads are one after the other: us with 1 / 2 / 4 / 8 / 16,
+    // [2, 64 heads, 32768, 128] 1098 / 575 / 338 / 310 / 312, [1, 48, 663, 128] 11.6 / 7.8 / 5.3 / 5.2 / 6.7,
+    // [3, 16, 1999, 128] 27.6 / 16.1 / 11.0 / 9.2 / 10.7, [1, 32, 1, 64] 3.2 / 3.3 / 3.5 / 4.0 / 5.2.
+    int per = 8;
+    while (per > 1 && tiles * ((heads + per - 1) / per) < sms / 2) per /= 2;
     a->heads_per_cta = per;
     const dim3 grid((unsigned)tiles, (unsigned)((heads + per - 1) / per));
     void (*kernel)(RowsLaunch) = a->bf16 ? (a->interleaved ? rows_kernel<true, true> : rows_kernel<true, false>)
