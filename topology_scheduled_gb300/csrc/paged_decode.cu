@@ -128,6 +128,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     static_assert(kWarps * kQ * D * 4 <= kSmem, "the sums fit where the rings were");
     __shared__ float warp_m[kWarps][kQ], warp_l[kWarps][kQ], cta_m[kQ], cta_l[kQ];
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int share = a.H / a.HK, chunks = (share + kQ - 1) / kQ;
     const int rank = blockIdx.x % a.ranks, part = blockIdx.x / a.ranks % a.parts;
@@ -453,9 +454,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     if (a.ranks > 1) cluster_sync();  // no thread block leaves while its shared memory may be read
 }
 
-// Joins the parts' sums of one query, D dimensions.
+// Joins the parts' sums of one query, D dimensions.  (Launched while the kernel that makes them still runs; it
+// waits for all of that kernel before it reads.)
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(D) join_parts_kernel(const float *__restrict__ partial, uint16_t *__restrict__ O, int parts) {
+__global__ void __launch_bounds__(D) join_parts_kernel(const float *partial, uint16_t *O, int parts) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long row = blockIdx.x;
     const int d = threadIdx.x;
     const float *from = partial + row * parts * (D + 2);
@@ -490,8 +493,17 @@ tsa_status launch_one(const PagedDecodeLaunch &a) {
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, kBF16, kGroups>, a) != cudaSuccess) return TSA_ERR_CUDA;
     if (a.parts > 1) {
-        join_parts_kernel<D, kBF16><<<(unsigned)(a.B * a.H), D, 0, a.stream>>>(a.partial, a.O, a.parts);
-        if (cudaGetLastError() != cudaSuccess) return TSA_ERR_CUDA;
+        cudaLaunchConfig_t join = {};
+        join.gridDim = dim3((unsigned)(a.B * a.H));
+        join.blockDim = dim3(D);
+        join.stream = a.stream;
+        cudaLaunchAttribute early;
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        join.attrs = &early;
+        join.numAttrs = 1;
+        if (cudaLaunchKernelEx(&join, join_parts_kernel<D, kBF16>, (const float *)a.partial, a.O, a.parts) != cudaSuccess)
+            return TSA_ERR_CUDA;
     }
     return TSA_OK;
 }
