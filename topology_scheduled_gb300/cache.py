@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import math
 from array import array
+from functools import lru_cache
 
 import torch
 
@@ -184,6 +185,7 @@ def tsa_paged_append(Q, K, V, K_cache, V_cache, page_table, seq_lens, counts=Non
     return out
 
 
+@lru_cache(maxsize=1024)  # of sizes alone
 def tsa_paged_attention_decode_workspace_bytes(B: int, H: int, HK: int, D: int, page_size: int, max_pages: int,
                                                block: int = 64, nnz_cap: int = 0) -> int:
     return int(lib().tsa_paged_attention_decode_workspace_bytes(B, H, HK, D, page_size, max_pages, block, nnz_cap))
@@ -206,11 +208,10 @@ def tsa_paged_attention_decode(Q, K_cache, V_cache, page_table, seq_lens, row_pt
     ci = None if row_ptr is None else _schedule(row_ptr, col_idx, B, Q.device, other)
     nnz = 0 if ci is None else ci.numel()
     out = _output("out", out, Q, other)
-    L = lib()
-    need = L.tsa_paged_attention_decode_workspace_bytes(B, H, HK, D, size, page_table.shape[1], block, nnz)
+    need = tsa_paged_attention_decode_workspace_bytes(B, H, HK, D, size, page_table.shape[1], block, nnz)
     if need or workspace is not None:
-        workspace = _workspace(workspace, max(int(need), 1), Q.device, "tsa_paged_attention_decode", other)
-    _check(L.tsa_paged_attention_decode(
+        workspace = _workspace(workspace, max(need, 1), Q.device, "tsa_paged_attention_decode", other)
+    _check(lib().tsa_paged_attention_decode(
         Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), num, size, k_stride, v_stride, page_table.data_ptr(),
         page_table.shape[1], seq_lens.data_ptr(), None if ci is None else row_ptr.data_ptr(),
         None if ci is None else ci.data_ptr(), nnz, out.data_ptr(), _dtype_code(Q), B, H, HK, D, block,
