@@ -529,7 +529,7 @@ void split_paged_decode(PagedDecodeLaunch *a) {
     // of 6000 steps 212 -> 191; but 512 rows of 512 steps 290 -> 296, 256 of 250 steps 76 -> 78.
     const long long slots = 2 * 152, clusters = 32;
     long long ranks = 1, parts = 1;
-    while (ranks < 8 && 2 * ranks * rows <= slots && ranks * kWarps < steps) ranks *= 2;
+    while (ranks < 8 && 2 * ranks * rows <= slots && 2 * ranks * kWarps <= steps) ranks *= 2;
     if (ranks == 8) parts = std::max(1ll, std::min(clusters / rows, steps / (8 * kWarps * 2)));
     const long long blocks = rows * ranks * parts;
     if ((blocks <= slots || blocks % slots < slots / 2) && blocks < 4 * slots && steps >= 4 * ranks * parts * kWarps * 24)
