@@ -16,8 +16,8 @@ from __future__ import annotations
 
 import torch
 
-from .binding import tsa_scheduled_attention_backward, tsa_scheduled_attention_fwd
-from .cache import _frequencies, tsa_rotary
+from .binding import calls, tsa_scheduled_attention_backward, tsa_scheduled_attention_fwd
+from .cache import _frequencies
 from .terms import (_starts, tsa_biased_attention_backward, tsa_biased_attention_fwd,
                     tsa_differential_attention_backward, tsa_differential_attention_fwd)
 
@@ -106,51 +106,6 @@ def differential_attention(Q, K, V, row_ptr, col_idx, lambda_q1, lambda_k1, lamb
                                        float(lambda_init), scale, int(block))
 
 
-def _strided(t):
-    """`t` as the rotation reads it: whole rows, multiples of 16 bytes apart and from such a boundary on.  (The
-    gradient that reaches a backward pass may be any view.)"""
-    b, h, s, d = t.stride()
-    return t if d == 1 and (b | h | s) % 8 == 0 and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
-
-
-def _layout_of(t):
-    """How a gradient of `t` is laid out: as t where t is dense with heads or tokens first, None for contiguous."""
-    return None if t is None or not t.transpose(1, 2).is_contiguous() else t.stride()
-
-
-class Rotary(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, Q, K, frequencies, positions, interleaved, magnitude, inverse):
-        frequencies = frequencies[:]  # a copy: the caller's may change before the backward
-        ctx.settings = frequencies, interleaved, magnitude, inverse, _layout_of(Q), _layout_of(K)
-        if positions is not None:
-            ctx.save_for_backward(positions)
-        ctx.set_materialize_grads(False)
-        return tsa_rotary(_strided(Q), None if K is None else _strided(K), frequencies, positions,
-                          interleaved=interleaved, magnitude=magnitude, inverse=inverse)
-
-    @staticmethod
-    def backward(ctx, dQ, dK=None):
-        # the rotation back, which is one of these itself where its own gradient is wanted
-        frequencies, interleaved, magnitude, inverse, *layouts = ctx.settings
-        positions = ctx.saved_tensors[0] if ctx.saved_tensors else None
-        at = [i for i, g in enumerate((dQ, dK)) if g is not None and ctx.needs_input_grad[i]]
-        back = [None] * 7
-        if at:
-            grads = [(dQ, dK)[i] for i in at] + [None] * (2 - len(at))
-            if torch.is_grad_enabled():
-                r = Rotary.apply(*grads, frequencies, positions, interleaved, magnitude, not inverse)
-            else:
-                grads = [None if g is None else _strided(g) for g in grads]
-                outs = [None if layouts[i] is None else torch.empty_strided(g.shape, layouts[i], dtype=g.dtype, device=g.device)
-                        for i, g in zip(at, grads)] + [None]
-                r = tsa_rotary(*grads, frequencies, positions, interleaved=interleaved, magnitude=magnitude,
-                               inverse=not inverse, out=outs[0], out_k=outs[1])
-            for i, x in zip(at, (r,) if len(at) == 1 else r):
-                back[i] = x
-        return tuple(back)
-
-
 def rotary(Q, K, frequencies, positions=None, interleaved: bool = False, magnitude: float = 1.0):
     """tsa_rotary of Q and K (or of Q alone, K None) with gradients for both, in their layouts."""
-    return Rotary.apply(Q, K, _frequencies(frequencies), positions, bool(interleaved), float(magnitude), False)
+    return calls().rotary_autograd(Q, K, _frequencies(frequencies), positions, interleaved, magnitude)

@@ -7,6 +7,7 @@ fallback: if the library is missing or a call fails, the functions raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -26,6 +27,7 @@ TIE_RULES = {"index": 0, "content": 1}
 
 _LOCK = threading.Lock()
 _LIB = None
+_CALLS = None
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -118,6 +120,21 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
                 fn.argtypes = args
             _LIB = L
     return _LIB
+
+
+def calls():
+    """The loaded module of the calls that are marshalled natively (csrc/calls.cpp)."""
+    global _CALLS
+    if _CALLS is None:
+        lib()  # built with it
+        with _LOCK:
+            if _CALLS is None:
+                spec = importlib.util.spec_from_file_location("tsa_calls", _build.CALLS)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                module.set_error(TsaError)
+                _CALLS = module
+    return _CALLS
 
 
 def _check(status: int, where: str):

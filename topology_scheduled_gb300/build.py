@@ -1,4 +1,5 @@
-"""Build libtsa.so in-tree with nvcc for sm_103a (no torch extension, no cmake).
+"""Build libtsa.so in-tree with nvcc for sm_103a (no torch extension, no cmake), and tsa_calls.so, the
+module that marshals some of its calls, with g++.
 
     python -m topology_scheduled_gb300.build
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtsa.so")
+CALLS = os.path.join(BUILD, "tsa_calls.so")
 
 SOURCES = ["api.cu", "schedule.cu", "segment.cu", "attention.cu", "attention_biased.cu",
            "attention_differential.cu", "terms_api.cu", "backward.cu", "backward_biased.cu", "backward_differential.cu",
@@ -32,6 +35,21 @@ LINK = ARCH + ["-cudart", "shared", "-shared"]
 FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 
+
+
+def _calls_flags() -> tuple[list[str], list[str]]:
+    """Compiler and linker flags of tsa_calls.so: Python's, PyTorch's and the CUDA runtime's headers."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    return (["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"] +
+            [x for d in include for x in ("-I", d)],
+            ["-shared", "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+             "-L", BUILD, "-l:libtsa.so", "-Wl,-rpath,$ORIGIN"])
+
+
 def _nvcc() -> str:
     for cand in (shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -41,10 +59,12 @@ def _nvcc() -> str:
 
 def _digest() -> str:
     h = hashlib.sha1()
-    for p in [os.path.join(CSRC, s) for s in SOURCES] + HEADERS:
+    for p in [os.path.join(CSRC, s) for s in SOURCES + ["calls.cpp"]] + HEADERS:
         with open(p, "rb") as f:
             h.update(f.read())
-    h.update(" ".join(FLAGS + LINK).encode())
+    flags, link = _calls_flags()
+    import torch
+    h.update(" ".join(FLAGS + LINK + flags + link + [torch.__version__]).encode())
     return h.hexdigest()[:16]
 
 
@@ -53,7 +73,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     stamp = os.path.join(BUILD, "stamp")
     digest = _digest()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp):
+    if not force and os.path.exists(LIB) and os.path.exists(CALLS) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == digest:
                 return LIB
@@ -71,13 +91,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    calls_flags, calls_link = _calls_flags()
+    calls_obj = os.path.join(BUILD, "calls.o")
+
+    def compile_calls() -> None:
+        r = subprocess.run(["g++"] + calls_flags + ["-c", os.path.join(CSRC, "calls.cpp"), "-o", calls_obj],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls_done = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, SOURCES))
+        calls_done.result()
     tmp = f"{LIB}.{os.getpid()}.tmp"
     r = subprocess.run([nvcc] + LINK + ["-o", tmp] + objs, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = f"{CALLS}.{os.getpid()}.tmp"
+    r = subprocess.run(["g++", calls_obj, "-o", tmp] + calls_link, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
     with open(stamp, "w") as f:
         f.write(digest)
     return LIB
