@@ -145,25 +145,21 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
                                                 a.Q + ((long long)b * a.H + first_q + 8 * m + g) * D + t * 8 + 32 * c))
                                           : make_uint4(0u, 0u, 0u, 0u);
 
-    int len = __ldg(a.lens + b);
-    int n16 = 0, first = 0;  // groups of 16 keys to visit
-    const int per_block = a.block / 16, cap = a.max_pages << a.page_shift;
+    int len = __ldg(a.lens + b), first = 0, entries = 0;
+    if (a.row_ptr) {
+        first = __ldg(a.row_ptr + b);
+        entries = __ldg(a.row_ptr + b + 1) - first;
+    }
+    const int per_block = a.block / 16, cap = a.max_pages << a.page_shift, nb = (cap + a.block - 1) / a.block;
     if (len < 0 || len > cap) {
         if (tid == 0) raise_status(a.flags, kDevBadSchedule);
         len = 0;
     }
-    const int nb = (cap + a.block - 1) / a.block;
-    if (a.row_ptr) {
-        first = __ldg(a.row_ptr + b);
-        int entries = __ldg(a.row_ptr + b + 1) - first;
-        if (first < 0 || entries < 0 || entries > nb || first > a.nnz_cap - entries) {
-            if (tid == 0) raise_status(a.flags, kDevBadSchedule);
-            entries = 0;
-        }
-        n16 = len > 0 ? entries * per_block : 0;
-    } else {
-        n16 = (len + 15) / 16;
+    if (a.row_ptr && (first < 0 || entries < 0 || entries > nb || first > a.nnz_cap - entries)) {
+        if (tid == 0) raise_status(a.flags, kDevBadSchedule);
+        entries = 0;
     }
+    const int n16 = !a.row_ptr ? (len + 15) / 16 : len > 0 ? entries * per_block : 0;  // groups of 16 keys to visit
     const int workers = a.ranks * a.parts * kWarps, worker = (part * a.ranks + rank) * kWarps + warp;
     const int steps = (n16 + kSub - 1) / kSub;  // of all workers, dealt out in turn
 
@@ -202,7 +198,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     const long long head_at = (long long)kvh << a.page_shift;
     auto row_at = [&](int k0, int page, int64_t page_stride) { return page * page_stride + (head_at + (k0 & mask)) * D; };
 
-    int k0_now, page_now, k0_next, page_next;  // of this batch of steps, and the one after
+    int k0_now, page_now, k0_next = 0, page_next = 0;  // of this batch of steps, and the one after
     places(0, k0_now, page_now);
     // The copies of step n, 16 keys and then 16 values at a time, a group of copies in any case.
     const uint32_t ring = smem_u32(smem) + warp * kRing;
@@ -244,7 +240,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
         if (n < mine) copy_step(n, 0);
         copies_begun();
     }
-    places(1, k0_next, page_next);
+    if (mine > kBatch) places(1, k0_next, page_next);
     // a lane's pieces of a step's keys (rows g and g + 8) and values (rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9)
     const uint32_t k_even = ring + g * 2 * D + ((t ^ ((g & 1) << 2)) << 4), k_odd = k_even ^ 64;
     const uint32_t v_at = ring + kHalf + 2 * t * 2 * D + ((g ^ (t << 1)) << 4);
@@ -263,7 +259,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
         if (n > 0 && n % kBatch == 0) {
             k0_now = k0_next;
             page_now = page_next;
-            places(batch + 1, k0_next, page_next);
+            if (mine > (batch + 1) * kBatch) places(batch + 1, k0_next, page_next);
         }
         if (n + kStages - 1 < mine) copy_step(n + kStages - 1, batch);
         copies_begun();
