@@ -126,6 +126,8 @@ def test_strides():
         assert _rotary(strides=s) == INVALID, (at, value)
     s = array("q", (0, 0, 0) + (0, 0, 0) + dense + k)  # inputs may be broadcast
     assert _passes(_rotary(strides=s))
+    s = array("q", dense + (-1, -1, -1) + dense + (-1, -1, -1))  # nor is a missing tensor's read
+    assert _passes(_rotary(strides=s, K=None, K_out=None))
     s = array("q", (-3, 7, 5) * 4)  # an axis of one has no stride
     assert _passes(_rotary(strides=s, B=1, H=1, HK=1, S=1))
 

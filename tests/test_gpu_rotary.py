@@ -37,7 +37,8 @@ def test_positions(interleaved):
     """Far, negative and repeated positions, per batch and shared; frequencies from whole turns to none."""
     S, D = 12, 64
     x = _normal(2, 3, S, D, dtype=torch.float16, seed=3)
-    f = [65536.0, -3.5, 2 * math.pi, 1.0, 0.3, 1e-3, 1e-9, 0.0] + list(tsa.rotary_frequencies(48, 1e6))
+    f = [65536.0, -3.5, 2 * math.pi, 1.0, 0.3, 1e-3, 1e-9, 0.0, -1e-9, -0.0, -65536.0, 1e-300, -0.3, 4096.25, -1e-5, 1e-16]
+    f += list(tsa.rotary_frequencies(32, 1e6))
     rows = [[0, 1, -1, 2, 1 << 20, 1 << 30, (1 << 31) - 1, -(1 << 31), 131071, 5, 5, -77777],
             [1000003 * i for i in range(S)]]
     pos = torch.tensor(rows, dtype=torch.int32, device=DEV)
@@ -47,6 +48,14 @@ def test_positions(interleaved):
     out = tsa.tsa_rotary(x.to(DEV), None, f, pos[0].contiguous(), interleaved=interleaved)
     for b in range(2):
         close(out[b], *rotated(x[b], rows[0], f, interleaved), f"shared, batch {b}")
+
+
+def test_many_heads():
+    x = _normal(1, 30000, 1, 16, dtype=torch.bfloat16, seed=5)
+    f = tsa.rotary_frequencies(16, 100.0)
+    out = tsa.tsa_rotary(x.to(DEV), x[:, :7].to(DEV), f, torch.tensor([77], dtype=torch.int32, device=DEV))
+    close(out[0], *rotated(x, [77], f))
+    close(out[1], *rotated(x[:, :7], [77], f))
 
 
 def test_inverse_undoes():

@@ -78,8 +78,8 @@ struct Rows {
 // may not share memory.
 tsa_status rows_in(const void *p, const int64_t *strides, int64_t B, int64_t heads, int64_t S, int64_t D, bool output,
                    Rows *r) {
-    r->p = p;
-    r->heads = heads;
+    *r = {p, heads, {0, 0, 0}};
+    if (!p) return TSA_OK;
     const int64_t dense[3] = {heads * S * D, S * D, D}, n[3] = {B, heads, S};
     for (int i = 0; i < 3; ++i) {
         r->stride[i] = n[i] == 1 ? 0 : strides ? strides[i] : dense[i];
@@ -117,13 +117,13 @@ RowsPart part_of(const Rows &from, const Rows &to, bool rotated) {
 }
 
 // A pair's turns per position, f / 2 pi, as a 64-bit fraction of a turn (modulo whole turns): the product with
-// 1 / 2 pi in two binary64 parts, whose sum is off by less than 2^-100 turns times max(f, 1).
+// 1 / 2 pi in two binary64 parts, whose sum is off by less than 2^-100 turns times max(|f|, 1).
 uint64_t fraction_of_turn(double f) {
     constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+    if (f < 0.0) return 0 - fraction_of_turn(-f);
     double p = f * kHi;
     const double e = std::fma(f, kHi, -p) + f * kLo;
-    p -= std::floor(p);                       // exact, in [0, 1]
-    if (p >= 1.0) p = 0.0;
+    p -= std::floor(p);  // exact: p is not negative
     const double x = p * 0x1p64, whole = std::floor(x);
     return (uint64_t)whole + (uint64_t)(int64_t)std::llrint((x - whole) + e * 0x1p64);
 }
