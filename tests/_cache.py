@@ -2,10 +2,12 @@
 bounds; r is the unit roundoff of the inputs' type (2^-8 bf16, 2^-11 f16), eta half its subnormal spacing.
 
 * Rotation.  The reference's angles are exact (rationals, reduced by whole turns) up to binary64.  The kernel's
-  fraction of a turn is off by |p| 2^-65 (2^-34 for the largest position: below 2^-31 as an angle); rounding it
-  to binary32 moves an angle of at most pi by pi 2^-24; sincospif is 1 ulp off, 2^-24 at most; the magnitude's own rounding and the
-  product with it 2 x 2^-24: a cosine or sine is at most (pi + 1 + 2 + 1) 2^-24 m off.  The two roundings of the
-  pair's sum are 2 x 2^-24 of the products: 10 2^-24 m (|a| + |b|) covers all, then the result is rounded (r).
+  fraction of a turn is off by |p| 2^-65 (2^-34 for the largest position: below 2^-31 as an angle), and its lower half,
+  2^-32 of a turn, is dropped; the rest of a quarter turn, at most pi / 4, is converted, scaled by a rounded factor and
+  rounded: 2.5 2^-24 of it, 1.94 2^-24.  Taylor's series leave out 2^-29 at most and lose 1.1 2^-24 to their roundings;
+  the magnitude's own rounding and the product with it lose 2 x 2^-24: a cosine or sine is at most 5.2 2^-24 m off.
+  (The bound was derived for 7.2 2^-24 m, sincospif's.)  The two roundings of the pair's sum are 2 x 2^-24 of the
+  products: 10 2^-24 m (|a| + |b|) covers all, then the result is rounded (r).
 * Attention.  A score is a binary32 sum of D exact products, each step of a tensor core's sum at most 2^-23 off:
   D 2^-23 scale |q|.|k|.  Its scaling and the subtraction of the maximum lose 4 2^-24 (|z| + |max|), exp2 (2 ulp)
   2^-22.  A weight is kept as two numbers: r^2 of it is lost, or in f16 (scaled by 2^14, below that half a
