@@ -7,15 +7,15 @@
 //  * a warp takes 16 keys at a time for up to 8 (or 16) queries.  Scores are S^T = K Q^T, keys as rows.  The
 //    order of a contraction is free, so a lane's 16-byte piece of a key serves as two k16 steps' fragment and
 //    the same piece of a query as their other operand;
-//  * O^T = V^T P^T, dimensions as rows.  A lane loads the same 8 dimensions of four keys, and a byte permute
-//    pairs two keys' elements: that is V^T's fragment.  P^T's is the scores' fragment, transposed (movmatrix);
+//  * O^T = V^T P^T, dimensions as rows.  V^T's fragment is read transposed (ldmatrix.trans); P^T's is the scores'
+//    fragment, transposed (movmatrix);
 //  * a weight is the sum of two numbers of the inputs' type, each with a product of its own, so weights keep
 //    16 (bf16) or 22 bits; in f16 they are scaled by 2^14 beforehand, so that none above 2^-38 of the largest
 //    vanishes.  Sums, maxima and denominators are binary32;
 //  * a warp copies its keys and values to a ring of its own in shared memory (cp.async), two steps ahead of
 //    the one it works on: up to 24 KB in flight per warp, whatever the registers hold.  16 keys of a page are
-//    one contiguous 2 D x 16 byte piece; its 16-byte pieces are stored with the row's bits exclusive-ored into
-//    their place, so that the reads of eight lanes meet all banks once.
+//    one contiguous 2 D x 16 byte piece; its 16-byte pieces are stored with bits of the row's number
+//    exclusive-ored into their place, so that the reads of eight lanes meet all banks once.
 // A (sequence, key head, group of queries) is split over the warps of a cluster of thread blocks, whose sums
 // are joined through shared memory in a fixed order; where eight blocks a row cannot fill the GPU, several
 // clusters share a row, leave their sums in the workspace, and a second kernel joins them.
@@ -23,7 +23,6 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
-#include <type_traits>
 
 #include "tsa_device.cuh"
 #include "tsa_internal.h"
@@ -78,12 +77,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Elements `i` (0..7) of two vectors, in one word.
-template <int i>
-__device__ __forceinline__ uint32_t pair_of(const uint4 &x, const uint4 &y) {
-    const uint32_t u = i / 2 == 0 ? x.x : i / 2 == 1 ? x.y : i / 2 == 2 ? x.z : x.w;
-    const uint32_t v = i / 2 == 0 ? y.x : i / 2 == 1 ? y.y : i / 2 == 2 ? y.z : y.w;
-    return __byte_perm(u, v, i % 2 == 0 ? 0x5410 : 0x7632);
+// Four 8 x 8 matrices of 16-bit elements, transposed; lane 8 i + r gives the place of matrix i's row r.
+__device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&x)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(at)
+                 : "memory");
 }
 
 // Two weights as a word of their roundings to the inputs' type and a word of what those leave.
@@ -117,7 +116,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     constexpr int kSub = D == 64 ? 2 : 1;
     constexpr int kVec = D / 32;   // 16-byte pieces of a key that a lane holds
-    constexpr int kV = D / 64;     // .. of a value row
     constexpr int kTiles = D / 16; // m16 tiles of the output's dimensions
     constexpr int kQ = 8 * kGroups;
     constexpr int kBatch = 32 / kSub;  // a warp's steps whose places it looks up at once
@@ -230,7 +228,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
 #pragma unroll
             for (int i = 0; i < 16 / kRows; ++i) {
                 const int r = i * kRows + row_in;
-                copy16(to + kHalf + s * 2048 + r * 2 * D + ((piece ^ ((r & 6))) << 4), v + i * 256, k0 + r < len);
+                copy16(to + kHalf + s * 2048 + r * 2 * D + ((piece ^ (r & 7)) << 4), v + i * 256, k0 + r < len);
             }
         }
     };
@@ -241,9 +239,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
         copies_begun();
     }
     if (mine > kBatch) places(1, k0_next, page_next);
-    // a lane's pieces of a step's keys (rows g and g + 8) and values (rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9)
+    // a lane's pieces of a step's keys (rows g and g + 8), and its row of the values' 8 x 8 matrices (keys below 8,
+    // then from 8 on; of two neighbouring pieces each)
     const uint32_t k_even = ring + g * 2 * D + ((t ^ ((g & 1) << 2)) << 4), k_odd = k_even ^ 64;
-    const uint32_t v_at = ring + kHalf + 2 * t * 2 * D + ((g ^ (t << 1)) << 4);
+    const uint32_t v_row = ring + kHalf + ((lane & 7) + (lane >> 4) * 8) * 2 * D, v_piece = ((lane >> 3 & 1) ^ (lane & 7)) << 4;
 
     float m[kGroups][2], l[kGroups][2], acc[kGroups][kTiles][4];
 #pragma unroll
@@ -351,32 +350,15 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
         }
 #pragma unroll
         for (int s = 0; s < kSub; ++s) {
-            uint4 vr[4][kV];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int c = 0; c < kV; ++c)
-                    vr[r][c] = load_piece(v_at + stage + s * 2048 + ((r & 1) + 8 * (r >> 1)) * 2 * D + 128 * c);
-            auto tile = [&](auto index) {
-                constexpr int j = decltype(index)::value, other = D == 64 ? j + 4 : j;
-                const uint32_t a0 = pair_of<j>(vr[0][0], vr[1][0]), a2 = pair_of<j>(vr[2][0], vr[3][0]);
-                const uint32_t a1 = pair_of<other>(vr[0][kV - 1], vr[1][kV - 1]);
-                const uint32_t a3 = pair_of<other>(vr[2][kV - 1], vr[3][kV - 1]);
+            for (int j = 0; j < kTiles; ++j) {
+                uint32_t v[4];
+                load_transposed(v_row + stage + s * 2048 + (v_piece ^ (j << 5 & 96)) + (j << 5 & ~96), v);
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
-                    mma<kBF16>(acc[i][j], a0, a1, a2, a3, hi[i][s][0], hi[i][s][1]);
-                    mma<kBF16>(acc[i][j], a0, a1, a2, a3, lo[i][s][0], lo[i][s][1]);
+                    mma<kBF16>(acc[i][j], v[0], v[1], v[2], v[3], hi[i][s][0], hi[i][s][1]);
+                    mma<kBF16>(acc[i][j], v[0], v[1], v[2], v[3], lo[i][s][0], lo[i][s][1]);
                 }
-            };
-            tile(std::integral_constant<int, 0>());
-            tile(std::integral_constant<int, 1>());
-            tile(std::integral_constant<int, 2>());
-            tile(std::integral_constant<int, 3>());
-            if constexpr (D == 128) {
-                tile(std::integral_constant<int, 4>());
-                tile(std::integral_constant<int, 5>());
-                tile(std::integral_constant<int, 6>());
-                tile(std::integral_constant<int, 7>());
             }
         }
         __syncwarp();  // the stage may be written again
@@ -398,8 +380,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
             }
 #pragma unroll
             for (int j = 0; j < kTiles; ++j) {
-                sum[warp][query][8 * g + j] = acc[i][j][e];
-                sum[warp][query][(D == 64 ? 8 * g + 4 : 64 + 8 * g) + j] = acc[i][j][e + 2];
+                sum[warp][query][16 * j + g] = acc[i][j][e];
+                sum[warp][query][16 * j + g + 8] = acc[i][j][e + 2];
             }
         }
     __syncthreads();
