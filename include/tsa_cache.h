@@ -12,7 +12,7 @@
  * A paged cache is two arrays K_cache, V_cache of num_pages pages; a page holds page_size tokens of every
  * key/value head, [HK, page_size, D] contiguous, and page p begins p * page_stride elements into its array
  * (page_stride >= HK * page_size * D, any for one page: both arrays may be slices of one).  page_table[b][i] is the page of
- * sequence b's tokens [i * page_size, (i + 1) * page_size); entries that no token reaches are not read.
+ * sequence b's tokens [i * page_size, (i + 1) * page_size); what entries that no token reaches hold does not matter.
  *
  * Rows of Q, K, V and of the rotated outputs are D contiguous elements; `strides` (int64 in HOST memory,
  * read during the call) gives, for each tensor in the order stated, the elements from one batch, head and

@@ -308,3 +308,49 @@ def test_refusals():
     with pytest.raises(TypeError):
         tsa.tsa_rotary(x.float(), None, f)
     assert tsa.tsa_last_device_status() == 0
+
+
+def test_several_host_threads():
+    """Threads with streams of their own, whose calls differ in size (some with a workspace): each gets what it gets alone."""
+    import threading
+
+    f = tsa.rotary_frequencies(64)
+
+    def inputs(i):
+        H, HK, n, page = ((4, 4, 300, 16), (8, 1, 30000, 64), (16, 2, 90, 32))[i % 3]
+        lengths = [n + i, 5]
+        table, pages = page_lists(lengths, page, seed=i)
+        x = [_normal(2, h, 1, 64, dtype=torch.float16, seed=10 * i + j).to(DEV) for j, h in enumerate((H, HK, HK))]
+        return x, [_normal(pages, HK, page, 64, dtype=torch.float16, seed=50 + 10 * i + j).to(DEV) for j in range(2)], table.to(DEV), \
+            _ints(lengths)
+
+    def run(x, caches, table, lens):
+        kc, vc = (c.clone() for c in caches)
+        q = tsa.tsa_paged_append(*x, kc, vc, table, lens, None, f)
+        return tsa.tsa_paged_attention_decode(q[:, :, 0], kc, vc, table, lens), kc, vc
+
+    data = [inputs(i) for i in range(6)]
+    alone = [run(*d) for d in data]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            torch.cuda.set_device(0)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = run(*data[i])
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, alone[i])):
+                        wrong.append(i)
+                        return
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    assert tsa.tsa_last_device_status() == 0

@@ -129,7 +129,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     static_assert(kWarps * kQ * D * 4 <= kSmem, "the sums fit where the rings were");
     __shared__ float warp_m[kWarps][kQ], warp_l[kWarps][kQ], cta_m[kQ], cta_l[kQ];
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (a.parts > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be launched
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int share = a.H / a.HK, chunks = (share + kQ - 1) / kQ;
     const int rank = blockIdx.x % a.ranks, part = blockIdx.x / a.ranks % a.parts;
