@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import topology_scheduled_gb300 as tsa
-from tests._cache import attention, gathered, page_lists, rotated
+from _cache import attention, gathered, page_lists, rotated
 from topology_scheduled_gb300.binding import SIGNATURES
 
 F = 1 << 20  # any aligned address: never read on these paths

@@ -5,7 +5,7 @@ import torch
 
 import topology_scheduled_gb300 as tsa
 from topology_scheduled_gb300 import autograd
-from tests._cache import U, attention, close, gathered, page_lists, rotated
+from _cache import U, attention, close, gathered, page_lists, rotated
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import topology_scheduled_gb300 as tsa
-from tests._cache import close, page_lists, rotated
+from _cache import close, page_lists, rotated
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import topology_scheduled_gb300 as tsa
-from tests._cache import attention, close, gathered, page_lists
+from _cache import attention, close, gathered, page_lists
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"

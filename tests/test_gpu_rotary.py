@@ -7,7 +7,7 @@ import torch
 
 import topology_scheduled_gb300 as tsa
 from topology_scheduled_gb300 import autograd
-from tests._cache import close, rotated
+from _cache import close, rotated
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
