@@ -313,10 +313,8 @@ tsa_status launch_one(const DecodeLaunch &a, const Terms &terms) {
     cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
     cfg.attrs = &cluster;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<D, kBF16, Terms>, a.Q, a.K, a.V, a.lens, a.row_ptr, a.col_idx,
-                              a.nnz_cap, a.O, a.H, a.cap, a.block, a.scale_log2, a.flags, terms) == cudaSuccess
-               ? TSA_OK
-               : TSA_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, decode_kernel<D, kBF16, Terms>, a.Q, a.K, a.V, a.lens, a.row_ptr, a.col_idx,
+                                       a.nnz_cap, a.O, a.H, a.cap, a.block, a.scale_log2, a.flags, terms));
 }
 
 template <class Terms>

@@ -129,6 +129,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     static_assert(kWarps * kQ * D * 4 <= kSmem, "the sums fit where the rings were");
     __shared__ float warp_m[kWarps][kQ], warp_l[kWarps][kQ], cta_m[kQ], cta_l[kQ];
 
+    wait_for_predecessor();
     if (a.parts > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be launched
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int share = a.H / a.HK, chunks = (share + kQ - 1) / kQ;
@@ -439,7 +440,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
 // waits for all of that kernel before it reads.)
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(D) join_parts_kernel(const float *partial, uint16_t *O, int parts) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_predecessor();
     const long long row = blockIdx.x;
     const int d = threadIdx.x;
     const float *from = partial + row * parts * (D + 2);
@@ -466,25 +467,22 @@ tsa_status launch_one(const PagedDecodeLaunch &a) {
     cfg.stream = a.stream;
     static std::atomic<unsigned long long> allowed{0};
     if (!allow_smem(allowed, reinterpret_cast<const void *>(paged_decode_kernel<D, kBF16, kGroups>), kSmem)) return TSA_ERR_CUDA;
-    cudaLaunchAttribute cluster;
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = (unsigned)a.ranks;
-    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-    cfg.attrs = &cluster;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, kBF16, kGroups>, a) != cudaSuccess) return TSA_ERR_CUDA;
+    cudaLaunchAttribute attrs[2] = {{}, set_up_early()};
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = (unsigned)a.ranks;
+    attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    TSA_TRY(launched(cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, kBF16, kGroups>, a)));
     if (a.parts > 1) {
         cudaLaunchConfig_t join = {};
         join.gridDim = dim3((unsigned)(a.B * a.H));
         join.blockDim = dim3(D);
         join.stream = a.stream;
-        cudaLaunchAttribute early;
-        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        early.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchAttribute early = set_up_early();
         join.attrs = &early;
         join.numAttrs = 1;
-        if (cudaLaunchKernelEx(&join, join_parts_kernel<D, kBF16>, (const float *)a.partial, a.O, a.parts) != cudaSuccess)
-            return TSA_ERR_CUDA;
+        TSA_TRY(launched(cudaLaunchKernelEx(&join, join_parts_kernel<D, kBF16>, (const float *)a.partial, a.O, a.parts)));
     }
     return TSA_OK;
 }

@@ -80,6 +80,7 @@ __device__ __forceinline__ void turn(uint4 &lo, uint4 &hi, const float (&cs)[8],
 template <bool kBF16, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads)
 rows_kernel(const __grid_constant__ RowsLaunch a) {
+    wait_for_predecessor();
     const int units = a.D / 16;  // of two 16-byte vectors each, per row
     const int per_cta = kThreads / units;
     const int tid = threadIdx.x;
@@ -180,11 +181,16 @@ tsa_status launch_rows(RowsLaunch *a, int sms) {
     int per = 8;
     while (per > 1 && tiles * ((heads + per - 1) / per) < sms / 2) per /= 2;
     a->heads_per_cta = per;
-    const dim3 grid((unsigned)tiles, (unsigned)((heads + per - 1) / per));
+    cudaLaunchAttribute early = set_up_early();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles, (unsigned)((heads + per - 1) / per));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = a->stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
     void (*kernel)(RowsLaunch) = a->bf16 ? (a->interleaved ? rows_kernel<true, true> : rows_kernel<true, false>)
                                          : (a->interleaved ? rows_kernel<false, true> : rows_kernel<false, false>);
-    kernel<<<grid, kThreads, 0, a->stream>>>(*a);
-    return cudaGetLastError() == cudaSuccess ? TSA_OK : TSA_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, kernel, *a));
 }
 
 }  // namespace tsa

@@ -477,4 +477,7 @@ __device__ __forceinline__ void widen8(const uint4 &w, float (&x)[8]) {
     }
 }
 
+// The end of the kernel before this one in its stream, all it wrote visible (at once where it has ended already).
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace tsa

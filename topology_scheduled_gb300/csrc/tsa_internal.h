@@ -77,6 +77,22 @@ inline bool allow_smem(std::atomic<unsigned long long> &done, const void *kernel
     return true;
 }
 
+// A launch's status; its error is not left for whoever asks the runtime next.
+inline tsa_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return TSA_OK;
+    (void)cudaGetLastError();
+    return TSA_ERR_CUDA;
+}
+
+// Launch attribute: the kernel may be set up while the one before it in its stream still runs, and waits for the end
+// of that one (wait_for_predecessor) before it reads or writes anything.  Saves 2.5 us between two kernels.
+inline cudaLaunchAttribute set_up_early() {
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
 struct AttnLaunch {
     const CUtensorMap *tmQ, *tmK, *tmV, *tmO;
     const CUtensorMap *tmO2;  // differential: the second map's output (otherwise tmO again)
