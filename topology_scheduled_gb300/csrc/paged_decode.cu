@@ -2,8 +2,8 @@
 // o = softmax(scale q.k) V over the sequence's keys, or those of the blocks its row of a schedule lists.
 //
 // Bound by memory: 4 D bytes per key and key head.  A key head's queries share them, so the arithmetic,
-// 4 D multiply-adds per key and query, goes to the tensor cores once several queries share a key; the
-// products are small enough for mma.sync (m16n8k16), whose fragments are plain 16-byte pieces of rows:
+// 2 D multiply-adds per key and query, goes to the tensor cores; half to eight multiply-adds a byte are few
+// enough for mma.sync (m16n8k16), whose fragments are pieces of rows as they lie in shared memory:
 //  * a warp takes 16 keys at a time for up to 8 (or 16) queries.  Scores are S^T = K Q^T, keys as rows.  The
 //    order of a contraction is free, so a lane's 16-byte piece of a key serves as two k16 steps' fragment and
 //    the same piece of a query as their other operand;
