@@ -354,3 +354,77 @@ def test_several_host_threads():
         t.join()
     assert not wrong, wrong
     assert tsa.tsa_last_device_status() == 0
+
+
+def test_captured_on_forked_streams():
+    """A capture that forks: keys are appended on one stream while queries are rotated on another, and the attention
+    waits for both; a copy and a fill stand before and behind. Replayed on new inputs, it gives what the eager calls give."""
+    B, H, HK, D, page = 4, 8, 4, 64, 32
+    lengths = [333, 70, 1, 128]
+    f = tsa.rotary_frequencies(D)
+    table, pages = page_lists(lengths, page, seed=6)
+    gtable, lens = table.to(DEV), _ints(lengths)
+    pos = (lens - 1)[:, None].contiguous()
+    kc0, vc0 = (_normal(pages, HK, page, D, dtype=torch.float16, seed=i).to(DEV) for i in (1, 2))
+
+    def inputs(seed):
+        return [_normal(B, n, 1, D, dtype=torch.float16, seed=seed + i).to(DEV) for i, n in enumerate((H, HK, HK))]
+
+    def eager(x):
+        kc, vc = kc0.clone(), vc0.clone()
+        tsa.tsa_paged_append(None, x[1], x[2], kc, vc, gtable, lens, None, f)
+        q = tsa.tsa_rotary(x[0], None, f, pos)
+        return tsa.tsa_paged_attention_decode(q[:, :, 0], kc, vc, gtable, lens)
+
+    held, kc, vc = inputs(100), kc0.clone(), vc0.clone()
+    kept = torch.empty((B, H, D), dtype=torch.float16, device=DEV)
+    eager(held)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        kc.copy_(kc0)
+        vc.copy_(vc0)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            tsa.tsa_paged_append(None, held[1], held[2], kc, vc, gtable, lens, None, f)
+        q = tsa.tsa_rotary(held[0], None, f, pos)
+        main.wait_stream(side)
+        out = tsa.tsa_paged_attention_decode(q[:, :, 0], kc, vc, gtable, lens)
+        kept.copy_(out)
+        out.zero_()
+    for seed in (200, 300, 400):
+        x = inputs(seed)
+        want = eager(x)
+        for a, b in zip(held, x):
+            a.copy_(b)
+        for _ in range(3):
+            kept.fill_(7)
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want)
+    assert tsa.tsa_last_device_status() == 0
+
+
+def test_back_to_back_on_one_buffer():
+    """Calls that follow at once, each reading what the one before wrote (a kernel is set up before its predecessor
+    has ended): a row rotated a hundred times in place, and a cache's one slot rewritten between its readers."""
+    f = [0.25] * 8
+    x = _normal(1, 64, 200, 64, dtype=torch.float16, seed=1).to(DEV)
+    want = x.clone()
+    for _ in range(100):
+        want = tsa.tsa_rotary(want, None, f)
+        torch.cuda.synchronize()
+    for _ in range(100):
+        tsa.tsa_rotary(x, None, f, out=x)
+    assert torch.equal(x, want)
+    kc = torch.zeros((1, 1, 16, 64), dtype=torch.float16, device=DEV)
+    vc = torch.zeros_like(kc)
+    table, lens = _ints([[0]]), _ints([1])
+    q = torch.ones((1, 1, 64), dtype=torch.float16, device=DEV)
+    values = torch.arange(1, 501, device=DEV).half()[:, None, None, None, None].expand(500, 1, 1, 1, 64).contiguous()
+    got = []
+    for i in range(500):
+        tsa.tsa_paged_append(None, values[i], values[i], kc, vc, table, lens)
+        got.append(tsa.tsa_paged_attention_decode(q, kc, vc, table, lens))
+    assert torch.equal(torch.cat(got)[:, 0], values[:, 0, 0, 0])
