@@ -352,18 +352,29 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
                     lo[i][s][h] = transpose8(lo[i][s][h]);
                 }
         }
+        // A tensor core rounds its sums towards 0, by up to 2^-23 of what they hold: a step's own sum is small, the smaller
+        // products go first, and it is added to the row's rounded to the nearest.
 #pragma unroll
-        for (int s = 0; s < kSub; ++s) {
+        for (int j = 0; j < kTiles; ++j) {
+            float step[kGroups][4];
 #pragma unroll
-            for (int j = 0; j < kTiles; ++j) {
+            for (int i = 0; i < kGroups; ++i) step[i][0] = step[i][1] = step[i][2] = step[i][3] = 0.f;
+#pragma unroll
+            for (int s = 0; s < kSub; ++s) {
                 uint32_t v[4];
                 load_transposed(v_row + stage + s * 2048 + (v_piece ^ (j << 5 & 96)) + (j << 5 & ~96), v);
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
-                    mma<kBF16>(acc[i][j], v[0], v[1], v[2], v[3], hi[i][s][0], hi[i][s][1]);
-                    mma<kBF16>(acc[i][j], v[0], v[1], v[2], v[3], lo[i][s][0], lo[i][s][1]);
+                    mma<kBF16>(step[i], v[0], v[1], v[2], v[3], lo[i][s][0], lo[i][s][1]);
+                    mma<kBF16>(step[i], v[0], v[1], v[2], v[3], hi[i][s][0], hi[i][s][1]);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2)
+                    f2_unpack(f2_add(f2_pack(acc[i][j][e], acc[i][j][e + 1]), f2_pack(step[i][e], step[i][e + 1])), acc[i][j][e],
+                              acc[i][j][e + 1]);
         }
         __syncwarp();  // the stage may be written again
     }
