@@ -109,9 +109,10 @@ tsa_status tsa_paged_append(const void *Q, const void *K, const void *V, const i
  *   workspace     >= tsa_paged_attention_decode_workspace_bytes(..) bytes, 256-byte aligned, or NULL where
  *                 that is 0; its contents on entry do not matter.  Calls that may run at the same time,
  *                 captured graphs among them, need one each.
- * Scores, weights and sums are binary32; a weight meets V as the sum of two numbers of `dtype`.  The result
- * does not depend on the order in which thread blocks run.  A NaN or +inf score makes the row NaN; V must be
- * finite in every key that is listed, also where a score of -inf leaves the key without weight.
+ * Scores, weights and sums are binary32; a weight meets V as a sum of numbers of `dtype`, in bf16 all of it, in f16
+ * all but 2^-22 of it or 2^-39 of the row's largest.  The result does not depend on the order in which thread blocks
+ * run.  A NaN or +inf score makes the row NaN; V must be finite in every key that is listed, also where a score of
+ * -inf leaves the key without weight.
  *
  * Limits: block in {32, 64, 128}, D in {64, 128}, H a multiple of HK, B * H <= 65535, page sizes and tables as
  * for tsa_paged_append, scale >= 1e-30.  Errors: those of tsa_paged_append and CAPACITY; on the device

@@ -9,9 +9,10 @@
 //    the same piece of a query as their other operand;
 //  * O^T = V^T P^T, dimensions as rows.  V^T's fragment is read transposed (ldmatrix.trans); P^T's is the scores'
 //    fragment, transposed (movmatrix);
-//  * a weight is the sum of two numbers of the inputs' type, each with a product of its own, so weights keep
-//    16 (bf16) or 22 bits; in f16 they are scaled by 2^14 beforehand, so that none above 2^-38 of the largest
-//    vanishes.  Sums, maxima and denominators are binary32;
+//  * a weight is a sum of numbers of the inputs' type, each with a product of its own. Three of bf16 are the weight itself,
+//    all 24 bits: values that cancel would show the 2^-17 that two lose. Two of f16 are off by 2^-22 of it at most, no more
+//    than exp2 is; they are scaled by 2^14 beforehand, so that what is lost is below 2^-39 of the largest weight however
+//    small the weight is.  Sums, maxima and denominators are binary32;
 //  * a warp copies its keys and values to a ring of its own in shared memory (cp.async), two steps ahead of
 //    the one it works on: up to 24 KB in flight per warp, whatever the registers hold.  16 keys of a page are
 //    one contiguous 2 D x 16 byte piece; its 16-byte pieces are stored with bits of the row's number
@@ -88,19 +89,22 @@ __device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&x)[4]) {
                  : "memory");
 }
 
-// Two weights as a word of their roundings to the inputs' type and a word of what those leave.
-template <bool kBF16>
-__device__ __forceinline__ void two_parts(float a, float b, uint32_t &hi, uint32_t &lo) {
-    if constexpr (kBF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
-    } else {
-        const __half2 h = __floats2half2_rn(a, b);
-        const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&l);
+// Two weights as words of the inputs' type whose sum they are: their roundings, and then the roundings of what is left.
+template <bool kBF16, int kParts>
+__device__ __forceinline__ void in_parts(float a, float b, uint32_t (&w)[kParts]) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        if constexpr (kBF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            a -= __low2float(h);
+            b -= __high2float(h);
+        } else {
+            const __half2 h = __floats2half2_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            a -= __low2float(h);
+            b -= __high2float(h);
+        }
     }
 }
 
@@ -122,6 +126,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     constexpr int kTiles = D / 16; // m16 tiles of the output's dimensions
     constexpr int kQ = 8 * kGroups;
     constexpr int kBatch = 32 / kSub;  // a warp's steps whose places it looks up at once
+    constexpr int kParts = kBF16 ? 3 : 2;  // numbers that a weight is the sum of
     // A weight is at most 2^(kLift + kSlack) as it is rounded: 2^15 in f16, whose weights are lifted.
     constexpr float kLift = kBF16 ? 0.f : 14.f, kSlack = kBF16 ? 8.f : 1.f;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -329,7 +334,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
                     m[i][e] = to;
                 }
         }
-        uint32_t hi[kGroups][kSub][2], lo[kGroups][kSub][2];
+        uint32_t w[kGroups][kSub][2][kParts];
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             float p[kSub][4];
@@ -347,9 +352,9 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
             for (int s = 0; s < kSub; ++s)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    two_parts<kBF16>(p[s][2 * h], p[s][2 * h + 1], hi[i][s][h], lo[i][s][h]);
-                    hi[i][s][h] = transpose8(hi[i][s][h]);
-                    lo[i][s][h] = transpose8(lo[i][s][h]);
+                    in_parts<kBF16>(p[s][2 * h], p[s][2 * h + 1], w[i][s][h]);
+#pragma unroll
+                    for (uint32_t &x : w[i][s][h]) x = transpose8(x);
                 }
         }
         // A tensor core rounds its sums towards 0, by up to 2^-23 of what they hold: a step's own sum is small, the smaller
@@ -364,10 +369,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
                 uint32_t v[4];
                 load_transposed(v_row + stage + s * 2048 + (v_piece ^ (j << 5 & 96)) + (j << 5 & ~96), v);
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i) {
-                    mma<kBF16>(step[i], v[0], v[1], v[2], v[3], lo[i][s][0], lo[i][s][1]);
-                    mma<kBF16>(step[i], v[0], v[1], v[2], v[3], hi[i][s][0], hi[i][s][1]);
-                }
+                for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+                    for (int k = kParts - 1; k >= 0; --k)
+                        mma<kBF16>(step[i], v[0], v[1], v[2], v[3], w[i][s][0][k], w[i][s][1][k]);
             }
 #pragma unroll
             for (int i = 0; i < kGroups; ++i)
