@@ -148,14 +148,14 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
     for (int m = 0; m < kGroups; ++m)
 #pragma unroll
         for (int c = 0; c < kVec; ++c)
-            q[m][c] = 8 * m + g < queries ? __ldg(reinterpret_cast<const uint4 *>(
-                                                a.Q + ((long long)b * a.H + first_q + 8 * m + g) * D + t * 8 + 32 * c))
+            q[m][c] = 8 * m + g < queries ? *reinterpret_cast<const uint4 *>(
+                                                a.Q + ((long long)b * a.H + first_q + 8 * m + g) * D + t * 8 + 32 * c)
                                           : make_uint4(0u, 0u, 0u, 0u);
 
-    int len = __ldg(a.lens + b), first = 0, entries = 0;
+    int len = a.lens[b], first = 0, entries = 0;
     if (a.row_ptr) {
-        first = __ldg(a.row_ptr + b);
-        entries = __ldg(a.row_ptr + b + 1) - first;
+        first = a.row_ptr[b];
+        entries = a.row_ptr[b + 1] - first;
     }
     const int per_block = a.block / 16, cap = a.max_pages << a.page_shift, nb = (cap + a.block - 1) / a.block;
     if (len < 0 || len > cap) {
@@ -179,7 +179,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
         if (a.row_ptr) {
             if (u >= n16) return;
             const int e = (int)u / per_block, *entry = a.col_idx + first + e;
-            const int j = __ldg(entry), before = e > 0 ? __ldg(entry - 1) : -1;
+            const int j = *entry, before = e > 0 ? entry[-1] : -1;
             if (j < 0 || j >= nb || j <= before) {
                 raise_status(a.flags, kDevBadSchedule);
                 return;
@@ -187,7 +187,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeLaunch a) {
             k = (long long)j * a.block + u % per_block * 16;
         }
         if (k >= cap) return;
-        const int p = __ldg(a.page_table + (long long)b * a.max_pages + (k >> a.page_shift));
+        const int p = a.page_table[(long long)b * a.max_pages + (k >> a.page_shift)];
         if (k >= len) return;
         if (p < 0 || p >= a.num_pages) {
             raise_status(a.flags, kDevBadSchedule);

@@ -93,13 +93,13 @@ rows_kernel(const __grid_constant__ RowsLaunch a) {
     bool there = true;             // the row is a token's
     long long page = -1, slot = 0; // where it goes in the cache
     if (a.seq_lens) {
-        const int len = __ldg(a.seq_lens + b), fresh = a.counts ? __ldg(a.counts + b) : a.S;
+        const int len = a.seq_lens[b], fresh = a.counts ? a.counts[b] : a.S;
         const bool bad = len < 0 || len > (a.max_pages << a.page_shift) || fresh < 0 || fresh > a.S;
         position = len - fresh + s;
         there = !bad && s < fresh && position >= 0;
         if (bad && s == 0 && unit == 0 && blockIdx.y == 0) raise_status(a.flags, kDevBadSchedule);
         if (there) {
-            page = __ldg(a.page_table + (long long)b * a.max_pages + (position >> a.page_shift));
+            page = a.page_table[(long long)b * a.max_pages + (position >> a.page_shift)];
             slot = position & ((1 << a.page_shift) - 1);
             if (page < 0 || page >= a.num_pages) {
                 if (unit == 0 && blockIdx.y == 0) raise_status(a.flags, kDevBadSchedule);
@@ -107,7 +107,7 @@ rows_kernel(const __grid_constant__ RowsLaunch a) {
             }
         }
     } else if (a.positions) {
-        position = __ldg(a.positions + (a.position_rows > 1 ? (long long)b * a.S : 0) + s);
+        position = a.positions[(a.position_rows > 1 ? (long long)b * a.S : 0) + s];
     }
 
     // Vectors of the unit: two of the rotated part, R / 2 apart, or two of the copied rest.

@@ -478,6 +478,8 @@ __device__ __forceinline__ void widen8(const uint4 &w, float (&x)[8]) {
 }
 
 // The end of the kernel before this one in its stream, all it wrote visible (at once where it has ended already).
+// What is read after it is read by ordinary loads: those of the read-only path (__ldg) are for memory that nothing writes while
+// the kernel is there, and this one was there, if waiting, while its predecessor wrote.
 __device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace tsa
