@@ -165,7 +165,9 @@ struct Rotary : torch::autograd::Function<Rotary> {
             if (grads[i].defined() && ctx->needs_input_grad(i)) wanted[n++] = i;
         if (n == 0) return back;
         if (c10::GradMode::is_enabled()) {
-            const auto r = Rotary::apply(grads[wanted[0]], n == 2 ? std::optional<Tensor>(grads[wanted[1]]) : std::nullopt,
+            // (a copy of a gradient in another layout is part of the graph)
+            const auto r = Rotary::apply(readable(grads[wanted[0]]),
+                                         n == 2 ? std::optional<Tensor>(readable(grads[wanted[1]])) : std::nullopt,
                                          at.defined() ? std::optional<Tensor>(at) : std::nullopt, f, interleaved, magnitude,
                                          inverse);
             for (int i = 0; i < n; ++i) back[wanted[i]] = r[i];
