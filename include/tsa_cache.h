@@ -45,8 +45,10 @@ extern "C" {
  *                 value, negative ones too.  NULL: 0 .. S - 1.
  *   frequencies   in,  R / 2 binary64 in HOST memory, read during the call: finite, |f| <= 65536.
  *   Q_out, K_out  out, shaped as Q and K.  They may be Q and K themselves, with the same strides;
- *                 otherwise outputs share no memory with an input or one another (rows of one array that
- *                 alternate, as the heads of Q and K in a joint projection do, share none).
+ *                 otherwise outputs share no memory with an input or one another.  Tensors whose rows lie in
+ *                 one another's gaps, as parts of a joint projection do ([B, S, H + 2 HK, D], [B, S, H, 3, D],
+ *                 [B, H + 2 HK, S, D]), share none; they need the same strides, a batch's a multiple of a
+ *                 token's or the reverse.
  * Angles are kept as 64-bit fractions of a turn: |p| 2^-65 turns off at most, whatever the position;
  * products and sums are binary32, results rounded once.
  *

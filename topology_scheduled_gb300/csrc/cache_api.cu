@@ -12,17 +12,17 @@ namespace {
 
 static_assert(kMaxRotaryDim == TSA_MAX_ROTARY_DIM, "the header's limit");
 
-// Memory of rows: `inner` contiguous-enough elements (a row's heads, a page) repeated over two strided axes.
+// Memory of rows: `inner` contiguous elements repeated over strided axes (batch, head and token; a cache's pages).
 struct Field {
     const void *p = nullptr;
-    int64_t n[2] = {1, 1}, stride[2] = {0, 0}, inner = 0;  // elements of 2 bytes
+    int64_t n[3] = {1, 1, 1}, stride[3] = {0, 0, 0}, inner = 0;  // elements of 2 bytes
 };
 
 constexpr int64_t kMaxExtent = int64_t{1} << 58;  // elements: no sum of offsets below overflows
 
 bool extent(const Field &f, int64_t *elements) {
     __int128 e = f.inner;
-    for (int i = 0; i < 2; ++i) e += (__int128)(f.n[i] - 1) * f.stride[i];
+    for (int i = 0; i < 3; ++i) e += (__int128)(f.n[i] - 1) * f.stride[i];
     *elements = (int64_t)e;
     return e <= kMaxExtent;
 }
@@ -33,26 +33,60 @@ Span span_of(const Field &f) {
     return {f.p, (size_t)e * 2};
 }
 
-// Whether two fields share no memory: their extents do not meet, or both repeat with the same strides and
-// the shorter period holds one's elements beside the other's.
+// Two fields that repeat with the same strides, largest first.
+struct Pair {
+    int64_t na[3], nb[3], stride[3], inner_a, inner_b;
+
+    // Whether rows of the axes from `axis` on meet, b's `delta` elements behind a's.  The axis's steps count only as far
+    // as what is left of a and b reaches: two where one of the fields does not overlap itself.  (More are not looked
+    // into, and taken to meet.)
+    bool meet(int axis, int64_t delta) const {
+        int64_t ea = inner_a, eb = inner_b;
+        for (int i = axis; i < 3; ++i) {
+            ea += (na[i] - 1) * stride[i];
+            eb += (nb[i] - 1) * stride[i];
+        }
+        if (delta >= ea || delta <= -eb) return false;
+        if (axis == 3) return true;
+        const int64_t s = stride[axis];
+        if (s == 0) return meet(axis + 1, delta);
+        // steps d from a's to b's, -na < d < nb, whose distance delta + d s is between what is left of b and of a
+        const int64_t ra = ea - (na[axis] - 1) * s, rb = eb - (nb[axis] - 1) * s;
+        const auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+        const int64_t low = std::max(1 - na[axis], floor_div(-rb - delta, s) + 1);
+        const int64_t high = std::min(nb[axis] - 1, -floor_div(delta - ra, s) - 1);
+        if (high - low > 3) return true;
+        for (int64_t d = low; d <= high; ++d)
+            if (meet(axis + 1, delta + d * s)) return true;
+        return false;
+    }
+};
+
+// Whether two fields share no memory: their extents do not meet, or both repeat with the same strides, of which the
+// batch's is a multiple of the token's or the reverse, and no row of one is a row of the other.
 bool apart(const Field &a, const Field &b) {
     if (!a.p || !b.p) return true;
     const Span x = span_of(a), y = span_of(b);
     if (!overlaps(x.p, x.bytes, y.p, y.bytes)) return true;
-    int64_t period = 0;
-    for (int i = 0; i < 2; ++i) {
-        if (a.n[i] != b.n[i]) return false;
-        if (a.n[i] == 1) continue;
-        if (a.stride[i] != b.stride[i] || a.stride[i] <= 0) return false;
-        period = period == 0 ? a.stride[i] : std::min(period, a.stride[i]);
+    Pair pair;
+    int64_t stride[3];
+    for (int i = 0; i < 3; ++i) {  // (an axis of one has no stride)
+        if (a.n[i] > 1 && b.n[i] > 1 && a.stride[i] != b.stride[i]) return false;
+        stride[i] = a.n[i] > 1 ? a.stride[i] : b.n[i] > 1 ? b.stride[i] : 0;
     }
-    if (period == 0) return false;
-    for (int i = 0; i < 2; ++i)
-        if (a.n[i] > 1 && a.stride[i] % period != 0) return false;
-    const int64_t pa = (int64_t)reinterpret_cast<uintptr_t>(a.p), pb = (int64_t)reinterpret_cast<uintptr_t>(b.p);
-    int64_t delta = (pb - pa) % (2 * period);  // bytes from a's elements to b's, within a period
-    if (delta < 0) delta += 2 * period;
-    return delta >= 2 * a.inner && delta + 2 * b.inner <= 2 * period;
+    const int64_t low = std::min(stride[0], stride[2]), high = std::max(stride[0], stride[2]);
+    if (low > 0 && high % low != 0) return false;
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int i, int j) { return stride[i] > stride[j]; });
+    for (int i = 0; i < 3; ++i) {
+        pair.na[i] = a.n[order[i]];
+        pair.nb[i] = b.n[order[i]];
+        pair.stride[i] = stride[order[i]];
+    }
+    pair.inner_a = a.inner;
+    pair.inner_b = b.inner;
+    const auto bytes = reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p);
+    return !pair.meet(0, bytes / 2);
 }
 
 struct Rows {
@@ -62,11 +96,10 @@ struct Rows {
     Field field(int64_t B, int64_t S, int64_t D) const {
         Field f;
         f.p = p;
-        f.n[0] = B;
-        f.n[1] = S;
-        f.stride[0] = stride[0];
-        f.stride[1] = stride[2];
-        f.inner = (heads - 1) * stride[1] + D;
+        const int64_t n[3] = {B, heads, S};
+        std::copy(n, n + 3, f.n);
+        std::copy(stride, stride + 3, f.stride);
+        f.inner = D;
         return f;
     }
     bool same(const Rows &o) const {
