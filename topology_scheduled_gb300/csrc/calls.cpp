@@ -198,7 +198,7 @@ Pages check_pages(const Tensor &Kc, const Tensor &Vc, const Tensor &table, const
     const int64_t size = Kc.size(2);
     for (const Tensor *t : {&Kc, &Vc}) {
         TORCH_CHECK_VALUE(t->sizes() == Kc.sizes() && t->scalar_type() == like.scalar_type() && t->device() == like.device() &&
-                              t->stride(1) == size * D && t->stride(2) == D && t->stride(3) == 1,
+                              (HK == 1 || t->stride(1) == size * D) && t->stride(2) == D && t->stride(3) == 1,
                           t == &Kc ? "K_cache" : "V_cache",
                           " must be a [pages, HK, page_size, D] tensor of the inputs' type and device, its pages contiguous");
     }
