@@ -6,7 +6,9 @@
 
 Like the calls of ``binding`` they run in libtsa.so on the current stream (or ``stream``) and
 raise when a call fails; there is no fallback. Their arguments are checked and marshalled in
-csrc/calls.cpp: single tokens are too short for the interpreter.
+csrc/calls.cpp: single tokens are too short for the interpreter. They have no gradients
+(``autograd.rotary`` has): a tensor that they write in place may require none while gradients
+are recorded, and counts as changed where autograd has kept it for a backward pass.
 """
 from __future__ import annotations
 

@@ -60,10 +60,22 @@ void check_rows(const char *name, const Tensor &t, const Tensor *like = nullptr)
     }
 }
 
+// A tensor that a call writes in place: there is no gradient of that.
+void check_written(const char *name, const Tensor &t) {
+    TORCH_CHECK_VALUE(!t.defined() || !t.requires_grad() || !c10::GradMode::is_enabled(), name,
+                      " requires a gradient, and is written in place, without one");
+}
+
+// It was written: autograd will notice if it had kept it for a backward pass.  (Inference tensors keep no versions.)
+void written_to(const Tensor &t) {
+    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // `t`, or a new contiguous tensor shaped as `like`.
 Tensor rows_out(const char *name, const Tensor &t, const Tensor &like) {
     if (!t.defined()) return at::empty(like.sizes(), like.options());
     check_rows(name, t, &like);
+    check_written(name, t);
     TORCH_CHECK_VALUE(t.sizes() == like.sizes(), name, " must have the shape ", like.sizes());
     return t;
 }
@@ -111,6 +123,8 @@ std::array<Tensor, 2> rotary(const Tensor &Q, const Tensor &K, Frequencies f, co
                      inverse, written(q), written(k), dtype, B, Q.size(1),
                      K.defined() ? K.size(1) : 0, S, Q.size(3), stream_of(Q)),
           "tsa_rotary");
+    written_to(out);
+    written_to(out_k);
     return {q, k};
 }
 
@@ -223,6 +237,8 @@ Tensor paged_append(const Tensor &Q, const Tensor &K, const Tensor &V, const Ten
         TORCH_CHECK_VALUE(!out.defined(), "out without Q");
     }
     const Pages p = check_pages(Kc, Vc, table, lens, B, HK, D, K);
+    check_written("K_cache", Kc);
+    check_written("V_cache", Vc);
     const int32_t *const fresh = counts.defined() ? check_list("counts", counts, {B}, K) : nullptr;
     const tsa_dtype dtype = dtype_of(K);
     const Tensor q = Q.defined() ? rows_out("out", out, Q) : Tensor();
@@ -236,6 +252,7 @@ Tensor paged_append(const Tensor &Q, const Tensor &K, const Tensor &V, const Ten
                            f ? f->values : nullptr, f ? 2 * f->n : 0, interleaved, (float)magnitude, written(q),
                            dtype, B, Q.defined() ? Q.size(1) : 0, HK, T, D, stream_of(K)),
           "tsa_paged_append");
+    for (const Tensor *t : {&Kc, &Vc, &out}) written_to(*t);
     return q;
 }
 
@@ -265,6 +282,7 @@ Tensor paged_decode(const Tensor &Q, const Tensor &Kc, const Tensor &Vc, const T
         TORCH_CHECK_VALUE(out.sizes() == Q.sizes() && out.scalar_type() == Q.scalar_type() && out.device() == Q.device() &&
                               out.is_contiguous(),
                           "out must be a contiguous tensor of Q's type, shape and device");
+        check_written("out", out);
     }
     const Tensor o = out.defined() ? out : at::empty(Q.sizes(), Q.options());
     const size_t need = tsa_paged_attention_decode_workspace_bytes(B, H, HK, D, p.size, p.most, block, nnz);
@@ -280,6 +298,7 @@ Tensor paged_decode(const Tensor &Q, const Tensor &Kc, const Tensor &Vc, const T
                                      (float)(scale ? *scale : 1.0 / std::sqrt((double)D)), written(w),
                                      w.defined() ? (size_t)w.numel() : 0, stream_of(Q)),
           "tsa_paged_attention_decode");
+    written_to(out);
     return o;
 }
 
