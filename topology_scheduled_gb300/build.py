@@ -32,9 +32,9 @@ HEADERS = [os.path.join(CSRC, h) for h in ("attention_kernel.cuh", "backward_ker
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # the CUDA runtime is the one PyTorch has loaded: a second, static one beside it costs 2 us per call
 LINK = ARCH + ["-cudart", "shared", "-shared"]
-FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
-
-
+FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC"]
+CALLS_FLAGS = ["-O2", "-std=c++17", "-fPIC"]
+CALLS_LINK = ["-shared", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-l:libtsa.so", "-Wl,-rpath,$ORIGIN"]
 
 
 def _calls_flags() -> tuple[list[str], list[str]]:
@@ -44,10 +44,9 @@ def _calls_flags() -> tuple[list[str], list[str]]:
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
-    return (["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"] +
+    return (CALLS_FLAGS + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"] +
             [x for d in include for x in ("-I", d)],
-            ["-shared", "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
-             "-L", BUILD, "-l:libtsa.so", "-Wl,-rpath,$ORIGIN"])
+            ["-L", os.path.join(home, "lib"), "-L", BUILD] + CALLS_LINK)
 
 
 def _nvcc() -> str:
@@ -58,13 +57,14 @@ def _nvcc() -> str:
 
 
 def _digest() -> str:
+    """Of the sources, the flags and the interpreter and PyTorch that tsa_calls.so is for; of no folder, so that a built
+    tree may be moved, and used where there is no compiler."""
+    import torch
     h = hashlib.sha1()
     for p in [os.path.join(CSRC, s) for s in SOURCES + ["calls.cpp"]] + HEADERS:
         with open(p, "rb") as f:
             h.update(f.read())
-    flags, link = _calls_flags()
-    import torch
-    h.update(" ".join(FLAGS + LINK + flags + link + [torch.__version__]).encode())
+    h.update(" ".join(FLAGS + LINK + CALLS_FLAGS + CALLS_LINK + [torch.__version__, sys.version]).encode())
     return h.hexdigest()[:16]
 
 
@@ -81,7 +81,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [nvcc] + FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [nvcc] + FLAGS + ["-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         r = subprocess.run(cmd, capture_output=True, text=True)
