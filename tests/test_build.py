@@ -2,7 +2,6 @@
 import os
 import shutil
 
-import topology_scheduled_gb300 as tsa
 from topology_scheduled_gb300 import build
 
 
@@ -11,7 +10,7 @@ def _gone(*_):
 
 
 def test_a_built_library_needs_no_compiler(monkeypatch):
-    tsa.lib()
+    build.build()
     before = os.stat(build.LIB).st_mtime_ns
     monkeypatch.setattr(build, "_nvcc", _gone)
     monkeypatch.setattr(build.subprocess, "run", _gone)

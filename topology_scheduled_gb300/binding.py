@@ -109,7 +109,7 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
         if _LIB is None:
             path = _build.LIB
             if build_if_missing:
-                path = _build.build()
+                path = _build.build_library()
             if not os.path.exists(path):
                 raise RuntimeError(f"libtsa.so is not built ({path}); run "
                                    "`python -m topology_scheduled_gb300.build`")
@@ -123,12 +123,13 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
 
 
 def calls():
-    """The loaded module of the calls that are marshalled natively (csrc/calls.cpp)."""
+    """The loaded module of the calls that are marshalled natively (csrc/calls.cpp; built on first use, too)."""
     global _CALLS
     if _CALLS is None:
-        lib()  # built with it
+        lib()
         with _LOCK:
             if _CALLS is None:
+                _build.build_calls(library=library_path)  # the one that is loaded
                 spec = importlib.util.spec_from_file_location("tsa_calls", _build.CALLS)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)

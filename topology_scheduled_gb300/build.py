@@ -56,27 +56,42 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libtsa")
 
 
-def _digest() -> str:
-    """Of the sources, the flags and the interpreter and PyTorch that tsa_calls.so is for; of no folder, so that a built
-    tree may be moved, and used where there is no compiler."""
-    import torch
+def _digest(sources=SOURCES, headers=None, flags=FLAGS + LINK) -> str:
+    """Of sources, headers (None: all) and flags, and of no folder: a built tree may be moved, and used where there is no
+    compiler."""
     h = hashlib.sha1()
-    for p in [os.path.join(CSRC, s) for s in SOURCES + ["calls.cpp"]] + HEADERS:
+    for p in [os.path.join(CSRC, s) for s in sources] + (HEADERS if headers is None else headers):
         with open(p, "rb") as f:
             h.update(f.read())
-    h.update(" ".join(FLAGS + LINK + CALLS_FLAGS + CALLS_LINK + [torch.__version__, sys.version]).encode())
+    h.update(" ".join(flags).encode())
     return h.hexdigest()[:16]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libtsa.so; returns its path."""
+def _stamped(path: str, stamp: str, digest: str) -> bool:
+    """Whether `path` was built from what has this digest."""
+    if not os.path.exists(path) or not os.path.exists(stamp):
+        return False
+    with open(stamp) as f:
+        return f.read().strip() == digest
+
+
+def _linked(cmd: list[str], path: str, stamp: str, digest: str) -> None:
+    tmp = f"{path}.{os.getpid()}.tmp"
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+    with open(stamp, "w") as f:
+        f.write(digest)
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link libtsa.so, which takes nvcc and its host compiler alone; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     stamp = os.path.join(BUILD, "stamp")
     digest = _digest()
-    if not force and os.path.exists(LIB) and os.path.exists(CALLS) and os.path.exists(stamp):
-        with open(stamp) as f:
-            if f.read().strip() == digest:
-                return LIB
+    if not force and _stamped(LIB, stamp, digest):
+        return LIB
     nvcc = _nvcc()
 
     def compile_one(src: str) -> str:
@@ -91,31 +106,42 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    calls_flags, calls_link = _calls_flags()
-    calls_obj = os.path.join(BUILD, "calls.o")
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+        objs = list(ex.map(compile_one, SOURCES))
+    _linked([nvcc] + LINK + objs, LIB, stamp, digest)
+    return LIB
 
-    def compile_calls() -> None:
-        r = subprocess.run(["g++"] + calls_flags + ["-c", os.path.join(CSRC, "calls.cpp"), "-o", calls_obj],
-                           capture_output=True, text=True)
+
+def build_calls(force: bool = False, library=build_library) -> str:
+    """Compile tsa_calls.so and link it with libtsa.so (`library` builds that meanwhile); returns its path.  It takes the
+    headers of Python, PyTorch and the CUDA runtime, and is for this Python and this PyTorch."""
+    import torch
+    os.makedirs(BUILD, exist_ok=True)
+    stamp, obj = os.path.join(BUILD, "calls.stamp"), os.path.join(BUILD, "calls.o")
+    digest = _digest(["calls.cpp"], [os.path.join(INCLUDE, h) for h in ("tsa.h", "tsa_cache.h")],
+                     CALLS_FLAGS + CALLS_LINK + [torch.__version__, sys.version])
+    if not force and _stamped(CALLS, stamp, digest):
+        library()
+        return CALLS
+
+    def compile_calls() -> list[str]:
+        flags, link = _calls_flags()
+        r = subprocess.run(["g++"] + flags + ["-c", os.path.join(CSRC, "calls.cpp"), "-o", obj], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed on calls.cpp:\n{r.stdout}\n{r.stderr}")
+        return link
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls_done = ex.submit(compile_calls)
-        objs = list(ex.map(compile_one, SOURCES))
-        calls_done.result()
-    tmp = f"{LIB}.{os.getpid()}.tmp"
-    r = subprocess.run([nvcc] + LINK + ["-o", tmp] + objs, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = f"{CALLS}.{os.getpid()}.tmp"
-    r = subprocess.run(["g++", calls_obj, "-o", tmp] + calls_link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
-    with open(stamp, "w") as f:
-        f.write(digest)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        compiled = ex.submit(compile_calls)
+        library()
+        link = compiled.result()
+    _linked(["g++", obj] + link, CALLS, stamp, digest)
+    return CALLS
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Build libtsa.so and tsa_calls.so; returns libtsa.so's path."""
+    build_calls(force, lambda: build_library(force, verbose))
     return LIB
 
 
