@@ -28,8 +28,9 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str |
     ``"linear"`` divides every frequency by factor; ``"base"`` enlarges the base to
     base * factor ** (rotary_dim / (rotary_dim - 2)), which divides the last pair's by factor and leaves the
     first pair's; ``"ramp"`` divides the pairs that turn less than ``low`` times in original_length tokens,
-    leaves those that turn more than ``high`` times, and blends linearly between (its attention is sharpened
-    by ``rotary_magnitude``)."""
+    leaves those that turn more than ``high`` times, and blends between, linearly in the number of turns (its
+    attention is sharpened by ``rotary_magnitude``). A model trained with another blend, such as one that is
+    linear in the pair's number, is given its own frequencies: the calls take any."""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and positive")
     if not base > 0 or not factor > 0 or not math.isfinite(base) or not math.isfinite(factor):

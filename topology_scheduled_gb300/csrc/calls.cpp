@@ -2,9 +2,9 @@
 // tensors, outputs and workspaces from PyTorch's allocator, and the C entry points of include/tsa_cache.h.
 //
 // These calls serve single tokens, whose kernels take 3 to 20 us: marshalled in Python (ctypes) a call took 18 to
-// 25 us of the host, here it takes 6 to 9.  The rotation's gradient is a C++ node of the autograd graph, so that a
+// 25 us of the host, here it takes 7 to 9.  The rotation's gradient is a C++ node of the autograd graph, so that a
 // backward pass runs it without the interpreter: a training step's call and gradient took 250 us with a Python
-// node, 150 here, where PyTorch's own x * 2 and its gradient take 100.
+// node, 150 to 160 here, where PyTorch's own x * 2 and its gradient take 100.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

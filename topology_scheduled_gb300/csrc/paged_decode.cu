@@ -2,8 +2,9 @@
 // o = softmax(scale q.k) V over the sequence's keys, or those of the blocks its row of a schedule lists.
 //
 // Bound by memory: 4 D bytes per key and key head.  A key head's queries share them, so the arithmetic,
-// 2 D multiply-adds per key and query, goes to the tensor cores; half to eight multiply-adds a byte are few
-// enough for mma.sync (m16n8k16), whose fragments are pieces of rows as they lie in shared memory:
+// 2 D multiply-adds per key and query (4 D in bf16 and 3 D in f16 as issued, a weight's numbers each with a product of their
+// own), goes to the tensor cores; one to sixteen multiply-adds a byte are few enough for mma.sync (m16n8k16), whose fragments
+// are pieces of rows as they lie in shared memory:
 //  * a warp takes 16 keys at a time for up to 8 (or 16) queries.  Scores are S^T = K Q^T, keys as rows.  The
 //    order of a contraction is free, so a lane's 16-byte piece of a key serves as two k16 steps' fragment and
 //    the same piece of a query as their other operand;
@@ -21,9 +22,10 @@
 // are joined through shared memory in a fixed order; where eight blocks a row cannot fill the GPU, several
 // clusters share a row, leave their sums in the workspace, and a second kernel joins them.
 // Keys at the length and beyond are neither read nor counted.
-// Measured (bf16, D = 128): 16 sequences of 8192 keys, 32 heads with keys of their own (2.15 GB) 289-296 us = 7.3 TB/s;
-// 64 ragged ones to 8192, 32 heads on 4, 109 us = 6.5; one of 131072, 32 heads on 8, 83 us = 6.5. A step is 265
-// instructions of a warp (8 queries), 21 % of the issue slots, and the tensor pipe is busy 15 %.
+// Measured (bf16, D = 128): 16 sequences of 8192 keys, 32 heads with keys of their own (2.15 GB) 290-296 us = 7.3 TB/s;
+// 64 ragged ones to 8192, 32 heads on 4, 110 us = 6.4; one of 131072, 32 heads on 8, 82-85 us = 6.4. A step is 305
+// instructions of a warp (8 queries), 24 % of the issue slots, and the tensor pipe is busy 20 %. (With weights of two
+// numbers, and sums left to the tensor cores, 265, 21 and 15 %: 1 to 2 % faster, 14 and 21 % with 16 and 32 queries a key.)
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -517,11 +519,13 @@ void split_paged_decode(PagedDecodeLaunch *a) {
     const long long keys = a->nnz_cap > 0 ? std::min(cap, ((long long)a->nnz_cap * a->block + a->B - 1) / a->B) : cap;
     const long long steps = (keys + kStep - 1) / kStep;  // of a row
     // Thread blocks per row.  As many as the GPU holds at once (two per multiprocessor, 32 clusters of eight)
-    // while every warp has a step, clusters first: us with 1 / 2 / 4 / 8 of them, 16 rows of 32 steps 8.1 / 6.3 /
-    // 5.0 / 4.9; 128 rows of 86 steps 19.4 / 17.3 / 22.1 / 30.2; with 1 / 4 clusters of eight, 8 rows of 8192 steps
-    // 161 / 85, of 256 steps 9.6 / 8.6.  Four times as many where each warp is left 24 steps and the blocks would
-    // not fill their last wave, so that short and long rows even out: 256 ragged rows of 384 steps 119 -> 111, 32
-    // of 6000 steps 212 -> 191; but 512 rows of 512 steps 290 -> 296, 256 of 250 steps 76 -> 78.
+    // while every warp has a step, clusters first: us with 1 / 2 / 4 / 8 of them, 16 rows of 32 steps 7.9 / 6.7 /
+    // 5.2 / 5.3; 128 ragged rows of 86 steps 17.2 / 16.7 / 20.3 / 28.6 (all of one length 18.6 / 19.2 / 23.3 / 31.6); with
+    // 1 / 4 clusters of eight, 8 rows of 8192 steps 139 / 83, of 256 steps 9.0 / 7.7.  Four times as many where each warp is
+    // left 24 steps and the blocks would not fill their last wave, so that short and long rows even out: 256 ragged rows
+    // of 384 steps 119 -> 110, 32 of 6000 steps, some empty, 206 -> 191 (none empty 257 -> 257); but 512 rows of 512 steps
+    // 295 -> 297, 256 of 250 steps 83 -> 90 (ragged 63.3 -> 62.6).  Rows are taken as alike, and as long as the table is
+    // wide: a long one among short ones has no more thread blocks than they.
     const long long slots = 2 * 152, clusters = 32;
     long long ranks = 1, parts = 1;
     while (ranks < 8 && 2 * ranks * rows <= slots && 2 * ranks * kWarps <= steps) ranks *= 2;
