@@ -84,3 +84,14 @@ def test_rows_of_any_strides():
         taken += got
         refused += not got
     assert taken > 500 and refused > 500
+
+
+@pytest.mark.parametrize("B,S", [(1, 1), (1, 100), (3, 1), (3, 100)])
+def test_heads_of_other_strides(B, S):
+    """[B, S, 4 x 64 + 2 x 128]: Q's heads are 64 elements apart, K's 128, of which the first 64 are rotated."""
+    H, HK, D, token = 4, 2, 64, 512
+    q, k = (S * token, D, token), (S * token, 2 * D, token)
+    if S > 1 or B > 1:
+        assert _rotary(B, S, H, HK, D, q, k, H * D)
+    assert not _rotary(B, S, H, HK, D, q, k, H * D - 8)
+    assert not _rotary(B, S, H, HK, D, q, k, token + D) or (B, S) == (1, 1)

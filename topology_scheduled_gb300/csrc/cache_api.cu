@@ -64,10 +64,16 @@ struct Pair {
 
 // Whether two fields share no memory: their extents do not meet, or both repeat with the same strides, of which the
 // batch's is a multiple of the token's or the reverse, and no row of one is a row of the other.
-bool apart(const Field &a, const Field &b) {
+// (Heads that are not as far apart in both count as one piece, gaps and all.)
+bool apart(Field a, Field b) {
     if (!a.p || !b.p) return true;
     const Span x = span_of(a), y = span_of(b);
     if (!overlaps(x.p, x.bytes, y.p, y.bytes)) return true;
+    if (a.n[1] > 1 && b.n[1] > 1 && a.stride[1] != b.stride[1])
+        for (Field *f : {&a, &b}) {
+            f->inner += (f->n[1] - 1) * f->stride[1];
+            f->n[1] = 1;
+        }
     Pair pair;
     int64_t stride[3];
     for (int i = 0; i < 3; ++i) {  // (an axis of one has no stride)
